@@ -269,6 +269,118 @@ int gptq_linear_fp16(const void *X, int64_t n, int64_t d, const void *W16, int64
                      gptq_stream_t stream);
 
 /*
+ * The packed layer in use: the norm in front of a layer with its result in 8
+ * bits, the product from the packed weights, and an act-order layer's columns
+ * laid out by group for it.  The quantisers are the weights' own ("LLM
+ * 量化技术" §1.2: symmetric, s = max|x| / (2^(bits-1) - 1); asymmetric codes with
+ * integer zero points), and [Card] §计算设置 runs the quantised layers at
+ * inference.
+ *
+ * Types of activations: GPTQ_F16 (IEEE binary16), GPTQ_BF16 (bfloat16),
+ * GPTQ_F32, GPTQ_I8 (signed 8-bit codes).
+ */
+#define GPTQ_F16 0
+#define GPTQ_BF16 1
+#define GPTQ_F32 2
+#define GPTQ_I8 3
+
+/*
+ * gptq_rmsnorm_int8 -- residual addition, root-mean-square norm and symmetric
+ * 8-bit codes with one scale per token:
+ *   h = x + residual, rounded to the type (h = x without a residual)
+ *   u = gamma * h / sqrt(mean(h^2) + eps)
+ *   scale = max|u| / 127 (1 for a row of zeros)
+ *   code = clamp(rint(u / scale), -128, 127), rint to nearest, ties to even
+ *   xhat = scale * code, rounded to the type
+ *
+ *   x, residual, h   device [n x d] of `dtype` (GPTQ_F16 or GPTQ_BF16),
+ *            row-major, 16-byte aligned.  residual may be NULL; h may be NULL
+ *            (not written) and may be x or residual itself.
+ *   gamma    device [d] of `dtype`, 16-byte aligned.
+ *   n, d     n >= 0, d > 0, d % 32 == 0, d <= 65536.
+ *   eps      > 0 and finite.
+ *   perm     device int32 [d] or NULL: codes and xhat are written in the order
+ *            of gptq_regroup, entry j taken from column perm[j] (entries
+ *            outside [0, d) are clamped to it).  h keeps the order of x.
+ *   codes    device int8 [n x d], 16-byte aligned, written.
+ *   scales   device fp32 [n], written.
+ *   xhat     device [n x d] of `dtype`, 16-byte aligned, or NULL.  It may be
+ *            h, x or residual only when it is NULL; the outputs must not
+ *            overlap each other.
+ *   A row with a NaN or an infinity has scale NaN, codes 0 and xhat NaN; other
+ *   rows are not touched by it.  Sums in fp32; a row whose squares leave the
+ *   fp32 range is summed again with scaled values.
+ *   n == 0: nothing to do.  Asynchronous: one kernel.
+ */
+int gptq_rmsnorm_int8(const void *x, const void *residual, const void *gamma, int dtype,
+                      int64_t n, int64_t d, float eps, const int32_t *perm, void *h,
+                      int8_t *codes, float *scales, void *xhat, gptq_stream_t stream);
+
+/*
+ * gptq_packed_linear -- y = x W^^T + bias from the packed layer, without a
+ * dequantised copy of W^ in memory, for any number of tokens:
+ *   y[t, i] = xs[t] * sum_j scales[i, j / group] (q[i, j] - zeros[i, j / group]) x[t, p(j)] + bias[i]
+ * with q the bits-bit code of column j in row i's stream, group 0 for group =
+ * -1, p(j) = perm[j] when perm is given, else j, and xs = x_scales (1 when x
+ * is in 16 bits).
+ *
+ *   x        device [n x d] of `xtype`: GPTQ_F16, GPTQ_BF16 or GPTQ_I8,
+ *            row-major, 16-byte aligned.
+ *   x_scales device fp32 [n] with GPTQ_I8 (as gptq_rmsnorm_int8 writes), NULL
+ *            otherwise.
+ *   qweight, scales, zeros   as gptq_dequant_gemv.  Zero points outside
+ *            [0, 2^bits - 1] are clamped to it.
+ *   perm     device int32 [d] or NULL (act-order layers: gptq_regroup's order;
+ *            entries outside [0, d) are clamped).  With x from
+ *            gptq_rmsnorm_int8 in that order already, pass NULL.
+ *   r, d     r >= 0, d > 0, d % 32 == 0, d <= 65536;  bits 2, 3, 4 or 8;
+ *   group    -1 or a multiple of 32 that divides d.
+ *   bias     device [r] of `ytype`, or NULL.
+ *   y        device [n x r] of `ytype`: `xtype` when x is in 16 bits, GPTQ_F16 or
+ *            GPTQ_BF16 with GPTQ_I8; or GPTQ_F32 with any x.  Element aligned.
+ *   workspace  device scratch of gptq_packed_linear_workspace_bytes(...) bytes,
+ *            256-byte aligned (NULL when the query returns 0); contents on
+ *            entry are ignored.  Calls whose work may overlap need one each.
+ *   Sums in fp32 (exact integers inside a group for GPTQ_I8 and few tokens),
+ *   one rounding to `ytype`.  For few tokens the products use q - z exactly;
+ *   for many, weights s (q - z) are rounded once to the 16-bit type of the
+ *   tensor-core product, as gptq_dequant_fp16 does.  Results do not change
+ *   from call to call.
+ *   n == 0 or r == 0: nothing to do.  Asynchronous; a bounded in-kernel wait
+ *   that runs out is reported by gptq_check_device_status.
+ *
+ * gptq_packed_linear_workspace_bytes: 0 for invalid arguments too.  `permuted`:
+ * whether perm will be given.
+ */
+size_t gptq_packed_linear_workspace_bytes(int64_t n, int64_t r, int64_t d, int bits, int group,
+                                          int xtype, int permuted);
+int gptq_packed_linear(const void *x, int xtype, const float *x_scales, int64_t n,
+                       const int32_t *qweight, const float *scales, const int32_t *zeros,
+                       const int32_t *perm, int64_t r, int64_t d, int bits, int group,
+                       const void *bias, void *y, int ytype, void *workspace,
+                       size_t workspace_bytes, gptq_stream_t stream);
+
+/*
+ * gptq_regroup -- the columns of a packed act-order layer laid out by group
+ *   ([Explainer] §三: desc_act scatters a group's columns over the row): column j
+ *   of the result is column perm[j] of qweight, perm the stable order of the
+ *   columns by g_idx, so that position j belongs to group j / group and
+ *   scales and zeros serve as they are.  Done once per layer.
+ *
+ *   qweight  device int32 [r x d*bits/32];  g_idx device int32 [d], each of the
+ *            d / group groups given to exactly `group` columns (as
+ *            gptq_quantize_layer writes it).
+ *   out      device int32 [r x d*bits/32], written; must not overlap qweight.
+ *   perm     device int32 [d], written.
+ *   r >= 0; d, bits as gptq_dequant_gemv; group a multiple of 32 that divides d.
+ *   Synchronises `stream` once, at the end: a g_idx with another number of
+ *   columns in some group returns GPTQ_ERR_INVALID_ARG (outputs unspecified).
+ *   It cannot be captured into a graph.
+ */
+int gptq_regroup(const int32_t *qweight, const int32_t *g_idx, int64_t r, int64_t d, int bits,
+                 int group, int32_t *out, int32_t *perm, gptq_stream_t stream);
+
+/*
  * gptq_quantize_layer_noalloc -- gptq_quantize_layer for callers that cannot
  * allocate device memory.  (The GPTQ pages have no counterpart: this is a
  * deployment convenience of this library, not a step of the method.)

@@ -24,6 +24,8 @@ from .gptq_ref import (  # noqa: F401
     quant_params,
     quantize,
     quantize_chain,
+    regroup,
+    rmsnorm_int8,
     rtn,
     unpack_rows,
 )

@@ -638,3 +638,25 @@ def quantize_chain(X0: np.ndarray, Ws: list, *, bits: int, group: int, block: in
         if not np.all(np.isfinite(X)):
             raise ValueError("layer outputs overflow fp16")
     return outs
+
+
+# ---------------------------------------------------------------------------
+# The packed layer in use  ("LLM 量化技术" §1.2: the symmetric quantiser, here with
+# 8 bits over one token; "一文读懂GPTQ" §三: desc_act's scattered groups)
+# ---------------------------------------------------------------------------
+
+def rmsnorm_int8(h: np.ndarray, gamma: np.ndarray, eps: float) -> tuple[np.ndarray, np.ndarray]:
+    """(codes int64 [n x d], scales [n]) of u = gamma * h / sqrt(mean(h^2) + eps) per row:
+    scale = max|u| / 127 (1 for a zero row), code = clamp(rint(u / scale), -128, 127)."""
+    h = np.asarray(h, dtype=F64)
+    u = np.asarray(gamma, dtype=F64) * h / np.sqrt(np.mean(h * h, axis=1, keepdims=True) + eps)
+    top = np.abs(u).max(axis=1)
+    scales = np.where(top > 0, top / 127.0, 1.0)
+    codes = np.clip(np.round(u / scales[:, None]), -128, 127).astype(np.int64)
+    return codes, scales
+
+
+def regroup(codes: np.ndarray, g_idx: np.ndarray) -> tuple[np.ndarray, np.ndarray]:
+    """(codes with the columns in the stable order of g_idx, that order)."""
+    perm = np.argsort(np.asarray(g_idx), kind="stable")
+    return np.asarray(codes)[:, perm], perm

@@ -25,9 +25,13 @@ from .gptq import (  # noqa: F401
     gptq_gemm_pair_form,
     gptq_linear_fp16,
     gptq_pack,
+    gptq_packed_linear,
+    gptq_packed_linear_workspace_bytes,
     gptq_quantize_layer,
     gptq_quantize_with_factor,
     gptq_quantize_workspace_bytes,
+    gptq_regroup,
+    gptq_rmsnorm_int8,
     gptq_set_gemm_pair,
     gptq_set_phase_timing,
     gptq_solve_layer_host,

@@ -44,6 +44,15 @@ SIGNATURES = {
     "gptq_dequant_fp16": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int,
                                   c_int, c_void_p, c_void_p]),
     "gptq_linear_fp16": (c_int, [c_void_p, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_void_p]),
+    "gptq_rmsnorm_int8": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int64, c_int64, c_float,
+                                  c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "gptq_packed_linear_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64, c_int, c_int,
+                                                      c_int, c_int]),
+    "gptq_packed_linear": (c_int, [c_void_p, c_int, c_void_p, c_int64, c_void_p, c_void_p,
+                                   c_void_p, c_void_p, c_int64, c_int64, c_int, c_int, c_void_p,
+                                   c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
+    "gptq_regroup": (c_int, [c_void_p, c_void_p, c_int64, c_int64, c_int, c_int, c_void_p,
+                             c_void_p, c_void_p]),
     "gptq_quantize_layer_noalloc": (c_int, [c_void_p, c_int64, c_int64, c_void_p, c_int, c_int,
                                             c_int, c_float, c_int, c_void_p, c_void_p, c_void_p,
                                             c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),

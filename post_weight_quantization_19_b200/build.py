@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgptq_b200.so")
 SOURCES = ["hessian_tc.cu", "gemm_tc.cu", "factor.cu", "leaf.cu", "sweep.cu", "pack.cu", "api.cu",
-           "noalloc.cu", "gemv.cu", "linear_tc.cu"]
+           "noalloc.cu", "gemv.cu", "linear_tc.cu", "rmsnorm.cu", "regroup.cu",
+           "packed_linear.cu"]
 
 
 def nvcc() -> str:

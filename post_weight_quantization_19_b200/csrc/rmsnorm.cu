@@ -1,0 +1,291 @@
+// gptq_rmsnorm_int8: residual addition, root-mean-square norm, and symmetric
+// 8-bit codes with one scale per token.
+//
+// Mathematics.  h = T(x + residual), u = gamma h / sqrt(mean(h^2) + eps), scale
+// = max|u| / 127, code = rint(u / scale) -- the symmetric quantiser of "LLM
+// 量化技术" §1.2 with 8 bits over a token.  The factor 1 / sqrt(...) cancels in
+// u / scale, so code = rint(gamma h * (127 / max|gamma h|)): one pass over the
+// row gathers sum h^2 and max|gamma h| together, and the codes do not wait for
+// the square root.
+//
+// A row stays in registers (packed in its 16-bit type) between that pass and
+// the writing of the codes, so every input is read once and every output
+// written once: n d (2 [+ 2 residual] + 1 [+ 2 h] [+ 2 xhat]) bytes.  One CTA
+// per row, one barrier for both sums (rows of up to 2048: one warp per row).
+// Sums and scales in fp32; a row whose squares or products leave the safe fp32
+// range (bf16 values above 1e19) is gathered again from the registers with
+// values scaled by a power of two.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "gptq_internal.h"
+
+namespace gptq {
+namespace {
+
+template <typename T>
+struct Cvt;
+template <>
+struct Cvt<__half> {
+  static __device__ __forceinline__ float2 up(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+  }
+  static __device__ __forceinline__ uint32_t down(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+  static __device__ __forceinline__ __half one(float a) { return __float2half_rn(a); }
+};
+template <>
+struct Cvt<__nv_bfloat16> {
+  static __device__ __forceinline__ float2 up(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ uint32_t down(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+  static __device__ __forceinline__ __nv_bfloat16 one(float a) { return __float2bfloat16_rn(a); }
+};
+
+struct NormArgs {
+  const void *x, *residual, *gamma;
+  const int32_t *perm;
+  void *h;
+  int8_t *codes;
+  float *scales;
+  void *xhat;
+  int64_t n;
+  int d;
+  float eps;
+};
+
+// sum of v and maximum of the non-negative m over the row's threads, in every
+// thread; a NaN in m survives (its bits compare above every number's).
+template <bool WARP_ROW>
+__device__ __forceinline__ void row_reduce(float &v, float &m, float2 *part) {
+  uint32_t mb = __float_as_uint(m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  mb = __reduce_max_sync(0xffffffffu, mb);
+  if constexpr (!WARP_ROW) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    __syncthreads();   // part may hold the previous reduction's values
+    if (lane == 0) part[warp] = make_float2(v, __uint_as_float(mb));
+    __syncthreads();
+    const float2 p = lane < nw ? part[lane] : make_float2(0.f, 0.f);
+    v = p.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    mb = __reduce_max_sync(0xffffffffu, __float_as_uint(p.y));
+  }
+  m = __uint_as_float(mb);
+}
+
+__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
+  // |value| <= 127 by construction up to one rounding of the quotient; the
+  // conversion saturates to [-128, 127]
+  uint32_t r;
+  int ia = __float2int_rn(a), ib = __float2int_rn(b), ic = __float2int_rn(c), id = __float2int_rn(d);
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, 0;" : "=r"(r) : "r"(id), "r"(ic));
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %0;" : "+r"(r) : "r"(ib), "r"(ia));
+  return r;
+}
+
+template <typename T, int V, bool WARP_ROW>
+__global__ void __launch_bounds__(WARP_ROW ? 256 : 1024) rmsnorm_int8_kernel(NormArgs a) {
+  extern __shared__ __align__(16) int8_t row_codes[];   // perm: [rows of the CTA][d]
+  __shared__ float2 part[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = WARP_ROW ? lane : (int)threadIdx.x;
+  const int nt = WARP_ROW ? 32 : (int)blockDim.x;
+  const int64_t row = WARP_ROW ? (int64_t)blockIdx.x * (blockDim.x >> 5) + warp : (int64_t)blockIdx.x;
+  if (row >= a.n) return;   // whole warps (WARP_ROW) or whole CTAs
+  const int nvec = a.d / 8;
+  const uint4 *x = reinterpret_cast<const uint4 *>(a.x) + row * nvec;
+  const uint4 *res = reinterpret_cast<const uint4 *>(a.residual) + row * nvec;
+  const uint4 *gam = reinterpret_cast<const uint4 *>(a.gamma);
+  uint4 hv[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int k = tid + v * nt;
+    hv[v] = k < nvec ? x[k] : make_uint4(0, 0, 0, 0);
+  }
+  if (a.residual) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int k = tid + v * nt;
+      if (k < nvec) {
+        const uint4 rv = res[k];
+        const uint32_t p[4] = {hv[v].x, hv[v].y, hv[v].z, hv[v].w};
+        const uint32_t q[4] = {rv.x, rv.y, rv.z, rv.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = Cvt<T>::up(p[i]), g = Cvt<T>::up(q[i]);
+          o[i] = Cvt<T>::down(f.x + g.x, f.y + g.y);
+        }
+        hv[v] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+  if (a.h) {
+    uint4 *h = reinterpret_cast<uint4 *>(a.h) + row * nvec;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int k = tid + v * nt;
+      if (k < nvec) h[k] = hv[v];
+    }
+  }
+  // the powers of two that h is scaled by in the sum and in the maximum (1
+  // except where the first pass left the safe range)
+  float ps = 1.f, pt = 1.f, ss, top;
+  for (int pass = 0;; ++pass) {
+    ss = 0.f;
+    uint32_t mb = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int k = tid + v * nt;
+      if (k < nvec) {
+        const uint4 gv = __ldg(gam + k);
+        const uint32_t p[4] = {hv[v].x, hv[v].y, hv[v].z, hv[v].w};
+        const uint32_t q[4] = {gv.x, gv.y, gv.z, gv.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float2 f = Cvt<T>::up(p[i]);
+          const float2 g = Cvt<T>::up(q[i]);
+          mb = max(mb, max(__float_as_uint(f.x * pt * g.x) & 0x7FFFFFFFu,
+                           __float_as_uint(f.y * pt * g.y) & 0x7FFFFFFFu));
+          f.x *= ps;
+          f.y *= ps;
+          ss = fmaf(f.x, f.x, fmaf(f.y, f.y, ss));
+        }
+      }
+    }
+    top = __uint_as_float(mb);
+    row_reduce<WARP_ROW>(ss, top, part);
+    if (pass == 1 || (ss < 1e37f && top < 1e37f && (top > 1e-30f || top == 0.f))) break;
+    ps = ss < 1e37f ? 1.f : 0x1p-96f;
+    pt = top < 1e37f ? (top > 1e-30f ? 1.f : 0x1p96f) : 0x1p-96f;
+  }
+  float scale, inv;
+  if (!(ss < 3.4e38f) || !(top < 3.4e38f)) {   // NaN or infinity in the row
+    scale = __uint_as_float(0x7FC00000u);
+    inv = 0.f;
+  } else if (top == 0.f) {
+    scale = 1.f;
+    inv = 0.f;
+  } else if (ps == 1.f && pt == 1.f) {
+    scale = top / (127.f * sqrtf(ss / (float)a.d + a.eps));
+    inv = 127.f / top;
+  } else {
+    const double mean = (double)ss / a.d / ps / ps;
+    scale = (float)((double)top / pt / (127.0 * sqrt(mean + (double)a.eps)));
+    inv = 127.f / top;
+  }
+  const bool lost = scale != scale;
+  if (tid == 0) a.scales[row] = scale;
+  int8_t *crow = a.perm ? row_codes + (WARP_ROW ? (size_t)warp * a.d : 0) : a.codes + row * a.d;
+  uint4 *xh = a.perm ? nullptr : reinterpret_cast<uint4 *>(a.xhat);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int k = tid + v * nt;
+    if (k < nvec) {
+      const uint4 gv = __ldg(gam + k);
+      const uint32_t p[4] = {hv[v].x, hv[v].y, hv[v].z, hv[v].w};
+      const uint32_t q[4] = {gv.x, gv.y, gv.z, gv.w};
+      float u[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = Cvt<T>::up(p[i]), g = Cvt<T>::up(q[i]);
+        u[2 * i] = lost ? 0.f : f.x * pt * g.x * inv;
+        u[2 * i + 1] = lost ? 0.f : f.y * pt * g.y * inv;
+      }
+      uint2 c;
+      c.x = pack4(u[0], u[1], u[2], u[3]);
+      c.y = pack4(u[4], u[5], u[6], u[7]);
+      *reinterpret_cast<uint2 *>(crow + (size_t)k * 8) = c;
+      if (xh) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = i < 2 ? c.x : c.y;
+          const int s0 = (i & 1) * 16;
+          o[i] = Cvt<T>::down(scale * (float)(int8_t)(w >> s0), scale * (float)(int8_t)(w >> (s0 + 8)));
+        }
+        xh[row * nvec + k] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+  if (a.perm) {
+    if constexpr (WARP_ROW)
+      __syncwarp();
+    else
+      __syncthreads();
+    T *xhp = reinterpret_cast<T *>(a.xhat);
+    for (int j = tid; j < a.d; j += nt) {
+      int from = __ldg(a.perm + j);
+      from = from < 0 ? 0 : (from >= a.d ? a.d - 1 : from);
+      const int8_t c = crow[from];
+      a.codes[row * a.d + j] = c;
+      if (xhp) xhp[row * a.d + j] = Cvt<T>::one(scale * (float)c);
+    }
+  }
+}
+
+template <typename T, int V>
+int launch_norm(const NormArgs &a, bool warp_row, int threads, cudaStream_t st) {
+  if (warp_row) {
+    const size_t smem = a.perm ? (size_t)8 * a.d : 0;   // d <= 2048 V / 8
+    rmsnorm_int8_kernel<T, V, true>
+        <<<(unsigned)((a.n + 7) / 8), 256, smem, st>>>(a);
+  } else {
+    static std::atomic<bool> attr[64] = {};
+    if (a.perm)
+      if (const int rc = ensure_smem_attr(rmsnorm_int8_kernel<T, V, false>, 65536, attr)) return rc;
+    rmsnorm_int8_kernel<T, V, false>
+        <<<(unsigned)a.n, threads, a.perm ? (size_t)a.d : 0, st>>>(a);
+  }
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
+}
+
+template <typename T>
+int launch_norm_t(const NormArgs &a, cudaStream_t st) {
+  const int nvec = a.d / 8;
+  if (a.d <= 2048) {
+    if (nvec <= 32) return launch_norm<T, 1>(a, true, 0, st);
+    if (nvec <= 64) return launch_norm<T, 2>(a, true, 0, st);
+    if (nvec <= 128) return launch_norm<T, 4>(a, true, 0, st);
+    return launch_norm<T, 8>(a, true, 0, st);
+  }
+  auto threads = [&](int v) { return ((nvec + v - 1) / v + 31) / 32 * 32; };
+  if (threads(1) <= 1024) return launch_norm<T, 1>(a, false, threads(1), st);
+  if (threads(2) <= 1024) return launch_norm<T, 2>(a, false, threads(2), st);
+  if (threads(4) <= 1024) return launch_norm<T, 4>(a, false, threads(4), st);
+  return launch_norm<T, 8>(a, false, threads(8), st);
+}
+
+}  // namespace
+}  // namespace gptq
+
+using namespace gptq;
+
+extern "C" int gptq_rmsnorm_int8(const void *x, const void *residual, const void *gamma, int dtype,
+                                 int64_t n, int64_t d, float eps, const int32_t *perm, void *h,
+                                 int8_t *codes, float *scales, void *xhat, gptq_stream_t stream) {
+  if (dtype != GPTQ_F16 && dtype != GPTQ_BF16) return GPTQ_ERR_INVALID_ARG;
+  if (n < 0 || n > (int64_t)INT32_MAX) return GPTQ_ERR_INVALID_ARG;
+  if (d <= 0 || d % 32 != 0 || d > 65536) return GPTQ_ERR_INVALID_ARG;
+  if (!(eps > 0.f) || !(eps < 3.0e38f)) return GPTQ_ERR_INVALID_ARG;
+  if (n == 0) return GPTQ_OK;
+  if (!x || !gamma || !codes || !scales) return GPTQ_ERR_INVALID_ARG;
+  for (const void *p : {x, residual, gamma, (const void *)h, (const void *)codes, (const void *)xhat})
+    if (reinterpret_cast<uintptr_t>(p) % 16) return GPTQ_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(scales) % 4 || reinterpret_cast<uintptr_t>(perm) % 4)
+    return GPTQ_ERR_INVALID_ARG;
+  if (xhat && (xhat == h || xhat == x || xhat == residual)) return GPTQ_ERR_INVALID_ARG;
+  const NormArgs a{x, residual, gamma, perm, h, codes, scales, xhat, n, (int)d, eps};
+  cudaStream_t st = (cudaStream_t)stream;
+  return dtype == GPTQ_F16 ? launch_norm_t<__half>(a, st) : launch_norm_t<__nv_bfloat16>(a, st);
+}

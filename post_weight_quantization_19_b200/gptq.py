@@ -247,6 +247,168 @@ def gptq_linear_fp16(X: torch.Tensor, W16: torch.Tensor, Y: torch.Tensor | None 
     return Y
 
 
+# Types of activations (include/gptq.h).
+_DTYPE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2, torch.int8: 3}
+
+
+def _shaped(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, device: torch.device,
+            name: str) -> int | None:
+    """Pointer of a contiguous tensor of this type, shape and device (None for None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _activations(x: torch.Tensor, dtypes: tuple, name: str = "x") -> None:
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be [tokens, features]")
+    if x.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {', '.join(map(str, dtypes))}, got {x.dtype}")
+
+
+def _launch(device: torch.device, stream, fn, *args) -> int:
+    """fn(*args, stream) with the tensors' device current; the stream is the
+    given one or that device's current stream."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, _stream(stream))
+    with torch.cuda.device(device):
+        return fn(*args, _stream(stream))
+
+
+def gptq_rmsnorm_int8(x: torch.Tensor, gamma: torch.Tensor, *, eps: float,
+                      residual: torch.Tensor | None = None, perm: torch.Tensor | None = None,
+                      xhat: bool = False, outputs: dict | None = None, stream=None) -> dict:
+    """h = x + residual, its root-mean-square norm times gamma, in symmetric 8-bit
+    codes with one scale per token.
+
+    x, residual [n, d] and gamma [d] fp16 or bf16.  Returns ``codes`` int8
+    [n, d], ``scales`` fp32 [n], ``h`` when there is a residual, and ``xhat`` =
+    scales * codes in x's type when asked for.  ``perm`` (from ``gptq_regroup``)
+    gives codes and xhat in that column order.  ``outputs`` may hold
+    preallocated tensors of these names (an ``xhat`` or ``h`` among them is
+    written; ``h`` may be x or residual).
+    """
+    lib = _abi.load()
+    _activations(x, (torch.float16, torch.bfloat16))
+    n, d = x.shape
+    dev, T = x.device, x.dtype
+    out = dict(outputs or {})
+    codes, scales, xh, h = (out.get(k) for k in ("codes", "scales", "xhat", "h"))
+    if codes is None:
+        codes = torch.empty((n, d), dtype=torch.int8, device=dev)
+    if scales is None:
+        scales = torch.empty(n, dtype=torch.float32, device=dev)
+    if xh is None and xhat:
+        xh = torch.empty((n, d), dtype=T, device=dev)
+    if h is None and residual is not None:
+        h = torch.empty((n, d), dtype=T, device=dev)
+    _check(_launch(
+        dev, stream, lib.gptq_rmsnorm_int8, _shaped(x, T, (n, d), dev, "x"),
+        _shaped(residual, T, (n, d), dev, "residual"), _shaped(gamma, T, (d,), dev, "gamma"),
+        _DTYPE[T], n, d, float(eps), _shaped(perm, torch.int32, (d,), dev, "perm"),
+        _shaped(h, T, (n, d), dev, "h"), _shaped(codes, torch.int8, (n, d), dev, "codes"),
+        _shaped(scales, torch.float32, (n,), dev, "scales"),
+        _shaped(xh, T, (n, d), dev, "xhat")), "gptq_rmsnorm_int8")
+    res = {"codes": codes, "scales": scales}
+    if h is not None:
+        res["h"] = h
+    if xh is not None:
+        res["xhat"] = xh
+    return res
+
+
+def gptq_packed_linear_workspace_bytes(n: int, r: int, d: int, bits: int, group: int, *,
+                                       x_dtype: torch.dtype = torch.float16,
+                                       permuted: bool = False) -> int:
+    if x_dtype not in (torch.float16, torch.bfloat16, torch.int8):
+        raise ValueError(f"x must be float16, bfloat16 or int8, got {x_dtype}")
+    return int(_abi.load().gptq_packed_linear_workspace_bytes(n, r, d, bits, group,
+                                                              _DTYPE[x_dtype], int(permuted)))
+
+
+def gptq_packed_linear(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
+                       zeros: torch.Tensor, bits: int, group: int, *,
+                       x_scales: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                       perm: torch.Tensor | None = None, dtype: torch.dtype | None = None,
+                       y: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """y [n, r] = x [n, d] W^^T + bias from the packed layer, for any number of tokens.
+
+    x fp16 or bf16, or int8 codes with ``x_scales`` fp32 [n] (as
+    ``gptq_rmsnorm_int8`` returns them).  y has ``dtype`` (or the given y's type):
+    x's own type by default (fp16 for int8 x), or float32.  ``perm`` is
+    ``gptq_regroup``'s order when the layer was quantised with act-order and x is
+    in its own column order.
+    """
+    lib = _abi.load()
+    _activations(x, (torch.float16, torch.bfloat16, torch.int8))
+    n, d = x.shape
+    r, dev = qweight.shape[0], x.device
+    if bits not in (2, 3, 4, 8) or (group != -1 and (group <= 0 or d % group)):
+        raise GPTQError(1, "gptq_packed_linear")
+    G = 1 if group == -1 else d // group
+    if y is None:
+        if dtype is None:
+            dtype = torch.float16 if x.dtype == torch.int8 else x.dtype
+        y = torch.empty((n, r), dtype=dtype, device=dev)
+    elif dtype is not None and y.dtype != dtype:
+        raise ValueError(f"y must be {dtype}, got {y.dtype}")
+    if y.dtype not in _DTYPE:
+        raise ValueError(f"y must be float16, bfloat16 or float32, got {y.dtype}")
+    xt = _DTYPE[x.dtype]
+    need = lib.gptq_packed_linear_workspace_bytes(n, r, d, bits, group, xt, perm is not None)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is not None and workspace.device != dev:
+        raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
+    _check(_launch(
+        dev, stream, lib.gptq_packed_linear, _shaped(x, x.dtype, (n, d), dev, "x"), xt,
+        _shaped(x_scales, torch.float32, (n,), dev, "x_scales"), n,
+        _shaped(qweight, torch.int32, (r, d * bits // 32), dev, "qweight"),
+        _shaped(scales, torch.float32, (r, G), dev, "scales"),
+        _shaped(zeros, torch.int32, (r, G), dev, "zeros"),
+        _shaped(perm, torch.int32, (d,), dev, "perm"), r, d, bits, group,
+        _shaped(bias, y.dtype, (r,), dev, "bias"), _shaped(y, y.dtype, (n, r), dev, "y"),
+        _DTYPE[y.dtype], _ptr(workspace, None, "workspace"),
+        0 if workspace is None else workspace.numel() * workspace.element_size()),
+        "gptq_packed_linear")
+    return y
+
+
+def gptq_regroup(qweight: torch.Tensor, g_idx: torch.Tensor, bits: int, group: int, *,
+                 out: torch.Tensor | None = None, perm: torch.Tensor | None = None,
+                 stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The columns of a packed act-order layer sorted by group, and their order:
+    column j of the first result is column perm[j] of ``qweight``."""
+    lib = _abi.load()
+    if not g_idx.is_cuda or g_idx.dim() != 1:
+        raise ValueError("g_idx must be a CUDA tensor [d]")
+    d, r, dev = g_idx.shape[0], qweight.shape[0], g_idx.device
+    if out is None:
+        out = torch.empty_like(qweight)
+    if perm is None:
+        perm = torch.empty_like(g_idx)
+    words = (r, d * bits // 32)
+    _check(_launch(
+        dev, stream, lib.gptq_regroup, _shaped(qweight, torch.int32, words, dev, "qweight"),
+        _shaped(g_idx, torch.int32, (d,), dev, "g_idx"), r, d, bits, group,
+        _shaped(out, torch.int32, words, dev, "out"),
+        _shaped(perm, torch.int32, (d,), dev, "perm")), "gptq_regroup")
+    return out, perm
+
+
 def gptq_pack(codes: torch.Tensor, bits: int, qweight: torch.Tensor | None = None,
               stream=None) -> torch.Tensor:
     lib = _abi.load()
