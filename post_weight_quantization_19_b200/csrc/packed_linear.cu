@@ -10,44 +10,31 @@
 //
 // One warp per row and four tokens: lane l takes the 32-code chunks l, l + 32,
 // ..., whose codes belong to one group each.  fp32 sums.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "gptq_internal.h"
+#include "packed_linear.h"
 #include "unpack_bits.cuh"
 
 namespace gptq {
 namespace {
 
+constexpr int FEW_TOKENS = 16;   // up to here the weights' bytes bound the product
+
+// x in the layer's column order: out[t, j] = x[t, perm[j]], entries outside
+// [0, d) clamped.  One CTA per token (8 n d or 6 n d bytes, from L2 for few).
+template <typename T>
+__global__ void __launch_bounds__(256) gather_columns_kernel(const T *__restrict__ x,
+                                                             const int32_t *__restrict__ perm, int d,
+                                                             T *__restrict__ out) {
+  const int64_t row = (int64_t)blockIdx.x * d;
+  for (int j = threadIdx.x; j < d; j += blockDim.x)
+    out[row + j] = x[row + min(max(__ldg(perm + j), 0), d - 1)];
+}
+
 constexpr int SIMPLE_WARPS = 8;
 constexpr int SIMPLE_TOKENS = 4;
 
-struct PackedArgs {
-  const void *x;
-  const float *x_scales;
-  const uint32_t *qweight;
-  const float *scales;
-  const int32_t *zeros, *perm;
-  const void *bias;
-  void *y;
-  int64_t n, r;
-  int d, group, G, xtype, ytype;
-};
-
-__device__ __forceinline__ float load_as_float(const void *p, int type, int64_t i) {
-  if (type == GPTQ_F16) return __half2float(reinterpret_cast<const __half *>(p)[i]);
-  if (type == GPTQ_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[i]);
+__device__ __forceinline__ float load_x(const void *p, int type, int64_t i) {
   if (type == GPTQ_I8) return (float)reinterpret_cast<const int8_t *>(p)[i];
-  return reinterpret_cast<const float *>(p)[i];
-}
-
-__device__ __forceinline__ void store_float(void *p, int type, int64_t i, float v) {
-  if (type == GPTQ_F16)
-    reinterpret_cast<__half *>(p)[i] = __float2half_rn(v);
-  else if (type == GPTQ_BF16)
-    reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
-  else
-    reinterpret_cast<float *>(p)[i] = v;
+  return load_as_float(p, type, i);
 }
 
 template <int BITS>
@@ -70,11 +57,10 @@ __global__ void __launch_bounds__(32 * SIMPLE_WARPS) packed_linear_simple_kernel
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         const float wv = s * (float)((int)code_at<BITS>(w, j) - z);
-        int c = k * 32 + j;
-        if (a.perm) c = min(max(__ldg(a.perm + c), 0), a.d - 1);
+        const int c = k * 32 + j;
 #pragma unroll
         for (int t = 0; t < SIMPLE_TOKENS; ++t)
-          if (t0 + t < a.n) acc[t] = fmaf(wv, load_as_float(a.x, a.xtype, (t0 + t) * a.d + c), acc[t]);
+          if (t0 + t < a.n) acc[t] = fmaf(wv, load_x(a.x, a.xtype, (t0 + t) * a.d + c), acc[t]);
       }
     }
 #pragma unroll
@@ -108,9 +94,8 @@ using namespace gptq;
 
 extern "C" size_t gptq_packed_linear_workspace_bytes(int64_t n, int64_t r, int64_t d, int bits,
                                                      int group, int xtype, int permuted) {
-  (void)permuted;
-  if (!valid_packed(n, r, d, bits, group, xtype)) return 0;
-  return 0;
+  if (!valid_packed(n, r, d, bits, group, xtype) || n == 0 || r == 0) return 0;
+  return permuted ? align_up((size_t)n * d * (xtype == GPTQ_I8 ? 1 : 2), 256) : 0;
 }
 
 extern "C" int gptq_packed_linear(const void *x, int xtype, const float *x_scales, int64_t n,
@@ -131,9 +116,20 @@ extern "C" int gptq_packed_linear(const void *x, int xtype, const float *x_scale
     return GPTQ_ERR_INVALID_ARG;
   const size_t need = gptq_packed_linear_workspace_bytes(n, r, d, bits, group, xtype, perm != nullptr);
   if (need > 0 && (!workspace || workspace_bytes < need)) return GPTQ_ERR_NO_MEMORY;
-  const PackedArgs a{x, x_scales, reinterpret_cast<const uint32_t *>(qweight), scales, zeros, perm,
-                     bias, y, n, r, (int)d, group, group < 0 ? 1 : (int)(d / group), xtype, ytype};
   cudaStream_t st = (cudaStream_t)stream;
+  if (perm) {
+    if (xtype == GPTQ_I8)
+      gather_columns_kernel<<<(unsigned)n, 256, 0, st>>>(static_cast<const uint8_t *>(x), perm, (int)d,
+                                                         static_cast<uint8_t *>(workspace));
+    else
+      gather_columns_kernel<<<(unsigned)n, 256, 0, st>>>(static_cast<const uint16_t *>(x), perm, (int)d,
+                                                         static_cast<uint16_t *>(workspace));
+    GPTQ_LAUNCH_CHECK();
+    x = workspace;
+  }
+  const PackedArgs a{x, x_scales, reinterpret_cast<const uint32_t *>(qweight), scales, zeros,
+                     bias, y, n, r, (int)d, bits, group, group < 0 ? 1 : (int)(d / group), xtype, ytype};
+  if (n <= FEW_TOKENS) return launch_packed_few(a, st);
   const int64_t tb = (n + SIMPLE_TOKENS - 1) / SIMPLE_TOKENS;
   const dim3 grid((unsigned)((r + SIMPLE_WARPS - 1) / SIMPLE_WARPS), (unsigned)(tb < 4096 ? tb : 4096));
   switch (bits) {
