@@ -486,6 +486,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) packed_few_kernel(const FewArg
       for (int w = 1; w < FEW_WARPS; ++w) v += red[w * CELLS + i];
       red[i] = v;                                   // cell i is this thread's alone
     }
+    __syncwarp();
     cluster_sync();
   }
   for (int i = first + threadIdx.x; i < first + per; i += blockDim.x) {
@@ -509,7 +510,10 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) packed_few_kernel(const FewArg
       store_float(a.p.y, a.p.ytype, (tok0 + col) * a.p.r + row, v);
     }
   }
-  if (a.ctas_k > 1) cluster_sync();                 // the partial sums stay until all have read them
+  if (a.ctas_k > 1) {                               // the partial sums stay until all have read them
+    __syncwarp();
+    cluster_sync();
+  }
 }
 
 template <int BITS, int XT, int NT>

@@ -8,10 +8,11 @@
 //
 //   y[t, i] = xs[t] sum_j s[i, j/g] (q[i, j] - z[i, j/g]) x[t, p(j)] + bias[i]
 //
-// One warp per row and four tokens: lane l takes the 32-code chunks l, l + 32,
-// ..., whose codes belong to one group each.  fp32 sums.
+// Up to FEW_TOKENS tokens the product is bound by reading the packed weights
+// (packed_few.cu); beyond, by conversion and then by the tensor cores
+// (packed_many.cu).  This file checks the arguments, brings x into the
+// layer's column order and, for many tokens, 8-bit codes into fp16.
 #include "packed_linear.h"
-#include "unpack_bits.cuh"
 
 namespace gptq {
 namespace {
@@ -29,51 +30,20 @@ __global__ void __launch_bounds__(256) gather_columns_kernel(const T *__restrict
     out[row + j] = x[row + min(max(__ldg(perm + j), 0), d - 1)];
 }
 
-constexpr int SIMPLE_WARPS = 8;
-constexpr int SIMPLE_TOKENS = 4;
-
-__device__ __forceinline__ float load_x(const void *p, int type, int64_t i) {
-  if (type == GPTQ_I8) return (float)reinterpret_cast<const int8_t *>(p)[i];
-  return load_as_float(p, type, i);
-}
-
-template <int BITS>
-__global__ void __launch_bounds__(32 * SIMPLE_WARPS) packed_linear_simple_kernel(PackedArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * SIMPLE_WARPS + (threadIdx.x >> 5);
-  if (row >= a.r) return;
-  const int nchunk = a.d / 32;
-  const uint32_t *qrow = a.qweight + row * nchunk * BITS;
-  for (int64_t t0 = (int64_t)blockIdx.y * SIMPLE_TOKENS; t0 < a.n;
-       t0 += (int64_t)gridDim.y * SIMPLE_TOKENS) {
-    float acc[SIMPLE_TOKENS] = {};
-    for (int k = lane; k < nchunk; k += 32) {
-      uint32_t w[BITS];
-#pragma unroll
-      for (int i = 0; i < BITS; ++i) w[i] = __ldg(qrow + (int64_t)k * BITS + i);
-      const int gi = a.group > 0 ? k * 32 / a.group : 0;
-      const float s = __ldg(a.scales + row * a.G + gi);
-      const int z = min(max(__ldg(a.zeros + row * a.G + gi), 0), (1 << BITS) - 1);
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float wv = s * (float)((int)code_at<BITS>(w, j) - z);
-        const int c = k * 32 + j;
-#pragma unroll
-        for (int t = 0; t < SIMPLE_TOKENS; ++t)
-          if (t0 + t < a.n) acc[t] = fmaf(wv, load_x(a.x, a.xtype, (t0 + t) * a.d + c), acc[t]);
-      }
+// 8-bit codes as fp16 (exact), in the layer's column order if perm is given:
+// the operand of the tensor-core product.  3 n d bytes.
+__global__ void __launch_bounds__(256) widen_codes_kernel(const int8_t *__restrict__ x,
+                                                          const int32_t *__restrict__ perm, int d,
+                                                          __half *__restrict__ out) {
+  const int64_t row = (int64_t)blockIdx.x * d;
+  for (int j = threadIdx.x * 2; j < d; j += blockDim.x * 2) {
+    int a = j, b = j + 1;
+    if (perm) {
+      a = min(max(__ldg(perm + j), 0), d - 1);
+      b = min(max(__ldg(perm + j + 1), 0), d - 1);
     }
-#pragma unroll
-    for (int t = 0; t < SIMPLE_TOKENS; ++t) {
-      float v = acc[t];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0 && t0 + t < a.n) {
-        if (a.x_scales) v *= a.x_scales[t0 + t];
-        if (a.bias) v += load_as_float(a.bias, a.ytype, row);
-        store_float(a.y, a.ytype, (t0 + t) * a.r + row, v);
-      }
-    }
+    *reinterpret_cast<__half2 *>(out + row + j) =
+        __halves2half2(__short2half_rn(x[row + a]), __short2half_rn(x[row + b]));
   }
 }
 
@@ -95,7 +65,9 @@ using namespace gptq;
 extern "C" size_t gptq_packed_linear_workspace_bytes(int64_t n, int64_t r, int64_t d, int bits,
                                                      int group, int xtype, int permuted) {
   if (!valid_packed(n, r, d, bits, group, xtype) || n == 0 || r == 0) return 0;
-  return permuted ? align_up((size_t)n * d * (xtype == GPTQ_I8 ? 1 : 2), 256) : 0;
+  const bool widen = xtype == GPTQ_I8 && n > FEW_TOKENS;
+  if (!permuted && !widen) return 0;
+  return align_up((size_t)n * d * (xtype == GPTQ_I8 && !widen ? 1 : 2), 256);
 }
 
 extern "C" int gptq_packed_linear(const void *x, int xtype, const float *x_scales, int64_t n,
@@ -117,7 +89,13 @@ extern "C" int gptq_packed_linear(const void *x, int xtype, const float *x_scale
   const size_t need = gptq_packed_linear_workspace_bytes(n, r, d, bits, group, xtype, perm != nullptr);
   if (need > 0 && (!workspace || workspace_bytes < need)) return GPTQ_ERR_NO_MEMORY;
   cudaStream_t st = (cudaStream_t)stream;
-  if (perm) {
+  if (xtype == GPTQ_I8 && n > FEW_TOKENS) {
+    widen_codes_kernel<<<(unsigned)n, 256, 0, st>>>(static_cast<const int8_t *>(x), perm, (int)d,
+                                                    static_cast<__half *>(workspace));
+    GPTQ_LAUNCH_CHECK();
+    x = workspace;
+    xtype = GPTQ_F16;
+  } else if (perm) {
     if (xtype == GPTQ_I8)
       gather_columns_kernel<<<(unsigned)n, 256, 0, st>>>(static_cast<const uint8_t *>(x), perm, (int)d,
                                                          static_cast<uint8_t *>(workspace));
@@ -129,15 +107,5 @@ extern "C" int gptq_packed_linear(const void *x, int xtype, const float *x_scale
   }
   const PackedArgs a{x, x_scales, reinterpret_cast<const uint32_t *>(qweight), scales, zeros,
                      bias, y, n, r, (int)d, bits, group, group < 0 ? 1 : (int)(d / group), xtype, ytype};
-  if (n <= FEW_TOKENS) return launch_packed_few(a, st);
-  const int64_t tb = (n + SIMPLE_TOKENS - 1) / SIMPLE_TOKENS;
-  const dim3 grid((unsigned)((r + SIMPLE_WARPS - 1) / SIMPLE_WARPS), (unsigned)(tb < 4096 ? tb : 4096));
-  switch (bits) {
-    case 2: packed_linear_simple_kernel<2><<<grid, 32 * SIMPLE_WARPS, 0, st>>>(a); break;
-    case 3: packed_linear_simple_kernel<3><<<grid, 32 * SIMPLE_WARPS, 0, st>>>(a); break;
-    case 4: packed_linear_simple_kernel<4><<<grid, 32 * SIMPLE_WARPS, 0, st>>>(a); break;
-    default: packed_linear_simple_kernel<8><<<grid, 32 * SIMPLE_WARPS, 0, st>>>(a); break;
-  }
-  GPTQ_LAUNCH_CHECK();
-  return GPTQ_OK;
+  return n <= FEW_TOKENS ? launch_packed_few(a, st) : launch_packed_many(a, st);
 }

@@ -22,6 +22,9 @@ struct PackedArgs {
 
 // Few tokens: warp-level products on codes straight from the packed rows.
 int launch_packed_few(const PackedArgs &a, cudaStream_t st);
+// Many tokens: weights dequantised into tensor memory, tcgen05 products.  x in
+// 16 bits (xtype GPTQ_F16 or GPTQ_BF16; x_scales may still be given).
+int launch_packed_many(const PackedArgs &a, cudaStream_t st);
 
 __device__ __forceinline__ float load_as_float(const void *p, int type, int64_t i) {
   if (type == GPTQ_F16) return __half2float(reinterpret_cast<const __half *>(p)[i]);

@@ -1,0 +1,661 @@
+// gptq_packed_linear for many tokens: y = x W^^T + bias on the 5th-generation
+// tensor cores, the weights dequantised on their way into tensor memory.
+//
+// One CTA per tile of 128 rows of W and N <= 192 tokens.  The weights are the
+// MMA's A operand, in tensor memory: thread i of a converter warpgroup owns row
+// i of the tile, reads the row's packed codes straight from global memory into
+// registers (four steps of 64 columns ahead), turns them into 16-bit weights
+// and writes them to its TMEM lane (tcgen05.st).  x is the B operand: tiles of
+// 64 features x N tokens that TMA places in 128-byte-swizzled shared memory.
+// So shared memory carries only x, and a code costs 2.5 instructions once per
+// N tokens.
+//
+//   w = T16(s (q - z)):  q - z is exact in 16 bits (code bits in the mantissa of
+//   a power of two M, minus M + z); s is split in two 16-bit parts, so w =
+//   fma(q - z, s_hi, (q - z) s_lo) is s (q - z) rounded once (up to the second
+//   part's own rounding, 2^-10 of half a step).  This rounding is
+//   gptq_dequant_fp16's; fp32 weights would need three times the tensor work.
+//   With fp16, s is divided by a power of two per row (the largest scale's) and
+//   the row's sums multiplied by it again, so scales outside fp16's range lose
+//   nothing.
+//
+// Warp 0 issues TMA, warp 1 the MMAs (one thread each); warps 4-11 are the two
+// converter warpgroups, which take alternate steps; warps 12-15 drain one of
+// two accumulators while the other fills.  With fewer tiles than SMs the k
+// range is split over a cluster, whose CTAs add their sums through distributed
+// shared memory in a fixed order.
+#include <mutex>
+
+#include "packed_linear.h"
+
+namespace gptq {
+namespace {
+
+constexpr int PM = 128;                 // rows of W per tile (UMMA M)
+constexpr int PN = 192;                 // most tokens per tile (UMMA N)
+constexpr int PK = 64;                  // features per step (one 128-byte row of x)
+constexpr int ASTAGES = 4;              // TMEM stages of A: 32 columns each
+constexpr int MAXB = 8;                 // shared-memory stages of x at most
+constexpr uint32_t TM_A = 2 * PN;       // TMEM column of the first A stage
+constexpr int MANY_THREADS = 512;
+constexpr size_t B_BYTES = 200 * 1024;  // shared memory for x
+
+struct ManyArgs {
+  PackedArgs p;
+  int N;              // tokens per tile, a multiple of 16
+  int nM, nN;         // tiles
+  int ctas_k;         // CTAs of a cluster, along k
+  int bstages;
+  int aligned;        // 16-byte loads of the codes
+  int *status;
+};
+
+struct ManyShared {
+  uint64_t full_b[MAXB], empty_b[MAXB];
+  uint64_t full_a[ASTAGES], empty_a[ASTAGES];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands, fp32 accumulate.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void many_timeout(int *status, ManyShared &sh) {
+  atomicCAS(status, 0, (int)GPTQ_ERR_TIMEOUT);
+  *(volatile int *)&sh.abort = 1;
+}
+
+// Pairs of 16-bit numbers in a register.
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__half> {
+  static constexpr uint32_t M = 0x64006400u;   // 1024: mantissa steps of 1
+  static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
+    const __half2 v = __hsub2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  static __device__ __forceinline__ uint32_t mul(uint32_t a, uint32_t b) {
+    const __half2 v = __hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
+    const __half2 v = __hfma2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b),
+                              *reinterpret_cast<__half2 *>(&c));
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  static __device__ __forceinline__ uint32_t both(float s) {
+    const __half2 v = __half2half2(__float2half_rn(s));
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  static __device__ __forceinline__ float low(uint32_t v) {
+    return __low2float(*reinterpret_cast<const __half2 *>(&v));
+  }
+};
+template <>
+struct Pair<__nv_bfloat16> {
+  static constexpr uint32_t M = 0x43004300u;   // 128
+  static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 v =
+        __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  static __device__ __forceinline__ uint32_t mul(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 v =
+        __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
+    const __nv_bfloat162 v =
+        __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b),
+                *reinterpret_cast<__nv_bfloat162 *>(&c));
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  static __device__ __forceinline__ uint32_t both(float s) {
+    const __nv_bfloat162 v = __bfloat162bfloat162(__float2bfloat16_rn(s));
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  static __device__ __forceinline__ float low(uint32_t v) { return __uint_as_float(v << 16); }
+};
+
+// A group's scale and zero point, ready for code pairs.
+template <int BITS, typename T>
+struct Group {
+  uint32_t mz, hi, lo;   // M + z; s = hi + lo
+  float s, z;            // 8-bit codes in bf16: through fp32
+  __device__ __forceinline__ void set(float scale, int zero) {
+    const uint32_t u = (uint32_t)min(max(zero, 0), (1 << BITS) - 1);
+    if constexpr (BITS == 8 && sizeof(T) == 2 && Pair<T>::M == 0x43004300u) {
+      s = scale;
+      z = 8388608.f + (float)u;
+    } else {
+      mz = Pair<T>::M + (u | u << 16);
+      hi = Pair<T>::both(scale);
+      const float rest = scale - Pair<T>::low(hi);
+      lo = Pair<T>::both(rest == rest ? rest : 0.f);   // inf - inf: hi carries it
+    }
+  }
+  __device__ __forceinline__ uint32_t weight(uint32_t magic_plus_q) const {
+    const uint32_t v = Pair<T>::sub(magic_plus_q, mz);
+    return Pair<T>::fma(v, hi, Pair<T>::mul(v, lo));
+  }
+};
+
+// 32 codes of one row and group as 16 pairs of weights, in column order.
+template <int BITS, typename T>
+__device__ __forceinline__ void chunk_weights(const uint32_t *w, const Group<BITS, T> &g,
+                                              uint32_t (&o)[16]) {
+  constexpr uint32_t M = Pair<T>::M;
+  if constexpr (BITS == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = w[i], h = v >> 4;   // byte k: codes 2k (low nibble of v), 2k + 1 (of h)
+      o[4 * i + 0] = g.weight((__byte_perm(v, h, 0x0400) & 0x000F000Fu) | M);
+      o[4 * i + 1] = g.weight((__byte_perm(v, h, 0x0501) & 0x000F000Fu) | M);
+      o[4 * i + 2] = g.weight((__byte_perm(v, h, 0x0602) & 0x000F000Fu) | M);
+      o[4 * i + 3] = g.weight((__byte_perm(v, h, 0x0703) & 0x000F000Fu) | M);
+    }
+  } else if constexpr (BITS == 2) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t v = w[i], h = v >> 2;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {   // byte k: codes 4k .. 4k + 3
+        const uint32_t b = __byte_perm(v, h, 0x0400 + 0x0101 * k);
+        o[8 * i + 2 * k] = g.weight((b & 0x00030003u) | M);
+        o[8 * i + 2 * k + 1] = g.weight(((b >> 4) & 0x00030003u) | M);
+      }
+    }
+  } else if constexpr (BITS == 3) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {   // six bits from stream bit 6 i
+      const int pos = 6 * i, wi = pos >> 5, off = pos & 31;
+      const uint32_t v = off + 6 > 32 ? __funnelshift_r(w[wi], w[wi + 1], off) : w[wi] >> off;
+      o[i] = g.weight((v & 7u) | ((v << 13) & 0x00070000u) | M);
+    }
+  } else if constexpr (M == 0x64006400u) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      o[2 * i] = g.weight(__byte_perm(w[i], 0x64646464u, 0x4140));
+      o[2 * i + 1] = g.weight(__byte_perm(w[i], 0x64646464u, 0x4342));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t v = w[i >> 1];
+      const float a = __uint_as_float(__byte_perm(v, 0x4B000000u, (i & 1) ? 0x7442 : 0x7440)) - g.z;
+      const float b = __uint_as_float(__byte_perm(v, 0x4B000000u, (i & 1) ? 0x7443 : 0x7441)) - g.z;
+      const __nv_bfloat162 p = __floats2bfloat162_rn(a * g.s, b * g.s);
+      o[i] = *reinterpret_cast<const uint32_t *>(&p);
+    }
+  }
+}
+
+// The power of two that a row's scales are divided by for fp16: the largest
+// one's, over the groups that columns [k0, k1) belong to.  Its exponent bits;
+// 2^(254 - e) is its reciprocal.
+__device__ __forceinline__ uint32_t row_exponent(const PackedArgs &p, int64_t row, int k0, int k1) {
+  const float *s = p.scales + (row < p.r ? row : p.r - 1) * p.G;
+  const int g0 = p.group > 0 ? k0 / p.group : 0;
+  const int g1 = p.group > 0 ? min(p.G, (k1 + p.group - 1) / p.group) : 1;
+  uint32_t top = 0;
+  for (int g = g0; g < g1; ++g) top = max(top, __float_as_uint(__ldg(s + g)) & 0x7FFFFFFFu);
+  return min(max(top >> 23, 1u), 253u);
+}
+
+template <int BITS, typename T>
+__global__ void __launch_bounds__(MANY_THREADS, 1)
+    packed_many_kernel(const __grid_constant__ CUtensorMap tmX, const ManyArgs a) {
+  constexpr bool HALF = Pair<T>::M == 0x64006400u;
+  constexpr int WORDS = 2 * BITS;                       // of a row per step
+  constexpr int AHEAD = BITS == 8 ? 2 : 4;              // own steps a converter loads ahead
+  extern __shared__ uint8_t dyn_smem[];
+  __shared__ ManyShared sh;
+  uint8_t *smem =
+      reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int N = a.N, bstage_bytes = N * PK * 2;
+  const int crank = blockIdx.x % a.ctas_k;
+  const int ctas = gridDim.x / a.ctas_k, cta = blockIdx.x / a.ctas_k;
+  const int tiles = a.nM * a.nN;
+  const int total = (a.p.d + PK - 1) / PK;
+  const int ks0 = (int)((int64_t)total * crank / a.ctas_k);
+  const int ks1 = (int)((int64_t)total * (crank + 1) / a.ctas_k);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < MAXB; ++s) {
+      mbar_init(&sh.full_b[s], 1);
+      mbar_init(&sh.empty_b[s], 1);
+    }
+    for (int s = 0; s < ASTAGES; ++s) {
+      mbar_init(&sh.full_a[s], 4);
+      mbar_init(&sh.empty_a[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh.acc_full[b], 1);
+      mbar_init(&sh.acc_empty[b], 4);
+    }
+    mbar_init(&sh.drain, 1);
+    sh.abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- x by TMA
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, issued_par = 0;
+      bool ok = true;
+      for (int t = cta; t < tiles && ok; t += ctas) {
+        const int n0 = (t / a.nM) * N;
+        for (int ks = ks0; ks < ks1; ++ks) {
+          if (*(volatile int *)&sh.abort) {
+            ok = false;
+            break;
+          }
+          if (!mbar_wait_bounded(&sh.empty_b[stage], phase ^ 1)) {
+            many_timeout(a.status, sh);
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&sh.full_b[stage], bstage_bytes);
+          issued |= 1u << stage;
+          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+          // feature offset: a multiple of 64 16-bit values = 128 bytes
+          tma_load_2d(smem + (size_t)stage * bstage_bytes, &tmX, ks * PK, n0, &sh.full_b[stage]);
+          if (++stage == a.bstages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      for (int s = 0; s < MAXB; ++s)
+        if (issued & (1u << s)) (void)mbar_wait_bounded(&sh.full_b[s], (issued_par >> s) & 1u);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- the MMAs
+    if (lane == 0) {
+      const uint32_t fmt = HALF ? 0u : 1u;
+      const uint32_t idesc = instr_desc(fmt, fmt, 0, 0, PM, N);
+      int bstage = 0, as = 0;
+      uint32_t bphase = 0, aphase = 0, abuf = 0, cphase = 0;
+      bool ok = true;
+      for (int t = cta; t < tiles && ok; t += ctas) {
+        if (!mbar_wait_bounded(&sh.acc_empty[abuf], cphase ^ 1)) {
+          many_timeout(a.status, sh);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t dt = tmem + abuf * PN;
+        for (int ks = ks0; ks < ks1; ++ks) {
+          if (!mbar_wait_bounded(&sh.full_b[bstage], bphase) ||
+              !mbar_wait_bounded(&sh.full_a[as], aphase)) {
+            many_timeout(a.status, sh);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t b0 = smem_u32(smem + (size_t)bstage * bstage_bytes);
+          const uint32_t a0 = tmem + TM_A + as * (PK / 2);
+#pragma unroll
+          for (int kk = 0; kk < PK / 16; ++kk)
+            umma_f16_ts(dt, a0 + kk * 8, smem_desc(b0 + kk * 32, 16, 1024, 2), idesc,
+                        (ks > ks0 || kk > 0) ? 1u : 0u);
+          umma_commit(&sh.empty_b[bstage]);
+          umma_commit(&sh.empty_a[as]);
+          if (++bstage == a.bstages) {
+            bstage = 0;
+            bphase ^= 1;
+          }
+          if (++as == ASTAGES) {
+            as = 0;
+            aphase ^= 1;
+          }
+        }
+        if (!ok) break;
+        umma_commit(&sh.acc_full[abuf]);
+        abuf ^= 1;
+        if (abuf == 0) cphase ^= 1;
+      }
+      umma_commit(&sh.drain);
+      (void)mbar_wait_bounded(&sh.drain, 0);
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // ---------------------------------------------------------------- weights to TMEM
+    const int wg = (warp - 4) >> 2, quarter = warp & 3;
+    const int lrow = quarter * 32 + lane;
+    const int64_t wpr = (int64_t)(a.p.d / 32) * BITS;
+    const int nst = ks1 - ks0;
+    const int mine = (tiles - cta + ctas - 1) / ctas;   // tiles of this CTA
+    const int64_t nq = (int64_t)(mine > 0 ? mine : 0) * nst;
+    struct Pre {
+      uint32_t w[WORDS];
+      float s[2];
+      int z[2];
+    };
+    Pre pre[AHEAD];
+    // the loading cursor runs AHEAD of this warpgroup's steps in front of the converting one
+    int lt = cta, lk = wg;
+    while (lk >= nst && lt < tiles) lk -= nst, lt += ctas;
+    auto load = [&](Pre &p) {
+      if (lt < tiles) {
+        const int64_t at = (int64_t)(lt % a.nM) * PM + lrow;
+        const int64_t row = at < a.p.r ? at : a.p.r - 1;   // rows past the last: its codes again, dropped
+        const int ks = ks0 + lk;
+        const bool second = ks * PK + 32 < a.p.d;       // the step's second 32 columns exist
+        const uint32_t *src = a.p.qweight + row * wpr + (int64_t)ks * WORDS;
+        if (a.aligned) {
+#pragma unroll
+          for (int i = 0; i < WORDS; i += 4) {
+            if constexpr (WORDS % 4 == 0) {
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (i < BITS || second) v = __ldg(reinterpret_cast<const uint4 *>(src + i));
+              p.w[i] = v.x, p.w[i + 1] = v.y, p.w[i + 2] = v.z, p.w[i + 3] = v.w;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < WORDS; ++i) p.w[i] = (i < BITS || second) ? __ldg(src + i) : 0u;
+        }
+        const int g0 = a.p.group > 0 ? ks * PK / a.p.group : 0;
+        const int g1 = a.p.group > 0 && second ? (ks * PK + 32) / a.p.group : g0;
+        p.s[0] = __ldg(a.p.scales + row * a.p.G + g0);
+        p.z[0] = __ldg(a.p.zeros + row * a.p.G + g0);
+        p.s[1] = p.s[0];
+        p.z[1] = p.z[0];
+        if (g1 != g0) {
+          p.s[1] = __ldg(a.p.scales + row * a.p.G + g1);
+          p.z[1] = __ldg(a.p.zeros + row * a.p.G + g1);
+        }
+        lk += 2;
+        while (lk >= nst && lt < tiles) lk -= nst, lt += ctas;
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) load(pre[i]);
+    int ck = wg, ct = cta, ordinal = 0;   // converting cursor: step, tile, tile's ordinal
+    while (ck >= nst && ct < tiles) ck -= nst, ct += ctas, ++ordinal;
+    int as = wg;                           // A stage of step q is q % ASTAGES
+    uint32_t aphase = 0;
+    int factored = -1;
+    float inv = 1.f;
+    bool ok = true;
+    for (int64_t q = wg; q < nq && ok;) {
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        if (q < nq && ok) {
+          if constexpr (HALF) {
+            if (factored != ordinal) {   // a new tile: the row's factor
+              factored = ordinal;
+              const int64_t rg = (int64_t)(ct % a.nM) * PM + lrow;
+              inv = __uint_as_float((254u - row_exponent(a.p, rg, ks0 * PK, ks1 * PK)) << 23);
+            }
+          }
+          uint32_t o[32];
+          Pre &p = pre[u];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            Group<BITS, T> g;
+            g.set(HALF ? p.s[h] * inv : p.s[h], p.z[h]);
+            uint32_t c[16];
+            chunk_weights<BITS, T>(p.w + h * BITS, g, c);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[16 * h + i] = c[i];
+          }
+          load(p);
+          if (!mbar_wait_bounded(&sh.empty_a[as], aphase ^ 1)) {
+            if (lane == 0) many_timeout(a.status, sh);
+            ok = false;
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            tc_fence_after();
+            const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + TM_A + as * (PK / 2);
+            uint32_t c[16];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) c[i] = o[16 * h + i];
+              tmem_st_x16(dst + 16 * h, c);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.full_a[as]);
+          }
+          as += 2;
+          if (as >= ASTAGES) {
+            as -= ASTAGES;
+            aphase ^= 1;
+          }
+          ck += 2;
+          while (ck >= nst && ct < tiles) ck -= nst, ct += ctas, ++ordinal;
+          q += 2;
+        }
+      }
+    }
+  } else if (warp >= 12) {
+    // ---------------------------------------------------------------- results
+    const int quarter = warp & 3;
+    const int lrow = quarter * 32 + lane;
+    uint32_t abuf = 0, cphase = 0;
+    float *part = reinterpret_cast<float *>(smem);   // split k: [N][PM] sums of this CTA
+    for (int t = cta; t < tiles; t += ctas) {
+      const int64_t row = (int64_t)(t % a.nM) * PM + lrow;
+      const int64_t t0 = (int64_t)(t / a.nM) * N;
+      float f = 1.f;
+      if constexpr (HALF) f = __uint_as_float(row_exponent(a.p, row, ks0 * PK, ks1 * PK) << 23);
+      bool ok = mbar_wait_bounded(&sh.acc_full[abuf], cphase);
+      if (!ok && lane == 0) many_timeout(a.status, sh);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const float bias = a.p.bias && row < a.p.r ? load_as_float(a.p.bias, a.p.ytype, row) : 0.f;
+      const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + abuf * PN;
+      for (int c0 = 0; c0 < N; c0 += 16) {
+        float v[16];
+        tmem_ld_32x32b_x16(base + c0, v);
+        tmem_wait_ld();
+        if (a.ctas_k > 1) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) part[(c0 + i) * PM + lrow] = v[i] * f;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int64_t tok = t0 + c0 + i;
+            if (tok < a.p.n && row < a.p.r) {
+              float y = v[i] * f;
+              if (a.p.x_scales) y *= __ldg(a.p.x_scales + tok);
+              store_float(a.p.y, a.p.ytype, tok * a.p.r + row, y + bias);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.acc_empty[abuf]);
+      abuf ^= 1;
+      if (abuf == 0) cphase ^= 1;
+    }
+  }
+
+  __syncthreads();
+  if (a.ctas_k > 1) {
+    // one tile per cluster: add the CTAs' sums, each CTA its share of the tokens
+    __syncwarp();
+    cluster_sync();
+    if (cta < tiles && !*(volatile int *)&sh.abort) {
+      const float *part = reinterpret_cast<const float *>(smem);
+      const int64_t m0 = (int64_t)(cta % a.nM) * PM, t0 = (int64_t)(cta / a.nM) * N;
+      const int c0 = N * crank / a.ctas_k, c1 = N * (crank + 1) / a.ctas_k;
+      for (int i = c0 * PM + threadIdx.x; i < c1 * PM; i += MANY_THREADS) {
+        const int64_t tok = t0 + i / PM, row = m0 + i % PM;
+        if (tok >= a.p.n || row >= a.p.r) continue;
+        float y = 0.f;
+        for (int k = 0; k < a.ctas_k; ++k) {
+          float o;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(cluster_addr(part + i, k)));
+          y += o;
+        }
+        if (a.p.x_scales) y *= __ldg(a.p.x_scales + tok);
+        if (a.p.bias) y += load_as_float(a.p.bias, a.p.ytype, row);
+        store_float(a.p.y, a.p.ytype, tok * a.p.r + row, y);
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+template <int BITS, typename T>
+int launch_many(const PackedArgs &p, cudaStream_t st) {
+  ManyArgs a{};
+  a.p = p;
+  const int sms = num_sms();
+  const int64_t nM = (p.r + PM - 1) / PM;
+  const int steps = (p.d + PK - 1) / PK;
+  // Tokens per tile: all of them when they fit; else the width that wastes
+  // least, a round of tiles over the SMs costing N tokens of MMAs (or the
+  // conversion of the weights, about as long as 104 tokens').
+  int N = (int)((p.n + 15) / 16 * 16);
+  if (p.n > PN) {
+    int64_t best = INT64_MAX;
+    for (int c = PN; c >= 96; c -= 16) {
+      const int64_t rounds = (nM * ((p.n + c - 1) / c) + sms - 1) / sms;
+      const int64_t cost = rounds * (c > 104 ? c : 104);
+      if (cost < best) best = cost, N = c;
+    }
+  }
+  const int64_t nN = (p.n + N - 1) / N;
+  if (nM * nN > INT32_MAX / 8) return GPTQ_ERR_INVALID_ARG;
+  a.N = N;
+  a.nM = (int)nM;
+  a.nN = (int)nN;
+  const int64_t tiles = nM * nN;
+  // k split over a cluster while SMs stay idle and a CTA keeps eight steps
+  int ck = 1;
+  while (ck < 8 && tiles * (ck + 1) <= sms && steps >= 8 * (ck + 1)) ++ck;
+  a.ctas_k = ck;
+  const int stage = N * PK * 2;
+  int nb = (int)(B_BYTES / stage);
+  a.bstages = nb > MAXB ? MAXB : nb;
+  size_t bytes = (size_t)a.bstages * stage;
+  const size_t part = ck > 1 ? (size_t)N * PM * 4 : 0;
+  if (bytes < part) bytes = part;
+  a.aligned = BITS != 3 && reinterpret_cast<uintptr_t>(p.qweight) % 16 == 0 &&
+              ((int64_t)(p.d / 32) * BITS) % 4 == 0;
+  a.status = device_status_word();
+  if (!a.status) return GPTQ_ERR_CUDA;
+  EncodeTiledFn enc = encode_fn();
+  CUtensorMap tx;
+  const cuuint64_t gdim[2] = {(cuuint64_t)p.d, (cuuint64_t)p.n};
+  const cuuint64_t gstride[1] = {(cuuint64_t)p.d * 2};
+  const cuuint32_t box[2] = {(cuuint32_t)PK, (cuuint32_t)N};
+  const cuuint32_t es[2] = {1, 1};
+  if (!enc || enc(&tx, Pair<T>::M == 0x64006400u ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  2, const_cast<void *>(p.x), gdim, gstride, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+    set_last_error_msg(__FILE__, __LINE__, "cuTensorMapEncodeTiled rejected the activations");
+    return GPTQ_ERR_CUDA;
+  }
+  static std::atomic<bool> attr[64] = {};
+  if (const int rc = ensure_smem_attr(packed_many_kernel<BITS, T>, B_BYTES + 1024, attr)) return rc;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ck;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(ck > 1 ? tiles * ck : (tiles < sms ? tiles : sms)));
+  cfg.blockDim = dim3(MANY_THREADS);
+  cfg.dynamicSmemBytes = bytes + 1024;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = ck > 1 ? 1 : 0;
+  count_launch();
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, packed_many_kernel<BITS, T>, tx, a);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    set_last_error(__FILE__, __LINE__, "kernel launch", e);
+    return GPTQ_ERR_CUDA;
+  }
+  return GPTQ_OK;
+}
+
+template <typename T>
+int launch_many_type(const PackedArgs &p, cudaStream_t st) {
+  switch (p.bits) {
+    case 2: return launch_many<2, T>(p, st);
+    case 3: return launch_many<3, T>(p, st);
+    case 4: return launch_many<4, T>(p, st);
+    default: return launch_many<8, T>(p, st);
+  }
+}
+
+}  // namespace
+
+int launch_packed_many(const PackedArgs &p, cudaStream_t st) {
+  return p.xtype == GPTQ_BF16 ? launch_many_type<__nv_bfloat16>(p, st)
+                              : launch_many_type<__half>(p, st);
+}
+
+}  // namespace gptq
