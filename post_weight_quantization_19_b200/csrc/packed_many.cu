@@ -3,11 +3,11 @@
 //
 // One CTA per tile of 128 rows of W and N <= 192 tokens.  The weights are the
 // MMA's A operand, in tensor memory: thread i of a converter warpgroup owns row
-// i of the tile, reads the row's packed codes straight from global memory into
-// registers (four steps of 64 columns ahead), turns them into 16-bit weights
-// and writes them to its TMEM lane (tcgen05.st).  x is the B operand: tiles of
+// i of the tile, copies the row's packed codes to shared memory (cp.async, up
+// to twelve steps of 64 columns ahead), turns them into 16-bit weights and
+// writes them to its TMEM lane (tcgen05.st).  x is the B operand: tiles of
 // 64 features x N tokens that TMA places in 128-byte-swizzled shared memory.
-// So shared memory carries only x, and a code costs 2.5 instructions once per
+// So shared memory carries x and the codes, not the weights, and a code costs 2.5 instructions once per
 // N tokens.
 //
 //   w = T16(s (q - z)):  q - z is exact in 16 bits (code bits in the mantissa of
@@ -19,8 +19,8 @@
 //   the row's sums multiplied by it again, so scales outside fp16's range lose
 //   nothing.
 //
-// Warp 0 issues TMA, warp 1 the MMAs (one thread each); warps 4-11 are the two
-// converter warpgroups, which take alternate steps; warps 12-15 drain one of
+// Warp 0 issues TMA, warp 1 the MMAs (one thread each); warps 4-19 are four
+// converter warpgroups, which take the steps in turn; warps 20-23 drain one of
 // two accumulators while the other fills.  With fewer tiles than SMs the k
 // range is split over a cluster, whose CTAs add their sums through distributed
 // shared memory in a fixed order.
@@ -37,8 +37,19 @@ constexpr int PK = 64;                  // features per step (one 128-byte row o
 constexpr int ASTAGES = 4;              // TMEM stages of A: 32 columns each
 constexpr int MAXB = 8;                 // shared-memory stages of x at most
 constexpr uint32_t TM_A = 2 * PN;       // TMEM column of the first A stage
-constexpr int MANY_THREADS = 512;
-constexpr size_t B_BYTES = 200 * 1024;  // shared memory for x
+constexpr int WGS = 4;                  // converter warpgroups
+constexpr int MANY_THREADS = 32 * (4 + 4 * WGS + 4);
+constexpr size_t MANY_SMEM = 224 * 1024;   // x and codes, after alignment
+
+// The codes, scales and zeros of one step: 16-byte chunks [chunk][row] (3-bit:
+// words [word][row]), then scales [2][row] and zeros [2][row].
+template <int BITS>
+struct CodeStage {
+  static constexpr int WORDS = 2 * BITS;            // of a row per step
+  static constexpr int DEPTH = BITS == 8 ? 2 : 3;   // steps a warpgroup loads ahead
+  static constexpr int BYTES = PM * (WORDS * 4 + 16);
+  static constexpr int ALL = WGS * DEPTH * BYTES;
+};
 
 struct ManyArgs {
   PackedArgs p;
@@ -47,6 +58,7 @@ struct ManyArgs {
   int ctas_k;         // CTAs of a cluster, along k
   int bstages;
   int aligned;        // 16-byte loads of the codes
+  uint32_t gdiv;      // ceil(2^31 / (group / 32)), 0 for one group
   int *status;
 };
 
@@ -57,6 +69,7 @@ struct ManyShared {
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
+  uint32_t exponent[2][PM];   // fp16: row_exponent of a tile's rows
 };
 
 // D[tmem] (+)= A[tmem] * B[smem], 16-bit operands, fp32 accumulate.
@@ -213,24 +226,32 @@ __device__ __forceinline__ void chunk_weights(const uint32_t *w, const Group<BIT
   }
 }
 
-// The power of two that a row's scales are divided by for fp16: the largest
-// one's, over the groups that columns [k0, k1) belong to.  Its exponent bits;
-// 2^(254 - e) is its reciprocal.
-__device__ __forceinline__ uint32_t row_exponent(const PackedArgs &p, int64_t row, int k0, int k1) {
-  const float *s = p.scales + (row < p.r ? row : p.r - 1) * p.G;
-  const int g0 = p.group > 0 ? k0 / p.group : 0;
-  const int g1 = p.group > 0 ? min(p.G, (k1 + p.group - 1) / p.group) : 1;
-  uint32_t top = 0;
-  for (int g = g0; g < g1; ++g) top = max(top, __float_as_uint(__ldg(s + g)) & 0x7FFFFFFFu);
+// Group of the 32-column chunk c of a row.
+__device__ __forceinline__ int group_of(const ManyArgs &a, int c) {
+  return (int)(((uint64_t)(uint32_t)c * a.gdiv) >> 31);
+}
+
+// Exponent bits of the power of two that a row's scales are divided by for
+// fp16: the largest one's, from the bits of its magnitude; 2^(254 - e) is its
+// reciprocal.
+__device__ __forceinline__ uint32_t safe_exponent(uint32_t top) {
   return min(max(top >> 23, 1u), 253u);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
 }
 
 template <int BITS, typename T>
 __global__ void __launch_bounds__(MANY_THREADS, 1)
     packed_many_kernel(const __grid_constant__ CUtensorMap tmX, const ManyArgs a) {
   constexpr bool HALF = Pair<T>::M == 0x64006400u;
-  constexpr int WORDS = 2 * BITS;                       // of a row per step
-  constexpr int AHEAD = BITS == 8 ? 2 : 4;              // own steps a converter loads ahead
+  using S = CodeStage<BITS>;
   extern __shared__ uint8_t dyn_smem[];
   __shared__ ManyShared sh;
   uint8_t *smem =
@@ -351,121 +372,155 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       umma_commit(&sh.drain);
       (void)mbar_wait_bounded(&sh.drain, 0);
     }
-  } else if (warp >= 4 && warp < 12) {
+  } else if (warp >= 4 && warp < 4 + 4 * WGS) {
     // ---------------------------------------------------------------- weights to TMEM
     const int wg = (warp - 4) >> 2, quarter = warp & 3;
     const int lrow = quarter * 32 + lane;
     const int64_t wpr = (int64_t)(a.p.d / 32) * BITS;
     const int nst = ks1 - ks0;
-    const int mine = (tiles - cta + ctas - 1) / ctas;   // tiles of this CTA
-    const int64_t nq = (int64_t)(mine > 0 ? mine : 0) * nst;
-    struct Pre {
-      uint32_t w[WORDS];
-      float s[2];
-      int z[2];
-    };
-    Pre pre[AHEAD];
-    // the loading cursor runs AHEAD of this warpgroup's steps in front of the converting one
+    const uint32_t ring = smem_u32(smem) + a.bstages * bstage_bytes + wg * S::DEPTH * S::BYTES;
+    // The loading cursor (step lk of tile lt) runs DEPTH own steps in front of
+    // the converting one.  A thread copies and reads its own row only.
     int lt = cta, lk = wg;
-    while (lk >= nst && lt < tiles) lk -= nst, lt += ctas;
-    auto load = [&](Pre &p) {
-      if (lt < tiles) {
+    const uint32_t *lq = nullptr;
+    const float *ls = nullptr;
+    const int32_t *lz = nullptr;
+    auto settle = [&]() {   // the cursor moved: carry into the next tile
+      while (lk >= nst && lt < tiles) lk -= nst, lt += ctas, lq = nullptr;
+      if (!lq && lt < tiles) {
         const int64_t at = (int64_t)(lt % a.nM) * PM + lrow;
-        const int64_t row = at < a.p.r ? at : a.p.r - 1;   // rows past the last: its codes again, dropped
-        const int ks = ks0 + lk;
-        const bool second = ks * PK + 32 < a.p.d;       // the step's second 32 columns exist
-        const uint32_t *src = a.p.qweight + row * wpr + (int64_t)ks * WORDS;
-        if (a.aligned) {
-#pragma unroll
-          for (int i = 0; i < WORDS; i += 4) {
-            if constexpr (WORDS % 4 == 0) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (i < BITS || second) v = __ldg(reinterpret_cast<const uint4 *>(src + i));
-              p.w[i] = v.x, p.w[i + 1] = v.y, p.w[i + 2] = v.z, p.w[i + 3] = v.w;
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < WORDS; ++i) p.w[i] = (i < BITS || second) ? __ldg(src + i) : 0u;
-        }
-        const int g0 = a.p.group > 0 ? ks * PK / a.p.group : 0;
-        const int g1 = a.p.group > 0 && second ? (ks * PK + 32) / a.p.group : g0;
-        p.s[0] = __ldg(a.p.scales + row * a.p.G + g0);
-        p.z[0] = __ldg(a.p.zeros + row * a.p.G + g0);
-        p.s[1] = p.s[0];
-        p.z[1] = p.z[0];
-        if (g1 != g0) {
-          p.s[1] = __ldg(a.p.scales + row * a.p.G + g1);
-          p.z[1] = __ldg(a.p.zeros + row * a.p.G + g1);
-        }
-        lk += 2;
-        while (lk >= nst && lt < tiles) lk -= nst, lt += ctas;
+        const int64_t row = at < a.p.r ? at : a.p.r - 1;   // past the last: its codes again, dropped
+        lq = a.p.qweight + row * wpr;
+        ls = a.p.scales + row * a.p.G;
+        lz = a.p.zeros + row * a.p.G;
       }
     };
+    settle();
+    auto load = [&](int slot) {
+      if (lt < tiles) {
+        const int ks = ks0 + lk;
+        const bool second = ks * PK + 32 < a.p.d;       // the step's second 32 columns exist
+        const uint32_t dst = ring + slot * S::BYTES;
+        const uint32_t *src = lq + (int64_t)ks * S::WORDS;
+        bool done = false;
+        if constexpr (BITS != 3) {
+          if (a.aligned) {
+            done = true;
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) load(pre[i]);
-    int ck = wg, ct = cta, ordinal = 0;   // converting cursor: step, tile, tile's ordinal
-    while (ck >= nst && ct < tiles) ck -= nst, ct += ctas, ++ordinal;
-    int as = wg;                           // A stage of step q is q % ASTAGES
+            for (int i = 0; i < S::WORDS; i += 4) {
+              const bool in = i < BITS || second;
+              cp_async16(dst + (i / 4 * PM + lrow) * 16, src + (in ? i : 0), in ? 16 : 0);
+            }
+          }
+        }
+        if (!done) {
+#pragma unroll
+          for (int i = 0; i < S::WORDS; ++i) {
+            const bool in = i < BITS || second;
+            const uint32_t at = BITS == 3 ? (i * PM + lrow) * 4 : (i / 4 * PM + lrow) * 16 + i % 4 * 4;
+            cp_async4(dst + at, src + (in ? i : 0), in ? 4 : 0);
+          }
+        }
+        const int g0 = group_of(a, ks * 2), g1 = second ? group_of(a, ks * 2 + 1) : g0;
+        const uint32_t sz = dst + PM * S::WORDS * 4 + lrow * 4;
+        cp_async4(sz, ls + g0, 4);
+        cp_async4(sz + PM * 8, lz + g0, 4);
+        if (g1 != g0) {
+          cp_async4(sz + PM * 4, ls + g1, 4);
+          cp_async4(sz + PM * 12, lz + g1, 4);
+        }
+        lk += WGS;
+        settle();
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < S::DEPTH; ++i) load(i);
+    int slot = 0, as = wg % ASTAGES, ck = wg, parity = 0;   // A stage of step q is q % ASTAGES
     uint32_t aphase = 0;
-    int factored = -1;
-    float inv = 1.f;
     bool ok = true;
-    for (int64_t q = wg; q < nq && ok;) {
+    // (a warp that gave up still walks the tiles: the others wait for it at their barrier)
+    for (int t = cta; t < tiles; t += ctas, parity ^= 1, ck -= nst) {
+      float inv = 1.f;
+      if constexpr (HALF) {
+        // the largest scale of each row over this CTA's columns: a warp takes
+        // PM / (4 WGS) rows, lanes along the groups
+        const int ga = group_of(a, ks0 * 2), gb = group_of(a, min(ks1 * 2, a.p.d / 32) - 1);
+        constexpr int EACH = PM / (4 * WGS);
+        uint32_t top[EACH];
 #pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
-        if (q < nq && ok) {
-          if constexpr (HALF) {
-            if (factored != ordinal) {   // a new tile: the row's factor
-              factored = ordinal;
-              const int64_t rg = (int64_t)(ct % a.nM) * PM + lrow;
-              inv = __uint_as_float((254u - row_exponent(a.p, rg, ks0 * PK, ks1 * PK)) << 23);
-            }
-          }
-          uint32_t o[32];
-          Pre &p = pre[u];
+        for (int i = 0; i < EACH; ++i) {
+          const int64_t at = (int64_t)(t % a.nM) * PM + (warp - 4) * EACH + i;
+          const float *srow = a.p.scales + (at < a.p.r ? at : a.p.r - 1) * a.p.G;
+          top[i] = 0;
+          for (int g = ga + lane; g <= gb; g += 32)
+            top[i] = max(top[i], __float_as_uint(__ldg(srow + g)) & 0x7FFFFFFFu);
+        }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            Group<BITS, T> g;
-            g.set(HALF ? p.s[h] * inv : p.s[h], p.z[h]);
-            uint32_t c[16];
-            chunk_weights<BITS, T>(p.w + h * BITS, g, c);
+        for (int i = 0; i < EACH; ++i) {
+          const uint32_t e = safe_exponent(__reduce_max_sync(0xffffffffu, top[i]));
+          if (lane == 0) sh.exponent[parity][(warp - 4) * EACH + i] = e;
+        }
+        // (the other parity's values were read before this barrier)
+        asm volatile("bar.sync 1, %0;" ::"n"(128 * WGS) : "memory");
+        inv = __uint_as_float((254u - sh.exponent[parity][lrow]) << 23);
+      }
+      for (; ck < nst && ok; ck += WGS) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S::DEPTH - 1) : "memory");
+        const uint32_t src = ring + slot * S::BYTES;
+        const uint32_t sz = src + PM * S::WORDS * 4 + lrow * 4;
+        uint32_t w[S::WORDS];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[16 * h + i] = c[i];
+        for (int i = 0; i < S::WORDS; ++i) {
+          if constexpr (BITS == 3) {
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i]) : "r"(src + (i * PM + lrow) * 4));
+          } else if (i % 4 == 0) {
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                         : "r"(src + (i / 4 * PM + lrow) * 16));
           }
-          load(p);
-          if (!mbar_wait_bounded(&sh.empty_a[as], aphase ^ 1)) {
-            if (lane == 0) many_timeout(a.status, sh);
-            ok = false;
-          }
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-            tc_fence_after();
-            const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + TM_A + as * (PK / 2);
-            uint32_t c[16];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) c[i] = o[16 * h + i];
-              tmem_st_x16(dst + 16 * h, c);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.full_a[as]);
-          }
-          as += 2;
-          if (as >= ASTAGES) {
-            as -= ASTAGES;
-            aphase ^= 1;
-          }
-          ck += 2;
-          while (ck >= nst && ct < tiles) ck -= nst, ct += ctas, ++ordinal;
-          q += 2;
+        }
+        const int ks = ks0 + ck;
+        const bool two = ks * PK + 32 < a.p.d && group_of(a, ks * 2 + 1) != group_of(a, ks * 2);
+        Group<BITS, T> g;
+        float s;
+        int z;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(sz));
+        asm volatile("ld.shared.s32 %0, [%1];" : "=r"(z) : "r"(sz + PM * 8));
+        g.set(s * inv, z);
+        uint32_t c[16];
+        chunk_weights<BITS, T>(w, g, c);
+        if (!mbar_wait_bounded(&sh.empty_a[as], aphase ^ 1)) {
+          if (lane == 0) many_timeout(a.status, sh);
+          ok = false;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + TM_A + as * (PK / 2);
+        tmem_st_x16(dst, c);
+        if (two) {
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(sz + PM * 4));
+          asm volatile("ld.shared.s32 %0, [%1];" : "=r"(z) : "r"(sz + PM * 12));
+          g.set(s * inv, z);
+        }
+        chunk_weights<BITS, T>(w + BITS, g, c);
+        tmem_st_x16(dst + 16, c);
+        load(slot);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.full_a[as]);
+        if (++slot == S::DEPTH) slot = 0;
+        as += WGS % ASTAGES;
+        if (WGS % ASTAGES == 0 || as >= ASTAGES) {
+          as -= WGS % ASTAGES == 0 ? 0 : ASTAGES;
+          aphase ^= 1;
         }
       }
     }
-  } else if (warp >= 12) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  } else if (warp >= 4 + 4 * WGS) {
     // ---------------------------------------------------------------- results
     const int quarter = warp & 3;
     const int lrow = quarter * 32 + lane;
@@ -475,7 +530,14 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       const int64_t row = (int64_t)(t % a.nM) * PM + lrow;
       const int64_t t0 = (int64_t)(t / a.nM) * N;
       float f = 1.f;
-      if constexpr (HALF) f = __uint_as_float(row_exponent(a.p, row, ks0 * PK, ks1 * PK) << 23);
+      if constexpr (HALF) {
+        const float *srow = a.p.scales + (row < a.p.r ? row : a.p.r - 1) * a.p.G;
+        const int ga = group_of(a, ks0 * 2), gb = group_of(a, min(ks1 * 2, a.p.d / 32) - 1);
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int g = ga; g <= gb; ++g) top = max(top, __float_as_uint(__ldg(srow + g)) & 0x7FFFFFFFu);
+        f = __uint_as_float(safe_exponent(top) << 23);
+      }
       bool ok = mbar_wait_bounded(&sh.acc_full[abuf], cphase);
       if (!ok && lane == 0) many_timeout(a.status, sh);
       ok = __all_sync(0xffffffffu, ok);
@@ -594,13 +656,14 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
   while (ck < 8 && tiles * (ck + 1) <= sms && steps >= 8 * (ck + 1)) ++ck;
   a.ctas_k = ck;
   const int stage = N * PK * 2;
-  int nb = (int)(B_BYTES / stage);
+  const int nb = (int)((MANY_SMEM - CodeStage<BITS>::ALL) / stage);
+  static_assert((MANY_SMEM - CodeStage<BITS>::ALL) / (PN * PK * 2) >= 4, "too few stages of x");
   a.bstages = nb > MAXB ? MAXB : nb;
-  size_t bytes = (size_t)a.bstages * stage;
-  const size_t part = ck > 1 ? (size_t)N * PM * 4 : 0;
-  if (bytes < part) bytes = part;
+  // (the sums of a split k, N PM floats, take the place of at least four stages of x)
+  const size_t bytes = (size_t)a.bstages * stage + CodeStage<BITS>::ALL;
   a.aligned = BITS != 3 && reinterpret_cast<uintptr_t>(p.qweight) % 16 == 0 &&
               ((int64_t)(p.d / 32) * BITS) % 4 == 0;
+  a.gdiv = p.group > 0 ? (uint32_t)(((1ull << 31) + p.group / 32 - 1) / (p.group / 32)) : 0;
   a.status = device_status_word();
   if (!a.status) return GPTQ_ERR_CUDA;
   EncodeTiledFn enc = encode_fn();
@@ -619,7 +682,7 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
     return GPTQ_ERR_CUDA;
   }
   static std::atomic<bool> attr[64] = {};
-  if (const int rc = ensure_smem_attr(packed_many_kernel<BITS, T>, B_BYTES + 1024, attr)) return rc;
+  if (const int rc = ensure_smem_attr(packed_many_kernel<BITS, T>, MANY_SMEM + 1024, attr)) return rc;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = ck;
