@@ -2,10 +2,12 @@
 // tensor cores, the weights dequantised on their way into tensor memory.
 //
 // One CTA per tile of 128 rows of W and N <= 192 tokens.  The weights are the
-// MMA's A operand, in tensor memory: thread i of a converter warpgroup owns row
-// i of the tile, copies the row's packed codes to shared memory (cp.async, up
-// to twelve steps of 64 columns ahead), turns them into 16-bit weights and
-// writes them to its TMEM lane (tcgen05.st).  x is the B operand: tiles of
+// MMA's A operand, in tensor memory: two loader warps bring blocks of 128 rows x
+// 256 columns of codes to shared memory (cp.async, whole lines per row; threads
+// that each copied their own row's 32 bytes spent a tag lookup per 16 bytes and
+// ran at half this speed), and thread i of a converter warpgroup, which owns
+// row i, turns 64 columns of it into 16-bit weights and writes them to its TMEM
+// lane (tcgen05.st).  x is the B operand: tiles of
 // 64 features x N tokens that TMA places in 128-byte-swizzled shared memory.
 // So shared memory carries x and the codes, not the weights, and a code costs 2.5 instructions once per
 // N tokens.
@@ -19,9 +21,9 @@
 //   the row's sums multiplied by it again, so scales outside fp16's range lose
 //   nothing.
 //
-// Warp 0 issues TMA, warp 1 the MMAs (one thread each); warps 4-19 are four
-// converter warpgroups, which take the steps in turn; warps 20-23 drain one of
-// two accumulators while the other fills.  With fewer tiles than SMs the k
+// Warp 0 issues TMA, warp 1 the MMAs (one thread each), warps 2-3 load codes;
+// warps 4-19 are four converter warpgroups, one for each 64 columns of a block;
+// warps 20-23 drain one of two accumulators while the other fills.  With fewer tiles than SMs the k
 // range is split over a cluster, whose CTAs add their sums through distributed
 // shared memory in a fixed order.
 #include <mutex>
@@ -41,14 +43,21 @@ constexpr int WGS = 4;                  // converter warpgroups
 constexpr int MANY_THREADS = 32 * (4 + 4 * WGS + 4);
 constexpr size_t MANY_SMEM = 224 * 1024;   // x and codes, after alignment
 
-// The codes, scales and zeros of one step: 16-byte chunks [chunk][row] (3-bit:
-// words [word][row]), then scales [2][row] and zeros [2][row].
+constexpr int BLK = WGS;                // steps per block of codes
+constexpr int BCOLS = BLK * PK;         // its columns
+constexpr int LOADERS = 64;
+static_assert(ASTAGES == BLK, "step j of a block uses A stage j");
+
+// A block of codes in shared memory: rows padded by 16 bytes (the 8 rows that
+// a quarter-warp's 16-byte reads touch fall on different banks), then scales
+// [sub][row] and zeros [sub][row] of its `subs` parts of equal group.
 template <int BITS>
-struct CodeStage {
-  static constexpr int WORDS = 2 * BITS;            // of a row per step
-  static constexpr int DEPTH = BITS == 8 ? 2 : 3;   // steps a warpgroup loads ahead
-  static constexpr int BYTES = PM * (WORDS * 4 + 16);
-  static constexpr int ALL = WGS * DEPTH * BYTES;
+struct CodeBlock {
+  static constexpr int ROW = BCOLS * BITS / 8;      // bytes of a row
+  static constexpr int PITCH = ROW + 16;
+  static constexpr int CODES = PM * PITCH;
+  static constexpr int DEPTH = BITS == 8 ? 2 : 3;
+  static __host__ __device__ constexpr int bytes(int subs) { return CODES + PM * 8 * subs; }
 };
 
 struct ManyArgs {
@@ -59,12 +68,14 @@ struct ManyArgs {
   int bstages;
   int aligned;        // 16-byte loads of the codes
   uint32_t gdiv;      // ceil(2^31 / (group / 32)), 0 for one group
+  int subs;           // parts of a block that lie in one group each: 1, 2, 4 or 8
   int *status;
 };
 
 struct ManyShared {
   uint64_t full_b[MAXB], empty_b[MAXB];
   uint64_t full_a[ASTAGES], empty_a[ASTAGES];
+  uint64_t full_c[3], empty_c[3];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
@@ -251,7 +262,7 @@ template <int BITS, typename T>
 __global__ void __launch_bounds__(MANY_THREADS, 1)
     packed_many_kernel(const __grid_constant__ CUtensorMap tmX, const ManyArgs a) {
   constexpr bool HALF = Pair<T>::M == 0x64006400u;
-  using S = CodeStage<BITS>;
+  using C = CodeBlock<BITS>;
   extern __shared__ uint8_t dyn_smem[];
   __shared__ ManyShared sh;
   uint8_t *smem =
@@ -261,9 +272,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
   const int crank = blockIdx.x % a.ctas_k;
   const int ctas = gridDim.x / a.ctas_k, cta = blockIdx.x / a.ctas_k;
   const int tiles = a.nM * a.nN;
-  const int total = (a.p.d + PK - 1) / PK;
-  const int ks0 = (int)((int64_t)total * crank / a.ctas_k);
-  const int ks1 = (int)((int64_t)total * (crank + 1) / a.ctas_k);
+  const int total = (a.p.d + PK - 1) / PK, blocks = (total + BLK - 1) / BLK;
+  const int kb0 = (int)((int64_t)blocks * crank / a.ctas_k);          // this CTA's blocks
+  const int kb1 = (int)((int64_t)blocks * (crank + 1) / a.ctas_k);
+  const int ks0 = kb0 * BLK, ks1 = min(kb1 * BLK, total);             // and steps
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < MAXB; ++s) {
@@ -273,6 +285,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     for (int s = 0; s < ASTAGES; ++s) {
       mbar_init(&sh.full_a[s], 4);
       mbar_init(&sh.empty_a[s], 1);
+    }
+    for (int c = 0; c < C::DEPTH; ++c) {
+      mbar_init(&sh.full_c[c], LOADERS);
+      mbar_init(&sh.empty_c[c], 4 * WGS);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh.acc_full[b], 1);
@@ -329,8 +345,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     if (lane == 0) {
       const uint32_t fmt = HALF ? 0u : 1u;
       const uint32_t idesc = instr_desc(fmt, fmt, 0, 0, PM, N);
-      int bstage = 0, as = 0;
-      uint32_t bphase = 0, aphase = 0, abuf = 0, cphase = 0;
+      int bstage = 0;
+      uint32_t bphase = 0, aphases = 0, abuf = 0, cphase = 0;
       bool ok = true;
       for (int t = cta; t < tiles && ok; t += ctas) {
         if (!mbar_wait_bounded(&sh.acc_empty[abuf], cphase ^ 1)) {
@@ -340,8 +356,9 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         tc_fence_after();
         const uint32_t dt = tmem + abuf * PN;
         for (int ks = ks0; ks < ks1; ++ks) {
+          const int as = (ks - ks0) % BLK;
           if (!mbar_wait_bounded(&sh.full_b[bstage], bphase) ||
-              !mbar_wait_bounded(&sh.full_a[as], aphase)) {
+              !mbar_wait_bounded(&sh.full_a[as], (aphases >> as) & 1u)) {
             many_timeout(a.status, sh);
             ok = false;
             break;
@@ -359,10 +376,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
             bstage = 0;
             bphase ^= 1;
           }
-          if (++as == ASTAGES) {
-            as = 0;
-            aphase ^= 1;
-          }
+          aphases ^= 1u << as;
         }
         if (!ok) break;
         umma_commit(&sh.acc_full[abuf]);
@@ -372,75 +386,83 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       umma_commit(&sh.drain);
       (void)mbar_wait_bounded(&sh.drain, 0);
     }
-  } else if (warp >= 4 && warp < 4 + 4 * WGS) {
+  } else if (warp < 4) {
+    // ---------------------------------------------------------------- codes to shared memory
+    const int id = threadIdx.x - 64;
+    const int64_t pitch = (int64_t)(a.p.d / 32) * BITS * 4;   // bytes per row
+    const uint32_t ring = smem_u32(smem) + a.bstages * bstage_bytes;
+    const int block_bytes = C::bytes(a.subs);
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = cta; t < tiles && ok; t += ctas) {
+      const int64_t m0 = (int64_t)(t % a.nM) * PM;
+      const int rows = (int)min((int64_t)PM, a.p.r - m0);
+      const char *q0 = reinterpret_cast<const char *>(a.p.qweight) + m0 * pitch;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait_bounded(&sh.empty_c[slot], phase ^ 1)) {
+          if (lane == 0) many_timeout(a.status, sh);
+          ok = false;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t dst = ring + slot * block_bytes;
+        const int k0 = kb * BCOLS;
+        const int valid = min(BCOLS, a.p.d - k0) * BITS / 8;   // bytes of a row that exist
+        const char *src = q0 + k0 * BITS / 8;
+        // rows past the last and columns past the row are filled with zeros
+        if (a.aligned) {
+          constexpr int PPR = C::ROW / 16;
+#pragma unroll 4
+          for (int i = 0; i < PM * PPR / LOADERS; ++i) {
+            const int p = id + LOADERS * i, row = p / PPR, col = p % PPR * 16;
+            const bool in = row < rows && col < valid;
+            cp_async16(dst + row * C::PITCH + col, in ? src + row * pitch + col : src,
+                       in ? min(16, valid - col) : 0);
+          }
+        } else {
+          constexpr int PPR = C::ROW / 4;
+#pragma unroll 4
+          for (int i = 0; i < PM * PPR / LOADERS; ++i) {
+            const int p = id + LOADERS * i, row = p / PPR, col = p % PPR * 4;
+            const bool in = row < rows && col < valid;
+            cp_async4(dst + row * C::PITCH + col, in ? src + row * pitch + col : src, in ? 4 : 0);
+          }
+        }
+        for (int sub = 0; sub < a.subs; ++sub) {
+          const int g = group_of(a, min(kb * (BCOLS / 32) + sub * (BCOLS / 32 / a.subs), a.p.d / 32 - 1));
+          const uint32_t sz = dst + C::CODES + sub * (PM * 4);
+#pragma unroll
+          for (int i = 0; i < PM / LOADERS; ++i) {
+            const int row = id + LOADERS * i;
+            const int64_t at = (m0 + (row < rows ? row : 0)) * a.p.G + g;
+            cp_async4(sz + row * 4, a.p.scales + at, row < rows ? 4 : 0);
+            cp_async4(sz + a.subs * (PM * 4) + row * 4, a.p.zeros + at, row < rows ? 4 : 0);
+          }
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                         smem_u32(&sh.full_c[slot]))
+                     : "memory");
+        if (++slot == C::DEPTH) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp < 4 + 4 * WGS) {
     // ---------------------------------------------------------------- weights to TMEM
     const int wg = (warp - 4) >> 2, quarter = warp & 3;
     const int lrow = quarter * 32 + lane;
-    const int64_t wpr = (int64_t)(a.p.d / 32) * BITS;
-    const int nst = ks1 - ks0;
-    const uint32_t ring = smem_u32(smem) + a.bstages * bstage_bytes + wg * S::DEPTH * S::BYTES;
-    // The loading cursor (step lk of tile lt) runs DEPTH own steps in front of
-    // the converting one.  A thread copies and reads its own row only.
-    int lt = cta, lk = wg;
-    const uint32_t *lq = nullptr;
-    const float *ls = nullptr;
-    const int32_t *lz = nullptr;
-    auto settle = [&]() {   // the cursor moved: carry into the next tile
-      while (lk >= nst && lt < tiles) lk -= nst, lt += ctas, lq = nullptr;
-      if (!lq && lt < tiles) {
-        const int64_t at = (int64_t)(lt % a.nM) * PM + lrow;
-        const int64_t row = at < a.p.r ? at : a.p.r - 1;   // past the last: its codes again, dropped
-        lq = a.p.qweight + row * wpr;
-        ls = a.p.scales + row * a.p.G;
-        lz = a.p.zeros + row * a.p.G;
-      }
-    };
-    settle();
-    auto load = [&](int slot) {
-      if (lt < tiles) {
-        const int ks = ks0 + lk;
-        const bool second = ks * PK + 32 < a.p.d;       // the step's second 32 columns exist
-        const uint32_t dst = ring + slot * S::BYTES;
-        const uint32_t *src = lq + (int64_t)ks * S::WORDS;
-        bool done = false;
-        if constexpr (BITS != 3) {
-          if (a.aligned) {
-            done = true;
-#pragma unroll
-            for (int i = 0; i < S::WORDS; i += 4) {
-              const bool in = i < BITS || second;
-              cp_async16(dst + (i / 4 * PM + lrow) * 16, src + (in ? i : 0), in ? 16 : 0);
-            }
-          }
-        }
-        if (!done) {
-#pragma unroll
-          for (int i = 0; i < S::WORDS; ++i) {
-            const bool in = i < BITS || second;
-            const uint32_t at = BITS == 3 ? (i * PM + lrow) * 4 : (i / 4 * PM + lrow) * 16 + i % 4 * 4;
-            cp_async4(dst + at, src + (in ? i : 0), in ? 4 : 0);
-          }
-        }
-        const int g0 = group_of(a, ks * 2), g1 = second ? group_of(a, ks * 2 + 1) : g0;
-        const uint32_t sz = dst + PM * S::WORDS * 4 + lrow * 4;
-        cp_async4(sz, ls + g0, 4);
-        cp_async4(sz + PM * 8, lz + g0, 4);
-        if (g1 != g0) {
-          cp_async4(sz + PM * 4, ls + g1, 4);
-          cp_async4(sz + PM * 12, lz + g1, 4);
-        }
-        lk += WGS;
-        settle();
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-#pragma unroll
-    for (int i = 0; i < S::DEPTH; ++i) load(i);
-    int slot = 0, as = wg % ASTAGES, ck = wg, parity = 0;   // A stage of step q is q % ASTAGES
-    uint32_t aphase = 0;
+    const uint32_t ring = smem_u32(smem) + a.bstages * bstage_bytes;
+    const int block_bytes = C::bytes(a.subs);
+    // the parts of the block that this step's two 32-column chunks lie in
+    const int sub0 = 2 * wg * a.subs / 8, sub1 = (2 * wg + 1) * a.subs / 8;
+    int slot = 0, parity = 0;
+    uint32_t phase = 0, aphase = 0;
     bool ok = true;
     // (a warp that gave up still walks the tiles: the others wait for it at their barrier)
-    for (int t = cta; t < tiles; t += ctas, parity ^= 1, ck -= nst) {
+    for (int t = cta; t < tiles; t += ctas, parity ^= 1) {
       float inv = 1.f;
       if constexpr (HALF) {
         // the largest scale of each row over this CTA's columns: a warp takes
@@ -465,62 +487,71 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         asm volatile("bar.sync 1, %0;" ::"n"(128 * WGS) : "memory");
         inv = __uint_as_float((254u - sh.exponent[parity][lrow]) << 23);
       }
-      for (; ck < nst && ok; ck += WGS) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(S::DEPTH - 1) : "memory");
-        const uint32_t src = ring + slot * S::BYTES;
-        const uint32_t sz = src + PM * S::WORDS * 4 + lrow * 4;
-        uint32_t w[S::WORDS];
-#pragma unroll
-        for (int i = 0; i < S::WORDS; ++i) {
-          if constexpr (BITS == 3) {
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i]) : "r"(src + (i * PM + lrow) * 4));
-          } else if (i % 4 == 0) {
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                         : "r"(src + (i / 4 * PM + lrow) * 16));
-          }
-        }
-        const int ks = ks0 + ck;
-        const bool two = ks * PK + 32 < a.p.d && group_of(a, ks * 2 + 1) != group_of(a, ks * 2);
-        Group<BITS, T> g;
-        float s;
-        int z;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(sz));
-        asm volatile("ld.shared.s32 %0, [%1];" : "=r"(z) : "r"(sz + PM * 8));
-        g.set(s * inv, z);
-        uint32_t c[16];
-        chunk_weights<BITS, T>(w, g, c);
-        if (!mbar_wait_bounded(&sh.empty_a[as], aphase ^ 1)) {
+      for (int kb = kb0; kb < kb1 && ok; ++kb) {
+        if (!mbar_wait_bounded(&sh.full_c[slot], phase)) {
           if (lane == 0) many_timeout(a.status, sh);
           ok = false;
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        tc_fence_after();
-        const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + TM_A + as * (PK / 2);
-        tmem_st_x16(dst, c);
-        if (two) {
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(sz + PM * 4));
-          asm volatile("ld.shared.s32 %0, [%1];" : "=r"(z) : "r"(sz + PM * 12));
+        if (kb * BLK + wg < ks1) {
+          const uint32_t src = ring + slot * block_bytes + lrow * C::PITCH + wg * (PK * BITS / 8);
+          const uint32_t sz = ring + slot * block_bytes + C::CODES + lrow * 4;
+          uint32_t w[2 * BITS];
+          if constexpr (BITS == 3) {
+#pragma unroll
+            for (int i = 0; i < 6; i += 2)
+              asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                           : "=r"(w[i]), "=r"(w[i + 1]) : "r"(src + i * 4));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2 * BITS; i += 4)
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                           : "r"(src + i * 4));
+          }
+          float s;
+          int z;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(sz + sub0 * (PM * 4)));
+          asm volatile("ld.shared.s32 %0, [%1];" : "=r"(z) : "r"(sz + (a.subs + sub0) * (PM * 4)));
+          Group<BITS, T> g;
           g.set(s * inv, z);
-        }
-        chunk_weights<BITS, T>(w + BITS, g, c);
-        tmem_st_x16(dst + 16, c);
-        load(slot);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.full_a[as]);
-        if (++slot == S::DEPTH) slot = 0;
-        as += WGS % ASTAGES;
-        if (WGS % ASTAGES == 0 || as >= ASTAGES) {
-          as -= WGS % ASTAGES == 0 ? 0 : ASTAGES;
+          uint32_t c[16];
+          chunk_weights<BITS, T>(w, g, c);
+          if (!mbar_wait_bounded(&sh.empty_a[wg], aphase ^ 1)) {
+            if (lane == 0) many_timeout(a.status, sh);
+            ok = false;
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + TM_A + wg * (PK / 2);
+          tmem_st_x16(dst, c);
+          if (sub1 != sub0) {
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(sz + sub1 * (PM * 4)));
+            asm volatile("ld.shared.s32 %0, [%1];" : "=r"(z) : "r"(sz + (a.subs + sub1) * (PM * 4)));
+            g.set(s * inv, z);
+          }
+          chunk_weights<BITS, T>(w + BITS, g, c);
+          tmem_st_x16(dst + 16, c);
           aphase ^= 1;
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sh.full_a[wg]);
+            mbar_arrive(&sh.empty_c[slot]);
+          }
+        } else if (lane == 0) {
+          mbar_arrive(&sh.empty_c[slot]);
+        }
+        if (++slot == C::DEPTH) {
+          slot = 0;
+          phase ^= 1;
         }
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-  } else if (warp >= 4 + 4 * WGS) {
+  } else {
     // ---------------------------------------------------------------- results
     const int quarter = warp & 3;
     const int lrow = quarter * 32 + lane;
@@ -651,17 +682,21 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
   a.nM = (int)nM;
   a.nN = (int)nN;
   const int64_t tiles = nM * nN;
-  // k split over a cluster while SMs stay idle and a CTA keeps eight steps
+  // k split over a cluster while SMs stay idle and a CTA keeps two blocks
   int ck = 1;
-  while (ck < 8 && tiles * (ck + 1) <= sms && steps >= 8 * (ck + 1)) ++ck;
+  while (ck < 8 && tiles * (ck + 1) <= sms && steps >= 2 * BLK * (ck + 1)) ++ck;
   a.ctas_k = ck;
   const int stage = N * PK * 2;
-  const int nb = (int)((MANY_SMEM - CodeStage<BITS>::ALL) / stage);
-  static_assert((MANY_SMEM - CodeStage<BITS>::ALL) / (PN * PK * 2) >= 4, "too few stages of x");
+  using C = CodeBlock<BITS>;
+  a.subs = p.group < 0 || p.group % 256 == 0 ? 1 : p.group % 128 == 0 ? 2 : p.group % 64 == 0 ? 4 : 8;
+  const size_t codes = (size_t)C::DEPTH * C::bytes(a.subs);
+  const int nb = (int)((MANY_SMEM - codes) / stage);
+  static_assert((MANY_SMEM - (size_t)C::DEPTH * C::bytes(8)) / (PN * PK * 2) >= 4,
+                "too few stages of x");
   a.bstages = nb > MAXB ? MAXB : nb;
   // (the sums of a split k, N PM floats, take the place of at least four stages of x)
-  const size_t bytes = (size_t)a.bstages * stage + CodeStage<BITS>::ALL;
-  a.aligned = BITS != 3 && reinterpret_cast<uintptr_t>(p.qweight) % 16 == 0 &&
+  const size_t bytes = (size_t)a.bstages * stage + codes;
+  a.aligned = reinterpret_cast<uintptr_t>(p.qweight) % 16 == 0 &&
               ((int64_t)(p.d / 32) * BITS) % 4 == 0;
   a.gdiv = p.group > 0 ? (uint32_t)(((1ull << 31) + p.group / 32 - 1) / (p.group / 32)) : 0;
   a.status = device_status_word();
