@@ -35,18 +35,19 @@ namespace {
 
 constexpr int PM = 128;                 // rows of W per tile (UMMA M)
 constexpr int PN = 192;                 // most tokens per tile (UMMA N)
-constexpr int PK = 64;                  // features per step (one 128-byte row of x)
-constexpr int ASTAGES = 4;              // TMEM stages of A: 32 columns each
-constexpr int MAXB = 8;                 // shared-memory stages of x at most
+constexpr int PK = 64;                  // features per box of x (one 128-byte row)
+constexpr int SK = 2 * PK;              // features per step: two boxes, eight MMAs
+constexpr int ASTAGES = 2;              // TMEM stages of A: 64 columns each
+constexpr int MAXB = 6;                 // shared-memory stages of x at most
 constexpr uint32_t TM_A = 2 * PN;       // TMEM column of the first A stage
 constexpr int WGS = 4;                  // converter warpgroups
 constexpr int MANY_THREADS = 32 * (4 + 4 * WGS + 4);
 constexpr size_t MANY_SMEM = 224 * 1024;   // x and codes, after alignment
 
-constexpr int BLK = WGS;                // steps per block of codes
-constexpr int BCOLS = BLK * PK;         // its columns
+constexpr int BLK = 2;                  // steps per block of codes; a warpgroup takes half a step
+constexpr int BCOLS = BLK * SK;         // its columns
 constexpr int LOADERS = 64;
-static_assert(ASTAGES == BLK, "step j of a block uses A stage j");
+static_assert(ASTAGES == BLK && WGS == 2 * BLK, "step j of a block uses A stage j");
 
 // A block of codes in shared memory: rows padded by 16 bytes (the 8 rows that
 // a quarter-warp's 16-byte reads touch fall on different banks), then scales
@@ -268,11 +269,11 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
   uint8_t *smem =
       reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int N = a.N, bstage_bytes = N * PK * 2;
+  const int N = a.N, box_bytes = N * PK * 2, bstage_bytes = 2 * box_bytes;
   const int crank = blockIdx.x % a.ctas_k;
   const int ctas = gridDim.x / a.ctas_k, cta = blockIdx.x / a.ctas_k;
   const int tiles = a.nM * a.nN;
-  const int total = (a.p.d + PK - 1) / PK, blocks = (total + BLK - 1) / BLK;
+  const int total = (a.p.d + SK - 1) / SK, blocks = (total + BLK - 1) / BLK;
   const int kb0 = (int)((int64_t)blocks * crank / a.ctas_k);          // this CTA's blocks
   const int kb1 = (int)((int64_t)blocks * (crank + 1) / a.ctas_k);
   const int ks0 = kb0 * BLK, ks1 = min(kb1 * BLK, total);             // and steps
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       mbar_init(&sh.empty_b[s], 1);
     }
     for (int s = 0; s < ASTAGES; ++s) {
-      mbar_init(&sh.full_a[s], 4);
+      mbar_init(&sh.full_a[s], 8);
       mbar_init(&sh.empty_a[s], 1);
     }
     for (int c = 0; c < C::DEPTH; ++c) {
@@ -329,8 +330,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           mbar_arrive_expect_tx(&sh.full_b[stage], bstage_bytes);
           issued |= 1u << stage;
           issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-          // feature offset: a multiple of 64 16-bit values = 128 bytes
-          tma_load_2d(smem + (size_t)stage * bstage_bytes, &tmX, ks * PK, n0, &sh.full_b[stage]);
+          // feature offsets: multiples of 64 16-bit values = 128 bytes (past d: zeros)
+          uint8_t *dst = smem + (size_t)stage * bstage_bytes;
+          tma_load_2d(dst, &tmX, ks * SK, n0, &sh.full_b[stage]);
+          tma_load_2d(dst + box_bytes, &tmX, ks * SK + PK, n0, &sh.full_b[stage]);
           if (++stage == a.bstages) {
             stage = 0;
             phase ^= 1;
@@ -343,11 +346,41 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------------- the MMAs
     if (lane == 0) {
+      // One thread issues everything, so the loop is kept short: descriptors
+      // advance by constants (16-byte units) and a step is eight MMAs.
       const uint32_t fmt = HALF ? 0u : 1u;
       const uint32_t idesc = instr_desc(fmt, fmt, 0, 0, PM, N);
+      const uint64_t first = smem_desc(smem_u32(smem), 16, 1024, 2);
+      const uint32_t box = (uint32_t)box_bytes >> 4;
+      uint64_t bdesc = first;
       int bstage = 0;
-      uint32_t bphase = 0, aphases = 0, abuf = 0, cphase = 0;
+      uint32_t bphase = 0, aphase = 0, abuf = 0, cphase = 0;
       bool ok = true;
+      auto step = [&](uint32_t dt, int j, uint32_t acc) {
+        if (!mbar_wait_bounded(&sh.full_b[bstage], bphase) ||
+            !mbar_wait_bounded(&sh.full_a[j], (aphase >> j) & 1u)) {
+          many_timeout(a.status, sh);
+          ok = false;
+          return;
+        }
+        tc_fence_after();
+        const uint32_t ad = tmem + TM_A + j * (SK / 2);
+        umma_f16_ts(dt, ad, bdesc, idesc, acc);
+#pragma unroll
+        for (int kk = 1; kk < 4; ++kk) umma_f16_ts(dt, ad + kk * 8, bdesc + kk * 2, idesc, 1u);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_f16_ts(dt, ad + 32 + kk * 8, bdesc + box + kk * 2, idesc, 1u);
+        umma_commit(&sh.empty_b[bstage]);
+        umma_commit(&sh.empty_a[j]);
+        aphase ^= 1u << j;
+        bdesc += 2 * box;
+        if (++bstage == a.bstages) {
+          bstage = 0;
+          bphase ^= 1;
+          bdesc = first;
+        }
+      };
       for (int t = cta; t < tiles && ok; t += ctas) {
         if (!mbar_wait_bounded(&sh.acc_empty[abuf], cphase ^ 1)) {
           many_timeout(a.status, sh);
@@ -355,28 +388,9 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         }
         tc_fence_after();
         const uint32_t dt = tmem + abuf * PN;
-        for (int ks = ks0; ks < ks1; ++ks) {
-          const int as = (ks - ks0) % BLK;
-          if (!mbar_wait_bounded(&sh.full_b[bstage], bphase) ||
-              !mbar_wait_bounded(&sh.full_a[as], (aphases >> as) & 1u)) {
-            many_timeout(a.status, sh);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t b0 = smem_u32(smem + (size_t)bstage * bstage_bytes);
-          const uint32_t a0 = tmem + TM_A + as * (PK / 2);
-#pragma unroll
-          for (int kk = 0; kk < PK / 16; ++kk)
-            umma_f16_ts(dt, a0 + kk * 8, smem_desc(b0 + kk * 32, 16, 1024, 2), idesc,
-                        (ks > ks0 || kk > 0) ? 1u : 0u);
-          umma_commit(&sh.empty_b[bstage]);
-          umma_commit(&sh.empty_a[as]);
-          if (++bstage == a.bstages) {
-            bstage = 0;
-            bphase ^= 1;
-          }
-          aphases ^= 1u << as;
+        for (int ks = ks0; ks < ks1 && ok; ks += BLK) {
+          step(dt, 0, ks > ks0 ? 1u : 0u);
+          if (ok && ks + 1 < ks1) step(dt, 1, 1u);
         }
         if (!ok) break;
         umma_commit(&sh.acc_full[abuf]);
@@ -453,6 +467,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
   } else if (warp < 4 + 4 * WGS) {
     // ---------------------------------------------------------------- weights to TMEM
     const int wg = (warp - 4) >> 2, quarter = warp & 3;
+    const int as = wg / 2;                   // step of the block, A stage
     const int lrow = quarter * 32 + lane;
     const uint32_t ring = smem_u32(smem) + a.bstages * bstage_bytes;
     const int block_bytes = C::bytes(a.subs);
@@ -467,7 +482,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       if constexpr (HALF) {
         // the largest scale of each row over this CTA's columns: a warp takes
         // PM / (4 WGS) rows, lanes along the groups
-        const int ga = group_of(a, ks0 * 2), gb = group_of(a, min(ks1 * 2, a.p.d / 32) - 1);
+        const int ga = group_of(a, ks0 * (SK / 32)), gb = group_of(a, min(ks1 * (SK / 32), a.p.d / 32) - 1);
         constexpr int EACH = PM / (4 * WGS);
         uint32_t top[EACH];
 #pragma unroll
@@ -494,7 +509,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (kb * BLK + wg < ks1) {
+        if (kb * BLK + as < ks1) {
           const uint32_t src = ring + slot * block_bytes + lrow * C::PITCH + wg * (PK * BITS / 8);
           const uint32_t sz = ring + slot * block_bytes + C::CODES + lrow * 4;
           uint32_t w[2 * BITS];
@@ -518,7 +533,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           g.set(s * inv, z);
           uint32_t c[16];
           chunk_weights<BITS, T>(w, g, c);
-          if (!mbar_wait_bounded(&sh.empty_a[wg], aphase ^ 1)) {
+          if (!mbar_wait_bounded(&sh.empty_a[as], aphase ^ 1)) {
             if (lane == 0) many_timeout(a.status, sh);
             ok = false;
           }
@@ -539,7 +554,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&sh.full_a[wg]);
+            mbar_arrive(&sh.full_a[as]);
             mbar_arrive(&sh.empty_c[slot]);
           }
         } else if (lane == 0) {
@@ -563,7 +578,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       float f = 1.f;
       if constexpr (HALF) {
         const float *srow = a.p.scales + (row < a.p.r ? row : a.p.r - 1) * a.p.G;
-        const int ga = group_of(a, ks0 * 2), gb = group_of(a, min(ks1 * 2, a.p.d / 32) - 1);
+        const int ga = group_of(a, ks0 * (SK / 32)), gb = group_of(a, min(ks1 * (SK / 32), a.p.d / 32) - 1);
         uint32_t top = 0;
 #pragma unroll 4
         for (int g = ga; g <= gb; ++g) top = max(top, __float_as_uint(__ldg(srow + g)) & 0x7FFFFFFFu);
@@ -663,7 +678,7 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
   a.p = p;
   const int sms = num_sms();
   const int64_t nM = (p.r + PM - 1) / PM;
-  const int steps = (p.d + PK - 1) / PK;
+  const int steps = (p.d + SK - 1) / SK;
   // Tokens per tile: all of them when they fit; else the width that wastes
   // least, a round of tiles over the SMs costing N tokens of MMAs (or the
   // conversion of the weights, about as long as 104 tokens').
@@ -686,15 +701,15 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
   int ck = 1;
   while (ck < 8 && tiles * (ck + 1) <= sms && steps >= 2 * BLK * (ck + 1)) ++ck;
   a.ctas_k = ck;
-  const int stage = N * PK * 2;
+  const int stage = N * SK * 2;
   using C = CodeBlock<BITS>;
   a.subs = p.group < 0 || p.group % 256 == 0 ? 1 : p.group % 128 == 0 ? 2 : p.group % 64 == 0 ? 4 : 8;
   const size_t codes = (size_t)C::DEPTH * C::bytes(a.subs);
   const int nb = (int)((MANY_SMEM - codes) / stage);
-  static_assert((MANY_SMEM - (size_t)C::DEPTH * C::bytes(8)) / (PN * PK * 2) >= 4,
+  static_assert((MANY_SMEM - (size_t)C::DEPTH * C::bytes(8)) / (PN * SK * 2) >= 2,
                 "too few stages of x");
   a.bstages = nb > MAXB ? MAXB : nb;
-  // (the sums of a split k, N PM floats, take the place of at least four stages of x)
+  // (the sums of a split k, N PM floats, take the place of two stages of x)
   const size_t bytes = (size_t)a.bstages * stage + codes;
   a.aligned = reinterpret_cast<uintptr_t>(p.qweight) % 16 == 0 &&
               ((int64_t)(p.d / 32) * BITS) % 4 == 0;
