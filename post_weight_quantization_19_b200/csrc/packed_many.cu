@@ -531,8 +531,14 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           asm volatile("ld.shared.s32 %0, [%1];" : "=r"(z) : "r"(sz + (a.subs + sub0) * (PM * 4)));
           Group<BITS, T> g;
           g.set(s * inv, z);
-          uint32_t c[16];
-          chunk_weights<BITS, T>(w, g, c);
+          uint32_t c0[16], c1[16];
+          chunk_weights<BITS, T>(w, g, c0);
+          if (sub1 != sub0) {
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(sz + sub1 * (PM * 4)));
+            asm volatile("ld.shared.s32 %0, [%1];" : "=r"(z) : "r"(sz + (a.subs + sub1) * (PM * 4)));
+            g.set(s * inv, z);
+          }
+          chunk_weights<BITS, T>(w + BITS, g, c1);
           if (!mbar_wait_bounded(&sh.empty_a[as], aphase ^ 1)) {
             if (lane == 0) many_timeout(a.status, sh);
             ok = false;
@@ -541,14 +547,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + TM_A + wg * (PK / 2);
-          tmem_st_x16(dst, c);
-          if (sub1 != sub0) {
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(sz + sub1 * (PM * 4)));
-            asm volatile("ld.shared.s32 %0, [%1];" : "=r"(z) : "r"(sz + (a.subs + sub1) * (PM * 4)));
-            g.set(s * inv, z);
-          }
-          chunk_weights<BITS, T>(w + BITS, g, c);
-          tmem_st_x16(dst + 16, c);
+          tmem_st_x16(dst, c0);
+          tmem_st_x16(dst + 16, c1);
           aphase ^= 1;
           tmem_wait_st();
           tc_fence_before();
