@@ -5,10 +5,11 @@
 // (g_idx).  With perm the stable order of the columns by g_idx, column j of
 // the result is column perm[j], and position j belongs to group j / group.
 //
-// Two kernels.  The order: one warp per group reads g_idx 128 entries at a time
-// and places the columns of its group by ballot, in order; a slot that stays
-// empty (a group with too few columns) is marked -1, so perm holds a -1 if and
-// only if some group has another number of columns than `group`.
+// Two kernels.  The order, one CTA: each of its 32 warps takes a run of columns
+// and counts its groups (match_any gives a column's rank among the 32 that a
+// warp reads at once), the counts are summed over the warps, and a second pass
+// places the columns.  A group with another number of columns than `group` makes
+// perm[0] = -1, which the host reads, and the rest of perm the identity.
 //
 // The rows, r*d*bits/8 bytes in and out: a CTA takes eight rows (four of 8-bit
 // codes) and transposes them so that one shared-memory word holds a column's
@@ -24,58 +25,74 @@
 namespace gptq {
 namespace {
 
-constexpr int ORDER_WARPS = 8;
+constexpr int ORDER_WARPS = 32;
 constexpr int ROW_THREADS = 256;
 
 __global__ void __launch_bounds__(32 * ORDER_WARPS)
     group_order_kernel(const int32_t *__restrict__ g_idx, int d, int group, int G,
                        int32_t *__restrict__ perm) {
-  extern __shared__ __align__(16) uint16_t groups[];   // g_idx, 0xFFFF for entries outside [0, G)
-  for (int c = threadIdx.x; c < d; c += 32 * ORDER_WARPS) {
-    const int v = __ldg(g_idx + c);
-    groups[c] = v >= 0 && v < G ? (uint16_t)v : (uint16_t)0xFFFFu;   // G <= 2048
+  extern __shared__ __align__(16) uint16_t counts[];   // [ORDER_WARPS][G]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint16_t *mine = counts + warp * G;
+  const int chunks = d / 32;                            // d % 32 == 0
+  const int c0 = chunks * warp / ORDER_WARPS, c1 = chunks * (warp + 1) / ORDER_WARPS;
+  for (int i = threadIdx.x; i < ORDER_WARPS * G; i += 32 * ORDER_WARPS) counts[i] = 0;
+  __syncthreads();
+  int bad = 0;
+#pragma unroll 4
+  for (int c = c0; c < c1; ++c) {
+    const int g = __ldg(g_idx + c * 32 + lane);
+    const uint32_t same = __match_any_sync(0xffffffffu, g);
+    if (g < 0 || g >= G)
+      bad = 1;
+    else if ((same & ((1u << lane) - 1u)) == 0)         // the first of its group
+      mine[g] += (uint16_t)__popc(same);
+    __syncwarp();
   }
   __syncthreads();
-  const int g = blockIdx.x * ORDER_WARPS + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (g >= G) return;
-  int32_t *slots = perm + (int64_t)g * group;
-  int found = 0;
-#pragma unroll 2
-  for (int c0 = 0; c0 < d; c0 += 128) {   // d % 32 == 0
-    int v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = c0 + 32 * k < d ? groups[c0 + 32 * k + lane] : 0xFFFF;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const bool mine = v[k] == g;
-      const uint32_t hit = __ballot_sync(0xffffffffu, mine);
-      const int at = found + __popc(hit & ((1u << lane) - 1u));
-      if (mine && at < group) slots[at] = c0 + 32 * k + lane;
-      found += __popc(hit);
+  for (int g = threadIdx.x; g < G; g += 32 * ORDER_WARPS) {
+    int sum = 0;
+#pragma unroll 8
+    for (int w = 0; w < ORDER_WARPS; ++w) {
+      const int v = counts[w * G + g];
+      counts[w * G + g] = (uint16_t)sum;                // of the warps before
+      sum += v;
     }
+    bad |= sum != group;
   }
-  for (int at = found + lane; at < group; at += 32) slots[at] = -1;
-}
-
-// perm[0] < 0 if any entry is: what the host reads.
-__device__ void report_order(int32_t *perm, int d) {
-  int bad = 0;
-  for (int j = threadIdx.x; j < d; j += blockDim.x) bad |= perm[j] < 0;
-  if (__syncthreads_or(bad) && threadIdx.x == 0) perm[0] = -1;
+  if (__syncthreads_or(bad)) {
+    for (int j = threadIdx.x; j < d; j += 32 * ORDER_WARPS) perm[j] = j == 0 ? -1 : j;
+    return;
+  }
+#pragma unroll 4
+  for (int c = c0; c < c1; ++c) {
+    const int g = __ldg(g_idx + c * 32 + lane);
+    const uint32_t same = __match_any_sync(0xffffffffu, g);
+    const int before = __popc(same & ((1u << lane) - 1u));
+    const int base = mine[g];
+    __syncwarp();
+    if (before == 0) mine[g] = (uint16_t)(base + __popc(same));
+    __syncwarp();
+    perm[g * group + base + before] = c * 32 + lane;
+  }
 }
 
 // ---- eight codes of a row as the nibbles of a word, low first
 
-__device__ __forceinline__ uint32_t nibbles_of_3(uint32_t v) {   // 24 bits
-  v = (v & 0x00000FFFu) | ((v << 4) & 0x0FFF0000u);
-  v = (v & 0x003F003Fu) | ((v << 2) & 0x3F003F00u);
-  return (v & 0x07070707u) | ((v << 1) & 0x70707070u);
+// (v where the mask is set, w elsewhere: one instruction)
+__device__ __forceinline__ uint32_t choose(uint32_t mask, uint32_t v, uint32_t w) {
+  return (v & mask) | (w & ~mask);
+}
+__device__ __forceinline__ uint32_t nibbles_of_3(uint32_t v) {   // 24 bits; above them anything
+  v = choose(0x0000FFFFu, v, v << 4);   // 12 bits in each half, 6 in each byte, 3 in each nibble,
+  v = choose(0x00FF00FFu, v, v << 2);   // with others' bits between them until the end
+  v = choose(0x0F0F0F0Fu, v, v << 1);
+  return v & 0x77777777u;
 }
 __device__ __forceinline__ uint32_t threes_of_nibbles(uint32_t v) {
-  v = (v & 0x07070707u) | ((v >> 1) & 0x38383838u);
-  v = (v & 0x003F003Fu) | ((v >> 2) & 0x0FC00FC0u);
-  return (v & 0x00000FFFu) | ((v >> 4) & 0x00FFF000u);
+  v -= (v & 0x70707070u) >> 1;          // lo + 16 hi -> lo + 8 hi, and so on
+  v -= (v & 0x3F003F00u) / 4 * 3;
+  return v - (v & 0x0FFF0000u) / 16 * 15;
 }
 __device__ __forceinline__ uint32_t nibbles_of_2(uint32_t v) {   // 16 bits
   v = (v | (v << 8)) & 0x00FF00FFu;
@@ -100,9 +117,9 @@ struct Unit {
     if constexpr (BITS == 8 || BITS == 4) o[0] = w[0];
     if constexpr (BITS == 2) o[0] = nibbles_of_2(w[0] & 0xFFFFu), o[1] = nibbles_of_2(w[0] >> 16);
     if constexpr (BITS == 3) {
-      o[0] = nibbles_of_3(w[0] & 0xFFFFFFu);
-      o[1] = nibbles_of_3(__funnelshift_r(w[0], w[1], 24) & 0xFFFFFFu);
-      o[2] = nibbles_of_3(__funnelshift_r(w[1], w[2], 16) & 0xFFFFFFu);
+      o[0] = nibbles_of_3(w[0]);
+      o[1] = nibbles_of_3(__funnelshift_r(w[0], w[1], 24));
+      o[2] = nibbles_of_3(__funnelshift_r(w[1], w[2], 16));
       o[3] = nibbles_of_3(w[2] >> 8);
     }
   }
@@ -151,89 +168,91 @@ __device__ __forceinline__ int place(int c) { return c ^ ((c >> 5 & 7) << 2); }
 // from global memory once in whole lines.
 template <int BITS, bool STAGED>
 __global__ void __launch_bounds__(ROW_THREADS)
-    regroup_rows_kernel(const uint32_t *__restrict__ qweight, int32_t *perm, int64_t r, int d,
+    regroup_rows_kernel(const uint32_t *__restrict__ qweight, const int32_t *__restrict__ perm,
+                        int64_t r, int d,
                         uint32_t *__restrict__ out) {
   using U = Unit<BITS>;
   extern __shared__ __align__(16) uint32_t columns[];   // [d]: a column's codes of the CTA's rows
-  if (blockIdx.x == gridDim.x - 1) {
-    report_order(perm, d);
-    return;
-  }
-  const int64_t wpr = (int64_t)(d / 32) * BITS;
+  const int pitch = d / 32 * BITS;   // words per row
   const int units = d / U::COLS;
-  const int64_t row0 = (int64_t)blockIdx.x * U::ROWS;
-  const int rows = (int)min((int64_t)U::ROWS, r - row0);
   uint16_t *order = reinterpret_cast<uint16_t *>(columns + d);
   if constexpr (STAGED) {
-    for (int j = threadIdx.x; j < d; j += ROW_THREADS) {
-      const int from = *(volatile const int32_t *)(perm + j);
-      order[j] = (uint16_t)place(from < 0 ? 0 : from);
-    }
+#pragma unroll 4
+    for (int j = threadIdx.x; j < d; j += ROW_THREADS)
+      order[j] = (uint16_t)place(max(__ldg(perm + j), 0));
   }
-  for (int u = threadIdx.x; u < units; u += ROW_THREADS) {
-    uint32_t n[U::ROWS][U::OUT];
-#pragma unroll
-    for (int i = 0; i < U::ROWS; ++i) {
-      uint32_t w[U::IN];
-#pragma unroll
-      for (int k = 0; k < U::IN; ++k)
-        w[k] = i < rows ? __ldg(qweight + (row0 + i) * wpr + (int64_t)u * U::IN + k) : 0u;
-      U::widen(w, n[i]);
-    }
-#pragma unroll
-    for (int k = 0; k < U::OUT; ++k) {
-      uint32_t a[U::ROWS];
-#pragma unroll
-      for (int i = 0; i < U::ROWS; ++i) a[i] = n[i][k];
-      transpose<U::ROWS>(a);
-#pragma unroll
-      for (int i = 0; i < U::ROWS; i += 4)
-        *reinterpret_cast<uint4 *>(columns + place(u * U::COLS + k * U::ROWS + i)) =
-            make_uint4(a[i], a[i + 1], a[i + 2], a[i + 3]);
-    }
-  }
-  __syncthreads();
-  for (int u = threadIdx.x; u < units; u += ROW_THREADS) {
-    uint32_t n[U::ROWS][U::OUT];
-#pragma unroll
-    for (int k = 0; k < U::OUT; ++k) {
-      uint32_t a[U::ROWS];
+  const int64_t groups = (r + U::ROWS - 1) / U::ROWS;
+  for (int64_t block = blockIdx.x; block < groups; block += gridDim.x) {
+    const int rows = (int)min((int64_t)U::ROWS, r - block * U::ROWS);
+    const uint32_t *src = qweight + block * U::ROWS * pitch;
+    uint32_t *dst = out + block * U::ROWS * pitch;
+    for (int u = threadIdx.x; u < units; u += ROW_THREADS) {
+      uint32_t n[U::ROWS][U::OUT];
 #pragma unroll
       for (int i = 0; i < U::ROWS; ++i) {
-        const int j = u * U::COLS + k * U::ROWS + i;
-        if constexpr (STAGED) {
-          a[i] = columns[order[j]];
-        } else {
-          const int from = *(volatile const int32_t *)(perm + j);
-          a[i] = columns[place(from < 0 ? 0 : from)];
-        }
+        uint32_t w[U::IN];
+#pragma unroll
+        for (int k = 0; k < U::IN; ++k)
+          w[k] = i < rows ? __ldg(src + i * pitch + u * U::IN + k) : 0u;
+        U::widen(w, n[i]);
       }
-      transpose<U::ROWS>(a);
 #pragma unroll
-      for (int i = 0; i < U::ROWS; ++i) n[i][k] = a[i];
+      for (int k = 0; k < U::OUT; ++k) {
+        uint32_t a[U::ROWS];
+#pragma unroll
+        for (int i = 0; i < U::ROWS; ++i) a[i] = n[i][k];
+        transpose<U::ROWS>(a);
+#pragma unroll
+        for (int i = 0; i < U::ROWS; i += 4)
+          *reinterpret_cast<uint4 *>(columns + place(u * U::COLS + k * U::ROWS + i)) =
+              make_uint4(a[i], a[i + 1], a[i + 2], a[i + 3]);
+      }
     }
+    __syncthreads();
+    for (int u = threadIdx.x; u < units; u += ROW_THREADS) {
+      uint32_t n[U::ROWS][U::OUT];
 #pragma unroll
-    for (int i = 0; i < U::ROWS; ++i) {
-      uint32_t w[U::IN];
-      U::narrow(n[i], w);
-      if (i < rows)
+      for (int k = 0; k < U::OUT; ++k) {
+        uint32_t a[U::ROWS];
+        const int j = u * U::COLS + k * U::ROWS;
+        if constexpr (STAGED) {
 #pragma unroll
-        for (int k = 0; k < U::IN; ++k) out[(row0 + i) * wpr + (int64_t)u * U::IN + k] = w[k];
+          for (int i = 0; i < U::ROWS; i += 4) {
+            const uint2 o = *reinterpret_cast<const uint2 *>(order + j + i);
+            a[i] = columns[o.x & 0xFFFFu];
+            a[i + 1] = columns[o.x >> 16];
+            a[i + 2] = columns[o.y & 0xFFFFu];
+            a[i + 3] = columns[o.y >> 16];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < U::ROWS; ++i) a[i] = columns[place(max(__ldg(perm + j + i), 0))];
+        }
+        transpose<U::ROWS>(a);
+#pragma unroll
+        for (int i = 0; i < U::ROWS; ++i) n[i][k] = a[i];
+      }
+#pragma unroll
+      for (int i = 0; i < U::ROWS; ++i) {
+        uint32_t w[U::IN];
+        U::narrow(n[i], w);
+        if (i < rows)
+#pragma unroll
+          for (int k = 0; k < U::IN; ++k) dst[i * pitch + u * U::IN + k] = w[k];
+      }
     }
+    __syncthreads();   // columns is free for the next rows
   }
 }
 
 template <int BITS>
 __global__ void __launch_bounds__(ROW_THREADS)
-    regroup_kernel(const uint32_t *__restrict__ qweight, int32_t *perm, int64_t r, int d,
+    regroup_kernel(const uint32_t *__restrict__ qweight, const int32_t *__restrict__ perm,
+                   int64_t r, int d,
                    uint32_t *__restrict__ out) {
   extern __shared__ __align__(16) uint8_t row_codes[];   // [d]
   const int nchunk = d / 32;
-  if (blockIdx.x == gridDim.x - 1) {
-    report_order(perm, d);
-    return;
-  }
-  for (int64_t row = blockIdx.x; row < r; row += gridDim.x - 1) {
+  for (int64_t row = blockIdx.x; row < r; row += gridDim.x) {
     const uint32_t *src = qweight + row * nchunk * BITS;
     uint32_t *dst = out + row * nchunk * BITS;
     __syncthreads();   // the previous row's gathers are done
@@ -255,7 +274,7 @@ __global__ void __launch_bounds__(ROW_THREADS)
       uint32_t c[32], w[BITS];
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
-        const int from = *(volatile const int32_t *)(perm + k * 32 + j);
+        const int from = __ldg(perm + k * 32 + j);
         c[j] = row_codes[from < 0 ? 0 : from];
       }
       pack32<BITS>(c, w);
@@ -272,9 +291,13 @@ template <int BITS, bool STAGED>
 int launch_rows(const uint32_t *q, int32_t *perm, int64_t r, int d, uint32_t *out, cudaStream_t st) {
   static std::atomic<bool> attr[64] = {};
   if (const int rc = ensure_smem_attr(regroup_rows_kernel<BITS, STAGED>, 192 * 1024, attr)) return rc;
-  const int64_t ctas = (r + Unit<BITS>::ROWS - 1) / Unit<BITS>::ROWS;
+  // as many CTAs as fit at once, each keeping the order for all its rows
+  const size_t smem = (size_t)d * (STAGED ? 6 : 4);
+  int per_sm = (int)((200u << 10) / (smem + 1024));
+  per_sm = per_sm < 1 ? 1 : (per_sm > 8 ? 8 : per_sm);
+  const int64_t most = (r + Unit<BITS>::ROWS - 1) / Unit<BITS>::ROWS, fit = (int64_t)num_sms() * per_sm;
   regroup_rows_kernel<BITS, STAGED>
-      <<<(unsigned)ctas + 1, ROW_THREADS, (size_t)d * (STAGED ? 6 : 4), st>>>(q, perm, r, d, out);
+      <<<(unsigned)(most < fit ? most : fit), ROW_THREADS, smem, st>>>(q, perm, r, d, out);
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
@@ -282,12 +305,12 @@ int launch_rows(const uint32_t *q, int32_t *perm, int64_t r, int d, uint32_t *ou
 template <int BITS>
 int launch_regroup(const uint32_t *q, int32_t *perm, int64_t r, int d, uint32_t *out,
                    cudaStream_t st) {
-  // one more CTA than the rows need: it reports the order
+  if (r == 0) return GPTQ_OK;
   if (d > LONGEST) {
     static std::atomic<bool> attr[64] = {};
     if (const int rc = ensure_smem_attr(regroup_kernel<BITS>, 65536, attr)) return rc;
     const int64_t cap = (int64_t)num_sms() * 8;
-    regroup_kernel<BITS><<<(unsigned)(r < cap ? r : cap) + 1, ROW_THREADS, (size_t)d, st>>>(
+    regroup_kernel<BITS><<<(unsigned)(r < cap ? r : cap), ROW_THREADS, (size_t)d, st>>>(
         q, perm, r, d, out);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
@@ -315,9 +338,9 @@ extern "C" int gptq_regroup(const int32_t *qweight, const int32_t *g_idx, int64_
   cudaStream_t st = (cudaStream_t)stream;
   const int G = (int)(d / group);
   static std::atomic<bool> attr[64] = {};
-  if (const int arc = ensure_smem_attr(group_order_kernel, 2 * 65536, attr)) return arc;
-  group_order_kernel<<<(G + ORDER_WARPS - 1) / ORDER_WARPS, 32 * ORDER_WARPS, (size_t)d * 2, st>>>(
-      g_idx, (int)d, group, G, perm);
+  if (const int arc = ensure_smem_attr(group_order_kernel, ORDER_WARPS * 2048 * 2, attr)) return arc;
+  group_order_kernel<<<1, 32 * ORDER_WARPS, (size_t)ORDER_WARPS * G * 2, st>>>(g_idx, (int)d, group, G,
+                                                                             perm);
   GPTQ_LAUNCH_CHECK();
   const uint32_t *q = reinterpret_cast<const uint32_t *>(qweight);
   uint32_t *o = reinterpret_cast<uint32_t *>(out);
