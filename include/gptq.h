@@ -375,7 +375,7 @@ int gptq_packed_linear(const void *x, int xtype, const float *x_scales, int64_t 
  *   r >= 0; d, bits as gptq_dequant_gemv; group a multiple of 32 that divides d.
  *   Synchronises `stream` once, at the end: a g_idx with another number of
  *   columns in some group returns GPTQ_ERR_INVALID_ARG (outputs unspecified).
- *   It cannot be captured into a graph.
+ *   On a stream that is being captured: GPTQ_ERR_INVALID_ARG.
  */
 int gptq_regroup(const int32_t *qweight, const int32_t *g_idx, int64_t r, int64_t d, int bits,
                  int group, int32_t *out, int32_t *perm, gptq_stream_t stream);

@@ -8,8 +8,8 @@
 // Two kernels.  The order, one CTA: each of its 32 warps takes a run of columns
 // and counts its groups (match_any gives a column's rank among the 32 that a
 // warp reads at once), the counts are summed over the warps, and a second pass
-// places the columns.  A group with another number of columns than `group` makes
-// perm[0] = -1, which the host reads, and the rest of perm the identity.
+// places the columns.  A group with another number of columns than `group` is
+// reported in a word of mapped host memory, and perm becomes the identity.
 //
 // The rows, r*d*bits/8 bytes in and out: a CTA takes eight rows (four of 8-bit
 // codes) and transposes them so that one shared-memory word holds a column's
@@ -18,6 +18,9 @@
 // one by one took 490 us where this takes about 10 (8192 x 8192, 3 bits).
 // Codes of 2 and 3 bits travel as nibbles.  Rows too long for that (d > 49152)
 // go through bytes in shared memory, one row at a time.
+#include <mutex>
+#include <vector>
+
 #include "gptq_internal.h"
 #include "pack_bits.cuh"
 #include "unpack_bits.cuh"
@@ -30,7 +33,7 @@ constexpr int ROW_THREADS = 256;
 
 __global__ void __launch_bounds__(32 * ORDER_WARPS)
     group_order_kernel(const int32_t *__restrict__ g_idx, int d, int group, int G,
-                       int32_t *__restrict__ perm) {
+                       int32_t *__restrict__ perm, volatile int *report) {
   extern __shared__ __align__(16) uint16_t counts[];   // [ORDER_WARPS][G]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint16_t *mine = counts + warp * G;
@@ -61,7 +64,8 @@ __global__ void __launch_bounds__(32 * ORDER_WARPS)
     bad |= sum != group;
   }
   if (__syncthreads_or(bad)) {
-    for (int j = threadIdx.x; j < d; j += 32 * ORDER_WARPS) perm[j] = j == 0 ? -1 : j;
+    for (int j = threadIdx.x; j < d; j += 32 * ORDER_WARPS) perm[j] = j;
+    if (threadIdx.x == 0) *report = 1;
     return;
   }
 #pragma unroll 4
@@ -177,9 +181,9 @@ __global__ void __launch_bounds__(ROW_THREADS)
   const int units = d / U::COLS;
   uint16_t *order = reinterpret_cast<uint16_t *>(columns + d);
   if constexpr (STAGED) {
-#pragma unroll 4
+#pragma unroll 16
     for (int j = threadIdx.x; j < d; j += ROW_THREADS)
-      order[j] = (uint16_t)place(max(__ldg(perm + j), 0));
+      order[j] = (uint16_t)place(__ldg(perm + j));
   }
   const int64_t groups = (r + U::ROWS - 1) / U::ROWS;
   for (int64_t block = blockIdx.x; block < groups; block += gridDim.x) {
@@ -226,7 +230,7 @@ __global__ void __launch_bounds__(ROW_THREADS)
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < U::ROWS; ++i) a[i] = columns[place(max(__ldg(perm + j + i), 0))];
+          for (int i = 0; i < U::ROWS; ++i) a[i] = columns[place(__ldg(perm + j + i))];
         }
         transpose<U::ROWS>(a);
 #pragma unroll
@@ -274,8 +278,7 @@ __global__ void __launch_bounds__(ROW_THREADS)
       uint32_t c[32], w[BITS];
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
-        const int from = __ldg(perm + k * 32 + j);
-        c[j] = row_codes[from < 0 ? 0 : from];
+        c[j] = row_codes[__ldg(perm + k * 32 + j)];
       }
       pack32<BITS>(c, w);
 #pragma unroll
@@ -319,6 +322,48 @@ int launch_regroup(const uint32_t *q, int32_t *perm, int64_t r, int d, uint32_t 
                              : launch_rows<BITS, false>(q, perm, r, d, out, st);
 }
 
+// Words of mapped host memory that calls report in: one per call in flight,
+// kept for later calls.  (A copy of one word to the host's stack cost more than
+// the kernels.)
+std::mutex g_words_mutex;
+std::vector<int *> g_words;
+
+int take_word(int **word) {
+  {
+    std::lock_guard<std::mutex> lock(g_words_mutex);
+    if (!g_words.empty()) {
+      *word = g_words.back();
+      g_words.pop_back();
+      return GPTQ_OK;
+    }
+  }
+  void *p = nullptr;
+  GPTQ_CUDA_TRY(cudaHostAlloc(&p, 64, cudaHostAllocMapped | cudaHostAllocPortable));
+  *word = static_cast<int *>(p);
+  return GPTQ_OK;
+}
+
+void give_word(int *word) {
+  std::lock_guard<std::mutex> lock(g_words_mutex);
+  g_words.push_back(word);
+}
+
+int enqueue_regroup(const uint32_t *q, const int32_t *g_idx, int64_t r, int d, int bits, int group,
+                    uint32_t *out, int32_t *perm, int *report, cudaStream_t st) {
+  const int G = d / group;
+  static std::atomic<bool> attr[64] = {};
+  if (const int rc = ensure_smem_attr(group_order_kernel, ORDER_WARPS * 2048 * 2, attr)) return rc;
+  group_order_kernel<<<1, 32 * ORDER_WARPS, (size_t)ORDER_WARPS * G * 2, st>>>(g_idx, d, group, G,
+                                                                             perm, report);
+  GPTQ_LAUNCH_CHECK();
+  switch (bits) {
+    case 2: return launch_regroup<2>(q, perm, r, d, out, st);
+    case 3: return launch_regroup<3>(q, perm, r, d, out, st);
+    case 4: return launch_regroup<4>(q, perm, r, d, out, st);
+    default: return launch_regroup<8>(q, perm, r, d, out, st);
+  }
+}
+
 }  // namespace
 }  // namespace gptq
 
@@ -336,24 +381,20 @@ extern "C" int gptq_regroup(const int32_t *qweight, const int32_t *g_idx, int64_
       reinterpret_cast<uintptr_t>(out) % 4 || reinterpret_cast<uintptr_t>(perm) % 4)
     return GPTQ_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
-  const int G = (int)(d / group);
-  static std::atomic<bool> attr[64] = {};
-  if (const int arc = ensure_smem_attr(group_order_kernel, ORDER_WARPS * 2048 * 2, attr)) return arc;
-  group_order_kernel<<<1, 32 * ORDER_WARPS, (size_t)ORDER_WARPS * G * 2, st>>>(g_idx, (int)d, group, G,
-                                                                             perm);
-  GPTQ_LAUNCH_CHECK();
-  const uint32_t *q = reinterpret_cast<const uint32_t *>(qweight);
-  uint32_t *o = reinterpret_cast<uint32_t *>(out);
-  int rc;
-  switch (bits) {
-    case 2: rc = launch_regroup<2>(q, perm, r, (int)d, o, st); break;
-    case 3: rc = launch_regroup<3>(q, perm, r, (int)d, o, st); break;
-    case 4: rc = launch_regroup<4>(q, perm, r, (int)d, o, st); break;
-    default: rc = launch_regroup<8>(q, perm, r, (int)d, o, st); break;
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  GPTQ_CUDA_TRY(cudaStreamIsCapturing(st, &capture));
+  if (capture != cudaStreamCaptureStatusNone) return GPTQ_ERR_INVALID_ARG;   // it waits for its result
+  int *word = nullptr;
+  if (const int rc = take_word(&word)) return rc;
+  *word = 0;
+  int rc = enqueue_regroup(reinterpret_cast<const uint32_t *>(qweight), g_idx, r, (int)d, bits, group,
+                           reinterpret_cast<uint32_t *>(out), perm, word, st);
+  const cudaError_t e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) {   // the word may still be written: not given back
+    set_last_error(__FILE__, __LINE__, "cudaStreamSynchronize", e);
+    return GPTQ_ERR_CUDA;
   }
-  if (rc != GPTQ_OK) return rc;
-  int32_t first = 0;
-  GPTQ_CUDA_TRY(cudaMemcpyAsync(&first, perm, sizeof(first), cudaMemcpyDeviceToHost, st));
-  GPTQ_CUDA_TRY(cudaStreamSynchronize(st));
-  return first < 0 ? GPTQ_ERR_INVALID_ARG : GPTQ_OK;
+  if (rc == GPTQ_OK && *static_cast<volatile int *>(word) != 0) rc = GPTQ_ERR_INVALID_ARG;
+  give_word(word);
+  return rc;
 }

@@ -422,6 +422,23 @@ def test_regroup_refuses_unequal_groups():
             g.gptq_regroup(*dev(q, g_idx), 4, 64)
 
 
+def test_regroup_refuses_a_capture():
+    import post_weight_quantization_19_b200 as g
+    q, _, _ = layer(4, 256, 4, 64, seed=1)
+    q, g_idx = dev(q, (np.arange(256) // 64).astype(np.int32))
+    g.gptq_regroup(q, g_idx, 4, 64)
+    x = torch.zeros(8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, perm = torch.empty_like(q), torch.empty_like(g_idx)
+        with pytest.raises(g.GPTQError):
+            g.gptq_regroup(q, g_idx, 4, 64, out=out, perm=perm)
+        x += 1
+    graph.replay()
+    torch.cuda.synchronize()
+    assert bool((x == 1).all())
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("n", [1, 20, 150])
