@@ -1,0 +1,647 @@
+// gptq_packed_linear for few tokens: y = x W^^T + bias, bound by reading the
+// packed weights once (r d bits/8 + 8 r G bytes) and by the instructions that
+// take the codes out of their words.
+//
+// A warp multiplies 32 rows of codes (two m16 tiles) with up to 8, 16 or 32
+// tokens on warp-level matrix instructions (mma.sync), whose operands come from
+// registers: a code goes from its packed word to an operand in about one
+// instruction, with nothing written back to shared or tensor memory on the way.
+// (mma.sync reaches a quarter of tcgen05's rate: 0.46 m16n8k16 per clock and SM
+// measured.  For 8 tokens the weights' bytes still take longer.)
+//
+// The order of k inside a matrix instruction is free as long as both operands
+// agree.  A thread takes eight codes of a row at a time (a unit): one 32-bit
+// word of 4-bit codes.  Where a group covers the 128 columns of a stage, thread
+// t of a row's four takes the units of the 32-column chunk t, which it reads at
+// once; smaller groups need all four threads inside one chunk, so thread t takes
+// unit t of every chunk (FINE).
+//
+// 16-bit x: the operand is B + q, whose bits are the code's bits and a constant:
+//   fp16: B = 0, the code as a subnormal number, q 2^-24 (exact, and so are its
+//         products in fp32); every second code stays one place higher, q 2^(bits -
+//         24), and is summed apart, which saves a shift;
+//   bf16: B = 16, 8 or 4 for 4-, 3- or 2-bit codes, the code in the upper
+//         mantissa bits.  (8-bit codes do not fit: q - z through fp32 instead.)
+// and one more product with a matrix of ones gives sum x, so that a group adds
+//   s (sum (B + q) x - (B + z) sum x).
+// The terms that cancel are at most (B + q + z) / |q - z| times what q - z itself
+// would sum, held in fp32.  8-bit x: q and x as integers, sums exact.
+//
+// Each warp runs its own ring of cp.async stages of 128 columns (weights, x,
+// scales, zeros) and meets the others only at the end: the k range is split
+// over the CTA's warps and over a cluster of CTAs, whose partial sums are added
+// through distributed shared memory in a fixed order.
+#pragma once
+
+#include "packed_linear.h"
+
+namespace gptq {
+namespace {
+
+constexpr int KS = 128;        // columns per stage
+constexpr int ROWS = 32;       // rows per warp (two m16 tiles)
+
+template <int BITS, int XT, int NT, bool FINE>
+struct Few {
+  static constexpr bool INT8 = XT == GPTQ_I8;
+  // 8-bit codes with bf16: operands q - z
+  static constexpr bool EXACT = BITS == 8 && XT == GPTQ_BF16;
+  // fp16 codes of fewer bits: the pairs at odd places are summed apart
+  static constexpr bool TWO = BITS != 8 && XT == GPTQ_F16;
+  // Row strides in shared memory, chosen so that the rows a warp reads at once
+  // fall on different banks.
+  static constexpr int WSTRIDE = FINE ? (BITS == 4 ? 80 : BITS == 8 ? 160 : 48)
+                                      : (BITS == 4 ? 64 : BITS == 8 ? 144 : BITS == 3 ? 48 : 32);
+  static constexpr int XB = INT8 ? 1 : 2;                         // bytes of an element of x
+  static constexpr int XROW = KS * XB;
+  static constexpr int XSTRIDE = INT8 ? (FINE ? 160 : 144) : 320;
+  static constexpr int WBYTES = ROWS * WSTRIDE;
+  static constexpr int SUBS = FINE ? 4 : 1;                       // groups of a stage
+  static constexpr int SZBYTES = ROWS * 4 * SUBS * 2;
+  static constexpr int STAGES = NT == 1 ? (BITS == 8 ? 3 : 4) : NT == 2 ? (BITS == 8 ? 2 : 3) : 2;
+  __host__ __device__ static constexpr int stage_bytes(int tokens) {
+    return (WBYTES + SZBYTES + tokens * XSTRIDE + 127) / 128 * 128;
+  }
+  static constexpr int MAX_WARPS = NT == 4 ? 8 : 16;              // of a CTA: 8 or 16 (registers)
+};
+constexpr size_t FEW_SMEM = 226 * 1024;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+
+// d = a b (+ d): with FIRST the sum starts here.
+template <int XT, bool FIRST>
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                      uint32_t a3, uint32_t b0, uint32_t b1) {
+  const float z = 0.f;
+  if constexpr (FIRST) {
+    if constexpr (XT == GPTQ_F16)
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+          "{%8,%9}, {%10,%10,%10,%10};"
+          : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+          : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z));
+    else
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+          "{%8,%9}, {%10,%10,%10,%10};"
+          : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+          : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z));
+  } else {
+    if constexpr (XT == GPTQ_F16)
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+          "{%8,%9}, {%0,%1,%2,%3};"
+          : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+          : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+          "{%8,%9}, {%0,%1,%2,%3};"
+          : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+          : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+}
+template <bool FIRST>
+__device__ __forceinline__ void mma8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                     uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (FIRST)
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A row's share of a stage, from shared memory: the four units of chunk t, or
+// (FINE) unit t of the four chunks; each as it lies in the stream (8-bit codes:
+// two words), low bits first, anything above.
+template <int BITS, bool FINE>
+__device__ __forceinline__ void row_units(uint32_t row, int t, uint2 (&u)[4]) {
+  if constexpr (FINE) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if constexpr (BITS == 4) u[c].x = lds32(row + c * 16 + t * 4);
+      if constexpr (BITS == 2) u[c].x = lds16(row + c * 8 + t * 2);
+      if constexpr (BITS == 8) u[c] = lds64(row + c * 32 + t * 8);
+      if constexpr (BITS == 3) {   // 24 bits from bit 24 t of the chunk's 96
+        const int at = (t * 24) >> 5;
+        const uint32_t lo = lds32(row + c * 12 + at * 4);
+        const uint32_t hi = lds32(row + c * 12 + min(at + 1, 2) * 4);
+        u[c].x = __funnelshift_r(lo, hi, (t * 24) & 31);
+      }
+    }
+  } else {
+    if constexpr (BITS == 4) {
+      const uint4 v = lds128(row + t * 16);
+      u[0].x = v.x, u[1].x = v.y, u[2].x = v.z, u[3].x = v.w;
+    }
+    if constexpr (BITS == 2) {
+      const uint2 v = lds64(row + t * 8);
+      u[0].x = v.x, u[1].x = v.x >> 16, u[2].x = v.y, u[3].x = v.y >> 16;
+    }
+    if constexpr (BITS == 8) {
+      const uint4 v = lds128(row + t * 32), w = lds128(row + t * 32 + 16);
+      u[0] = make_uint2(v.x, v.y), u[1] = make_uint2(v.z, v.w);
+      u[2] = make_uint2(w.x, w.y), u[3] = make_uint2(w.z, w.w);
+    }
+    if constexpr (BITS == 3) {
+      const uint32_t a = lds32(row + t * 12), b = lds32(row + t * 12 + 4), c = lds32(row + t * 12 + 8);
+      u[0].x = a;
+      u[1].x = __funnelshift_r(a, b, 24);
+      u[2].x = __funnelshift_r(b, c, 16);
+      u[3].x = c >> 8;
+    }
+  }
+}
+
+// B of the operand B + q (bf16), see above.
+template <int BITS, int XT>
+constexpr float operand_base() {
+  return XT == GPTQ_BF16 && BITS != 8 ? (BITS == 4 ? 16.f : BITS == 3 ? 8.f : 4.f) : 0.f;
+}
+
+// The eight codes of a unit as four pairs of operands: (0,4), (1,5), (2,6),
+// (3,7), or for 8-bit codes (0,1), (2,3), (4,5), (6,7); fp16 codes of fewer
+// bits: the second and fourth pair times 2^BITS.  zf = 2^23 + z, for 8-bit
+// codes with bf16 only.
+template <int BITS, int XT>
+__device__ __forceinline__ void code_pairs(uint2 w, float zf, uint32_t (&o)[4]) {
+  if constexpr (BITS == 8) {
+    if constexpr (XT == GPTQ_F16) {
+      o[0] = __byte_perm(w.x, 0, 0x4140), o[1] = __byte_perm(w.x, 0, 0x4342);
+      o[2] = __byte_perm(w.y, 0, 0x4140), o[3] = __byte_perm(w.y, 0, 0x4342);
+    } else {
+      // 8 bits do not fit bf16's mantissa beside a base: through fp32, whose upper
+      // half holds |q - z| <= 255 exactly
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t v = i < 2 ? w.x : w.y;
+        const float a = __uint_as_float(__byte_perm(v, 0x4B000000u, (i & 1) ? 0x7442 : 0x7440)) - zf;
+        const float b = __uint_as_float(__byte_perm(v, 0x4B000000u, (i & 1) ? 0x7443 : 0x7441)) - zf;
+        o[i] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+      }
+    }
+  } else {
+    // codes 0..3 to the low half, 4..7 to the high half, code i at bit i BITS
+    uint32_t v = w.x;
+    if constexpr (BITS == 3) v = (v & 0x0000FFFFu) | ((v << 4) & 0xFFFF0000u);
+    if constexpr (BITS == 2) v = __byte_perm(v, 0, 0x4140);
+    constexpr uint32_t mask = ((1u << BITS) - 1u) * 0x00010001u;
+    if constexpr (XT == GPTQ_F16) {
+      const uint32_t h = v >> (2 * BITS);
+      o[0] = v & mask, o[1] = v & (mask << BITS);
+      o[2] = h & mask, o[3] = h & (mask << BITS);
+    } else {
+      // at bit P, the top of the mantissa: exponent of 2^BITS
+      constexpr int P = 7 - BITS;
+      constexpr uint32_t base = (uint32_t)((127 + BITS) << 7) * 0x00010001u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int left = P - BITS * i;
+        o[i] = ((left > 0 ? v << (left > 0 ? left : 0) : v >> (left < 0 ? -left : 0)) & (mask << P)) | base;
+      }
+    }
+  }
+}
+
+// The eight codes as bytes: {0, 2, 4, 6}, {1, 3, 5, 7} for 4-bit codes, else
+// in order.
+template <int BITS>
+__device__ __forceinline__ uint2 code_bytes(uint2 w) {
+  if constexpr (BITS == 8) return w;
+  if constexpr (BITS == 4) return make_uint2(w.x & 0x0F0F0F0Fu, (w.x >> 4) & 0x0F0F0F0Fu);
+  uint32_t o[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (BITS == 3) {
+      const uint32_t v = i ? w.x >> 12 : w.x;
+      const uint32_t u = (v & 0x3Fu) | ((v << 10) & 0x003F0000u);
+      o[i] = (u & 0x00070007u) | ((u << 5) & 0x07000700u);
+    } else {
+      const uint32_t v = i ? w.x >> 8 : w.x;
+      const uint32_t u = (v & 0xFu) | ((v << 12) & 0x000F0000u);
+      o[i] = (u & 0x00030003u) | ((u << 6) & 0x03000300u);
+    }
+  }
+  return make_uint2(o[0], o[1]);
+}
+
+struct FewArgs {
+  PackedArgs p;
+  int ctas_k;        // CTAs of a cluster, along k
+  int stage_bytes;   // of one stage of one warp
+  int aligned;       // rows of codes start on 16-byte boundaries
+  uint32_t gdiv;     // ceil(2^31 / (group / 32)), 0 for one group
+};
+
+template <int BITS, int XT, int NT, bool FINE>
+__global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
+    packed_few_kernel(const FewArgs a) {
+  using F = Few<BITS, XT, NT, FINE>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int crank = blockIdx.x % a.ctas_k;
+  const int64_t row0 = (int64_t)(blockIdx.x / a.ctas_k) * ROWS;
+  const int64_t tok0 = (int64_t)blockIdx.y * (8 * NT);
+  const int ntok = (int)min((int64_t)(8 * NT), a.p.n - tok0);
+  const int d = a.p.d;
+  // this warp's stages
+  const int total = (d + KS - 1) / KS;
+  const int parts = a.ctas_k * warps, part_id = crank * warps + warp;
+  const int s0 = total * part_id / parts, s1 = total * (part_id + 1) / parts;
+
+  const uint32_t ring = smem_u32(smem) + warp * F::STAGES * a.stage_bytes;
+  const int pitch = d / 32 * BITS * 4;            // bytes per row
+  const int last = (int)min((int64_t)ROWS, a.p.r - row0) - 1;   // rows past it: its codes again, dropped
+  const char *wsrc = reinterpret_cast<const char *>(a.p.qweight) + row0 * pitch;
+  const char *xsrc = reinterpret_cast<const char *>(a.p.x) + tok0 * d * F::XB;
+  const int64_t szrow = (row0 + min(lane, last)) * a.p.G;
+
+  auto issue = [&](int s, int slot) {
+    const uint32_t base = ring + slot * a.stage_bytes;
+    const int k0 = s * KS, cols = min(KS, d - k0);
+    const char *w = wsrc + s * (KS * BITS / 8);
+    if (a.aligned && cols == KS) {
+#pragma unroll
+      for (int i = 0; i < BITS; ++i) {
+        const int p = lane + 32 * i, row = p / BITS, col = p % BITS * 16;
+        cp_async16(base + row * F::WSTRIDE + col, w + (min(row, last) * pitch + col), 16);
+      }
+    } else {
+      const int bytes = cols * BITS / 8;             // of a row
+#pragma unroll 4
+      for (int i = 0; i < 4 * BITS; ++i) {
+        const int p = lane + 32 * i, row = p / (4 * BITS), col = p % (4 * BITS) * 4;
+        const bool in = col < bytes;
+        cp_async4(base + row * F::WSTRIDE + col, w + (min(row, last) * pitch + (in ? col : 0)),
+                  in ? 4 : 0);
+      }
+    }
+    // scales and zeros: lane = row
+    const uint32_t sz = base + F::WBYTES + lane * (4 * F::SUBS);
+#pragma unroll
+    for (int c = 0; c < F::SUBS; ++c) {
+      const int chunk = FINE ? min(s * 4 + c, d / 32 - 1) : s * 4;
+      const int gi = (int)(((uint64_t)(uint32_t)chunk * a.gdiv) >> 31);
+      cp_async4(sz + c * 4, a.p.scales + szrow + gi, 4);
+      cp_async4(sz + ROWS * 4 * F::SUBS + c * 4, a.p.zeros + szrow + gi, 4);
+    }
+    // x: 16-byte pieces; 16-bit x of a coarse stage as [unit][chunk]
+    constexpr int PIECES = F::XROW / 16;
+    for (int p = lane; p < ntok * PIECES; p += 32) {
+      const int tok = p / PIECES, i = p % PIECES;
+      const bool in = i * 16 < cols * F::XB;
+      const int at = !F::INT8 && !FINE ? (i & 3) * 4 + (i >> 2) : i;
+      cp_async16(base + F::WBYTES + F::SZBYTES + tok * F::XSTRIDE + at * 16,
+                 xsrc + ((int64_t)tok * d + k0) * F::XB + (in ? i * 16 : 0), in ? 16 : 0);
+    }
+  };
+
+  float acc[2][NT][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.f;
+
+#pragma unroll
+  for (int i = 0; i < F::STAGES - 1; ++i) {
+    if (s0 + i < s1) issue(s0 + i, i);
+    cp_commit();
+  }
+  int slot = 0;
+  for (int s = s0; s < s1; ++s) {
+    cp_wait<F::STAGES - 2>();
+    __syncwarp();
+    {
+      const int nx = s + F::STAGES - 1;
+      int ns = slot + F::STAGES - 1;
+      if (ns >= F::STAGES) ns -= F::STAGES;
+      if (nx < s1) issue(nx, ns);
+      cp_commit();
+    }
+    const uint32_t base = ring + slot * a.stage_bytes;
+    const uint32_t xbase = base + F::WBYTES + F::SZBYTES;
+    const uint32_t sz = base + F::WBYTES;
+    uint2 lo[2][4], hi[2][4];   // rows g and g + 8 of the two tiles
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      row_units<BITS, FINE>(base + (m * 16 + g) * F::WSTRIDE, t, lo[m]);
+      row_units<BITS, FINE>(base + (m * 16 + 8 + g) * F::WSTRIDE, t, hi[m]);
+    }
+    float part[2][NT][4], odd[2][NT][4], sx[NT][4];
+    int ipart[2][NT][4], isx[NT][4];
+    float zf[2][2] = {};
+    auto zero_point = [&](int m, int h, int u) {
+      const int z = (int)lds32(sz + ROWS * 4 * F::SUBS + (m * 16 + h * 8 + g) * (4 * F::SUBS) +
+                               (FINE ? u * 4 : 0));
+      return min(max(z, 0), (1 << BITS) - 1);
+    };
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool first = FINE || u == 0;   // a sum starts with this unit
+      if constexpr (!F::INT8) {
+        if (F::EXACT && first) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) zf[m][h] = 8388608.f + (float)zero_point(m, h, u);
+        }
+        uint32_t xb[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          // (a coarse stage: piece t of unit u; FINE: piece t of chunk u -- the same place)
+          if (j * 8 + g < ntok) v = lds128(xbase + (j * 8 + g) * F::XSTRIDE + u * 64 + t * 16);
+          if constexpr (BITS == 8) {
+            xb[j][0] = v.x, xb[j][1] = v.y, xb[j][2] = v.z, xb[j][3] = v.w;
+          } else {
+            xb[j][0] = __byte_perm(v.x, v.z, 0x5410), xb[j][1] = __byte_perm(v.x, v.z, 0x7632);
+            xb[j][2] = __byte_perm(v.y, v.w, 0x5410), xb[j][3] = __byte_perm(v.y, v.w, 0x7632);
+          }
+          if constexpr (!F::EXACT) {
+            constexpr uint32_t one = XT == GPTQ_F16 ? 0x00010001u : 0x3F803F80u;   // 2^-24; 1
+            if (first)
+              mma16<XT, true>(sx[j], one, one, one, one, xb[j][0], xb[j][1]);
+            else
+              mma16<XT, false>(sx[j], one, one, one, one, xb[j][0], xb[j][1]);
+            mma16<XT, false>(sx[j], one, one, one, one, xb[j][2], xb[j][3]);
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          uint32_t pl[4], ph[4];
+          code_pairs<BITS, XT>(lo[m][u], zf[m][0], pl);
+          code_pairs<BITS, XT>(hi[m][u], zf[m][1], ph);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if constexpr (F::TWO) {
+              if (first) {
+                mma16<XT, true>(part[m][j], pl[0], ph[0], pl[2], ph[2], xb[j][0], xb[j][2]);
+                mma16<XT, true>(odd[m][j], pl[1], ph[1], pl[3], ph[3], xb[j][1], xb[j][3]);
+              } else {
+                mma16<XT, false>(part[m][j], pl[0], ph[0], pl[2], ph[2], xb[j][0], xb[j][2]);
+                mma16<XT, false>(odd[m][j], pl[1], ph[1], pl[3], ph[3], xb[j][1], xb[j][3]);
+              }
+            } else {
+              if (first)
+                mma16<XT, true>(part[m][j], pl[0], ph[0], pl[1], ph[1], xb[j][0], xb[j][1]);
+              else
+                mma16<XT, false>(part[m][j], pl[0], ph[0], pl[1], ph[1], xb[j][0], xb[j][1]);
+              mma16<XT, false>(part[m][j], pl[2], ph[2], pl[3], ph[3], xb[j][2], xb[j][3]);
+            }
+          }
+        }
+      } else {
+        uint32_t xb[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          uint2 v = make_uint2(0, 0);
+          if (j * 8 + g < ntok)
+            v = lds64(xbase + (j * 8 + g) * F::XSTRIDE + (FINE ? u * 32 + t * 8 : t * 32 + u * 8));
+          if constexpr (BITS == 4) {
+            xb[j][0] = __byte_perm(v.x, v.y, 0x6420), xb[j][1] = __byte_perm(v.x, v.y, 0x7531);
+          } else {
+            xb[j][0] = v.x, xb[j][1] = v.y;
+          }
+          constexpr uint32_t one = 0x01010101u;
+          if (first)
+            mma8<true>(isx[j], one, one, one, one, xb[j][0], xb[j][1]);
+          else
+            mma8<false>(isx[j], one, one, one, one, xb[j][0], xb[j][1]);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const uint2 bl = code_bytes<BITS>(lo[m][u]), bh = code_bytes<BITS>(hi[m][u]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if (first)
+              mma8<true>(ipart[m][j], bl.x, bh.x, bl.y, bh.y, xb[j][0], xb[j][1]);
+            else
+              mma8<false>(ipart[m][j], bl.x, bh.x, bl.y, bh.y, xb[j][0], xb[j][1]);
+          }
+        }
+      }
+      if (FINE || u == 3) {   // the group's (or stage's) sums, scaled
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float f = __uint_as_float(lds32(sz + (m * 16 + h * 8 + g) * (4 * F::SUBS) + (FINE ? u * 4 : 0)));
+            if constexpr (F::INT8) {
+              const int z = zero_point(m, h, u);
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  acc[m][j][2 * h + i] =
+                      fmaf(f, (float)(ipart[m][j][2 * h + i] - z * isx[j][i]), acc[m][j][2 * h + i]);
+            } else if constexpr (F::EXACT) {
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  acc[m][j][2 * h + i] = fmaf(f, part[m][j][2 * h + i], acc[m][j][2 * h + i]);
+            } else {
+              const float z = -(operand_base<BITS, XT>() + (float)zero_point(m, h, u));
+              if constexpr (XT == GPTQ_F16) f *= 16777216.f;   // 2^24
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  float v = part[m][j][2 * h + i];
+                  if constexpr (F::TWO) v = fmaf(1.f / (1 << BITS), odd[m][j][2 * h + i], v);
+                  acc[m][j][2 * h + i] = fmaf(f, fmaf(z, sx[j][i], v), acc[m][j][2 * h + i]);
+                }
+            }
+          }
+        }
+      }
+    }
+    if (++slot == F::STAGES) slot = 0;
+  }
+  cp_wait<0>();
+
+  // ---- the warps' sums, then the cluster's, each in a fixed order
+  constexpr int COLS = 8 * NT, CELLS = ROWS * COLS;
+  __syncthreads();                                  // every ring is drained
+  float *red = reinterpret_cast<float *>(smem);     // [warps][COLS][ROWS]
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        red[warp * CELLS + (j * 8 + t * 2 + (i & 1)) * ROWS + m * 16 + (i >> 1) * 8 + g] = acc[m][j][i];
+  __syncthreads();
+  const int per = CELLS / a.ctas_k;                 // cells this CTA finishes
+  const int first = crank * per;
+  if (a.ctas_k > 1) {
+    for (int i = threadIdx.x; i < CELLS; i += blockDim.x) {
+      float v = red[i];
+#pragma unroll 8
+      for (int w = 1; w < warps; ++w) v += red[w * CELLS + i];
+      red[i] = v;                                   // cell i is this thread's alone
+    }
+    __syncwarp();
+    cluster_sync();
+  }
+  for (int i = first + threadIdx.x; i < first + per; i += blockDim.x) {
+    float v = 0.f;
+    if (a.ctas_k > 1) {
+      for (int k = 0; k < a.ctas_k; ++k) {
+        float o;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(cluster_addr(red + i, k)));
+        v += o;
+      }
+    } else {
+      v = red[i];
+#pragma unroll 8
+      for (int w = 1; w < warps; ++w) v += red[w * CELLS + i];
+    }
+    const int col = i / ROWS;
+    const int64_t row = row0 + i % ROWS;
+    if (col < ntok && row < a.p.r) {
+      if constexpr (F::INT8) v *= a.p.x_scales[tok0 + col];
+      if (a.p.bias) v += load_as_float(a.p.bias, a.p.ytype, row);
+      store_float(a.p.y, a.p.ytype, (tok0 + col) * a.p.r + row, v);
+    }
+  }
+  if (a.ctas_k > 1) {                               // the partial sums stay until all have read them
+    __syncwarp();
+    cluster_sync();
+  }
+}
+
+template <int BITS, int XT, int NT, bool FINE>
+int launch_few(const PackedArgs &p, cudaStream_t st) {
+  using F = Few<BITS, XT, NT, FINE>;
+  static_assert((size_t)8 * F::STAGES * F::stage_bytes(8 * NT) <= FEW_SMEM, "ring too large");
+  FewArgs a{};
+  a.p = p;
+  a.stage_bytes = F::stage_bytes((int)(p.n < 8 * NT ? p.n : 8 * NT));
+  a.aligned = (p.d / 32 * BITS) % 4 == 0 && reinterpret_cast<uintptr_t>(p.qweight) % 16 == 0;
+  a.gdiv = p.group > 0 ? (uint32_t)(((1ull << 31) + p.group / 32 - 1) / (p.group / 32)) : 0;
+  static std::atomic<bool> attr[64] = {};
+  if (const int rc = ensure_smem_attr(packed_few_kernel<BITS, XT, NT, FINE>, FEW_SMEM, attr)) return rc;
+  const int64_t tiles = (p.r + ROWS - 1) / ROWS;
+  const int64_t blocks = (p.n + 8 * NT - 1) / (8 * NT);
+  const int stages = (p.d + KS - 1) / KS, sms = num_sms();
+  // Warps of a CTA and CTAs along k: the shape with the shortest estimate, in
+  // clocks: rounds of CTAs, each as long as its warps' stages (about 110 clocks of
+  // an SM per warp and stage, and at least 1000 of the warp) and its start and
+  // end (about 3000, 1500 more where CTAs add up their sums).  Measured on 4096 x
+  // 4096 and 12288 x 49152: 16 warps without a split of k beat 8 warps split
+  // over two CTAs.
+  int warps = 8, ck = 1;
+  size_t smem = 0;
+  int64_t best = INT64_MAX;
+  for (int w = 8; w <= F::MAX_WARPS; w *= 2) {
+    size_t need = (size_t)w * F::STAGES * a.stage_bytes;
+    const size_t red = (size_t)w * ROWS * 8 * NT * 4;
+    if (need < red) need = red;
+    if (need > FEW_SMEM) continue;
+    int res = (int)(FEW_SMEM / (need + 1024));
+    if (res > 16 / w) res = 16 / w;
+    if (res < 1) res = 1;
+    for (int c = 1; c <= 8; c *= 2) {
+      if (c > 1 && stages < w * c) break;
+      const int64_t ctas = tiles * blocks * c;
+      const int64_t rounds = (ctas + (int64_t)sms * res - 1) / ((int64_t)sms * res);
+      const int64_t busy = ctas >= (int64_t)sms * res ? res : (ctas + sms - 1) / sms;
+      const int64_t stage = 110 * w * busy > 1000 ? 110 * w * busy : 1000;
+      const int64_t cost = rounds * ((stages + w * c - 1) / (w * c) * stage + 3000 + (c > 1 ? 1500 : 0));
+      if (cost < best) best = cost, warps = w, ck = c, smem = need;
+    }
+  }
+  if (best == INT64_MAX) return GPTQ_ERR_INVALID_ARG;   // not reached: eight warps always fit
+  a.ctas_k = ck;
+  if (tiles * ck > INT32_MAX || blocks > 65535) return GPTQ_ERR_INVALID_ARG;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ck;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * ck), (unsigned)blocks);
+  cfg.blockDim = dim3(32 * warps);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = ck > 1 ? 1 : 0;
+  count_launch();
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, packed_few_kernel<BITS, XT, NT, FINE>, a);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    set_last_error(__FILE__, __LINE__, "kernel launch", e);
+    return GPTQ_ERR_CUDA;
+  }
+  return GPTQ_OK;
+}
+
+template <int BITS, int XT>
+int launch_few_bits(const PackedArgs &p, cudaStream_t st) {
+  const bool fine = p.group > 0 && p.group % KS != 0;
+  if (p.n <= 8) return fine ? launch_few<BITS, XT, 1, true>(p, st) : launch_few<BITS, XT, 1, false>(p, st);
+  // (a stage of 8-bit codes with 32 tokens in 16 bits does not fit: two blocks of 16)
+  if (p.n <= 16 || (BITS == 8 && XT != GPTQ_I8))
+    return fine ? launch_few<BITS, XT, 2, true>(p, st) : launch_few<BITS, XT, 2, false>(p, st);
+  if constexpr (BITS != 8 || XT == GPTQ_I8)
+    return fine ? launch_few<BITS, XT, 4, true>(p, st) : launch_few<BITS, XT, 4, false>(p, st);
+  return GPTQ_ERR_INVALID_ARG;   // not reached
+}
+
+template <int XT>
+int launch_few_type(const PackedArgs &p, cudaStream_t st) {
+  switch (p.bits) {
+    case 2: return launch_few_bits<2, XT>(p, st);
+    case 3: return launch_few_bits<3, XT>(p, st);
+    case 4: return launch_few_bits<4, XT>(p, st);
+    default: return launch_few_bits<8, XT>(p, st);
+  }
+}
+
+}  // namespace
+}  // namespace gptq

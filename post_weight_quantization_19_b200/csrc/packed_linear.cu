@@ -9,7 +9,7 @@
 //   y[t, i] = xs[t] sum_j s[i, j/g] (q[i, j] - z[i, j/g]) x[t, p(j)] + bias[i]
 //
 // Up to FEW_TOKENS tokens the product is bound by reading the packed weights
-// (packed_few.cu); beyond, by conversion and then by the tensor cores
+// (packed_few.cuh); beyond, by conversion and then by the tensor cores
 // (packed_many.cu).  This file checks the arguments, brings x into the
 // layer's column order and, for many tokens, 8-bit codes into fp16.
 #include "packed_linear.h"
@@ -17,7 +17,7 @@
 namespace gptq {
 namespace {
 
-constexpr int FEW_TOKENS = 16;   // up to here the weights' bytes bound the product
+constexpr int FEW_TOKENS = 16;   // up to here warp-level products are faster
 
 // x in the layer's column order: out[t, j] = x[t, perm[j]], entries outside
 // [0, d) clamped.  One CTA per token (8 n d or 6 n d bytes, from L2 for few).
@@ -107,5 +107,8 @@ extern "C" int gptq_packed_linear(const void *x, int xtype, const float *x_scale
   }
   const PackedArgs a{x, x_scales, reinterpret_cast<const uint32_t *>(qweight), scales, zeros,
                      bias, y, n, r, (int)d, bits, group, group < 0 ? 1 : (int)(d / group), xtype, ytype};
-  return n <= FEW_TOKENS ? launch_packed_few(a, st) : launch_packed_many(a, st);
+  if (n > FEW_TOKENS) return launch_packed_many(a, st);
+  return xtype == GPTQ_F16    ? launch_packed_few_f16(a, st)
+         : xtype == GPTQ_BF16 ? launch_packed_few_bf16(a, st)
+                              : launch_packed_few_i8(a, st);
 }

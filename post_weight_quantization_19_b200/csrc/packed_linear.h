@@ -21,7 +21,9 @@ struct PackedArgs {
 };
 
 // Few tokens: warp-level products on codes straight from the packed rows.
-int launch_packed_few(const PackedArgs &a, cudaStream_t st);
+int launch_packed_few_f16(const PackedArgs &a, cudaStream_t st);
+int launch_packed_few_bf16(const PackedArgs &a, cudaStream_t st);
+int launch_packed_few_i8(const PackedArgs &a, cudaStream_t st);
 // Many tokens: weights dequantised into tensor memory, tcgen05 products.  x in
 // 16 bits (xtype GPTQ_F16 or GPTQ_BF16; x_scales may still be given).
 int launch_packed_many(const PackedArgs &a, cudaStream_t st);
