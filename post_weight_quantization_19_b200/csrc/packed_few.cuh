@@ -2,7 +2,7 @@
 // packed weights once (r d bits/8 + 8 r G bytes) and by the instructions that
 // take the codes out of their words.
 //
-// A warp multiplies 32 rows of codes (two m16 tiles) with up to 8, 16 or 32
+// A warp multiplies 32 rows of codes (two m16 tiles) with up to 8 or 16
 // tokens on warp-level matrix instructions (mma.sync), whose operands come from
 // registers: a code goes from its packed word to an operand in about one
 // instruction, with nothing written back to shared or tensor memory on the way.
@@ -20,9 +20,12 @@
 //   fp16: B = 0, the code as a subnormal number, q 2^-24 (exact, and so are its
 //         products in fp32); every second code stays one place higher, q 2^(bits -
 //         24), and is summed apart, which saves a shift;
-//   bf16: B = 16, 8 or 4 for 4-, 3- or 2-bit codes, the code in the upper
-//         mantissa bits.  (8-bit codes do not fit: q - z through fp32 instead.)
-// and one more product with a matrix of ones gives sum x, so that a group adds
+//   bf16: B = 16 or 4 for 4- or 2-bit codes, the code in the upper mantissa
+//         bits; 3-bit codes B = 64 and 8 in turn, at two places of the mantissa,
+//         which saves two shifts of four.  (8-bit codes do not fit: q - z
+//         through fp32 instead.)
+// and one more product with a matrix of ones gives sum x (for each B), so that a
+// group adds
 //   s (sum (B + q) x - (B + z) sum x).
 // The terms that cancel are at most (B + q + z) / |q - z| times what q - z itself
 // would sum, held in fp32.  8-bit x: q and x as integers, sums exact.
@@ -48,6 +51,8 @@ struct Few {
   static constexpr bool EXACT = BITS == 8 && XT == GPTQ_BF16;
   // fp16 codes of fewer bits: the pairs at odd places are summed apart
   static constexpr bool TWO = BITS != 8 && XT == GPTQ_F16;
+  // bf16 codes of 3 bits: two bases
+  static constexpr bool BASES = BITS == 3 && XT == GPTQ_BF16;
   // Row strides in shared memory, chosen so that the rows a warp reads at once
   // fall on different banks.
   static constexpr int WSTRIDE = FINE ? (BITS == 4 ? 80 : BITS == 8 ? 160 : 48)
@@ -56,13 +61,19 @@ struct Few {
   static constexpr int XROW = KS * XB;
   static constexpr int XSTRIDE = INT8 ? (FINE ? 160 : 144) : 320;
   static constexpr int WBYTES = ROWS * WSTRIDE;
-  static constexpr int SUBS = FINE ? 4 : 1;                       // groups of a stage
-  static constexpr int SZBYTES = ROWS * 4 * SUBS * 2;
-  static constexpr int STAGES = NT == 1 ? (BITS == 8 ? 3 : 4) : NT == 2 ? (BITS == 8 ? 2 : 3) : 2;
+  static constexpr int STAGES = NT == 1 ? (BITS == 8 ? 3 : 4) : (BITS == 8 ? 2 : 3);
+  // Scales and zeros: FINE, those of a stage's four chunks lie in the stage; else
+  // blocks of four groups in slots of the warp's own, so that a 32-byte
+  // sector is fetched twice and not for every stage (which doubled the traffic
+  // from L2: 121 us instead of 81 for 12288 x 49152, 4 bits).
+  static constexpr int SZBYTES = FINE ? ROWS * 4 * 4 * 2 : 0;
+  static constexpr int SZSLOT = ROWS * 4 * 4 * 2;
+  static constexpr int SZSLOTS = STAGES + 1;   // one per stage in flight, at worst, and the last one's
+  static constexpr int SZWARP = FINE ? 0 : SZSLOTS * SZSLOT;
   __host__ __device__ static constexpr int stage_bytes(int tokens) {
     return (WBYTES + SZBYTES + tokens * XSTRIDE + 127) / 128 * 128;
   }
-  static constexpr int MAX_WARPS = NT == 4 ? 8 : 16;              // of a CTA: 8 or 16 (registers)
+  static constexpr int MAX_WARPS = 16;                            // of a CTA: 8 or 16
 };
 constexpr size_t FEW_SMEM = 226 * 1024;
 
@@ -195,10 +206,10 @@ __device__ __forceinline__ void row_units(uint32_t row, int t, uint2 (&u)[4]) {
   }
 }
 
-// B of the operand B + q (bf16), see above.
+// B of the operand B + q (bf16), see above; 3-bit codes: of the even pairs.
 template <int BITS, int XT>
 constexpr float operand_base() {
-  return XT == GPTQ_BF16 && BITS != 8 ? (BITS == 4 ? 16.f : BITS == 3 ? 8.f : 4.f) : 0.f;
+  return XT == GPTQ_BF16 && BITS != 8 ? (BITS == 4 ? 16.f : BITS == 3 ? 64.f : 4.f) : 0.f;
 }
 
 // The eight codes of a unit as four pairs of operands: (0,4), (1,5), (2,6),
@@ -232,6 +243,11 @@ __device__ __forceinline__ void code_pairs(uint2 w, float zf, uint32_t (&o)[4]) 
       const uint32_t h = v >> (2 * BITS);
       o[0] = v & mask, o[1] = v & (mask << BITS);
       o[2] = h & mask, o[3] = h & (mask << BITS);
+    } else if constexpr (BITS == 3) {
+      // codes 0 and 2 at bit 1 (64 + q), 1 and 3 at bit 4 (8 + q)
+      const uint32_t u = v << 1, h = v >> 5;
+      o[0] = (u & 0x000E000Eu) | 0x42804280u, o[1] = (u & 0x00700070u) | 0x41004100u;
+      o[2] = (h & 0x000E000Eu) | 0x42804280u, o[3] = (h & 0x00700070u) | 0x41004100u;
     } else {
       // at bit P, the top of the mantissa: exponent of 2^BITS
       constexpr int P = 7 - BITS;
@@ -272,6 +288,7 @@ struct FewArgs {
   int ctas_k;        // CTAs of a cluster, along k
   int stage_bytes;   // of one stage of one warp
   int aligned;       // rows of codes start on 16-byte boundaries
+  int sz_aligned;    // rows of scales and zeros too, in whole fours
   uint32_t gdiv;     // ceil(2^31 / (group / 32)), 0 for one group
 };
 
@@ -283,23 +300,42 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int crank = blockIdx.x % a.ctas_k;
-  const int64_t row0 = (int64_t)(blockIdx.x / a.ctas_k) * ROWS;
   const int64_t tok0 = (int64_t)blockIdx.y * (8 * NT);
   const int ntok = (int)min((int64_t)(8 * NT), a.p.n - tok0);
   const int d = a.p.d;
-  // this warp's stages
+  // this warp's stages of every tile
   const int total = (d + KS - 1) / KS;
   const int parts = a.ctas_k * warps, part_id = crank * warps + warp;
   const int s0 = total * part_id / parts, s1 = total * (part_id + 1) / parts;
+  const int tiles = (int)((a.p.r + ROWS - 1) / ROWS);
+  const int cta = blockIdx.x / a.ctas_k, ctas = gridDim.x / a.ctas_k;
 
-  const uint32_t ring = smem_u32(smem) + warp * F::STAGES * a.stage_bytes;
+  const uint32_t ring = smem_u32(smem) + warp * (F::STAGES * a.stage_bytes + F::SZWARP);
+  const uint32_t sz_ring = ring + F::STAGES * a.stage_bytes;
   const int pitch = d / 32 * BITS * 4;            // bytes per row
-  const int last = (int)min((int64_t)ROWS, a.p.r - row0) - 1;   // rows past it: its codes again, dropped
-  const char *wsrc = reinterpret_cast<const char *>(a.p.qweight) + row0 * pitch;
   const char *xsrc = reinterpret_cast<const char *>(a.p.x) + tok0 * d * F::XB;
-  const int64_t szrow = (row0 + min(lane, last)) * a.p.G;
+  // The loading cursor: stage ls of tile lt.  It runs ahead of the computing one
+  // into the CTA's next tile, so that no tile starts with an empty ring.
+  int lt = cta, ls = s0, last = 0;
+  const char *wsrc = nullptr;
+  int64_t szrow = 0;
+  auto open_tile = [&]() {
+    const int64_t row0 = (int64_t)lt * ROWS;
+    last = (int)min((int64_t)ROWS, a.p.r - row0) - 1;   // rows past it: its codes again, dropped
+    wsrc = reinterpret_cast<const char *>(a.p.qweight) + row0 * pitch;
+    szrow = (row0 + min(lane, last)) * a.p.G;
+  };
 
-  auto issue = [&](int s, int slot) {
+  auto group_of = [&](int chunk) { return (int)(((uint64_t)(uint32_t)chunk * a.gdiv) >> 31); };
+  int sz_block = -1, sz_slot = 0;   // the last block of four groups asked for, its slot
+  auto issue = [&](int slot) {
+    if (lt >= tiles || s0 >= s1) return;
+    if (ls == s0) {
+      open_tile();
+      sz_block = -1;
+    }
+    const int s = ls;
+    if (++ls == s1) ls = s0, lt += ctas;
     const uint32_t base = ring + slot * a.stage_bytes;
     const int k0 = s * KS, cols = min(KS, d - k0);
     const char *w = wsrc + s * (KS * BITS / 8);
@@ -320,13 +356,32 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
       }
     }
     // scales and zeros: lane = row
-    const uint32_t sz = base + F::WBYTES + lane * (4 * F::SUBS);
+    if constexpr (FINE) {
+      const uint32_t sz = base + F::WBYTES + lane * 16;
 #pragma unroll
-    for (int c = 0; c < F::SUBS; ++c) {
-      const int chunk = FINE ? min(s * 4 + c, d / 32 - 1) : s * 4;
-      const int gi = (int)(((uint64_t)(uint32_t)chunk * a.gdiv) >> 31);
-      cp_async4(sz + c * 4, a.p.scales + szrow + gi, 4);
-      cp_async4(sz + ROWS * 4 * F::SUBS + c * 4, a.p.zeros + szrow + gi, 4);
+      for (int c = 0; c < 4; ++c) {
+        const int gi = group_of(min(s * 4 + c, d / 32 - 1));
+        cp_async4(sz + c * 4, a.p.scales + szrow + gi, 4);
+        cp_async4(sz + ROWS * 16 + c * 4, a.p.zeros + szrow + gi, 4);
+      }
+    } else {
+      const int block = group_of(s * 4) >> 2;
+      if (block != sz_block) {
+        sz_block = block;
+        sz_slot = sz_slot + 1 == F::SZSLOTS ? 0 : sz_slot + 1;
+        const uint32_t sz = sz_ring + sz_slot * F::SZSLOT + lane * 16;
+        if (a.sz_aligned) {
+          cp_async16(sz, a.p.scales + szrow + block * 4, 16);
+          cp_async16(sz + ROWS * 16, a.p.zeros + szrow + block * 4, 16);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int gi = min(block * 4 + c, a.p.G - 1);
+            cp_async4(sz + c * 4, a.p.scales + szrow + gi, 4);
+            cp_async4(sz + ROWS * 16 + c * 4, a.p.zeros + szrow + gi, 4);
+          }
+        }
+      }
     }
     // x: 16-byte pieces; 16-bit x of a coarse stage as [unit][chunk]
     constexpr int PIECES = F::XROW / 16;
@@ -339,6 +394,15 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
     }
   };
 
+#pragma unroll
+  for (int i = 0; i < F::STAGES - 1; ++i) {
+    issue(i);
+    cp_commit();
+  }
+  int slot = 0, cslot = 0;
+  // [warps][COLS][ROWS]
+  float *red = reinterpret_cast<float *>(smem + warps * (F::STAGES * a.stage_bytes + F::SZWARP));
+  for (int tile = cta; tile < tiles; tile += ctas) {
   float acc[2][NT][4];
 #pragma unroll
   for (int m = 0; m < 2; ++m)
@@ -346,38 +410,39 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.f;
-
-#pragma unroll
-  for (int i = 0; i < F::STAGES - 1; ++i) {
-    if (s0 + i < s1) issue(s0 + i, i);
-    cp_commit();
-  }
-  int slot = 0;
+  int cblock = -1;   // as sz_block, of the computing cursor
   for (int s = s0; s < s1; ++s) {
     cp_wait<F::STAGES - 2>();
     __syncwarp();
     {
-      const int nx = s + F::STAGES - 1;
       int ns = slot + F::STAGES - 1;
       if (ns >= F::STAGES) ns -= F::STAGES;
-      if (nx < s1) issue(nx, ns);
+      issue(ns);
       cp_commit();
     }
     const uint32_t base = ring + slot * a.stage_bytes;
     const uint32_t xbase = base + F::WBYTES + F::SZBYTES;
-    const uint32_t sz = base + F::WBYTES;
+    // scales of rows 0, 1, ... of this stage's (first) group, 16 bytes apart; zeros behind
+    uint32_t sz = base + F::WBYTES;
+    if constexpr (!FINE) {
+      const int gi = group_of(s * 4);
+      if (gi >> 2 != cblock) {
+        cblock = gi >> 2;
+        cslot = cslot + 1 == F::SZSLOTS ? 0 : cslot + 1;
+      }
+      sz = sz_ring + cslot * F::SZSLOT + (gi & 3) * 4;
+    }
     uint2 lo[2][4], hi[2][4];   // rows g and g + 8 of the two tiles
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       row_units<BITS, FINE>(base + (m * 16 + g) * F::WSTRIDE, t, lo[m]);
       row_units<BITS, FINE>(base + (m * 16 + 8 + g) * F::WSTRIDE, t, hi[m]);
     }
-    float part[2][NT][4], odd[2][NT][4], sx[NT][4];
+    float part[2][NT][4], odd[2][NT][4], sx[NT][4], sx2[NT][4];
     int ipart[2][NT][4], isx[NT][4];
     float zf[2][2] = {};
     auto zero_point = [&](int m, int h, int u) {
-      const int z = (int)lds32(sz + ROWS * 4 * F::SUBS + (m * 16 + h * 8 + g) * (4 * F::SUBS) +
-                               (FINE ? u * 4 : 0));
+      const int z = (int)lds32(sz + ROWS * 16 + (m * 16 + h * 8 + g) * 16 + (FINE ? u * 4 : 0));
       return min(max(z, 0), (1 << BITS) - 1);
     };
 #pragma unroll
@@ -404,11 +469,21 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
           }
           if constexpr (!F::EXACT) {
             constexpr uint32_t one = XT == GPTQ_F16 ? 0x00010001u : 0x3F803F80u;   // 2^-24; 1
-            if (first)
-              mma16<XT, true>(sx[j], one, one, one, one, xb[j][0], xb[j][1]);
-            else
-              mma16<XT, false>(sx[j], one, one, one, one, xb[j][0], xb[j][1]);
-            mma16<XT, false>(sx[j], one, one, one, one, xb[j][2], xb[j][3]);
+            if constexpr (F::BASES) {
+              if (first) {
+                mma16<XT, true>(sx[j], one, one, one, one, xb[j][0], xb[j][2]);
+                mma16<XT, true>(sx2[j], one, one, one, one, xb[j][1], xb[j][3]);
+              } else {
+                mma16<XT, false>(sx[j], one, one, one, one, xb[j][0], xb[j][2]);
+                mma16<XT, false>(sx2[j], one, one, one, one, xb[j][1], xb[j][3]);
+              }
+            } else {
+              if (first)
+                mma16<XT, true>(sx[j], one, one, one, one, xb[j][0], xb[j][1]);
+              else
+                mma16<XT, false>(sx[j], one, one, one, one, xb[j][0], xb[j][1]);
+              mma16<XT, false>(sx[j], one, one, one, one, xb[j][2], xb[j][3]);
+            }
           }
         }
 #pragma unroll
@@ -470,7 +545,7 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
         for (int m = 0; m < 2; ++m) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float f = __uint_as_float(lds32(sz + (m * 16 + h * 8 + g) * (4 * F::SUBS) + (FINE ? u * 4 : 0)));
+            float f = __uint_as_float(lds32(sz + (m * 16 + h * 8 + g) * 16 + (FINE ? u * 4 : 0)));
             if constexpr (F::INT8) {
               const int z = zero_point(m, h, u);
 #pragma unroll
@@ -494,6 +569,7 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
                 for (int i = 0; i < 2; ++i) {
                   float v = part[m][j][2 * h + i];
                   if constexpr (F::TWO) v = fmaf(1.f / (1 << BITS), odd[m][j][2 * h + i], v);
+                  if constexpr (F::BASES) v = fmaf(z + 56.f, sx2[j][i], v);   // -(8 + z)
                   acc[m][j][2 * h + i] = fmaf(f, fmaf(z, sx[j][i], v), acc[m][j][2 * h + i]);
                 }
             }
@@ -503,12 +579,10 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
     }
     if (++slot == F::STAGES) slot = 0;
   }
-  cp_wait<0>();
 
   // ---- the warps' sums, then the cluster's, each in a fixed order
   constexpr int COLS = 8 * NT, CELLS = ROWS * COLS;
-  __syncthreads();                                  // every ring is drained
-  float *red = reinterpret_cast<float *>(smem);     // [warps][COLS][ROWS]
+  const int64_t row0 = (int64_t)tile * ROWS;
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -530,6 +604,9 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
     cluster_sync();
   }
   for (int i = first + threadIdx.x; i < first + per; i += blockDim.x) {
+    const int col = i / ROWS;
+    const int64_t row = row0 + i % ROWS;
+    if (col >= ntok || row >= a.p.r) continue;
     float v = 0.f;
     if (a.ctas_k > 1) {
       for (int k = 0; k < a.ctas_k; ++k) {
@@ -542,28 +619,32 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
 #pragma unroll 8
       for (int w = 1; w < warps; ++w) v += red[w * CELLS + i];
     }
-    const int col = i / ROWS;
-    const int64_t row = row0 + i % ROWS;
-    if (col < ntok && row < a.p.r) {
-      if constexpr (F::INT8) v *= a.p.x_scales[tok0 + col];
-      if (a.p.bias) v += load_as_float(a.p.bias, a.p.ytype, row);
-      store_float(a.p.y, a.p.ytype, (tok0 + col) * a.p.r + row, v);
-    }
+    if constexpr (F::INT8) v *= a.p.x_scales[tok0 + col];
+    if (a.p.bias) v += load_as_float(a.p.bias, a.p.ytype, row);
+    store_float(a.p.y, a.p.ytype, (tok0 + col) * a.p.r + row, v);
   }
-  if (a.ctas_k > 1) {                               // the partial sums stay until all have read them
+  if (a.ctas_k > 1) {                               // the sums stay until all have read them
     __syncwarp();
     cluster_sync();
+  } else if (tile + ctas < tiles) {
+    __syncthreads();                                // nor may the next tile's sums come early
   }
+  }
+  cp_wait<0>();
 }
 
 template <int BITS, int XT, int NT, bool FINE>
 int launch_few(const PackedArgs &p, cudaStream_t st) {
   using F = Few<BITS, XT, NT, FINE>;
-  static_assert((size_t)8 * F::STAGES * F::stage_bytes(8 * NT) <= FEW_SMEM, "ring too large");
+  constexpr size_t RED = (size_t)ROWS * 8 * NT * 4;   // a warp's sums
+  static_assert(8 * (F::STAGES * F::stage_bytes(8 * NT) + F::SZWARP + RED) <= FEW_SMEM, "ring too large");
   FewArgs a{};
   a.p = p;
   a.stage_bytes = F::stage_bytes((int)(p.n < 8 * NT ? p.n : 8 * NT));
   a.aligned = (p.d / 32 * BITS) % 4 == 0 && reinterpret_cast<uintptr_t>(p.qweight) % 16 == 0;
+  a.sz_aligned = (p.group < 0 ? 1 : p.d / p.group) % 4 == 0 &&
+                 reinterpret_cast<uintptr_t>(p.scales) % 16 == 0 &&
+                 reinterpret_cast<uintptr_t>(p.zeros) % 16 == 0;
   a.gdiv = p.group > 0 ? (uint32_t)(((1ull << 31) + p.group / 32 - 1) / (p.group / 32)) : 0;
   static std::atomic<bool> attr[64] = {};
   if (const int rc = ensure_smem_attr(packed_few_kernel<BITS, XT, NT, FINE>, FEW_SMEM, attr)) return rc;
@@ -572,17 +653,15 @@ int launch_few(const PackedArgs &p, cudaStream_t st) {
   const int stages = (p.d + KS - 1) / KS, sms = num_sms();
   // Warps of a CTA and CTAs along k: the shape with the shortest estimate, in
   // clocks: rounds of CTAs, each as long as its warps' stages (about 110 clocks of
-  // an SM per warp and stage, and at least 1000 of the warp) and its start and
-  // end (about 3000, 1500 more where CTAs add up their sums).  Measured on 4096 x
+  // an SM per warp and stage, and at least 1000 of the warp) and its sums (about
+  // 500, 1500 more where CTAs add up theirs).  Measured on 4096 x
   // 4096 and 12288 x 49152: 16 warps without a split of k beat 8 warps split
   // over two CTAs.
   int warps = 8, ck = 1;
   size_t smem = 0;
   int64_t best = INT64_MAX;
   for (int w = 8; w <= F::MAX_WARPS; w *= 2) {
-    size_t need = (size_t)w * F::STAGES * a.stage_bytes;
-    const size_t red = (size_t)w * ROWS * 8 * NT * 4;
-    if (need < red) need = red;
+    const size_t need = (size_t)w * (F::STAGES * a.stage_bytes + F::SZWARP + RED);
     if (need > FEW_SMEM) continue;
     int res = (int)(FEW_SMEM / (need + 1024));
     if (res > 16 / w) res = 16 / w;
@@ -593,19 +672,23 @@ int launch_few(const PackedArgs &p, cudaStream_t st) {
       const int64_t rounds = (ctas + (int64_t)sms * res - 1) / ((int64_t)sms * res);
       const int64_t busy = ctas >= (int64_t)sms * res ? res : (ctas + sms - 1) / sms;
       const int64_t stage = 110 * w * busy > 1000 ? 110 * w * busy : 1000;
-      const int64_t cost = rounds * ((stages + w * c - 1) / (w * c) * stage + 3000 + (c > 1 ? 1500 : 0));
+      const int64_t cost = rounds * ((stages + w * c - 1) / (w * c) * stage + 500 + (c > 1 ? 1500 : 0)) + 3000;
       if (cost < best) best = cost, warps = w, ck = c, smem = need;
     }
   }
   if (best == INT64_MAX) return GPTQ_ERR_INVALID_ARG;   // not reached: eight warps always fit
   a.ctas_k = ck;
   if (tiles * ck > INT32_MAX || blocks > 65535) return GPTQ_ERR_INVALID_ARG;
+  // CTAs that fit at once walk the tiles
+  int64_t clusters = (int64_t)sms * (FEW_SMEM / (smem + 1024) < (size_t)(16 / warps) ? FEW_SMEM / (smem + 1024) : 16 / warps);
+  clusters = clusters / (blocks * ck) < 1 ? 1 : clusters / (blocks * ck);
+  if (clusters > tiles) clusters = tiles;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = ck;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * ck), (unsigned)blocks);
+  cfg.gridDim = dim3((unsigned)(clusters * ck), (unsigned)blocks);
   cfg.blockDim = dim3(32 * warps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -625,12 +708,7 @@ template <int BITS, int XT>
 int launch_few_bits(const PackedArgs &p, cudaStream_t st) {
   const bool fine = p.group > 0 && p.group % KS != 0;
   if (p.n <= 8) return fine ? launch_few<BITS, XT, 1, true>(p, st) : launch_few<BITS, XT, 1, false>(p, st);
-  // (a stage of 8-bit codes with 32 tokens in 16 bits does not fit: two blocks of 16)
-  if (p.n <= 16 || (BITS == 8 && XT != GPTQ_I8))
-    return fine ? launch_few<BITS, XT, 2, true>(p, st) : launch_few<BITS, XT, 2, false>(p, st);
-  if constexpr (BITS != 8 || XT == GPTQ_I8)
-    return fine ? launch_few<BITS, XT, 4, true>(p, st) : launch_few<BITS, XT, 4, false>(p, st);
-  return GPTQ_ERR_INVALID_ARG;   // not reached
+  return fine ? launch_few<BITS, XT, 2, true>(p, st) : launch_few<BITS, XT, 2, false>(p, st);
 }
 
 template <int XT>

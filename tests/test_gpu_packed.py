@@ -10,8 +10,8 @@ bf16 2^-8, fp32 2^-24, relative to the value):
       128): a sum over d features runs through at most d / 32 + 128 additions
       one after the other in any of the kernels' orders, and the tensor core's
       fp32 additions may be off by up to four half steps (they truncate).
-      With 16-bit x a group's sum is s (sum (B + q) x - (B + z) sum x), B <= 16,
-      so what is added up is at most s (B + q + B + z) |x| in place of |w x|:
+      With 16-bit x a group's sum is s (sum (B + q) x - (B + z) sum x), B <= 64
+      (fp16: 0), so what is added up is at most s (B + q + B + z) |x| in place of |w x|:
       the part of a group (128 columns, 24 additions) adds 4 * 24 2^-24
       sum s (2 B + q + z) |x|.
   product, many tokens  the same, plus u sum |w x| for the rounding of each weight
@@ -81,7 +81,7 @@ def reference(x, q, s, z, bits, group, xs=None, bias=None, perm=None):
     W = s.astype(np.float64)[:, gi] * (codes - z[:, gi])
     y, a = X @ W.T, np.abs(X) @ np.abs(W).T
     if x.shape[0] <= 32 and x.dtype != I8:
-        parts = np.abs(s.astype(np.float64)[:, gi]) * (32 + codes + z[:, gi])
+        parts = np.abs(s.astype(np.float64)[:, gi]) * (2 * (64 if x.dtype == BF16 else 0) + codes + z[:, gi])
         a = a + 24 / (d / 32 + 128) * (np.abs(X) @ parts.T)
     if bias is not None:
         y, a = y + f64(bias), a + np.abs(f64(bias))
@@ -475,7 +475,7 @@ def test_norm_and_products_of_a_solved_layer(n, act):
     y16 = g.gptq_packed_linear(natural["xhat"], q, *args, perm=perm, dtype=F32)
     assert torch.equal(y8, y8n)
     w = f64(What)
-    wq = np.abs(f64(res["scales"])).max(1, keepdims=True) * (2 * 16 + 15 + 15)   # s (2 B + q + z)
+    wq = np.abs(f64(res["scales"])).max(1, keepdims=True) * (15 + 15)   # s (q + z)
     x8 = f64(natural["codes"]) * f64(natural["scales"])[:, None]
     for y, v in ((y8, x8), (y16, f64(natural["xhat"]))):
         parts = 24 / (d / 32 + 128) * (np.abs(v) @ np.broadcast_to(wq, w.shape).T)
