@@ -61,7 +61,7 @@ struct Few {
   static constexpr int XROW = KS * XB;
   static constexpr int XSTRIDE = INT8 ? (FINE ? 160 : 144) : 320;
   static constexpr int WBYTES = ROWS * WSTRIDE;
-  static constexpr int STAGES = NT == 1 ? (BITS == 8 ? 3 : 4) : (BITS == 8 ? 2 : 3);
+  static constexpr int STAGES = NT == 2 && BITS == 8 ? 2 : 3;
   // Scales and zeros: FINE, those of a stage's four chunks lie in the stage; else
   // blocks of four groups in slots of the warp's own, so that a 32-byte
   // sector is fetched twice and not for every stage (which doubled the traffic
@@ -313,16 +313,28 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
   const uint32_t ring = smem_u32(smem) + warp * (F::STAGES * a.stage_bytes + F::SZWARP);
   const uint32_t sz_ring = ring + F::STAGES * a.stage_bytes;
   const int pitch = d / 32 * BITS * 4;            // bytes per row
-  const char *xsrc = reinterpret_cast<const char *>(a.p.x) + tok0 * d * F::XB;
   // The loading cursor: stage ls of tile lt.  It runs ahead of the computing one
-  // into the CTA's next tile, so that no tile starts with an empty ring.
-  int lt = cta, ls = s0, last = 0;
+  // into the CTA's next tile, so that no tile starts with an empty ring.  What
+  // a thread copies keeps its place from stage to stage: 16-byte piece lane +
+  // 32 i of the rows of codes, and of the tokens.
+  constexpr int PIECES = F::XROW / 16;             // of a token
+  int lt = cta, ls = s0;
   const char *wsrc = nullptr;
+  int woff[BITS];
   int64_t szrow = 0;
+  const int xtok = lane / PIECES, xpiece = lane % PIECES;
+  // (16-bit x of a coarse stage as [unit][chunk])
+  const int xat = !F::INT8 && !FINE ? (xpiece & 3) * 4 + (xpiece >> 2) : xpiece;
+  const char *xsrc = reinterpret_cast<const char *>(a.p.x) + (tok0 + xtok) * d * F::XB + xpiece * 16;
   auto open_tile = [&]() {
     const int64_t row0 = (int64_t)lt * ROWS;
-    last = (int)min((int64_t)ROWS, a.p.r - row0) - 1;   // rows past it: its codes again, dropped
+    const int last = (int)min((int64_t)ROWS, a.p.r - row0) - 1;   // rows past it: its codes again, dropped
     wsrc = reinterpret_cast<const char *>(a.p.qweight) + row0 * pitch;
+#pragma unroll
+    for (int i = 0; i < BITS; ++i) {
+      const int p = lane + 32 * i;
+      woff[i] = min(p / BITS, last) * pitch + p % BITS * 16;
+    }
     szrow = (row0 + min(lane, last)) * a.p.G;
   };
 
@@ -334,7 +346,7 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
       open_tile();
       sz_block = -1;
     }
-    const int s = ls;
+    const int s = ls, tile = lt;
     if (++ls == s1) ls = s0, lt += ctas;
     const uint32_t base = ring + slot * a.stage_bytes;
     const int k0 = s * KS, cols = min(KS, d - k0);
@@ -342,11 +354,12 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
     if (a.aligned && cols == KS) {
 #pragma unroll
       for (int i = 0; i < BITS; ++i) {
-        const int p = lane + 32 * i, row = p / BITS, col = p % BITS * 16;
-        cp_async16(base + row * F::WSTRIDE + col, w + (min(row, last) * pitch + col), 16);
+        const int p = lane + 32 * i;
+        cp_async16(base + p / BITS * F::WSTRIDE + p % BITS * 16, w + woff[i], 16);
       }
     } else {
       const int bytes = cols * BITS / 8;             // of a row
+      const int last = (int)min((int64_t)ROWS, a.p.r - (int64_t)tile * ROWS) - 1;
 #pragma unroll 4
       for (int i = 0; i < 4 * BITS; ++i) {
         const int p = lane + 32 * i, row = p / (4 * BITS), col = p % (4 * BITS) * 4;
@@ -383,14 +396,14 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
         }
       }
     }
-    // x: 16-byte pieces; 16-bit x of a coarse stage as [unit][chunk]
-    constexpr int PIECES = F::XROW / 16;
-    for (int p = lane; p < ntok * PIECES; p += 32) {
-      const int tok = p / PIECES, i = p % PIECES;
-      const bool in = i * 16 < cols * F::XB;
-      const int at = !F::INT8 && !FINE ? (i & 3) * 4 + (i >> 2) : i;
-      cp_async16(base + F::WBYTES + F::SZBYTES + tok * F::XSTRIDE + at * 16,
-                 xsrc + ((int64_t)tok * d + k0) * F::XB + (in ? i * 16 : 0), in ? 16 : 0);
+    // x
+    const bool in = xpiece * 16 < cols * F::XB;
+    const char *x = xsrc + (int64_t)k0 * F::XB - (in ? 0 : xpiece * 16);
+    uint32_t xdst = base + F::WBYTES + F::SZBYTES + xtok * F::XSTRIDE + xat * 16;
+    for (int tok = xtok; tok < ntok; tok += 32 / PIECES) {
+      cp_async16(xdst, x, in ? 16 : 0);
+      x += (int64_t)d * (32 / PIECES * F::XB);
+      xdst += 32 / PIECES * F::XSTRIDE;
     }
   };
 
@@ -399,6 +412,10 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
     issue(i);
     cp_commit();
   }
+  // tokens past the last: its values again (their columns are dropped)
+  uint32_t xrow[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) xrow[j] = min(j * 8 + g, ntok - 1) * F::XSTRIDE;
   int slot = 0, cslot = 0;
   // [warps][COLS][ROWS]
   float *red = reinterpret_cast<float *>(smem + warps * (F::STAGES * a.stage_bytes + F::SZWARP));
@@ -458,9 +475,8 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
         uint32_t xb[NT][4];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          uint4 v = make_uint4(0, 0, 0, 0);
           // (a coarse stage: piece t of unit u; FINE: piece t of chunk u -- the same place)
-          if (j * 8 + g < ntok) v = lds128(xbase + (j * 8 + g) * F::XSTRIDE + u * 64 + t * 16);
+          const uint4 v = lds128(xbase + xrow[j] + u * 64 + t * 16);
           if constexpr (BITS == 8) {
             xb[j][0] = v.x, xb[j][1] = v.y, xb[j][2] = v.z, xb[j][3] = v.w;
           } else {
@@ -514,9 +530,7 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
         uint32_t xb[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          uint2 v = make_uint2(0, 0);
-          if (j * 8 + g < ntok)
-            v = lds64(xbase + (j * 8 + g) * F::XSTRIDE + (FINE ? u * 32 + t * 8 : t * 32 + u * 8));
+          const uint2 v = lds64(xbase + xrow[j] + (FINE ? u * 32 + t * 8 : t * 32 + u * 8));
           if constexpr (BITS == 4) {
             xb[j][0] = __byte_perm(v.x, v.y, 0x6420), xb[j][1] = __byte_perm(v.x, v.y, 0x7531);
           } else {
@@ -545,7 +559,7 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
         for (int m = 0; m < 2; ++m) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float f = __uint_as_float(lds32(sz + (m * 16 + h * 8 + g) * 16 + (FINE ? u * 4 : 0)));
+            const float f = __uint_as_float(lds32(sz + (m * 16 + h * 8 + g) * 16 + (FINE ? u * 4 : 0)));
             if constexpr (F::INT8) {
               const int z = zero_point(m, h, u);
 #pragma unroll
@@ -561,8 +575,9 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
                 for (int i = 0; i < 2; ++i)
                   acc[m][j][2 * h + i] = fmaf(f, part[m][j][2 * h + i], acc[m][j][2 * h + i]);
             } else {
-              const float z = -(operand_base<BITS, XT>() + (float)zero_point(m, h, u));
-              if constexpr (XT == GPTQ_F16) f *= 16777216.f;   // 2^24
+              // -(B + z), z in the mantissa of 2^23
+              const float z = (8388608.f - operand_base<BITS, XT>()) -
+                              __uint_as_float(0x4B000000u | (uint32_t)zero_point(m, h, u));
 #pragma unroll
               for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -620,6 +635,7 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
       for (int w = 1; w < warps; ++w) v += red[w * CELLS + i];
     }
     if constexpr (F::INT8) v *= a.p.x_scales[tok0 + col];
+    if constexpr (XT == GPTQ_F16) v *= 16777216.f;   // the codes were q 2^-24
     if (a.p.bias) v += load_as_float(a.p.bias, a.p.ytype, row);
     store_float(a.p.y, a.p.ytype, (tok0 + col) * a.p.r + row, v);
   }
