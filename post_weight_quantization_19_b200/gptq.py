@@ -256,7 +256,7 @@ def _shaped(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, device: to
     """Pointer of a contiguous tensor of this type, shape and device (None for None)."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -276,15 +276,26 @@ def _activations(x: torch.Tensor, dtypes: tuple, name: str = "x") -> None:
         raise ValueError(f"{name} must be one of {', '.join(map(str, dtypes))}, got {x.dtype}")
 
 
+# The current device's index and its current stream's handle, without building
+# torch's device and stream objects (about 2 us a call) where torch offers that.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(device: torch.device, stream, fn, *args) -> int:
     """fn(*args, stream) with the tensors' device current; the stream is the
     given one or that device's current stream."""
-    if stream is not None and stream.device != device:
+    if stream is None:
+        handle = _raw_stream(device.index)
+    elif stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        return fn(*args, _stream(stream))
+    else:
+        handle = stream.cuda_stream
+    if _current_device() == device.index:
+        return fn(*args, handle)
     with torch.cuda.device(device):
-        return fn(*args, _stream(stream))
+        return fn(*args, handle)
 
 
 def gptq_rmsnorm_int8(x: torch.Tensor, gamma: torch.Tensor, *, eps: float,
@@ -368,9 +379,10 @@ def gptq_packed_linear(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Ten
     if y.dtype not in _DTYPE:
         raise ValueError(f"y must be float16, bfloat16 or float32, got {y.dtype}")
     xt = _DTYPE[x.dtype]
-    need = lib.gptq_packed_linear_workspace_bytes(n, r, d, bits, group, xt, perm is not None)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is None and (perm is not None or xt == 3):   # 16-bit x in order needs none
+        need = lib.gptq_packed_linear_workspace_bytes(n, r, d, bits, group, xt, perm is not None)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if workspace is not None and workspace.device != dev:
         raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
     _check(_launch(
