@@ -35,6 +35,7 @@ namespace {
 
 constexpr int PM = 128;                 // rows of W per tile (UMMA M)
 constexpr int PN = 192;                 // most tokens per tile (UMMA N)
+constexpr int PN2 = 160;                // and per accumulator where a tile has two
 constexpr int PK = 64;                  // features per box of x (one 128-byte row)
 constexpr int SK = 2 * PK;              // features per step: two boxes, eight MMAs
 constexpr int ASTAGES = 2;              // TMEM stages of A: 64 columns each
@@ -63,7 +64,8 @@ struct CodeBlock {
 
 struct ManyArgs {
   PackedArgs p;
-  int N;              // tokens per tile, a multiple of 16
+  int N;              // tokens per accumulator, a multiple of 16
+  int halves;         // accumulators per tile: 1, or 2 that share the converted weights
   int nM, nN;         // tiles
   int ctas_k;         // CTAs of a cluster, along k
   int bstages;
@@ -250,6 +252,31 @@ __device__ __forceinline__ uint32_t safe_exponent(uint32_t top) {
   return min(max(top >> 23, 1u), 253u);
 }
 
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(__half *p, float v) { *p = __float2half_rn(v); }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// One accumulator of a warp's 32 rows, `count` tokens from t0, to y: a lane is a
+// row, so a token's values go out 32 rows at a time.
+template <typename Y>
+__device__ __forceinline__ void write_tile(uint32_t base, int count, float f, float bias,
+                                           const float *x_scales, int64_t t0, bool live, Y *y,
+                                           int64_t stride) {
+  for (int c0 = 0; c0 < count; c0 += 16) {
+    float v[16];
+    tmem_ld_32x32b_x16(base + c0, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (c0 + i < count) {
+        const float s = x_scales ? f * __ldg(x_scales + t0 + c0 + i) : f;
+        if (live) put(y, fmaf(v[i], s, bias));
+        y += stride;
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
@@ -316,8 +343,9 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       uint32_t phase = 0, issued = 0, issued_par = 0;
       bool ok = true;
       for (int t = cta; t < tiles && ok; t += ctas) {
-        const int n0 = (t / a.nM) * N;
-        for (int ks = ks0; ks < ks1; ++ks) {
+        const int n0 = (t / a.nM) * (N * a.halves);
+        for (int q = ks0 * a.halves; q < ks1 * a.halves; ++q) {
+          const int ks = a.halves == 2 ? q >> 1 : q, h = a.halves == 2 ? q & 1 : 0;
           if (*(volatile int *)&sh.abort) {
             ok = false;
             break;
@@ -332,8 +360,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
           // feature offsets: multiples of 64 16-bit values = 128 bytes (past d: zeros)
           uint8_t *dst = smem + (size_t)stage * bstage_bytes;
-          tma_load_2d(dst, &tmX, ks * SK, n0, &sh.full_b[stage]);
-          tma_load_2d(dst + box_bytes, &tmX, ks * SK + PK, n0, &sh.full_b[stage]);
+          tma_load_2d(dst, &tmX, ks * SK, n0 + h * N, &sh.full_b[stage]);
+          tma_load_2d(dst + box_bytes, &tmX, ks * SK + PK, n0 + h * N, &sh.full_b[stage]);
           if (++stage == a.bstages) {
             stage = 0;
             phase ^= 1;
@@ -354,48 +382,45 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       const uint32_t box = (uint32_t)box_bytes >> 4;
       uint64_t bdesc = first;
       int bstage = 0;
-      uint32_t bphase = 0, aphase = 0, abuf = 0, cphase = 0;
-      bool ok = true;
-      auto step = [&](uint32_t dt, int j, uint32_t acc) {
-        if (!mbar_wait_bounded(&sh.full_b[bstage], bphase) ||
-            !mbar_wait_bounded(&sh.full_a[j], (aphase >> j) & 1u)) {
-          many_timeout(a.status, sh);
-          ok = false;
-          return;
-        }
-        tc_fence_after();
-        const uint32_t ad = tmem + TM_A + j * (SK / 2);
-        umma_f16_ts(dt, ad, bdesc, idesc, acc);
+      uint32_t bphase = 0, aphase = 0, abuf = 0, cphase = 0;   // aphase, cphase: a bit per stage
+      for (int t = cta; t < tiles; t += ctas) {
+        for (int ks = ks0; ks < ks1; ++ks) {
+          const int j = (ks - ks0) & 1;
+          if (!mbar_wait_bounded(&sh.full_a[j], (aphase >> j) & 1u)) goto gave_up;
+          aphase ^= 1u << j;
+          const uint32_t ad = tmem + TM_A + j * (SK / 2);
+          for (int h = 0; h < a.halves; ++h) {
+            const uint32_t buf = a.halves == 2 ? h : abuf;
+            if (ks == ks0 && !mbar_wait_bounded(&sh.acc_empty[buf], ((cphase >> buf) & 1u) ^ 1u))
+              goto gave_up;
+            if (!mbar_wait_bounded(&sh.full_b[bstage], bphase)) goto gave_up;
+            tc_fence_after();
+            const uint32_t dt = tmem + buf * PN;
+            umma_f16_ts(dt, ad, bdesc, idesc, ks > ks0 ? 1u : 0u);
 #pragma unroll
-        for (int kk = 1; kk < 4; ++kk) umma_f16_ts(dt, ad + kk * 8, bdesc + kk * 2, idesc, 1u);
+            for (int kk = 1; kk < 4; ++kk) umma_f16_ts(dt, ad + kk * 8, bdesc + kk * 2, idesc, 1u);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_f16_ts(dt, ad + 32 + kk * 8, bdesc + box + kk * 2, idesc, 1u);
-        umma_commit(&sh.empty_b[bstage]);
-        umma_commit(&sh.empty_a[j]);
-        aphase ^= 1u << j;
-        bdesc += 2 * box;
-        if (++bstage == a.bstages) {
-          bstage = 0;
-          bphase ^= 1;
-          bdesc = first;
+            for (int kk = 0; kk < 4; ++kk)
+              umma_f16_ts(dt, ad + 32 + kk * 8, bdesc + box + kk * 2, idesc, 1u);
+            umma_commit(&sh.empty_b[bstage]);
+            if (ks == ks1 - 1) {
+              umma_commit(&sh.acc_full[buf]);
+              cphase ^= 1u << buf;
+            }
+            bdesc += 2 * box;
+            if (++bstage == a.bstages) {
+              bstage = 0;
+              bphase ^= 1;
+              bdesc = first;
+            }
+          }
+          umma_commit(&sh.empty_a[j]);
         }
-      };
-      for (int t = cta; t < tiles && ok; t += ctas) {
-        if (!mbar_wait_bounded(&sh.acc_empty[abuf], cphase ^ 1)) {
-          many_timeout(a.status, sh);
-          break;
-        }
-        tc_fence_after();
-        const uint32_t dt = tmem + abuf * PN;
-        for (int ks = ks0; ks < ks1 && ok; ks += BLK) {
-          step(dt, 0, ks > ks0 ? 1u : 0u);
-          if (ok && ks + 1 < ks1) step(dt, 1, 1u);
-        }
-        if (!ok) break;
-        umma_commit(&sh.acc_full[abuf]);
         abuf ^= 1;
-        if (abuf == 0) cphase ^= 1;
+      }
+      if (false) {
+      gave_up:
+        many_timeout(a.status, sh);
       }
       umma_commit(&sh.drain);
       (void)mbar_wait_bounded(&sh.drain, 0);
@@ -572,49 +597,54 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     const int lrow = quarter * 32 + lane;
     uint32_t abuf = 0, cphase = 0;
     float *part = reinterpret_cast<float *>(smem);   // split k: [N][PM] sums of this CTA
-    for (int t = cta; t < tiles; t += ctas) {
+    bool ok = true;
+    for (int t = cta; t < tiles && ok; t += ctas, abuf ^= 1) {
       const int64_t row = (int64_t)(t % a.nM) * PM + lrow;
-      const int64_t t0 = (int64_t)(t / a.nM) * N;
+      const bool live = row < a.p.r;
       float f = 1.f;
       if constexpr (HALF) {
-        const float *srow = a.p.scales + (row < a.p.r ? row : a.p.r - 1) * a.p.G;
+        const float *srow = a.p.scales + (live ? row : a.p.r - 1) * a.p.G;
         const int ga = group_of(a, ks0 * (SK / 32)), gb = group_of(a, min(ks1 * (SK / 32), a.p.d / 32) - 1);
         uint32_t top = 0;
 #pragma unroll 4
         for (int g = ga; g <= gb; ++g) top = max(top, __float_as_uint(__ldg(srow + g)) & 0x7FFFFFFFu);
         f = __uint_as_float(safe_exponent(top) << 23);
       }
-      bool ok = mbar_wait_bounded(&sh.acc_full[abuf], cphase);
-      if (!ok && lane == 0) many_timeout(a.status, sh);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const float bias = a.p.bias && row < a.p.r ? load_as_float(a.p.bias, a.p.ytype, row) : 0.f;
-      const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + abuf * PN;
-      for (int c0 = 0; c0 < N; c0 += 16) {
-        float v[16];
-        tmem_ld_32x32b_x16(base + c0, v);
-        tmem_wait_ld();
+      const float bias = a.p.bias && live ? load_as_float(a.p.bias, a.p.ytype, row) : 0.f;
+      for (int h = 0; h < a.halves; ++h) {
+        const uint32_t buf = a.halves == 2 ? h : abuf;
+        ok = mbar_wait_bounded(&sh.acc_full[buf], (cphase >> buf) & 1u);
+        if (!ok && lane == 0) many_timeout(a.status, sh);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        cphase ^= 1u << buf;
+        tc_fence_after();
+        const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + buf * PN;
+        const int64_t t0 = ((int64_t)(t / a.nM) * a.halves + h) * N;
+        // tokens of this accumulator that exist
+        const int count = (int)(a.p.n - t0 < N ? (a.p.n - t0 > 0 ? a.p.n - t0 : 0) : N);
         if (a.ctas_k > 1) {
+          for (int c0 = 0; c0 < N; c0 += 16) {
+            float v[16];
+            tmem_ld_32x32b_x16(base + c0, v);
+            tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) part[(c0 + i) * PM + lrow] = v[i] * f;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int64_t tok = t0 + c0 + i;
-            if (tok < a.p.n && row < a.p.r) {
-              float y = v[i] * f;
-              if (a.p.x_scales) y *= __ldg(a.p.x_scales + tok);
-              store_float(a.p.y, a.p.ytype, tok * a.p.r + row, y + bias);
-            }
+            for (int i = 0; i < 16; ++i) part[(c0 + i) * PM + lrow] = v[i] * f;
           }
+        } else if (a.p.ytype == GPTQ_F32) {
+          write_tile(base, count, f, bias, a.p.x_scales, t0, live,
+                     static_cast<float *>(a.p.y) + t0 * a.p.r + row, a.p.r);
+        } else if (a.p.ytype == GPTQ_F16) {
+          write_tile(base, count, f, bias, a.p.x_scales, t0, live,
+                     static_cast<__half *>(a.p.y) + t0 * a.p.r + row, a.p.r);
+        } else {
+          write_tile(base, count, f, bias, a.p.x_scales, t0, live,
+                     static_cast<__nv_bfloat16 *>(a.p.y) + t0 * a.p.r + row, a.p.r);
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.acc_empty[abuf]);
-      abuf ^= 1;
-      if (abuf == 0) cphase ^= 1;
     }
   }
 
@@ -679,27 +709,30 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
   const int sms = num_sms();
   const int64_t nM = (p.r + PM - 1) / PM;
   const int steps = (p.d + SK - 1) / SK;
-  // Tokens per tile: all of them when they fit; else the width that wastes
-  // least, a round of tiles over the SMs costing N tokens of MMAs (or the
-  // conversion of the weights, about as long as 104 tokens').
-  int N = (int)((p.n + 15) / 16 * 16);
+  // Tokens per tile: all of them when they fit one accumulator; else the width
+  // that wastes least.  A step of a tile takes its MMAs, about 4.7 clocks per
+  // token, or the conversion of its weights, about 2250 (measured), whichever is
+  // longer; two accumulators halve the conversions.
+  int N = (int)((p.n + 15) / 16 * 16), halves = 1;
   if (p.n > PN) {
     int64_t best = INT64_MAX;
-    for (int c = PN; c >= 96; c -= 16) {
-      const int64_t rounds = (nM * ((p.n + c - 1) / c) + sms - 1) / sms;
-      const int64_t cost = rounds * (c > 104 ? c : 104);
-      if (cost < best) best = cost, N = c;
-    }
+    for (int h = 1; h <= 2; ++h)
+      for (int c = h == 1 ? PN : PN2; c >= 80; c -= 16) {
+        const int64_t rounds = (nM * ((p.n + c * h - 1) / (c * h)) + sms - 1) / sms;
+        const int64_t mma = c * h * 47 / 10, cost = rounds * (mma > 2250 ? mma : 2250);
+        if (cost < best) best = cost, N = c, halves = h;
+      }
   }
-  const int64_t nN = (p.n + N - 1) / N;
+  const int64_t nN = (p.n + N * halves - 1) / (N * halves);
   if (nM * nN > INT32_MAX / 8) return GPTQ_ERR_INVALID_ARG;
   a.N = N;
+  a.halves = halves;
   a.nM = (int)nM;
   a.nN = (int)nN;
   const int64_t tiles = nM * nN;
   // k split over a cluster while SMs stay idle and a CTA keeps two blocks
   int ck = 1;
-  while (ck < 8 && tiles * (ck + 1) <= sms && steps >= 2 * BLK * (ck + 1)) ++ck;
+  while (halves == 1 && ck < 8 && tiles * (ck + 1) <= sms && steps >= 2 * BLK * (ck + 1)) ++ck;
   a.ctas_k = ck;
   const int stage = N * SK * 2;
   using C = CodeBlock<BITS>;

@@ -117,6 +117,8 @@ SHAPES = [
     (24, 130, 1152, 4, 128), (31, 255, 96, 8, 32), (33, 128, 2080, 2, 32), (64, 384, 512, 3, 128),
     (65, 129, 1056, 4, 96), (100, 1, 128, 4, -1), (128, 520, 320, 8, 64), (129, 127, 4096, 4, 128),
     (257, 300, 192, 3, 64), (300, 640, 1024, 2, 128), (520, 260, 736, 4, 32),
+    # tiles of two accumulators; the last tile's second one partly and wholly past the tokens
+    (1203, 4100, 288, 4, 32), (1100, 4100, 64, 3, -1), (1203, 4100, 416, 8, 416),
 ]
 IDS = ["n{}_r{}_d{}_b{}_g{}".format(*s) for s in SHAPES]
 
