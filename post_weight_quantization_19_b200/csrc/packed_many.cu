@@ -109,6 +109,13 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// True in one thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ void many_timeout(int *status, ManyShared &sh) {
   atomicCAS(status, 0, (int)GPTQ_ERR_TIMEOUT);
   *(volatile int *)&sh.abort = 1;
@@ -373,58 +380,68 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- the MMAs
-    if (lane == 0) {
-      // One thread issues everything, so the loop is kept short: descriptors
-      // advance by constants (16-byte units) and a step is eight MMAs.
-      const uint32_t fmt = HALF ? 0u : 1u;
-      const uint32_t idesc = instr_desc(fmt, fmt, 0, 0, PM, N);
-      const uint64_t first = smem_desc(smem_u32(smem), 16, 1024, 2);
-      const uint32_t box = (uint32_t)box_bytes >> 4;
-      uint64_t bdesc = first;
-      int bstage = 0;
-      uint32_t bphase = 0, aphase = 0, abuf = 0, cphase = 0;   // aphase, cphase: a bit per stage
-      for (int t = cta; t < tiles; t += ctas) {
-        for (int ks = ks0; ks < ks1; ++ks) {
-          const int j = (ks - ks0) & 1;
-          if (!mbar_wait_bounded(&sh.full_a[j], (aphase >> j) & 1u)) goto gave_up;
-          aphase ^= 1u << j;
-          const uint32_t ad = tmem + TM_A + j * (SK / 2);
-          for (int h = 0; h < a.halves; ++h) {
-            const uint32_t buf = a.halves == 2 ? h : abuf;
-            if (ks == ks0 && !mbar_wait_bounded(&sh.acc_empty[buf], ((cphase >> buf) & 1u) ^ 1u))
-              goto gave_up;
-            if (!mbar_wait_bounded(&sh.full_b[bstage], bphase)) goto gave_up;
-            tc_fence_after();
-            const uint32_t dt = tmem + buf * PN;
-            umma_f16_ts(dt, ad, bdesc, idesc, ks > ks0 ? 1u : 0u);
+    // The whole warp walks the loop, so that what the MMAs take (tensor-memory
+    // addresses, descriptors) stays in uniform registers, and one elected thread
+    // issues them; with a lone thread in the loop each MMA cost 60 clocks to
+    // issue, as long as 120 tokens take to multiply.  Descriptors advance by
+    // constants (16-byte units); a step is eight MMAs per accumulator.
+    const uint32_t fmt = HALF ? 0u : 1u;
+    const uint32_t idesc = instr_desc(fmt, fmt, 0, 0, PM, N);
+    const uint64_t first = smem_desc(smem_u32(smem), 16, 1024, 2);
+    const uint32_t box = (uint32_t)box_bytes >> 4;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const bool two = a.halves == 2;
+    uint64_t bdesc = first;
+    int bstage = 0;
+    uint32_t bphase = 0, aphase = 0, abuf = 0, cphase = 0;   // aphase, cphase: a bit per stage
+    bool ok = true;
+    // the MMAs of one step and accumulator
+    auto issue = [&](uint32_t buf, int j, bool fresh, bool last, bool frees_a) {
+      if (fresh) ok = mbar_wait_bounded(&sh.acc_empty[buf], ((cphase >> buf) & 1u) ^ 1u);
+      ok = ok && mbar_wait_bounded(&sh.full_b[bstage], bphase);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t dt = tm + buf * PN, ad = tm + TM_A + j * (SK / 2);
+        umma_f16_ts(dt, ad, bdesc, idesc, fresh ? 0u : 1u);
 #pragma unroll
-            for (int kk = 1; kk < 4; ++kk) umma_f16_ts(dt, ad + kk * 8, bdesc + kk * 2, idesc, 1u);
+        for (int kk = 1; kk < 4; ++kk) umma_f16_ts(dt, ad + kk * 8, bdesc + kk * 2, idesc, 1u);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_f16_ts(dt, ad + 32 + kk * 8, bdesc + box + kk * 2, idesc, 1u);
-            umma_commit(&sh.empty_b[bstage]);
-            if (ks == ks1 - 1) {
-              umma_commit(&sh.acc_full[buf]);
-              cphase ^= 1u << buf;
-            }
-            bdesc += 2 * box;
-            if (++bstage == a.bstages) {
-              bstage = 0;
-              bphase ^= 1;
-              bdesc = first;
-            }
-          }
-          umma_commit(&sh.empty_a[j]);
-        }
-        abuf ^= 1;
+        for (int kk = 0; kk < 4; ++kk)
+          umma_f16_ts(dt, ad + 32 + kk * 8, bdesc + box + kk * 2, idesc, 1u);
+        umma_commit(&sh.empty_b[bstage]);
+        if (frees_a) umma_commit(&sh.empty_a[j]);
+        if (last) umma_commit(&sh.acc_full[buf]);
       }
-      if (false) {
-      gave_up:
-        many_timeout(a.status, sh);
+      __syncwarp();
+      if (last) cphase ^= 1u << buf;
+      bdesc += 2 * box;
+      if (++bstage == a.bstages) {
+        bstage = 0;
+        bphase ^= 1;
+        bdesc = first;
       }
+    };
+    for (int t = cta; t < tiles && ok; t += ctas, abuf ^= 1) {
+      for (int ks = ks0; ks < ks1 && ok; ++ks) {
+        const int j = (ks - ks0) & 1;
+        const bool fresh = ks == ks0, last = ks == ks1 - 1;
+        ok = mbar_wait_bounded(&sh.full_a[j], (aphase >> j) & 1u);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        aphase ^= 1u << j;
+        issue(two ? 0u : abuf, j, fresh, last, !two);
+        if (two && ok) issue(1u, j, fresh, last, true);
+      }
+    }
+    if (!ok && lane == 0) many_timeout(a.status, sh);
+    __syncwarp();
+    if (elect_one()) {
       umma_commit(&sh.drain);
       (void)mbar_wait_bounded(&sh.drain, 0);
     }
+    __syncwarp();
   } else if (warp < 4) {
     // ---------------------------------------------------------------- codes to shared memory
     const int id = threadIdx.x - 64;
