@@ -674,18 +674,28 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       const float *part = reinterpret_cast<const float *>(smem);
       const int64_t m0 = (int64_t)(cta % a.nM) * PM, t0 = (int64_t)(cta / a.nM) * N;
       const int c0 = N * crank / a.ctas_k, c1 = N * (crank + 1) / a.ctas_k;
-      for (int i = c0 * PM + threadIdx.x; i < c1 * PM; i += MANY_THREADS) {
-        const int64_t tok = t0 + i / PM, row = m0 + i % PM;
+      // four rows of a token at a time, every CTA's share asked for before any is used
+      for (int i = c0 * (PM / 4) + threadIdx.x; i < c1 * (PM / 4); i += MANY_THREADS) {
+        const int64_t tok = t0 + i / (PM / 4), row = m0 + i % (PM / 4) * 4;
         if (tok >= a.p.n || row >= a.p.r) continue;
-        float y = 0.f;
-        for (int k = 0; k < a.ctas_k; ++k) {
-          float o;
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(cluster_addr(part + i, k)));
-          y += o;
+        float4 o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k < a.ctas_k)
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(o[k].x), "=f"(o[k].y), "=f"(o[k].z), "=f"(o[k].w)
+                         : "r"(cluster_addr(part + i * 4, k)));
         }
-        if (a.p.x_scales) y *= __ldg(a.p.x_scales + tok);
-        if (a.p.bias) y += load_as_float(a.p.bias, a.p.ytype, row);
-        store_float(a.p.y, a.p.ytype, tok * a.p.r + row, y);
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[0] += o[k].x, y[1] += o[k].y, y[2] += o[k].z, y[3] += o[k].w;
+        const float s = a.p.x_scales ? __ldg(a.p.x_scales + tok) : 1.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (row + q < a.p.r)
+            store_float(a.p.y, a.p.ytype, tok * a.p.r + row + q,
+                        fmaf(y[q], s, a.p.bias ? load_as_float(a.p.bias, a.p.ytype, row + q) : 0.f));
       }
     }
     __syncwarp();
@@ -728,15 +738,15 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
   const int steps = (p.d + SK - 1) / SK;
   // Tokens per tile: all of them when they fit one accumulator; else the width
   // that wastes least.  A step of a tile takes its MMAs, about 4.7 clocks per
-  // token, or the conversion of its weights, about 2250 (measured), whichever is
-  // longer; two accumulators halve the conversions.
+  // token, or the conversion of its weights, about 1000 (both measured), whichever
+  // is longer; two accumulators halve the conversions.
   int N = (int)((p.n + 15) / 16 * 16), halves = 1;
   if (p.n > PN) {
     int64_t best = INT64_MAX;
     for (int h = 1; h <= 2; ++h)
       for (int c = h == 1 ? PN : PN2; c >= 80; c -= 16) {
         const int64_t rounds = (nM * ((p.n + c * h - 1) / (c * h)) + sms - 1) / sms;
-        const int64_t mma = c * h * 47 / 10, cost = rounds * (mma > 2250 ? mma : 2250);
+        const int64_t mma = c * h * 47 / 10, cost = rounds * (mma > 1000 ? mma : 1000);
         if (cost < best) best = cost, N = c, halves = h;
       }
   }
