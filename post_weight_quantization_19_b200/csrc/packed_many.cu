@@ -2,10 +2,10 @@
 // tensor cores, the weights dequantised on their way into tensor memory.
 //
 // One CTA per tile of 128 rows of W and N <= 192 tokens.  The weights are the
-// MMA's A operand, in tensor memory: two loader warps bring blocks of 128 rows x
-// 256 columns of codes to shared memory (cp.async, whole lines per row; threads
-// that each copied their own row's 32 bytes spent a tag lookup per 16 bytes and
-// ran at half this speed), and thread i of a converter warpgroup, which owns
+// MMA's A operand, in tensor memory: TMA brings blocks of 128 rows x 256 columns
+// of codes to shared memory (rows that are not multiples of 16 bytes: cp.async;
+// threads that each copied their own row's 32 bytes ran at half the speed), and
+// thread i of a converter warpgroup, which owns
 // row i, turns 64 columns of it into 16-bit weights and writes them to its TMEM
 // lane (tcgen05.st).  x is the B operand: tiles of
 // 64 features x N tokens that TMA places in 128-byte-swizzled shared memory.
@@ -21,7 +21,7 @@
 //   the row's sums multiplied by it again, so scales outside fp16's range lose
 //   nothing.
 //
-// Warp 0 issues TMA, warp 1 the MMAs (one thread each), warps 2-3 load codes;
+// Warp 0 issues TMA, warp 1 the MMAs (one thread each), warps 2-3 load codes, scales and zeros;
 // warps 4-19 are four converter warpgroups, one for each 64 columns of a block;
 // warps 20-23 drain one of two accumulators while the other fills.  With fewer tiles than SMs the k
 // range is split over a cluster, whose CTAs add their sums through distributed
@@ -43,21 +43,29 @@ constexpr int MAXB = 6;                 // shared-memory stages of x at most
 constexpr uint32_t TM_A = 2 * PN;       // TMEM column of the first A stage
 constexpr int WGS = 4;                  // converter warpgroups
 constexpr int MANY_THREADS = 32 * (4 + 4 * WGS + 4);
-constexpr size_t MANY_SMEM = 224 * 1024;   // x and codes, after alignment
+constexpr size_t MANY_SMEM = 222 * 1024;   // x and codes, after alignment
 
 constexpr int BLK = 2;                  // steps per block of codes; a warpgroup takes half a step
 constexpr int BCOLS = BLK * SK;         // its columns
 constexpr int LOADERS = 64;
 static_assert(ASTAGES == BLK && WGS == 2 * BLK, "step j of a block uses A stage j");
 
-// A block of codes in shared memory: rows padded by 16 bytes (the 8 rows that
-// a quarter-warp's 16-byte reads touch fall on different banks), then scales
-// [sub][row] and zeros [sub][row] of its `subs` parts of equal group.
+// A block of codes in shared memory, as TMA lays it down: boxes of 128 rows x up
+// to 128 bytes, 16-byte chunks exchanged inside 128 bytes (TMA's 128- and 64-byte
+// swizzles) so that the rows that a quarter-warp reads at once fall on different
+// banks; 3-bit rows of 96 bytes have no swizzle.  Then scales [sub][row] and
+// zeros [sub][row] of its `subs` parts of equal group.
 template <int BITS>
 struct CodeBlock {
   static constexpr int ROW = BCOLS * BITS / 8;      // bytes of a row
-  static constexpr int PITCH = ROW + 16;
-  static constexpr int CODES = PM * PITCH;
+  static constexpr int BOX = ROW < 128 ? ROW : 128; // of it in a box
+  static constexpr int CODES = PM * ROW;
+  // place of byte `col` (16-byte chunks move as one) of a row
+  static __device__ __forceinline__ uint32_t place(int row, int col) {
+    if constexpr (BITS == 3) return row * ROW + col;
+    const int c = (col % BOX) >> 4, x = BOX == 128 ? row & 7 : (row >> 1) & 3;
+    return (col / BOX) * (PM * BOX) + row * BOX + ((c ^ x) << 4) + (col & 15);
+  }
   static constexpr int DEPTH = BITS == 8 ? 2 : 3;
   static __host__ __device__ constexpr int bytes(int subs) { return CODES + PM * 8 * subs; }
 };
@@ -84,6 +92,7 @@ struct ManyShared {
   uint32_t tmem_base;
   int abort;
   uint32_t exponent[2][PM];   // fp16: row_exponent of a tile's rows
+  alignas(16) uint4 stage[4][32];   // results on their way out, per warp
 };
 
 // D[tmem] (+)= A[tmem] * B[smem], 16-bit operands, fp32 accumulate.
@@ -263,23 +272,42 @@ __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__half *p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-// One accumulator of a warp's 32 rows, `count` tokens from t0, to y: a lane is a
-// row, so a token's values go out 32 rows at a time.
+// One accumulator of a warp's 32 rows, `count` tokens from t0, to y.  A lane is a
+// row; 16-bit results go through 512 bytes of shared memory, eight tokens of 32
+// rows at a time, and out 16 bytes per lane (where y's rows allow it), for
+// storing them as they lie cost 100 clocks a token.
 template <typename Y>
 __device__ __forceinline__ void write_tile(uint32_t base, int count, float f, float bias,
-                                           const float *x_scales, int64_t t0, bool live, Y *y,
-                                           int64_t stride) {
+                                           const float *x_scales, int64_t t0, int64_t row,
+                                           const PackedArgs &p, uint4 *stage, int lane) {
+  Y *y = static_cast<Y *>(p.y) + t0 * p.r + row;
+  const bool live = row < p.r;
+  bool wide = false;
+  if constexpr (sizeof(Y) == 2)
+    wide = p.r % 8 == 0 && row - lane + 32 <= p.r && reinterpret_cast<uintptr_t>(p.y) % 16 == 0;
+  Y *yw = y - lane + (lane & 3) * 8 + (int64_t)(lane >> 2) * p.r;   // this lane's 8 rows of token lane / 4
   for (int c0 = 0; c0 < count; c0 += 16) {
     float v[16];
     tmem_ld_32x32b_x16(base + c0, v);
+    const float mine = x_scales && c0 + lane < count ? __ldg(x_scales + t0 + c0 + (lane & 15)) : 1.f;
     tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (c0 + i < count) {
-        const float s = x_scales ? f * __ldg(x_scales + t0 + c0 + i) : f;
-        if (live) put(y, fmaf(v[i], s, bias));
-        y += stride;
+    for (int i = 0; i < 16; ++i)
+      v[i] = fmaf(v[i], f * (x_scales ? __shfl_sync(0xffffffffu, mine, i) : 1.f), bias);
+    if (wide) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) put(reinterpret_cast<Y *>(stage) + i * 32 + lane, v[h * 8 + i]);
+        __syncwarp();
+        if (c0 + h * 8 + (lane >> 2) < count)
+          *reinterpret_cast<uint4 *>(yw + (int64_t)(c0 + h * 8) * p.r) = stage[lane];
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (live && c0 + i < count) put(y + (int64_t)(c0 + i) * p.r, v[i]);
     }
   }
 }
@@ -295,7 +323,8 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int byt
 
 template <int BITS, typename T>
 __global__ void __launch_bounds__(MANY_THREADS, 1)
-    packed_many_kernel(const __grid_constant__ CUtensorMap tmX, const ManyArgs a) {
+    packed_many_kernel(const __grid_constant__ CUtensorMap tmX,
+                       const __grid_constant__ CUtensorMap tmW, const ManyArgs a) {
   constexpr bool HALF = Pair<T>::M == 0x64006400u;
   using C = CodeBlock<BITS>;
   extern __shared__ uint8_t dyn_smem[];
@@ -322,7 +351,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       mbar_init(&sh.empty_a[s], 1);
     }
     for (int c = 0; c < C::DEPTH; ++c) {
-      mbar_init(&sh.full_c[c], LOADERS);
+      mbar_init(&sh.full_c[c], LOADERS + 1);
       mbar_init(&sh.empty_c[c], 4 * WGS);
     }
     for (int b = 0; b < 2; ++b) {
@@ -333,6 +362,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     sh.abort = 0;
     fence_mbar_init();
     prefetch_tmap(&tmX);
+    if (a.aligned) prefetch_tmap(&tmW);
   }
   if (warp == 1) {
     tmem_alloc(&sh.tmem_base, 512);
@@ -468,13 +498,12 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         const char *src = q0 + k0 * BITS / 8;
         // rows past the last and columns past the row are filled with zeros
         if (a.aligned) {
-          constexpr int PPR = C::ROW / 16;
-#pragma unroll 4
-          for (int i = 0; i < PM * PPR / LOADERS; ++i) {
-            const int p = id + LOADERS * i, row = p / PPR, col = p % PPR * 16;
-            const bool in = row < rows && col < valid;
-            cp_async16(dst + row * C::PITCH + col, in ? src + row * pitch + col : src,
-                       in ? min(16, valid - col) : 0);
+          if (id == 0) {
+            mbar_arrive_expect_tx(&sh.full_c[slot], C::CODES);
+#pragma unroll
+            for (int x = 0; x < C::ROW; x += C::BOX)   // multiples of 16 bytes from multiples of 32 codes
+              tma_load_2d(smem + a.bstages * bstage_bytes + slot * block_bytes + x * PM, &tmW,
+                          kb * C::ROW + x, (int)m0, &sh.full_c[slot]);
           }
         } else {
           constexpr int PPR = C::ROW / 4;
@@ -482,8 +511,9 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           for (int i = 0; i < PM * PPR / LOADERS; ++i) {
             const int p = id + LOADERS * i, row = p / PPR, col = p % PPR * 4;
             const bool in = row < rows && col < valid;
-            cp_async4(dst + row * C::PITCH + col, in ? src + row * pitch + col : src, in ? 4 : 0);
+            cp_async4(dst + C::place(row, col), in ? src + row * pitch + col : src, in ? 4 : 0);
           }
+          if (id == 0) mbar_arrive(&sh.full_c[slot]);
         }
         for (int sub = 0; sub < a.subs; ++sub) {
           const int g = group_of(a, min(kb * (BCOLS / 32) + sub * (BCOLS / 32 / a.subs), a.p.d / 32 - 1));
@@ -526,14 +556,14 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         // PM / (4 WGS) rows, lanes along the groups
         const int ga = group_of(a, ks0 * (SK / 32)), gb = group_of(a, min(ks1 * (SK / 32), a.p.d / 32) - 1);
         constexpr int EACH = PM / (4 * WGS);
-        uint32_t top[EACH];
+        const int64_t m0 = (int64_t)(t % a.nM) * PM + (warp - 4) * EACH;
+        uint32_t top[EACH] = {};
+        for (int g = ga + lane; g <= gb; g += 32) {
 #pragma unroll
-        for (int i = 0; i < EACH; ++i) {
-          const int64_t at = (int64_t)(t % a.nM) * PM + (warp - 4) * EACH + i;
-          const float *srow = a.p.scales + (at < a.p.r ? at : a.p.r - 1) * a.p.G;
-          top[i] = 0;
-          for (int g = ga + lane; g <= gb; g += 32)
-            top[i] = max(top[i], __float_as_uint(__ldg(srow + g)) & 0x7FFFFFFFu);
+          for (int i = 0; i < EACH; ++i) {
+            const int64_t row = m0 + i < a.p.r ? m0 + i : a.p.r - 1;
+            top[i] = max(top[i], __float_as_uint(__ldg(a.p.scales + row * a.p.G + g)) & 0x7FFFFFFFu);
+          }
         }
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
@@ -552,20 +582,21 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (kb * BLK + as < ks1) {
-          const uint32_t src = ring + slot * block_bytes + lrow * C::PITCH + wg * (PK * BITS / 8);
+          const uint32_t src = ring + slot * block_bytes;
+          const int col = wg * (PK * BITS / 8);
           const uint32_t sz = ring + slot * block_bytes + C::CODES + lrow * 4;
           uint32_t w[2 * BITS];
           if constexpr (BITS == 3) {
 #pragma unroll
             for (int i = 0; i < 6; i += 2)
               asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                           : "=r"(w[i]), "=r"(w[i + 1]) : "r"(src + i * 4));
+                           : "=r"(w[i]), "=r"(w[i + 1]) : "r"(src + C::place(lrow, col + i * 4)));
           } else {
 #pragma unroll
             for (int i = 0; i < 2 * BITS; i += 4)
               asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                           : "r"(src + i * 4));
+                           : "r"(src + C::place(lrow, col + i * 4)));
           }
           float s;
           int z;
@@ -649,14 +680,12 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
             for (int i = 0; i < 16; ++i) part[(c0 + i) * PM + lrow] = v[i] * f;
           }
         } else if (a.p.ytype == GPTQ_F32) {
-          write_tile(base, count, f, bias, a.p.x_scales, t0, live,
-                     static_cast<float *>(a.p.y) + t0 * a.p.r + row, a.p.r);
+          write_tile<float>(base, count, f, bias, a.p.x_scales, t0, row, a.p, sh.stage[quarter], lane);
         } else if (a.p.ytype == GPTQ_F16) {
-          write_tile(base, count, f, bias, a.p.x_scales, t0, live,
-                     static_cast<__half *>(a.p.y) + t0 * a.p.r + row, a.p.r);
+          write_tile<__half>(base, count, f, bias, a.p.x_scales, t0, row, a.p, sh.stage[quarter], lane);
         } else {
-          write_tile(base, count, f, bias, a.p.x_scales, t0, live,
-                     static_cast<__nv_bfloat16 *>(a.p.y) + t0 * a.p.r + row, a.p.r);
+          write_tile<__nv_bfloat16>(base, count, f, bias, a.p.x_scales, t0, row, a.p, sh.stage[quarter],
+                                    lane);
         }
         tc_fence_before();
         __syncwarp();
@@ -693,9 +722,24 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         const float s = a.p.x_scales ? __ldg(a.p.x_scales + tok) : 1.f;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (row + q < a.p.r)
-            store_float(a.p.y, a.p.ytype, tok * a.p.r + row + q,
-                        fmaf(y[q], s, a.p.bias ? load_as_float(a.p.bias, a.p.ytype, row + q) : 0.f));
+          y[q] = fmaf(y[q], s, a.p.bias && row + q < a.p.r ? load_as_float(a.p.bias, a.p.ytype, row + q) : 0.f);
+        const int64_t at = tok * a.p.r + row;
+        if (a.p.ytype != GPTQ_F32 && a.p.r % 4 == 0 && reinterpret_cast<uintptr_t>(a.p.y) % 8 == 0) {
+          uint2 w;
+          if (a.p.ytype == GPTQ_F16) {
+            const __half2 lo = __floats2half2_rn(y[0], y[1]), hi = __floats2half2_rn(y[2], y[3]);
+            w = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+          } else {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(y[0], y[1]);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(y[2], y[3]);
+            w = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+          }
+          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.p.y) + at) = w;
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (row + q < a.p.r) store_float(a.p.y, a.p.ytype, at + q, y[q]);
+        }
       }
     }
     __syncwarp();
@@ -757,9 +801,19 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
   a.nM = (int)nM;
   a.nN = (int)nN;
   const int64_t tiles = nM * nN;
-  // k split over a cluster while SMs stay idle and a CTA keeps two blocks
+  // k split over a cluster: the number of CTAs along it whose rounds over the SMs
+  // take least, a CTA costing its steps and about ten more to start, fill and
+  // add up (at least two blocks of codes each)
   int ck = 1;
-  while (halves == 1 && ck < 8 && tiles * (ck + 1) <= sms && steps >= 2 * BLK * (ck + 1)) ++ck;
+  if (halves == 1) {
+    int64_t best = INT64_MAX;
+    for (int c = 1; c <= 8 && (c == 1 || steps >= 2 * BLK * c); ++c) {
+      // (one CTA walks several tiles without starting again; a split one does not)
+      const int64_t rounds = (tiles * c + sms - 1) / sms, each = (steps + c - 1) / c;
+      const int64_t cost = c == 1 ? rounds * each + 10 : rounds * (each + 12);
+      if (cost < best) best = cost, ck = c;
+    }
+  }
   a.ctas_k = ck;
   const int stage = N * SK * 2;
   using C = CodeBlock<BITS>;
@@ -791,6 +845,21 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
     set_last_error_msg(__FILE__, __LINE__, "cuTensorMapEncodeTiled rejected the activations");
     return GPTQ_ERR_CUDA;
   }
+  // codes as bytes; rows on 16-byte boundaries
+  CUtensorMap tw = tx;
+  if (a.aligned) {
+    const cuuint64_t wdim[2] = {(cuuint64_t)p.d * BITS / 8, (cuuint64_t)p.r};
+    const cuuint64_t wstride[1] = {(cuuint64_t)p.d * BITS / 8};
+    const cuuint32_t wbox[2] = {(cuuint32_t)C::BOX, (cuuint32_t)PM};
+    if (enc(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint32_t *>(p.qweight), wdim, wstride,
+            wbox, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            BITS == 3 ? CU_TENSOR_MAP_SWIZZLE_NONE
+                      : (C::BOX == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B),
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+      set_last_error_msg(__FILE__, __LINE__, "cuTensorMapEncodeTiled rejected the packed weights");
+      return GPTQ_ERR_CUDA;
+    }
+  }
   static std::atomic<bool> attr[64] = {};
   if (const int rc = ensure_smem_attr(packed_many_kernel<BITS, T>, MANY_SMEM + 1024, attr)) return rc;
   cudaLaunchAttribute at[1];
@@ -805,7 +874,7 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
   cfg.attrs = at;
   cfg.numAttrs = ck > 1 ? 1 : 0;
   count_launch();
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, packed_many_kernel<BITS, T>, tx, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, packed_many_kernel<BITS, T>, tx, tw, a);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     set_last_error(__FILE__, __LINE__, "kernel launch", e);
