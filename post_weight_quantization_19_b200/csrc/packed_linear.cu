@@ -12,6 +12,8 @@
 // (packed_few.cuh); beyond, by conversion and then by the tensor cores
 // (packed_many.cu).  This file checks the arguments, brings x into the
 // layer's column order and, for many tokens, 8-bit codes into fp16.
+#include <type_traits>
+
 #include "packed_linear.h"
 
 namespace gptq {
@@ -20,31 +22,43 @@ namespace {
 constexpr int FEW_TOKENS = 16;   // up to here warp-level products are faster
 
 // x in the layer's column order: out[t, j] = x[t, perm[j]], entries outside
-// [0, d) clamped.  One CTA per token (8 n d or 6 n d bytes, from L2 for few).
-template <typename T>
-__global__ void __launch_bounds__(256) gather_columns_kernel(const T *__restrict__ x,
-                                                             const int32_t *__restrict__ perm, int d,
-                                                             T *__restrict__ out) {
-  const int64_t row = (int64_t)blockIdx.x * d;
-  for (int j = threadIdx.x; j < d; j += blockDim.x)
-    out[row + j] = x[row + min(max(__ldg(perm + j), 0), d - 1)];
-}
+// [0, d) clamped; WIDEN: 8-bit codes as fp16 (exact), the operand of the
+// tensor-core product, in that order if perm is given.  A thread takes eight
+// columns of one token; the columns are spread over the grid so that a few
+// tokens fill the GPU.  Up to 8 bytes per element, from L2 for few tokens.
+constexpr int GATHER_THREADS = 128;
 
-// 8-bit codes as fp16 (exact), in the layer's column order if perm is given:
-// the operand of the tensor-core product.  3 n d bytes.
-__global__ void __launch_bounds__(256) widen_codes_kernel(const int8_t *__restrict__ x,
-                                                          const int32_t *__restrict__ perm, int d,
-                                                          __half *__restrict__ out) {
-  const int64_t row = (int64_t)blockIdx.x * d;
-  for (int j = threadIdx.x * 2; j < d; j += blockDim.x * 2) {
-    int a = j, b = j + 1;
-    if (perm) {
-      a = min(max(__ldg(perm + j), 0), d - 1);
-      b = min(max(__ldg(perm + j + 1), 0), d - 1);
-    }
-    *reinterpret_cast<__half2 *>(out + row + j) =
-        __halves2half2(__short2half_rn(x[row + a]), __short2half_rn(x[row + b]));
+template <typename T, bool WIDEN>
+__global__ void __launch_bounds__(GATHER_THREADS)
+    gather_columns_kernel(const T *__restrict__ x, const int32_t *__restrict__ perm, int d,
+                          void *__restrict__ out) {
+  using O = typename std::conditional<WIDEN, uint16_t, T>::type;
+  const int j0 = (blockIdx.y * GATHER_THREADS + threadIdx.x) * 8;
+  if (j0 >= d) return;   // d % 8 == 0
+  const T *row = x + (int64_t)blockIdx.x * d;
+  alignas(16) T v[8];
+  if (perm) {
+    int c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = __ldg(perm + j0 + i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __ldg(row + min(max(c[i], 0), d - 1));
+  } else {
+    *reinterpret_cast<uint2 *>(v) = __ldg(reinterpret_cast<const uint2 *>(row + j0));   // WIDEN only
   }
+  alignas(16) O o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (WIDEN)
+      o[i] = __half_as_ushort(__short2half_rn((short)(signed char)v[i]));
+    else
+      o[i] = v[i];
+  }
+  O *dst = static_cast<O *>(out) + (int64_t)blockIdx.x * d + j0;
+  if constexpr (sizeof(O) == 2)
+    *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(o);
+  else
+    *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(o);
 }
 
 bool valid_packed(int64_t n, int64_t r, int64_t d, int bits, int group, int xtype) {
@@ -89,21 +103,21 @@ extern "C" int gptq_packed_linear(const void *x, int xtype, const float *x_scale
   const size_t need = gptq_packed_linear_workspace_bytes(n, r, d, bits, group, xtype, perm != nullptr);
   if (need > 0 && (!workspace || workspace_bytes < need)) return GPTQ_ERR_NO_MEMORY;
   cudaStream_t st = (cudaStream_t)stream;
-  if (xtype == GPTQ_I8 && n > FEW_TOKENS) {
-    widen_codes_kernel<<<(unsigned)n, 256, 0, st>>>(static_cast<const int8_t *>(x), perm, (int)d,
-                                                    static_cast<__half *>(workspace));
-    GPTQ_LAUNCH_CHECK();
-    x = workspace;
-    xtype = GPTQ_F16;
-  } else if (perm) {
-    if (xtype == GPTQ_I8)
-      gather_columns_kernel<<<(unsigned)n, 256, 0, st>>>(static_cast<const uint8_t *>(x), perm, (int)d,
-                                                         static_cast<uint8_t *>(workspace));
+  const bool widen = xtype == GPTQ_I8 && n > FEW_TOKENS;
+  if (widen || perm) {
+    const dim3 grid((unsigned)n, (unsigned)((d / 8 + GATHER_THREADS - 1) / GATHER_THREADS));
+    if (widen)
+      gather_columns_kernel<uint8_t, true><<<grid, GATHER_THREADS, 0, st>>>(
+          static_cast<const uint8_t *>(x), perm, (int)d, workspace);
+    else if (xtype == GPTQ_I8)
+      gather_columns_kernel<uint8_t, false><<<grid, GATHER_THREADS, 0, st>>>(
+          static_cast<const uint8_t *>(x), perm, (int)d, workspace);
     else
-      gather_columns_kernel<<<(unsigned)n, 256, 0, st>>>(static_cast<const uint16_t *>(x), perm, (int)d,
-                                                         static_cast<uint16_t *>(workspace));
+      gather_columns_kernel<uint16_t, false><<<grid, GATHER_THREADS, 0, st>>>(
+          static_cast<const uint16_t *>(x), perm, (int)d, workspace);
     GPTQ_LAUNCH_CHECK();
     x = workspace;
+    if (widen) xtype = GPTQ_F16;
   }
   const PackedArgs a{x, x_scales, reinterpret_cast<const uint32_t *>(qweight), scales, zeros,
                      bias, y, n, r, (int)d, bits, group, group < 0 ? 1 : (int)(d / group), xtype, ytype};
