@@ -298,7 +298,7 @@ int gptq_linear_fp16(const void *X, int64_t n, int64_t d, const void *W16, int64
  *            (not written) and may be x or residual itself.
  *   gamma    device [d] of `dtype`, 16-byte aligned.
  *   n, d     n >= 0, d > 0, d % 32 == 0, d <= 65536.
- *   eps      > 0 and finite.
+ *   eps      in [1e-30, 1e30].
  *   perm     device int32 [d] or NULL: codes and xhat are written in the order
  *            of gptq_regroup, entry j taken from column perm[j] (entries
  *            outside [0, d) are clamped to it).  h keeps the order of x.
@@ -308,12 +308,14 @@ int gptq_linear_fp16(const void *X, int64_t n, int64_t d, const void *W16, int64
  *            h, x or residual only when it is NULL; the outputs must not
  *            overlap each other.
  *   A row with a NaN or an infinity has scale NaN, codes 0 and xhat NaN; other
- *   rows are not touched by it.  Sums in fp32; a row whose squares leave the
- *   fp32 range is summed again with scaled values.
+ *   rows are not touched by it.  The codes are those of the formula in 64 bits
+ *   (where u / scale is a tie but for their rounding: one of its neighbours); the
+ *   scale's sum is in fp32, and a row whose squares leave the fp32 range is
+ *   summed again with scaled values (its codes are then decided in fp32).
  *   n == 0: nothing to do.  Asynchronous: one kernel.
  */
 int gptq_rmsnorm_int8(const void *x, const void *residual, const void *gamma, int dtype,
-                      int64_t n, int64_t d, float eps, const int32_t *perm, void *h,
+                      int64_t n, int64_t d, double eps, const int32_t *perm, void *h,
                       int8_t *codes, float *scales, void *xhat, gptq_stream_t stream);
 
 /*

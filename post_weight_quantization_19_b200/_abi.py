@@ -18,8 +18,8 @@ STATUS = {
     5: "GPTQ_ERR_TIMEOUT",
 }
 
-c_void_p, c_int, c_int64, c_float, c_size_t = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
-                                              ctypes.c_float, ctypes.c_size_t)
+c_void_p, c_int, c_int64, c_float, c_double, c_size_t = (
+    ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_double, ctypes.c_size_t)
 
 # name -> (restype, argtypes); mirrors include/gptq.h one to one.
 SIGNATURES = {
@@ -44,7 +44,7 @@ SIGNATURES = {
     "gptq_dequant_fp16": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int,
                                   c_int, c_void_p, c_void_p]),
     "gptq_linear_fp16": (c_int, [c_void_p, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_void_p]),
-    "gptq_rmsnorm_int8": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int64, c_int64, c_float,
+    "gptq_rmsnorm_int8": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int64, c_int64, c_double,
                                   c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     "gptq_packed_linear_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64, c_int, c_int,
                                                       c_int, c_int]),

@@ -12,6 +12,15 @@
 // the writing of the codes, so every input is read once and every output
 // written once: n d (2 [+ 2 residual] + 1 [+ 2 h] [+ 2 xhat]) bytes.  One CTA
 // per row, one barrier for both sums (rows of up to 2048: one warp per row).
+// Codes are those of the formula in 64 bits: gamma h is exact in fp32 (a product of
+// two 16-bit numbers), so 127 gamma h / max|gamma h| in fp32 decides every code
+// that is not within 2e-5 of a border k + 1/2, and there the sign of 127 gamma h -
+// (k + 1/2) max|gamma h| does, each product taken with its exact rounding error
+// (fma).  Exact ties are real (half of the row's maximum lies at 63.5) and go to
+// the even code.  At 0.5, 1.5 and 2.5, where a step is most of the value, a tie
+// follows u / scale as it comes out in 64 bits instead, with scale = max|u| (1 /
+// 127), so that the result does not depend on who computes it: about one row in
+// 300 of 4096 columns.  That part comes last, when the row's registers are free.
 // Sums and scales in fp32; a row whose squares or products leave the safe fp32
 // range (bf16 values above 1e19) is gathered again from the registers with
 // values scaled by a power of two.
@@ -57,7 +66,7 @@ struct NormArgs {
   void *xhat;
   int64_t n;
   int d;
-  float eps;
+  double eps;
 };
 
 // sum of v and maximum of the non-negative m over the row's threads, in every
@@ -82,6 +91,29 @@ __device__ __forceinline__ void row_reduce(float &v, float &m, float2 *part) {
   m = __uint_as_float(mb);
 }
 
+// sum, or maximum of non-negative values, over the row's threads in 64 bits
+template <bool WARP_ROW>
+__device__ double row_reduce64(double v, bool largest, double *part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const double w = __shfl_xor_sync(0xffffffffu, v, o);
+    v = largest ? fmax(v, w) : v + w;
+  }
+  if constexpr (!WARP_ROW) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    __syncthreads();
+    if (lane == 0) part[warp] = v;
+    __syncthreads();
+    v = lane < nw ? part[lane] : 0.0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double w = __shfl_xor_sync(0xffffffffu, v, o);
+      v = largest ? fmax(v, w) : v + w;
+    }
+  }
+  return v;
+}
+
 __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
   // |value| <= 127 by construction up to one rounding of the quotient; the
   // conversion saturates to [-128, 127]
@@ -92,10 +124,78 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
   return r;
 }
 
+// 127 p against the border nearest to u = 127 p / top: the code, as a float (the
+// even one on the border), and whether p lies on one of the first borders exactly.
+__device__ __forceinline__ float near_code(float p, float top, float u, bool &tie) {
+  const float border = floorf(u) + 0.5f;
+  const float a = 127.f * p, ea = fmaf(127.f, p, -a);            // 127 p = a + ea
+  const float b = border * top, eb = fmaf(border, top, -b);      // border top = b + eb
+  const float over = (a - b) + (ea - eb);                        // a and b are close: a - b is exact
+  if (over == 0.f) {
+    tie |= fabsf(border) < 3.f;
+    return rintf(border);
+  }
+  return over > 0.f ? border + 0.5f : border - 0.5f;
+}
+
+// The row's ties, decided by u / scale formed in 64 bits and written over the
+// codes (and xhat), which the row's threads have stored: two elements at a
+// time, h from where it was written or from its terms.
+template <typename T, bool WARP_ROW>
+__device__ __forceinline__ void settle_ties(const NormArgs &a, int64_t row, int tid, int nt, float top,
+                                            float inv, float scale, int8_t *crow, T *xh,
+                                            double *part) {
+  const int words = a.d / 2;
+  const uint32_t *hsrc = reinterpret_cast<const uint32_t *>(a.h ? a.h : a.x) + row * words;
+  const uint32_t *res =
+      a.h || !a.residual ? nullptr : reinterpret_cast<const uint32_t *>(a.residual) + row * words;
+  const uint32_t *gam = reinterpret_cast<const uint32_t *>(a.gamma);
+  auto load = [&](int k) {
+    uint32_t v = hsrc[k];
+    if (res) {
+      const float2 f = Cvt<T>::up(v), e = Cvt<T>::up(__ldg(res + k));
+      v = Cvt<T>::down(f.x + e.x, f.y + e.y);
+    }
+    return Cvt<T>::up(v);
+  };
+  double acc = 0.0;
+#pragma unroll 4
+  for (int k = tid; k < words; k += nt) {
+    const float2 h = load(k);
+    acc += (double)h.x * h.x + (double)h.y * h.y;
+  }
+  const double root = sqrt(row_reduce64<WARP_ROW>(acc, false, part) / a.d + a.eps);
+  acc = 0.0;
+#pragma unroll 1
+  for (int k = tid; k < words; k += nt) {
+    const float2 h = load(k), g = Cvt<T>::up(__ldg(gam + k));
+    if (fabsf(h.x * g.x) == top) acc = fmax(acc, fabs((double)h.x / root * (double)g.x));
+    if (fabsf(h.y * g.y) == top) acc = fmax(acc, fabs((double)h.y / root * (double)g.y));
+  }
+  const double step = row_reduce64<WARP_ROW>(acc, true, part) * (1.0 / 127.0);
+#pragma unroll 1
+  for (int k = tid; k < words; k += nt) {
+    const float2 h = load(k), g = Cvt<T>::up(__ldg(gam + k));
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      const float x = i ? h.y : h.x, y = i ? g.y : g.x, u = x * y * inv;
+      bool tie = false;
+      if (fabsf(u - rintf(u)) > 0.49998f) (void)near_code(x * y, top, u, tie);
+      if (tie) {
+        const float code = (float)rint((double)x / root * (double)y / step);
+        crow[2 * k + i] = (int8_t)code;   // |code| <= 127
+        if (xh) xh[2 * k + i] = Cvt<T>::one(scale * code);
+      }
+    }
+  }
+}
+
 template <typename T, int V, bool WARP_ROW>
-__global__ void __launch_bounds__(WARP_ROW ? 256 : 1024) rmsnorm_int8_kernel(NormArgs a) {
+// (40 registers let 1536 threads share an SM; the ties' part spills, not the rest)
+__global__ void __maxnreg__(WARP_ROW ? 128 : V <= 2 ? 40 : 64) rmsnorm_int8_kernel(const NormArgs a) {
   extern __shared__ __align__(16) int8_t row_codes[];   // perm: [rows of the CTA][d]
   __shared__ float2 part[32];
+  __shared__ double part64[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tid = WARP_ROW ? lane : (int)threadIdx.x;
   const int nt = WARP_ROW ? 32 : (int)blockDim.x;
@@ -176,46 +276,70 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : 1024) rmsnorm_int8_kernel(Nor
     scale = 1.f;
     inv = 0.f;
   } else if (ps == 1.f && pt == 1.f) {
-    scale = top / (127.f * sqrtf(ss / (float)a.d + a.eps));
+    scale = top / (127.f * sqrtf(ss / (float)a.d + (float)a.eps));
     inv = 127.f / top;
   } else {
     const double mean = (double)ss / a.d / ps / ps;
-    scale = (float)((double)top / pt / (127.0 * sqrt(mean + (double)a.eps)));
+    scale = (float)((double)top / pt / (127.0 * sqrt(mean + a.eps)));
     inv = 127.f / top;
   }
   const bool lost = scale != scale;
+  const bool plain = !lost && ps == 1.f && pt == 1.f && inv > 0.f;
   if (tid == 0) a.scales[row] = scale;
+  // ---- the codes, eight of a vector in two words
+  uint2 c[V];
+  bool tie = false;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int k = tid + v * nt;
+    c[v] = make_uint2(0, 0);
+    if (k < nvec) {
+      const uint4 gv = __ldg(gam + k);
+      const uint32_t p[4] = {hv[v].x, hv[v].y, hv[v].z, hv[v].w};
+      const uint32_t q[4] = {gv.x, gv.y, gv.z, gv.w};
+      float u[8], far = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = Cvt<T>::up(p[i]), g = Cvt<T>::up(q[i]);
+        u[2 * i] = lost ? 0.f : f.x * pt * g.x * inv;
+        u[2 * i + 1] = lost ? 0.f : f.y * pt * g.y * inv;
+        far = fmaxf(far, fmaxf(fabsf(u[2 * i] - rintf(u[2 * i])), fabsf(u[2 * i + 1] - rintf(u[2 * i + 1]))));
+      }
+      if (plain && far > 0.49998f) {   // a border is near
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = Cvt<T>::up(p[i / 2]), g = Cvt<T>::up(q[i / 2]);
+          if (fabsf(u[i] - rintf(u[i])) > 0.49998f)
+            u[i] = near_code((i & 1) ? f.y * g.y : f.x * g.x, top, u[i], tie);
+        }
+      }
+      c[v].x = pack4(u[0], u[1], u[2], u[3]);
+      c[v].y = pack4(u[4], u[5], u[6], u[7]);
+    }
+  }
   int8_t *crow = a.perm ? row_codes + (WARP_ROW ? (size_t)warp * a.d : 0) : a.codes + row * a.d;
   uint4 *xh = a.perm ? nullptr : reinterpret_cast<uint4 *>(a.xhat);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int k = tid + v * nt;
     if (k < nvec) {
-      const uint4 gv = __ldg(gam + k);
-      const uint32_t p[4] = {hv[v].x, hv[v].y, hv[v].z, hv[v].w};
-      const uint32_t q[4] = {gv.x, gv.y, gv.z, gv.w};
-      float u[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = Cvt<T>::up(p[i]), g = Cvt<T>::up(q[i]);
-        u[2 * i] = lost ? 0.f : f.x * pt * g.x * inv;
-        u[2 * i + 1] = lost ? 0.f : f.y * pt * g.y * inv;
-      }
-      uint2 c;
-      c.x = pack4(u[0], u[1], u[2], u[3]);
-      c.y = pack4(u[4], u[5], u[6], u[7]);
-      *reinterpret_cast<uint2 *>(crow + (size_t)k * 8) = c;
+      *reinterpret_cast<uint2 *>(crow + (size_t)k * 8) = c[v];
       if (xh) {
         uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t w = i < 2 ? c.x : c.y;
+          const uint32_t w = i < 2 ? c[v].x : c[v].y;
           const int s0 = (i & 1) * 16;
           o[i] = Cvt<T>::down(scale * (float)(int8_t)(w >> s0), scale * (float)(int8_t)(w >> (s0 + 8)));
         }
         xh[row * nvec + k] = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
+  }
+  if (WARP_ROW ? __any_sync(0xffffffffu, tie) : __syncthreads_or(tie)) {   // the codes are stored
+    if constexpr (WARP_ROW) __syncwarp();
+    settle_ties<T, WARP_ROW>(a, row, tid, nt, top, inv, scale, crow,
+                             xh ? reinterpret_cast<T *>(xh + row * nvec) : nullptr, part64);
   }
   if (a.perm) {
     if constexpr (WARP_ROW)
@@ -272,12 +396,12 @@ int launch_norm_t(const NormArgs &a, cudaStream_t st) {
 using namespace gptq;
 
 extern "C" int gptq_rmsnorm_int8(const void *x, const void *residual, const void *gamma, int dtype,
-                                 int64_t n, int64_t d, float eps, const int32_t *perm, void *h,
+                                 int64_t n, int64_t d, double eps, const int32_t *perm, void *h,
                                  int8_t *codes, float *scales, void *xhat, gptq_stream_t stream) {
   if (dtype != GPTQ_F16 && dtype != GPTQ_BF16) return GPTQ_ERR_INVALID_ARG;
   if (n < 0 || n > (int64_t)INT32_MAX) return GPTQ_ERR_INVALID_ARG;
   if (d <= 0 || d % 32 != 0 || d > 65536) return GPTQ_ERR_INVALID_ARG;
-  if (!(eps > 0.f) || !(eps < 3.0e38f)) return GPTQ_ERR_INVALID_ARG;
+  if (!(eps >= 1e-30) || !(eps <= 1e30)) return GPTQ_ERR_INVALID_ARG;
   if (n == 0) return GPTQ_OK;
   if (!x || !gamma || !codes || !scales) return GPTQ_ERR_INVALID_ARG;
   for (const void *p : {x, residual, gamma, (const void *)h, (const void *)codes, (const void *)xhat})

@@ -19,9 +19,10 @@ bf16 2^-8, fp32 2^-24, relative to the value):
       of at most u (about 0.8 u expected: 1/sqrt(3) for the weights, the same
       for y).
   norm   scale: a sum of squares through at most 128 additions and five more
-      operations, 140 2^-24 relative.  A code may differ, by one, only where
-      u / scale lies within 127 * 16 * 2^-24 of a half.  h and xhat follow
-      from the outputs' definition bit for bit.
+      operations, 140 2^-24 relative.  A code may differ, by one, only where u /
+      scale lies within 1e-12 of a half (its value in 64 bits is good to 127 * 8
+      2^-53 < 1e-12), or within 127 * 16 * 2^-24 in rows that leave the fp32
+      range.  h and xhat follow from the outputs' definition bit for bit.
 """
 
 import numpy as np
@@ -296,7 +297,7 @@ def test_packed_linear_streams_graphs_and_repeats(n, kind, perm):
 
 # ------------------------------------------------------------------ the norm
 
-def assert_norm(x, res, gamma, out, eps=EPS, perm=None, T=None):
+def assert_norm(x, res, gamma, out, eps=EPS, perm=None, near=1e-12):
     n, d = x.shape
     T = x.dtype
     h = x if res is None else (x.float() + res.float()).to(T)
@@ -316,7 +317,7 @@ def assert_norm(x, res, gamma, out, eps=EPS, perm=None, T=None):
             v = v[:, perm]
         assert np.abs(got - codes).max() <= 1
         off = np.abs(np.abs(v[diff]) % 1 - 0.5)
-        assert off.max() <= 127 * 16 * 2.0 ** -24
+        assert off.max() <= near
     if "xhat" in out:
         assert torch.equal(out["xhat"], (out["codes"].float() * out["scales"][:, None]).to(T))
 
@@ -370,11 +371,38 @@ def test_rmsnorm_int8_hard_rows(d):
         assert np.isnan(s[bad]) and not c[bad].any()
         assert bool(torch.isnan(out["xhat"][bad]).all())
     good = [0, 3, 4, 5, 6, 7]
-    assert_norm(x[good], None, gamma, {k: v[good] for k, v in out.items()})
+    assert_norm(x[good], None, gamma, {k: v[good] for k, v in out.items()}, near=127 * 16 * 2.0 ** -24)
     perm = torch.arange(d, dtype=torch.int32, device="cuda")
     perm[0], perm[1] = -9, d + 5
     p = g.gptq_rmsnorm_int8(x, gamma, eps=EPS, perm=perm)
     assert torch.equal(p["codes"], out["codes"][:, perm.long().clamp(0, d - 1)])
+
+
+@pytest.mark.parametrize("d", [512, 4096])
+def test_rmsnorm_int8_ties(d):
+    # values in steps of 1/254 of the maximum: every second one is a tie and goes to the
+    # even code, but at 0.5, 1.5 and 2.5 as the formula's last bits in 64 bits say
+    # (scale = max|u| (1 / 127)); the sums of squares are exact.  Also with h over
+    # x, and in another column order
+    import post_weight_quantization_19_b200 as g
+    rng = np.random.default_rng(d)
+    x = (rng.integers(-254, 255, size=(64, d)) / 2).astype(np.float32)
+    x[:, 0] = 127
+    x = torch.from_numpy(x).to(F16).cuda()
+    gamma = torch.full((d,), 2.0, dtype=F16, device="cuda")
+    out = g.gptq_rmsnorm_int8(x, gamma, eps=EPS)
+    h = f64(x)
+    u = h / np.sqrt((h * h).mean(1, keepdims=True) + EPS) * 2.0
+    scale = np.abs(u).max(1, keepdims=True) * (1.0 / 127)
+    codes = np.where(np.abs(h) < 3, np.round(u / scale), np.round(h))
+    np.testing.assert_array_equal(out["codes"].cpu().numpy(), codes)
+    x2, half = x.clone() * 0.5, x.clone() * 0.5
+    again = g.gptq_rmsnorm_int8(x2, gamma, eps=EPS, residual=half, xhat=True, outputs={"h": x2})
+    assert torch.equal(again["codes"], out["codes"])
+    assert torch.equal(again["xhat"], (out["codes"].float() * out["scales"][:, None]).to(F16))
+    perm = torch.randperm(d, device="cuda").to(torch.int32)
+    p = g.gptq_rmsnorm_int8(half, gamma, eps=EPS, residual=half, perm=perm)
+    assert torch.equal(p["codes"], out["codes"][:, perm.long()])
 
 
 def test_rmsnorm_int8_streams_and_graph():

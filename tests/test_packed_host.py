@@ -26,7 +26,7 @@ def norm(lib, x=P, res=P, gamma=P, dtype=F16, n=4, d=64, eps=1e-5, perm=None, h=
 def test_rmsnorm_refusals(lib):
     for bad in (dict(dtype=F32), dict(dtype=I8), dict(dtype=-1), dict(n=-1), dict(n=1 << 31),
                 dict(d=0), dict(d=40), dict(d=65568), dict(eps=0.0), dict(eps=-1.0),
-                dict(eps=float("nan")), dict(eps=float("inf")), dict(x=None), dict(gamma=None),
+                dict(eps=float("nan")), dict(eps=float("inf")), dict(eps=1e-31), dict(eps=1e31), dict(x=None), dict(gamma=None),
                 dict(codes=None), dict(scales=None), dict(x=ODD), dict(res=ODD), dict(gamma=ODD),
                 dict(h=ODD), dict(codes=ODD), dict(xhat=ODD), dict(scales=ODD2), dict(perm=ODD2),
                 dict(xhat=P)):
