@@ -510,3 +510,54 @@ def test_norm_and_products_of_a_solved_layer(n, act):
     for y, v in ((y8, x8), (y16, f64(natural["xhat"]))):
         parts = 24 / (d / 32 + 128) * (np.abs(v) @ np.broadcast_to(wq, w.shape).T)
         assert_product(y, v @ w.T, np.abs(v) @ np.abs(w).T + parts, d, wtype=F16)
+
+
+@pytest.mark.parametrize("act", [False, True])
+def test_chain_with_norms_runs_on_its_codes(act):
+    # Two normed layers and a plain one: each layer's inputs, codes and next inputs
+    # are those its own results define, and the layer's loss is the oracle's on
+    # the same inputs (the single-layer tolerance).
+    import post_weight_quantization_19_b200 as g
+    from parity_util import assert_codes_close
+    from synth import make_activations, make_weights
+    bits, group, n = 4, 64, 2500
+    shapes = [(384, 256), (128, 384), (64, 128)]
+    Ws = [make_weights(rr, dd, seed=41 + i) for i, (rr, dd) in enumerate(shapes)]
+    gammas = [(1 + 0.2 * torch.randn(dd, device="cuda")).to(F16) for _, dd in shapes[:2]] + [None]
+    X0 = torch.from_numpy(make_activations(n, 256, seed=40)).cuda()
+    out = g.quantize_chain(X0, [torch.from_numpy(np.ascontiguousarray(W, dtype=np.float32)).cuda()
+                                for W in Ws], bits=bits, group=group, act_order=act,
+                           keep_inputs=True, norms=gammas, eps=EPS)
+    X = X0
+    for k, (o, W) in enumerate(zip(out, Ws)):
+        d = W.shape[1]
+        q = o["qweight"].cpu().numpy()
+        if gammas[k] is not None:
+            assert_norm(X, None, gammas[k], {"codes": o["in_codes"], "scales": o["in_scales"],
+                                             "xhat": o["inputs"]})
+        else:
+            assert torch.equal(o["inputs"], X) and "in_codes" not in o
+        if k == 0:
+            ref = oracle.gptq_quantize_layer(W, oracle.hessian(o["inputs"].cpu().numpy()), bits=bits,
+                                             group=group, act_order=act)
+            assert_codes_close(oracle.unpack_rows(q, bits, d), ref["codes"])
+            assert abs(o["loss"] - ref["loss"]) <= 5e-3 * ref["loss"]
+        nxt = out[k + 1]["inputs"] if k == 1 else (None if k == 0 else o["outputs"])
+        if gammas[k] is not None and nxt is not None:   # the plain layer's inputs: the product itself
+            s, z = o["scales"].cpu().numpy(), o["zeros"].cpu().numpy()
+            codes = oracle.unpack_rows(q, bits, d)
+            gi = o["g_idx"].cpu().numpy()
+            w = s.astype(np.float64)[:, gi] * (codes - z[:, gi])
+            v = f64(o["in_codes"]) * f64(o["in_scales"])[:, None]
+            assert_product(nxt, v @ w.T, np.abs(v) @ np.abs(w).T, d, wtype=F16)
+        if k == 0:   # the next layer's norm was taken of the product
+            s, z = o["scales"].cpu().numpy(), o["zeros"].cpu().numpy()
+            codes = oracle.unpack_rows(q, bits, d)
+            gi = o["g_idx"].cpu().numpy()
+            w = s.astype(np.float64)[:, gi] * (codes - z[:, gi])
+            v = f64(o["in_codes"]) * f64(o["in_scales"])[:, None]
+            args = (o["qweight_by_group"] if act else o["qweight"], o["scales"], o["zeros"], bits, group)
+            X = g.gptq_packed_linear(o["in_codes"], *args, x_scales=o["in_scales"], perm=o.get("perm"))
+            assert_product(X, v @ w.T, np.abs(v) @ np.abs(w).T, d, wtype=F16)
+        else:
+            X = nxt

@@ -123,3 +123,80 @@ def test_oracle_regroup_pins():
     a = oracle.dequant_gemv(oracle.pack_rows(codes, bits), s, z, bits, group, x, g_idx=g_idx)
     b = oracle.dequant_gemv(oracle.pack_rows(out, bits), s, z, bits, group, x[:, perm])
     np.testing.assert_allclose(a, b, rtol=1e-12)
+
+
+@pytest.mark.parametrize("act,static,group", [(False, False, 32), (True, False, 32), (True, True, 32),
+                                              (True, False, -1)])
+def test_chain_driver_with_norms(monkeypatch, act, static, group):
+    # A normed layer: norm to 8 bits, H from the codes' values, solve, columns by
+    # group under act-order, product from the codes -- with the entry points played
+    # by the oracle, equal to the steps written out.
+    from post_weight_quantization_19_b200 import chain
+    from synth import make_activations, make_weights
+    bits, eps = 4, 1e-5
+    exact, calls = {}, []
+
+    def hessian(X, H, stream=None):
+        exact[H.data_ptr()] = oracle.hessian(X.numpy())
+
+    def quantize_layer(W, H, *, bits, group, block, damp, act_order, sym, static_groups, g_idx,
+                       stream=None):
+        o = oracle.gptq_quantize_layer(W.numpy(), exact.pop(H.data_ptr()), bits=bits, group=group,
+                                       block=block, damp=damp, act_order=act_order, sym=sym,
+                                       static_groups=static_groups)
+        g_idx.copy_(torch.from_numpy(o["g_idx"]))
+        return {"qweight": torch.from_numpy(oracle.pack_rows(o["codes"], bits)),
+                "scales": torch.from_numpy(o["scales"]), "zeros": torch.from_numpy(o["zeros"]),
+                "loss": o["loss"], "g_idx": g_idx}
+
+    def rmsnorm(x, gamma, *, eps, xhat, stream=None):
+        c, s = oracle.rmsnorm_int8(x.numpy(), gamma.numpy(), eps)
+        s = s.astype(np.float32)
+        return {"codes": torch.from_numpy(c.astype(np.int8)), "scales": torch.from_numpy(s),
+                "xhat": torch.from_numpy((c * s[:, None]).astype(np.float16))}
+
+    def regroup(qweight, g_idx, bits, group, stream=None):
+        calls.append("regroup")
+        d = g_idx.numel()
+        c, perm = oracle.regroup(oracle.unpack_rows(qweight.numpy(), bits, d), g_idx.numpy())
+        return torch.from_numpy(oracle.pack_rows(c, bits)), torch.from_numpy(perm.astype(np.int32))
+
+    def product(x, qweight, scales, zeros, bits, group, *, x_scales, perm, stream=None):
+        v = x.numpy().astype(np.float64) * x_scales.numpy()[:, None]
+        if perm is not None:
+            v = v[:, perm.numpy()]
+        y = oracle.dequant_gemv(qweight.numpy(), scales.numpy(), zeros.numpy(), bits, group, v)
+        return torch.from_numpy(y.astype(np.float16))
+
+    for name, f in (("gptq_hessian_accumulate", hessian), ("gptq_quantize_layer", quantize_layer),
+                    ("gptq_rmsnorm_int8", rmsnorm), ("gptq_regroup", regroup),
+                    ("gptq_packed_linear", product)):
+        monkeypatch.setattr(chain, name, f)
+    X = make_activations(500, 64, seed=5)
+    Ws = [make_weights(96, 64, seed=6), make_weights(32, 96, seed=7)]
+    gammas = [np.linspace(0.5, 1.5, 64).astype(np.float16), np.ones(96, dtype=np.float16)]
+    got = chain.quantize_chain(torch.from_numpy(X), [torch.from_numpy(W) for W in Ws], bits=bits,
+                               group=group, act_order=act, static_groups=static, keep_inputs=True,
+                               norms=[torch.from_numpy(v) for v in gammas], eps=eps)
+    for k, (W, gamma) in enumerate(zip(Ws, gammas)):
+        c, s = oracle.rmsnorm_int8(X, gamma, eps)
+        s = s.astype(np.float32)
+        xhat = (c * s[:, None]).astype(np.float16)
+        np.testing.assert_array_equal(got[k]["inputs"].numpy(), xhat)
+        np.testing.assert_array_equal(got[k]["in_codes"].numpy(), c)
+        o = oracle.gptq_quantize_layer(W, oracle.hessian(xhat), bits=bits, group=group, act_order=act,
+                                       static_groups=static)
+        np.testing.assert_array_equal(got[k]["qweight"].numpy(), oracle.pack_rows(o["codes"], bits))
+        y = (c * s[:, None].astype(np.float64)) @ o["What"].T
+        X = y.astype(np.float16)
+        assert ("perm" in got[k]) == (act and group != -1 and not static)
+    np.testing.assert_allclose(got[-1]["outputs"].numpy().astype(np.float64), X.astype(np.float64),
+                               rtol=2.0 ** -10, atol=1e-6)
+    assert len(calls) == (2 if act and group != -1 and not static else 0)
+
+
+def test_chain_driver_refuses_other_counts_of_norms():
+    from post_weight_quantization_19_b200 import chain
+    with pytest.raises(ValueError):
+        chain.quantize_chain(torch.zeros((8, 64), dtype=torch.float16), [torch.zeros((32, 64))],
+                             bits=4, group=32, norms=[])
