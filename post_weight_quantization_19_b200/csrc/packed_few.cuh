@@ -200,6 +200,17 @@ constexpr float operand_base() {
   return XT == GPTQ_BF16 && BITS != 8 ? (BITS == 4 ? 16.f : BITS == 3 ? 64.f : 4.f) : 0.f;
 }
 
+// A zero point, clamped to the codes, as its group uses it: itself for 8-bit x, 2^23
+// + z for 8-bit codes with bf16, else -(B + z) (as float bits).
+template <int BITS, int XT>
+__device__ __forceinline__ uint32_t prepare_zero(uint32_t raw) {
+  const uint32_t z = (uint32_t)min(max((int)raw, 0), (1 << BITS) - 1);
+  if constexpr (XT == GPTQ_I8) return z;
+  const float f = __uint_as_float(0x4B000000u | z);   // 2^23 + z
+  if constexpr (BITS == 8 && XT == GPTQ_BF16) return __float_as_uint(f);
+  return __float_as_uint((8388608.f - operand_base<BITS, XT>()) - f);
+}
+
 // The eight codes of a unit as four pairs of operands: (0,4), (1,5), (2,6),
 // (3,7), or for 8-bit codes (0,1), (2,3), (4,5), (6,7); fp16 codes of fewer
 // bits: the second and fourth pair times 2^BITS.  zf = 2^23 + z, for 8-bit
@@ -400,6 +411,14 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
     issue(i);
     cp_commit();
   }
+  // The matrix of ones (fp16: 2^-24, the unit of its codes), as values the compiler
+  // does not see through: it would set four registers anew for every product.
+  uint32_t ones[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("mov.b32 %0, %1;"
+                 : "=r"(ones[i])
+                 : "n"(XT == GPTQ_F16 ? 0x00010001 : XT == GPTQ_BF16 ? 0x3F803F80 : 0x01010101));
   // tokens past the last: its values again (their columns are dropped)
   uint32_t xrow[NT];
 #pragma unroll
@@ -434,6 +453,13 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
       if (gi >> 2 != cblock) {
         cblock = gi >> 2;
         cslot = cslot + 1 == F::SZSLOTS ? 0 : cslot + 1;
+        // the block's zero points, made ready by the lane of their row
+        const uint32_t at = sz_ring + cslot * F::SZSLOT + ROWS * 16 + lane * 16;
+        uint4 z = lds128(at);
+        z.x = prepare_zero<BITS, XT>(z.x), z.y = prepare_zero<BITS, XT>(z.y);
+        z.z = prepare_zero<BITS, XT>(z.z), z.w = prepare_zero<BITS, XT>(z.w);
+        *reinterpret_cast<uint4 *>(__cvta_shared_to_generic(at)) = z;
+        __syncwarp();
       }
       sz = sz_ring + cslot * F::SZSLOT + (gi & 3) * 4;
     }
@@ -447,8 +473,8 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
     int ipart[2][NT][4], isx[NT][4];
     float zf[2][2] = {};
     auto zero_point = [&](int m, int h, int u) {
-      const int z = (int)lds32(sz + ROWS * 16 + (m * 16 + h * 8 + g) * 16 + (FINE ? u * 4 : 0));
-      return min(max(z, 0), (1 << BITS) - 1);
+      const uint32_t z = lds32(sz + ROWS * 16 + (m * 16 + h * 8 + g) * 16 + (FINE ? u * 4 : 0));
+      return FINE ? prepare_zero<BITS, XT>(z) : z;
     };
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -458,8 +484,11 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) zf[m][h] = 8388608.f + (float)zero_point(m, h, u);
+            for (int h = 0; h < 2; ++h) zf[m][h] = __uint_as_float(zero_point(m, h, u));
         }
+        // which pairs share a product: one choice for the codes and the ones, or x
+        // would be copied into other register pairs
+        constexpr int B1 = F::TWO || F::BASES ? 2 : 1, B2 = F::TWO || F::BASES ? 1 : 2;
         uint32_t xb[NT][4];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -472,21 +501,20 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
             xb[j][2] = __byte_perm(v.y, v.w, 0x5410), xb[j][3] = __byte_perm(v.y, v.w, 0x7632);
           }
           if constexpr (!F::EXACT) {
-            constexpr uint32_t one = XT == GPTQ_F16 ? 0x00010001u : 0x3F803F80u;   // 2^-24; 1
             if constexpr (F::BASES) {
               if (first) {
-                mma16<XT, true>(sx[j], one, one, one, one, xb[j][0], xb[j][2]);
-                mma16<XT, true>(sx2[j], one, one, one, one, xb[j][1], xb[j][3]);
+                mma16<XT, true>(sx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][2]);
+                mma16<XT, true>(sx2[j], ones[0], ones[1], ones[2], ones[3], xb[j][1], xb[j][3]);
               } else {
-                mma16<XT, false>(sx[j], one, one, one, one, xb[j][0], xb[j][2]);
-                mma16<XT, false>(sx2[j], one, one, one, one, xb[j][1], xb[j][3]);
+                mma16<XT, false>(sx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][2]);
+                mma16<XT, false>(sx2[j], ones[0], ones[1], ones[2], ones[3], xb[j][1], xb[j][3]);
               }
             } else {
               if (first)
-                mma16<XT, true>(sx[j], one, one, one, one, xb[j][0], xb[j][1]);
+                mma16<XT, true>(sx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][B1]);
               else
-                mma16<XT, false>(sx[j], one, one, one, one, xb[j][0], xb[j][1]);
-              mma16<XT, false>(sx[j], one, one, one, one, xb[j][2], xb[j][3]);
+                mma16<XT, false>(sx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][B1]);
+              mma16<XT, false>(sx[j], ones[0], ones[1], ones[2], ones[3], xb[j][B2], xb[j][3]);
             }
           }
         }
@@ -507,10 +535,10 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
               }
             } else {
               if (first)
-                mma16<XT, true>(part[m][j], pl[0], ph[0], pl[1], ph[1], xb[j][0], xb[j][1]);
+                mma16<XT, true>(part[m][j], pl[0], ph[0], pl[B1], ph[B1], xb[j][0], xb[j][B1]);
               else
-                mma16<XT, false>(part[m][j], pl[0], ph[0], pl[1], ph[1], xb[j][0], xb[j][1]);
-              mma16<XT, false>(part[m][j], pl[2], ph[2], pl[3], ph[3], xb[j][2], xb[j][3]);
+                mma16<XT, false>(part[m][j], pl[0], ph[0], pl[B1], ph[B1], xb[j][0], xb[j][B1]);
+              mma16<XT, false>(part[m][j], pl[B2], ph[B2], pl[3], ph[3], xb[j][B2], xb[j][3]);
             }
           }
         }
@@ -524,11 +552,10 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
           } else {
             xb[j][0] = v.x, xb[j][1] = v.y;
           }
-          constexpr uint32_t one = 0x01010101u;
           if (first)
-            mma8<true>(isx[j], one, one, one, one, xb[j][0], xb[j][1]);
+            mma8<true>(isx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][1]);
           else
-            mma8<false>(isx[j], one, one, one, one, xb[j][0], xb[j][1]);
+            mma8<false>(isx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][1]);
         }
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
@@ -549,7 +576,7 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
           for (int h = 0; h < 2; ++h) {
             const float f = __uint_as_float(lds32(sz + (m * 16 + h * 8 + g) * 16 + (FINE ? u * 4 : 0)));
             if constexpr (F::INT8) {
-              const int z = zero_point(m, h, u);
+              const int z = (int)zero_point(m, h, u);
 #pragma unroll
               for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -563,9 +590,7 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
                 for (int i = 0; i < 2; ++i)
                   acc[m][j][2 * h + i] = fmaf(f, part[m][j][2 * h + i], acc[m][j][2 * h + i]);
             } else {
-              // -(B + z), z in the mantissa of 2^23
-              const float z = (8388608.f - operand_base<BITS, XT>()) -
-                              __uint_as_float(0x4B000000u | (uint32_t)zero_point(m, h, u));
+              const float z = __uint_as_float(zero_point(m, h, u));   // -(B + z)
 #pragma unroll
               for (int j = 0; j < NT; ++j)
 #pragma unroll
