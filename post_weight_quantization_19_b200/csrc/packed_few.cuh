@@ -73,7 +73,7 @@ struct Few {
   __host__ __device__ static constexpr int stage_bytes(int tokens) {
     return (WBYTES + SZBYTES + tokens * XSTRIDE + 127) / 128 * 128;
   }
-  static constexpr int MAX_WARPS = 16;                            // of a CTA: 8 or 16
+  static constexpr int MAX_WARPS = 16;                            // of a CTA: 8, 12 or 16
 };
 constexpr size_t FEW_SMEM = 226 * 1024;
 
@@ -681,15 +681,15 @@ int launch_few(const PackedArgs &p, cudaStream_t st) {
   const int64_t blocks = (p.n + 8 * NT - 1) / (8 * NT);
   const int stages = (p.d + KS - 1) / KS, sms = num_sms();
   // Warps of a CTA and CTAs along k: the shape with the shortest estimate, in
-  // clocks: rounds of CTAs, each as long as its warps' stages (about 110 clocks of
-  // an SM per warp and stage, and at least 1000 of the warp) and its sums (about
-  // 500, 1500 more where CTAs add up theirs).  Measured on 4096 x
-  // 4096 and 12288 x 49152: 16 warps without a split of k beat 8 warps split
-  // over two CTAs.
-  int warps = 8, ck = 1;
+  // clocks: rounds of CTAs over the tiles, each as long as its warps' stages (480
+  // clocks and 110 more for each warp that shares the SM) and its sums (170 per
+  // warp, 1500 more where CTAs add up theirs).  Measured,
+  // one token, 4 bits: 4096 x 4096, 8 warps 5.7 us, 16 warps 6.5; 12288 x 49152, 16
+  // warps 91 us, 14 warps 96, 8 warps 116.
+  int warps = 8, ck = 1, fit = 1;   // fit: CTAs that share an SM
   size_t smem = 0;
   int64_t best = INT64_MAX;
-  for (int w = 8; w <= F::MAX_WARPS; w *= 2) {
+  for (int w = 8; w <= F::MAX_WARPS; w += 4) {
     const size_t need = (size_t)w * (F::STAGES * a.stage_bytes + F::SZWARP + RED);
     if (need > FEW_SMEM) continue;
     int res = (int)(FEW_SMEM / (need + 1024));
@@ -700,17 +700,17 @@ int launch_few(const PackedArgs &p, cudaStream_t st) {
       const int64_t ctas = tiles * blocks * c;
       const int64_t rounds = (ctas + (int64_t)sms * res - 1) / ((int64_t)sms * res);
       const int64_t busy = ctas >= (int64_t)sms * res ? res : (ctas + sms - 1) / sms;
-      const int64_t stage = 110 * w * busy > 1000 ? 110 * w * busy : 1000;
-      const int64_t cost = rounds * ((stages + w * c - 1) / (w * c) * stage + 500 + (c > 1 ? 1500 : 0)) + 3000;
-      if (cost < best) best = cost, warps = w, ck = c, smem = need;
+      const int64_t stage = 110 * w * busy + 480;
+      const int64_t cost = rounds * ((stages + w * c - 1) / (w * c) * stage + 170 * w + (c > 1 ? 1500 : 0)) + 3000;
+      if (cost <= best) best = cost, warps = w, ck = c, fit = res, smem = need;
     }
   }
   if (best == INT64_MAX) return GPTQ_ERR_INVALID_ARG;   // not reached: eight warps always fit
   a.ctas_k = ck;
   if (tiles * ck > INT32_MAX || blocks > 65535) return GPTQ_ERR_INVALID_ARG;
   // CTAs that fit at once walk the tiles
-  int64_t clusters = (int64_t)sms * (FEW_SMEM / (smem + 1024) < (size_t)(16 / warps) ? FEW_SMEM / (smem + 1024) : 16 / warps);
-  clusters = clusters / (blocks * ck) < 1 ? 1 : clusters / (blocks * ck);
+  int64_t clusters = (int64_t)sms * fit / (blocks * ck);
+  if (clusters < 1) clusters = 1;
   if (clusters > tiles) clusters = tiles;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
