@@ -370,11 +370,16 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
     // scales and zeros: lane = row
     if constexpr (FINE) {
       const uint32_t sz = base + F::WBYTES + lane * 16;
+      if (a.sz_aligned && a.p.group == 32) {
+        cp_async16(sz, a.p.scales + szrow + s * 4, 16);
+        cp_async16(sz + ROWS * 16, a.p.zeros + szrow + s * 4, 16);
+      } else {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int gi = group_of(min(s * 4 + c, d / 32 - 1));
-        cp_async4(sz + c * 4, a.p.scales + szrow + gi, 4);
-        cp_async4(sz + ROWS * 16 + c * 4, a.p.zeros + szrow + gi, 4);
+        for (int c = 0; c < 4; ++c) {
+          const int gi = group_of(min(s * 4 + c, d / 32 - 1));
+          cp_async4(sz + c * 4, a.p.scales + szrow + gi, 4);
+          cp_async4(sz + ROWS * 16 + c * 4, a.p.zeros + szrow + gi, 4);
+        }
       }
     } else {
       const int block = group_of(s * 4) >> 2;

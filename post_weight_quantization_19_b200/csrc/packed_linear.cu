@@ -8,8 +8,8 @@
 //
 //   y[t, i] = xs[t] sum_j s[i, j/g] (q[i, j] - z[i, j/g]) x[t, p(j)] + bias[i]
 //
-// Up to FEW_TOKENS tokens the product is bound by reading the packed weights
-// (packed_few.cuh); beyond, by conversion and then by the tensor cores
+// A few tokens' product is bound by reading and unpacking the weights
+// (packed_few.cuh); more tokens', by conversion and then by the tensor cores
 // (packed_many.cu).  This file checks the arguments, brings x into the
 // layer's column order and, for many tokens, 8-bit codes into fp16.
 #include <type_traits>
@@ -19,7 +19,17 @@
 namespace gptq {
 namespace {
 
-constexpr int FEW_TOKENS = 16;   // up to here warp-level products are faster
+constexpr int FEW_TOKENS = 16;   // the most that the warp-level products take
+
+// Which product: few tokens at once are bound by the weights' bytes and codes, and
+// warp-level products, which need no start-up, are faster: always up to 8
+// tokens, with 8-bit x up to 16, and with 16-bit x for layers of up to 2^25 codes.
+// Measured (warp-level, tcgen05; us): 16 tokens, 4 bits, fp16, 4096 x 4096 12.8,
+// 12.6; 9 tokens 8.9, 12.2; 8192 x 8192, 8 tokens 25.7, 25.1, 16 tokens 35.8,
+// 25.1; 16 tokens of 8-bit x, 11008 x 4096 16.2, 25.2.
+bool few_tokens(int64_t n, int64_t r, int64_t d, int xtype) {
+  return n <= 8 || (n <= FEW_TOKENS && (xtype == GPTQ_I8 || r * d <= (1 << 25)));
+}
 
 // x in the layer's column order: out[t, j] = x[t, perm[j]], entries outside
 // [0, d) clamped; WIDEN: 8-bit codes as fp16 (exact), the operand of the
@@ -79,7 +89,7 @@ using namespace gptq;
 extern "C" size_t gptq_packed_linear_workspace_bytes(int64_t n, int64_t r, int64_t d, int bits,
                                                      int group, int xtype, int permuted) {
   if (!valid_packed(n, r, d, bits, group, xtype) || n == 0 || r == 0) return 0;
-  const bool widen = xtype == GPTQ_I8 && n > FEW_TOKENS;
+  const bool widen = xtype == GPTQ_I8 && !few_tokens(n, r, d, xtype);
   if (!permuted && !widen) return 0;
   return align_up((size_t)n * d * (xtype == GPTQ_I8 && !widen ? 1 : 2), 256);
 }
@@ -103,7 +113,7 @@ extern "C" int gptq_packed_linear(const void *x, int xtype, const float *x_scale
   const size_t need = gptq_packed_linear_workspace_bytes(n, r, d, bits, group, xtype, perm != nullptr);
   if (need > 0 && (!workspace || workspace_bytes < need)) return GPTQ_ERR_NO_MEMORY;
   cudaStream_t st = (cudaStream_t)stream;
-  const bool widen = xtype == GPTQ_I8 && n > FEW_TOKENS;
+  const bool few = few_tokens(n, r, d, xtype), widen = xtype == GPTQ_I8 && !few;
   if (widen || perm) {
     const dim3 grid((unsigned)n, (unsigned)((d / 8 + GATHER_THREADS - 1) / GATHER_THREADS));
     if (widen)
@@ -121,7 +131,7 @@ extern "C" int gptq_packed_linear(const void *x, int xtype, const float *x_scale
   }
   const PackedArgs a{x, x_scales, reinterpret_cast<const uint32_t *>(qweight), scales, zeros,
                      bias, y, n, r, (int)d, bits, group, group < 0 ? 1 : (int)(d / group), xtype, ytype};
-  if (n > FEW_TOKENS) return launch_packed_many(a, st);
+  if (!few) return launch_packed_many(a, st);
   return xtype == GPTQ_F16    ? launch_packed_few_f16(a, st)
          : xtype == GPTQ_BF16 ? launch_packed_few_bf16(a, st)
                               : launch_packed_few_i8(a, st);
