@@ -85,6 +85,9 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int byt
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -373,12 +376,16 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
       if (a.sz_aligned && a.p.group == 32) {
         cp_async16(sz, a.p.scales + szrow + s * 4, 16);
         cp_async16(sz + ROWS * 16, a.p.zeros + szrow + s * 4, 16);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int gi = group_of(min(s * 4 + c, d / 32 - 1));
-          cp_async4(sz + c * 4, a.p.scales + szrow + gi, 4);
-          cp_async4(sz + ROWS * 16 + c * 4, a.p.zeros + szrow + gi, 4);
+      } else {   // the stage's groups, one behind the other: two but for rows of odd alignment
+        const int g0 = group_of(s * 4), g1 = group_of(min(s * 4 + 3, d / 32 - 1));
+        if (a.sz_aligned && (g0 & 1) == 0 && g1 <= g0 + 1) {
+          cp_async8(sz, a.p.scales + szrow + g0);
+          cp_async8(sz + ROWS * 16, a.p.zeros + szrow + g0);
+        } else {
+          for (int gi = g0; gi <= g1; ++gi) {
+            cp_async4(sz + (gi - g0) * 4, a.p.scales + szrow + gi, 4);
+            cp_async4(sz + ROWS * 16 + (gi - g0) * 4, a.p.zeros + szrow + gi, 4);
+          }
         }
       }
     } else {
@@ -468,6 +475,12 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
       }
       sz = sz_ring + cslot * F::SZSLOT + (gi & 3) * 4;
     }
+    uint32_t sub[4] = {};   // FINE: where the chunks' groups lie
+    if constexpr (FINE) {
+      const int g0 = group_of(s * 4);
+#pragma unroll
+      for (int u = 1; u < 4; ++u) sub[u] = (group_of(min(s * 4 + u, d / 32 - 1)) - g0) * 4;
+    }
     uint2 lo[2][4], hi[2][4];   // rows g and g + 8 of the two tiles
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
@@ -478,7 +491,7 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
     int ipart[2][NT][4], isx[NT][4];
     float zf[2][2] = {};
     auto zero_point = [&](int m, int h, int u) {
-      const uint32_t z = lds32(sz + ROWS * 16 + (m * 16 + h * 8 + g) * 16 + (FINE ? u * 4 : 0));
+      const uint32_t z = lds32(sz + ROWS * 16 + (m * 16 + h * 8 + g) * 16 + sub[u]);
       return FINE ? prepare_zero<BITS, XT>(z) : z;
     };
 #pragma unroll
@@ -579,7 +592,7 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
         for (int m = 0; m < 2; ++m) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float f = __uint_as_float(lds32(sz + (m * 16 + h * 8 + g) * 16 + (FINE ? u * 4 : 0)));
+            const float f = __uint_as_float(lds32(sz + (m * 16 + h * 8 + g) * 16 + sub[u]));
             if constexpr (F::INT8) {
               const int z = (int)zero_point(m, h, u);
 #pragma unroll
