@@ -217,9 +217,12 @@ __device__ __forceinline__ uint32_t prepare_zero(uint32_t raw) {
 // The eight codes of a unit as four pairs of operands: (0,4), (1,5), (2,6),
 // (3,7), or for 8-bit codes (0,1), (2,3), (4,5), (6,7); fp16 codes of fewer
 // bits: the second and fourth pair times 2^BITS.  zf = 2^23 + z, for 8-bit
-// codes with bf16 only.
+// codes with bf16 only.  base: the bits of the operands' B (bf16), of the even and
+// the odd pairs, in registers that the compiler does not see through, so that
+// mask and base take one instruction (which holds one constant).
 template <int BITS, int XT>
-__device__ __forceinline__ void code_pairs(uint2 w, float zf, uint32_t (&o)[4]) {
+__device__ __forceinline__ void code_pairs(uint2 w, float zf, const uint32_t (&base)[2],
+                                           uint32_t (&o)[4]) {
   if constexpr (BITS == 8) {
     if constexpr (XT == GPTQ_F16) {
       o[0] = __byte_perm(w.x, 0, 0x4140), o[1] = __byte_perm(w.x, 0, 0x4342);
@@ -248,16 +251,15 @@ __device__ __forceinline__ void code_pairs(uint2 w, float zf, uint32_t (&o)[4]) 
     } else if constexpr (BITS == 3) {
       // codes 0 and 2 at bit 1 (64 + q), 1 and 3 at bit 4 (8 + q)
       const uint32_t u = v << 1, h = v >> 5;
-      o[0] = (u & 0x000E000Eu) | 0x42804280u, o[1] = (u & 0x00700070u) | 0x41004100u;
-      o[2] = (h & 0x000E000Eu) | 0x42804280u, o[3] = (h & 0x00700070u) | 0x41004100u;
+      o[0] = (u & 0x000E000Eu) | base[0], o[1] = (u & 0x00700070u) | base[1];
+      o[2] = (h & 0x000E000Eu) | base[0], o[3] = (h & 0x00700070u) | base[1];
     } else {
       // at bit P, the top of the mantissa: exponent of 2^BITS
       constexpr int P = 7 - BITS;
-      constexpr uint32_t base = (uint32_t)((127 + BITS) << 7) * 0x00010001u;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int left = P - BITS * i;
-        o[i] = ((left > 0 ? v << (left > 0 ? left : 0) : v >> (left < 0 ? -left : 0)) & (mask << P)) | base;
+        o[i] = ((left > 0 ? v << (left > 0 ? left : 0) : v >> (left < 0 ? -left : 0)) & (mask << P)) | base[0];
       }
     }
   }
@@ -431,6 +433,12 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
     asm volatile("mov.b32 %0, %1;"
                  : "=r"(ones[i])
                  : "n"(XT == GPTQ_F16 ? 0x00010001 : XT == GPTQ_BF16 ? 0x3F803F80 : 0x01010101));
+  // bf16: 2^BITS at the top of the mantissa; 3-bit codes 64 and 8 (code_pairs)
+  uint32_t bases[2];
+  asm volatile("mov.b32 %0, %1;"
+               : "=r"(bases[0])
+               : "n"(BITS == 3 ? 0x42804280 : ((127 + BITS) << 7) * 0x00010001));
+  asm volatile("mov.b32 %0, %1;" : "=r"(bases[1]) : "n"(0x41004100));
   // tokens past the last: its values again (their columns are dropped)
   uint32_t xrow[NT];
 #pragma unroll
@@ -539,8 +547,8 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           uint32_t pl[4], ph[4];
-          code_pairs<BITS, XT>(lo[m][u], zf[m][0], pl);
-          code_pairs<BITS, XT>(hi[m][u], zf[m][1], ph);
+          code_pairs<BITS, XT>(lo[m][u], zf[m][0], bases, pl);
+          code_pairs<BITS, XT>(hi[m][u], zf[m][1], bases, ph);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             if constexpr (F::TWO) {

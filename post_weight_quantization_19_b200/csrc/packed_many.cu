@@ -207,18 +207,20 @@ struct Group {
 };
 
 // 32 codes of one row and group as 16 pairs of weights, in column order.
+// `magic`: M in a register that the compiler does not see through, so that mask and
+// M take one instruction (which holds one constant).
 template <int BITS, typename T>
 __device__ __forceinline__ void chunk_weights(const uint32_t *w, const Group<BITS, T> &g,
-                                              uint32_t (&o)[16]) {
+                                              uint32_t magic, uint32_t (&o)[16]) {
   constexpr uint32_t M = Pair<T>::M;
   if constexpr (BITS == 4) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t v = w[i], h = v >> 4;   // byte k: codes 2k (low nibble of v), 2k + 1 (of h)
-      o[4 * i + 0] = g.weight((__byte_perm(v, h, 0x0400) & 0x000F000Fu) | M);
-      o[4 * i + 1] = g.weight((__byte_perm(v, h, 0x0501) & 0x000F000Fu) | M);
-      o[4 * i + 2] = g.weight((__byte_perm(v, h, 0x0602) & 0x000F000Fu) | M);
-      o[4 * i + 3] = g.weight((__byte_perm(v, h, 0x0703) & 0x000F000Fu) | M);
+      o[4 * i + 0] = g.weight((__byte_perm(v, h, 0x0400) & 0x000F000Fu) | magic);
+      o[4 * i + 1] = g.weight((__byte_perm(v, h, 0x0501) & 0x000F000Fu) | magic);
+      o[4 * i + 2] = g.weight((__byte_perm(v, h, 0x0602) & 0x000F000Fu) | magic);
+      o[4 * i + 3] = g.weight((__byte_perm(v, h, 0x0703) & 0x000F000Fu) | magic);
     }
   } else if constexpr (BITS == 2) {
 #pragma unroll
@@ -227,8 +229,8 @@ __device__ __forceinline__ void chunk_weights(const uint32_t *w, const Group<BIT
 #pragma unroll
       for (int k = 0; k < 4; ++k) {   // byte k: codes 4k .. 4k + 3
         const uint32_t b = __byte_perm(v, h, 0x0400 + 0x0101 * k);
-        o[8 * i + 2 * k] = g.weight((b & 0x00030003u) | M);
-        o[8 * i + 2 * k + 1] = g.weight(((b >> 4) & 0x00030003u) | M);
+        o[8 * i + 2 * k] = g.weight((b & 0x00030003u) | magic);
+        o[8 * i + 2 * k + 1] = g.weight(((b >> 4) & 0x00030003u) | magic);
       }
     }
   } else if constexpr (BITS == 3) {
@@ -236,7 +238,7 @@ __device__ __forceinline__ void chunk_weights(const uint32_t *w, const Group<BIT
     for (int i = 0; i < 16; ++i) {   // six bits from stream bit 6 i
       const int pos = 6 * i, wi = pos >> 5, off = pos & 31;
       const uint32_t v = off + 6 > 32 ? __funnelshift_r(w[wi], w[wi + 1], off) : w[wi] >> off;
-      o[i] = g.weight((v & 7u) | ((v << 13) & 0x00070000u) | M);
+      o[i] = g.weight((v & 7u) | ((v << 13) & 0x00070000u) | magic);
     }
   } else if constexpr (M == 0x64006400u) {
 #pragma unroll
@@ -546,7 +548,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     // the parts of the block that this step's two 32-column chunks lie in
     const int sub0 = 2 * wg * a.subs / 8, sub1 = (2 * wg + 1) * a.subs / 8;
     int slot = 0, parity = 0;
-    uint32_t phase = 0, aphase = 0;
+    uint32_t phase = 0, aphase = 0, magic;
+    asm volatile("mov.b32 %0, %1;" : "=r"(magic) : "n"(Pair<T>::M));
     bool ok = true;
     // (a warp that gave up still walks the tiles: the others wait for it at their barrier)
     for (int t = cta; t < tiles; t += ctas, parity ^= 1) {
@@ -605,13 +608,13 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           Group<BITS, T> g;
           g.set(s * inv, z);
           uint32_t c0[16], c1[16];
-          chunk_weights<BITS, T>(w, g, c0);
+          chunk_weights<BITS, T>(w, g, magic, c0);
           if (sub1 != sub0) {
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(sz + sub1 * (PM * 4)));
             asm volatile("ld.shared.s32 %0, [%1];" : "=r"(z) : "r"(sz + (a.subs + sub1) * (PM * 4)));
             g.set(s * inv, z);
           }
-          chunk_weights<BITS, T>(w + BITS, g, c1);
+          chunk_weights<BITS, T>(w + BITS, g, magic, c1);
           if (!mbar_wait_bounded(&sh.empty_a[as], aphase ^ 1)) {
             if (lane == 0) many_timeout(a.status, sh);
             ok = false;
