@@ -7,6 +7,7 @@ no CPU path.  PyTorch provides device memory and streams.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -298,6 +299,12 @@ def _launch(device: torch.device, stream, fn, *args) -> int:
         return fn(*args, handle)
 
 
+def _on(stream):
+    """Where a call's own tensors are allocated: on the stream that it works on, so
+    that their memory, freed, is not taken while that stream still uses it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def gptq_rmsnorm_int8(x: torch.Tensor, gamma: torch.Tensor, *, eps: float,
                       residual: torch.Tensor | None = None, perm: torch.Tensor | None = None,
                       xhat: bool = False, outputs: dict | None = None, stream=None) -> dict:
@@ -317,14 +324,15 @@ def gptq_rmsnorm_int8(x: torch.Tensor, gamma: torch.Tensor, *, eps: float,
     dev, T = x.device, x.dtype
     out = dict(outputs or {})
     codes, scales, xh, h = (out.get(k) for k in ("codes", "scales", "xhat", "h"))
-    if codes is None:
-        codes = torch.empty((n, d), dtype=torch.int8, device=dev)
-    if scales is None:
-        scales = torch.empty(n, dtype=torch.float32, device=dev)
-    if xh is None and xhat:
-        xh = torch.empty((n, d), dtype=T, device=dev)
-    if h is None and residual is not None:
-        h = torch.empty((n, d), dtype=T, device=dev)
+    with _on(stream):
+        if codes is None:
+            codes = torch.empty((n, d), dtype=torch.int8, device=dev)
+        if scales is None:
+            scales = torch.empty(n, dtype=torch.float32, device=dev)
+        if xh is None and xhat:
+            xh = torch.empty((n, d), dtype=T, device=dev)
+        if h is None and residual is not None:
+            h = torch.empty((n, d), dtype=T, device=dev)
     _check(_launch(
         dev, stream, lib.gptq_rmsnorm_int8, _shaped(x, T, (n, d), dev, "x"),
         _shaped(residual, T, (n, d), dev, "residual"), _shaped(gamma, T, (d,), dev, "gamma"),
@@ -373,7 +381,8 @@ def gptq_packed_linear(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Ten
     if y is None:
         if dtype is None:
             dtype = torch.float16 if x.dtype == torch.int8 else x.dtype
-        y = torch.empty((n, r), dtype=dtype, device=dev)
+        with _on(stream):
+            y = torch.empty((n, r), dtype=dtype, device=dev)
     elif dtype is not None and y.dtype != dtype:
         raise ValueError(f"y must be {dtype}, got {y.dtype}")
     if y.dtype not in _DTYPE:
@@ -382,7 +391,8 @@ def gptq_packed_linear(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Ten
     if workspace is None and (perm is not None or xt == 3):   # 16-bit x in order needs none
         need = lib.gptq_packed_linear_workspace_bytes(n, r, d, bits, group, xt, perm is not None)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            with _on(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if workspace is not None and workspace.device != dev:
         raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
     _check(_launch(
@@ -408,10 +418,11 @@ def gptq_regroup(qweight: torch.Tensor, g_idx: torch.Tensor, bits: int, group: i
     if not g_idx.is_cuda or g_idx.dim() != 1:
         raise ValueError("g_idx must be a CUDA tensor [d]")
     d, r, dev = g_idx.shape[0], qweight.shape[0], g_idx.device
-    if out is None:
-        out = torch.empty_like(qweight)
-    if perm is None:
-        perm = torch.empty_like(g_idx)
+    with _on(stream):
+        if out is None:
+            out = torch.empty_like(qweight)
+        if perm is None:
+            perm = torch.empty_like(g_idx)
     words = (r, d * bits // 32)
     _check(_launch(
         dev, stream, lib.gptq_regroup, _shaped(qweight, torch.int32, words, dev, "qweight"),

@@ -428,6 +428,31 @@ def test_rmsnorm_int8_streams_and_graph():
             assert torch.equal(out[k], w[k])
 
 
+@pytest.mark.parametrize("n", [3, 40])
+def test_a_calls_own_memory_belongs_to_its_stream(n, monkeypatch):
+    # what a call on another stream allocates for itself is not handed out again
+    # to the current stream while that stream may still use it
+    import post_weight_quantization_19_b200 as g
+    from post_weight_quantization_19_b200 import gptq as binding
+    r, d = 96, 4096
+    q, s, z = dev(*layer(r, d, 4, 128, seed=5))
+    x = activations(n, d, 6)
+    perm = torch.randperm(d, device="cuda").to(torch.int32)
+    want = g.gptq_packed_linear(x, q, s, z, 4, 128, perm=perm)
+    seen, launch = [], binding._launch
+    monkeypatch.setattr(binding, "_launch",
+                        lambda *args: (seen.append(args[-2:]), launch(*args))[1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = g.gptq_packed_linear(x, q, s, z, 4, 128, perm=perm, stream=side)
+    (pointer, size), = seen
+    assert size > 0
+    others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    assert all(abs(t.data_ptr() - pointer) >= size for t in others)
+    side.synchronize()
+    assert torch.equal(y, want)
+
+
 # ------------------------------------------------------------------ columns by group
 
 @pytest.mark.parametrize("r,d,bits,group", [(1, 32, 4, 32), (3, 96, 3, 32), (70, 512, 2, 64),
