@@ -343,11 +343,11 @@ int gptq_rmsnorm_int8(const void *x, const void *residual, const void *gamma, in
  *   workspace  device scratch of gptq_packed_linear_workspace_bytes(...) bytes,
  *            256-byte aligned (NULL when the query returns 0); contents on
  *            entry are ignored.  Calls whose work may overlap need one each.
- *   Sums in fp32 (exact integers inside a group for GPTQ_I8 and few tokens),
- *   one rounding to `ytype`.  For few tokens the products use q - z exactly;
- *   for many, weights s (q - z) are rounded once to the 16-bit type of the
- *   tensor-core product, as gptq_dequant_fp16 does.  Results do not change
- *   from call to call.
+ *   Sums in fp32 (for few tokens of GPTQ_I8 exact integers over up to 128
+ *   columns), one rounding to `ytype`.  For few tokens (up to 8 at least) the
+ *   codes and zero points enter exactly; for many, weights s (q - z) are
+ *   rounded once to the 16-bit type of the tensor-core product, as
+ *   gptq_dequant_fp16 does.  Results do not change from call to call.
  *   n == 0 or r == 0: nothing to do.  Asynchronous; a bounded in-kernel wait
  *   that runs out is reported by gptq_check_device_status.
  *
@@ -375,8 +375,10 @@ int gptq_packed_linear(const void *x, int xtype, const float *x_scales, int64_t 
  *   out      device int32 [r x d*bits/32], written; must not overlap qweight.
  *   perm     device int32 [d], written.
  *   r >= 0; d, bits as gptq_dequant_gemv; group a multiple of 32 that divides d.
- *   Synchronises `stream` once, at the end: a g_idx with another number of
- *   columns in some group returns GPTQ_ERR_INVALID_ARG (outputs unspecified).
+ *   Waits until the order is known to be good -- for the work before it on
+ *   `stream`, then for the first part of its own; the rest follows on the
+ *   stream.  A g_idx with another number of columns in some group returns
+ *   GPTQ_ERR_INVALID_ARG (outputs unspecified).
  *   On a stream that is being captured: GPTQ_ERR_INVALID_ARG.
  */
 int gptq_regroup(const int32_t *qweight, const int32_t *g_idx, int64_t r, int64_t d, int bits,

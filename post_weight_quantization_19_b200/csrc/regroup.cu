@@ -8,14 +8,17 @@
 // Two kernels.  The order, one CTA: each of its 32 warps takes a run of columns
 // and counts its groups (match_any gives a column's rank among the 32 that a
 // warp reads at once), the counts are summed over the warps, and a second pass
-// places the columns.  A group with another number of columns than `group` is
-// reported in a word of mapped host memory, and perm becomes the identity.
+// places the columns.  Whether every group has `group` columns is reported in a
+// word of mapped host memory as soon as the counts are there; the host waits for
+// that alone, while the columns are placed and the rows move.  If one has not,
+// perm becomes the identity.
 //
 // The rows, r*d*bits/8 bytes in and out: a CTA takes eight rows (four of 8-bit
 // codes) and transposes them so that one shared-memory word holds a column's
 // codes of all its rows, a nibble (byte) each.  Moving a column is then one
 // random 4-byte read for eight codes instead of eight byte reads; reading codes
-// one by one took 490 us where this takes about 10 (8192 x 8192, 3 bits).
+// one by one took 490 us where this takes 28 (8192 x 8192, 3 bits: bound by the 5.7
+// instructions a code costs; 17 us for 11008 x 4096, 4 bits).
 // Codes of 2 and 3 bits travel as nibbles.  Rows too long for that (d > 49152)
 // go through bytes in shared memory, one row at a time.
 #include <mutex>
@@ -30,10 +33,12 @@ namespace {
 
 constexpr int ORDER_WARPS = 32;
 constexpr int ROW_THREADS = 256;
+enum { PENDING = 0, ACCEPTED, REFUSED };   // the order, in a call's word of host memory
 
 __global__ void __launch_bounds__(32 * ORDER_WARPS)
     group_order_kernel(const int32_t *__restrict__ g_idx, int d, int group, int G,
                        int32_t *__restrict__ perm, volatile int *report) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the rows: see below
   extern __shared__ __align__(16) uint16_t counts[];   // [ORDER_WARPS][G]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint16_t *mine = counts + warp * G;
@@ -65,9 +70,10 @@ __global__ void __launch_bounds__(32 * ORDER_WARPS)
   }
   if (__syncthreads_or(bad)) {
     for (int j = threadIdx.x; j < d; j += 32 * ORDER_WARPS) perm[j] = j;
-    if (threadIdx.x == 0) *report = 1;
+    if (threadIdx.x == 0) *report = REFUSED;
     return;
   }
+  if (threadIdx.x == 0) *report = ACCEPTED;
 #pragma unroll 4
   for (int c = c0; c < c1; ++c) {
     const int g = __ldg(g_idx + c * 32 + lane);
@@ -180,11 +186,6 @@ __global__ void __launch_bounds__(ROW_THREADS)
   const int pitch = d / 32 * BITS;   // words per row
   const int units = d / U::COLS;
   uint16_t *order = reinterpret_cast<uint16_t *>(columns + d);
-  if constexpr (STAGED) {
-#pragma unroll 16
-    for (int j = threadIdx.x; j < d; j += ROW_THREADS)
-      order[j] = (uint16_t)place(__ldg(perm + j));
-  }
   const int64_t groups = (r + U::ROWS - 1) / U::ROWS;
   for (int64_t block = blockIdx.x; block < groups; block += gridDim.x) {
     const int rows = (int)min((int64_t)U::ROWS, r - block * U::ROWS);
@@ -210,6 +211,15 @@ __global__ void __launch_bounds__(ROW_THREADS)
         for (int i = 0; i < U::ROWS; i += 4)
           *reinterpret_cast<uint4 *>(columns + place(u * U::COLS + k * U::ROWS + i)) =
               make_uint4(a[i], a[i + 1], a[i + 2], a[i + 3]);
+      }
+    }
+    if (block == blockIdx.x) {
+      // launched beside the order's kernel: nothing was written, nothing of it read
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      if constexpr (STAGED) {
+#pragma unroll 16
+        for (int j = threadIdx.x; j < d; j += ROW_THREADS)
+          order[j] = (uint16_t)place(__ldg(perm + j));
       }
     }
     __syncthreads();
@@ -255,6 +265,7 @@ __global__ void __launch_bounds__(ROW_THREADS)
                    int64_t r, int d,
                    uint32_t *__restrict__ out) {
   extern __shared__ __align__(16) uint8_t row_codes[];   // [d]
+  asm volatile("griddepcontrol.wait;" ::: "memory");     // perm
   const int nchunk = d / 32;
   for (int64_t row = blockIdx.x; row < r; row += gridDim.x) {
     const uint32_t *src = qweight + row * nchunk * BITS;
@@ -299,9 +310,8 @@ int launch_rows(const uint32_t *q, int32_t *perm, int64_t r, int d, uint32_t *ou
   int per_sm = (int)((200u << 10) / (smem + 1024));
   per_sm = per_sm < 1 ? 1 : (per_sm > 8 ? 8 : per_sm);
   const int64_t most = (r + Unit<BITS>::ROWS - 1) / Unit<BITS>::ROWS, fit = (int64_t)num_sms() * per_sm;
-  regroup_rows_kernel<BITS, STAGED>
-      <<<(unsigned)(most < fit ? most : fit), ROW_THREADS, smem, st>>>(q, perm, r, d, out);
-  GPTQ_LAUNCH_CHECK();
+  const dim3 grid((unsigned)(most < fit ? most : fit));
+  GPTQ_LAUNCH_PDL((regroup_rows_kernel<BITS, STAGED>), grid, dim3(ROW_THREADS), smem, st, q, perm, r, d, out);
   return GPTQ_OK;
 }
 
@@ -313,9 +323,8 @@ int launch_regroup(const uint32_t *q, int32_t *perm, int64_t r, int d, uint32_t 
     static std::atomic<bool> attr[64] = {};
     if (const int rc = ensure_smem_attr(regroup_kernel<BITS>, 65536, attr)) return rc;
     const int64_t cap = (int64_t)num_sms() * 8;
-    regroup_kernel<BITS><<<(unsigned)(r < cap ? r : cap), ROW_THREADS, (size_t)d, st>>>(
-        q, perm, r, d, out);
-    GPTQ_LAUNCH_CHECK();
+    const dim3 grid((unsigned)(r < cap ? r : cap));
+    GPTQ_LAUNCH_PDL((regroup_kernel<BITS>), grid, dim3(ROW_THREADS), (size_t)d, st, q, perm, r, d, out);
     return GPTQ_OK;
   }
   return d <= LONGEST_STAGED ? launch_rows<BITS, true>(q, perm, r, d, out, st)
@@ -386,15 +395,23 @@ extern "C" int gptq_regroup(const int32_t *qweight, const int32_t *g_idx, int64_
   if (capture != cudaStreamCaptureStatusNone) return GPTQ_ERR_INVALID_ARG;   // it waits for its result
   int *word = nullptr;
   if (const int rc = take_word(&word)) return rc;
-  *word = 0;
+  volatile int *seen = word;
+  *seen = PENDING;
   int rc = enqueue_regroup(reinterpret_cast<const uint32_t *>(qweight), g_idx, r, (int)d, bits, group,
                            reinterpret_cast<uint32_t *>(out), perm, word, st);
-  const cudaError_t e = cudaStreamSynchronize(st);
-  if (e != cudaSuccess) {   // the word may still be written: not given back
-    set_last_error(__FILE__, __LINE__, "cudaStreamSynchronize", e);
-    return GPTQ_ERR_CUDA;
+  // (before the order's kernel has run the word is pending; a launch that failed
+  // or a fault on the device ends the wait through the stream's state)
+  for (unsigned spins = 1; *seen == PENDING; ++spins) {
+    if (spins % 1024) continue;
+    const cudaError_t e = cudaStreamQuery(st);
+    if (e == cudaErrorNotReady) continue;
+    if (e != cudaSuccess) {   // the word may still be written: not given back
+      set_last_error(__FILE__, __LINE__, "cudaStreamQuery", e);
+      return GPTQ_ERR_CUDA;
+    }
+    if (*seen == PENDING) break;   // all that was enqueued is done: its launch failed
   }
-  if (rc == GPTQ_OK && *static_cast<volatile int *>(word) != 0) rc = GPTQ_ERR_INVALID_ARG;
+  if (rc == GPTQ_OK && *seen != ACCEPTED) rc = *seen == REFUSED ? GPTQ_ERR_INVALID_ARG : GPTQ_ERR_CUDA;
   give_word(word);
   return rc;
 }
