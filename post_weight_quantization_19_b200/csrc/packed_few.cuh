@@ -7,7 +7,7 @@
 // registers: a code goes from its packed word to an operand in about one
 // instruction, with nothing written back to shared or tensor memory on the way.
 // (mma.sync reaches a quarter of tcgen05's rate: 0.46 m16n8k16 per clock and SM
-// measured.  For 8 tokens the weights' bytes still take longer.)
+// measured.  For few tokens that is enough: turning codes into operands takes longer.)
 //
 // The order of k inside a matrix instruction is free as long as both operands
 // agree.  A thread takes eight codes of a row at a time (a unit): one 32-bit
@@ -34,6 +34,11 @@
 // scales, zeros) and meets the others only at the end: the k range is split
 // over the CTA's warps and over a cluster of CTAs, whose partial sums are added
 // through distributed shared memory in a fixed order.
+//
+// Measured, one token: 12288 x 49152, 3 bits, bf16 126 us (2.1 TB/s; the integer pipe
+// is busy 64 % of the time, 2.3 instructions per clock); 4 bits, fp16 91 us (3.7
+// TB/s); 4096 x 4096, 4 bits 5.9 us, most of it launch, fill and the last sums;
+// 11008 x 4096 with 8-bit x 9.6 us.
 #pragma once
 
 #include "packed_linear.h"
@@ -259,7 +264,8 @@ __device__ __forceinline__ void code_pairs(uint2 w, float zf, const uint32_t (&b
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int left = P - BITS * i;
-        o[i] = ((left > 0 ? v << (left > 0 ? left : 0) : v >> (left < 0 ? -left : 0)) & (mask << P)) | base[0];
+        const uint32_t u = left > 0 ? v << (left > 0 ? left : 0) : v >> (left < 0 ? -left : 0);
+        o[i] = (u & (mask << P)) | base[0];
       }
     }
   }
@@ -269,22 +275,26 @@ __device__ __forceinline__ void code_pairs(uint2 w, float zf, const uint32_t (&b
 // in order.
 template <int BITS>
 __device__ __forceinline__ uint2 code_bytes(uint2 w) {
-  if constexpr (BITS == 8) return w;
-  if constexpr (BITS == 4) return make_uint2(w.x & 0x0F0F0F0Fu, (w.x >> 4) & 0x0F0F0F0Fu);
-  uint32_t o[2];
+  if constexpr (BITS == 8) {
+    return w;
+  } else if constexpr (BITS == 4) {
+    return make_uint2(w.x & 0x0F0F0F0Fu, (w.x >> 4) & 0x0F0F0F0Fu);
+  } else {
+    uint32_t o[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if constexpr (BITS == 3) {
-      const uint32_t v = i ? w.x >> 12 : w.x;
-      const uint32_t u = (v & 0x3Fu) | ((v << 10) & 0x003F0000u);
-      o[i] = (u & 0x00070007u) | ((u << 5) & 0x07000700u);
-    } else {
-      const uint32_t v = i ? w.x >> 8 : w.x;
-      const uint32_t u = (v & 0xFu) | ((v << 12) & 0x000F0000u);
-      o[i] = (u & 0x00030003u) | ((u << 6) & 0x03000300u);
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (BITS == 3) {
+        const uint32_t v = i ? w.x >> 12 : w.x;
+        const uint32_t u = (v & 0x3Fu) | ((v << 10) & 0x003F0000u);
+        o[i] = (u & 0x00070007u) | ((u << 5) & 0x07000700u);
+      } else {
+        const uint32_t v = i ? w.x >> 8 : w.x;
+        const uint32_t u = (v & 0xFu) | ((v << 12) & 0x000F0000u);
+        o[i] = (u & 0x00030003u) | ((u << 6) & 0x03000300u);
+      }
     }
+    return make_uint2(o[0], o[1]);
   }
-  return make_uint2(o[0], o[1]);
 }
 
 struct FewArgs {
@@ -447,243 +457,243 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
   // [warps][COLS][ROWS]
   float *red = reinterpret_cast<float *>(smem + warps * (F::STAGES * a.stage_bytes + F::SZWARP));
   for (int tile = cta; tile < tiles; tile += ctas) {
-  float acc[2][NT][4];
+    float acc[2][NT][4];
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.f;
-  int cblock = -1;   // as sz_block, of the computing cursor
-  for (int s = s0; s < s1; ++s) {
-    cp_wait<F::STAGES - 2>();
-    __syncwarp();
-    {
-      int ns = slot + F::STAGES - 1;
-      if (ns >= F::STAGES) ns -= F::STAGES;
-      issue(ns);
-      cp_commit();
-    }
-    const uint32_t base = ring + slot * a.stage_bytes;
-    const uint32_t xbase = base + F::WBYTES + F::SZBYTES;
-    // scales of rows 0, 1, ... of this stage's (first) group, 16 bytes apart; zeros behind
-    uint32_t sz = base + F::WBYTES;
-    if constexpr (!FINE) {
-      const int gi = group_of(s * 4);
-      if (gi >> 2 != cblock) {
-        cblock = gi >> 2;
-        cslot = cslot + 1 == F::SZSLOTS ? 0 : cslot + 1;
-        // the block's zero points, made ready by the lane of their row
-        const uint32_t at = sz_ring + cslot * F::SZSLOT + ROWS * 16 + lane * 16;
-        uint4 z = lds128(at);
-        z.x = prepare_zero<BITS, XT>(z.x), z.y = prepare_zero<BITS, XT>(z.y);
-        z.z = prepare_zero<BITS, XT>(z.z), z.w = prepare_zero<BITS, XT>(z.w);
-        *reinterpret_cast<uint4 *>(__cvta_shared_to_generic(at)) = z;
-        __syncwarp();
+        for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.f;
+    int cblock = -1;   // as sz_block, of the computing cursor
+    for (int s = s0; s < s1; ++s) {
+      cp_wait<F::STAGES - 2>();
+      __syncwarp();
+      {
+        int ns = slot + F::STAGES - 1;
+        if (ns >= F::STAGES) ns -= F::STAGES;
+        issue(ns);
+        cp_commit();
       }
-      sz = sz_ring + cslot * F::SZSLOT + (gi & 3) * 4;
-    }
-    uint32_t sub[4] = {};   // FINE: where the chunks' groups lie
-    if constexpr (FINE) {
-      const int g0 = group_of(s * 4);
-#pragma unroll
-      for (int u = 1; u < 4; ++u) sub[u] = (group_of(min(s * 4 + u, d / 32 - 1)) - g0) * 4;
-    }
-    uint2 lo[2][4], hi[2][4];   // rows g and g + 8 of the two tiles
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      row_units<BITS, FINE>(base + (m * 16 + g) * F::WSTRIDE, t, lo[m]);
-      row_units<BITS, FINE>(base + (m * 16 + 8 + g) * F::WSTRIDE, t, hi[m]);
-    }
-    float part[2][NT][4], odd[2][NT][4], sx[NT][4], sx2[NT][4];
-    int ipart[2][NT][4], isx[NT][4];
-    float zf[2][2] = {};
-    auto zero_point = [&](int m, int h, int u) {
-      const uint32_t z = lds32(sz + ROWS * 16 + (m * 16 + h * 8 + g) * 16 + sub[u]);
-      return FINE ? prepare_zero<BITS, XT>(z) : z;
-    };
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const bool first = FINE || u == 0;   // a sum starts with this unit
-      if constexpr (!F::INT8) {
-        if (F::EXACT && first) {
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) zf[m][h] = __uint_as_float(zero_point(m, h, u));
+      const uint32_t base = ring + slot * a.stage_bytes;
+      const uint32_t xbase = base + F::WBYTES + F::SZBYTES;
+      // scales of rows 0, 1, ... of this stage's (first) group, 16 bytes apart; zeros behind
+      uint32_t sz = base + F::WBYTES;
+      if constexpr (!FINE) {
+        const int gi = group_of(s * 4);
+        if (gi >> 2 != cblock) {
+          cblock = gi >> 2;
+          cslot = cslot + 1 == F::SZSLOTS ? 0 : cslot + 1;
+          // the block's zero points, made ready by the lane of their row
+          const uint32_t at = sz_ring + cslot * F::SZSLOT + ROWS * 16 + lane * 16;
+          uint4 z = lds128(at);
+          z.x = prepare_zero<BITS, XT>(z.x), z.y = prepare_zero<BITS, XT>(z.y);
+          z.z = prepare_zero<BITS, XT>(z.z), z.w = prepare_zero<BITS, XT>(z.w);
+          *reinterpret_cast<uint4 *>(__cvta_shared_to_generic(at)) = z;
+          __syncwarp();
         }
-        // which pairs share a product: one choice for the codes and the ones, or x
-        // would be copied into other register pairs
-        constexpr int B1 = F::TWO || F::BASES ? 2 : 1, B2 = F::TWO || F::BASES ? 1 : 2;
-        uint32_t xb[NT][4];
+        sz = sz_ring + cslot * F::SZSLOT + (gi & 3) * 4;
+      }
+      uint32_t sub[4] = {};   // FINE: where the chunks' groups lie
+      if constexpr (FINE) {
+        const int g0 = group_of(s * 4);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          // (a coarse stage: piece t of unit u; FINE: piece t of chunk u -- the same place)
-          const uint4 v = lds128(xbase + xrow[j] + u * 64 + t * 16);
-          if constexpr (BITS == 8) {
-            xb[j][0] = v.x, xb[j][1] = v.y, xb[j][2] = v.z, xb[j][3] = v.w;
-          } else {
-            xb[j][0] = __byte_perm(v.x, v.z, 0x5410), xb[j][1] = __byte_perm(v.x, v.z, 0x7632);
-            xb[j][2] = __byte_perm(v.y, v.w, 0x5410), xb[j][3] = __byte_perm(v.y, v.w, 0x7632);
-          }
-          if constexpr (!F::EXACT) {
-            if constexpr (F::BASES) {
-              if (first) {
-                mma16<XT, true>(sx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][2]);
-                mma16<XT, true>(sx2[j], ones[0], ones[1], ones[2], ones[3], xb[j][1], xb[j][3]);
-              } else {
-                mma16<XT, false>(sx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][2]);
-                mma16<XT, false>(sx2[j], ones[0], ones[1], ones[2], ones[3], xb[j][1], xb[j][3]);
-              }
-            } else {
-              if (first)
-                mma16<XT, true>(sx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][B1]);
-              else
-                mma16<XT, false>(sx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][B1]);
-              mma16<XT, false>(sx[j], ones[0], ones[1], ones[2], ones[3], xb[j][B2], xb[j][3]);
-            }
-          }
-        }
+        for (int u = 1; u < 4; ++u) sub[u] = (group_of(min(s * 4 + u, d / 32 - 1)) - g0) * 4;
+      }
+      uint2 lo[2][4], hi[2][4];   // rows g and g + 8 of the two tiles
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          uint32_t pl[4], ph[4];
-          code_pairs<BITS, XT>(lo[m][u], zf[m][0], bases, pl);
-          code_pairs<BITS, XT>(hi[m][u], zf[m][1], bases, ph);
+      for (int m = 0; m < 2; ++m) {
+        row_units<BITS, FINE>(base + (m * 16 + g) * F::WSTRIDE, t, lo[m]);
+        row_units<BITS, FINE>(base + (m * 16 + 8 + g) * F::WSTRIDE, t, hi[m]);
+      }
+      float part[2][NT][4], odd[2][NT][4], sx[NT][4], sx2[NT][4];
+      int ipart[2][NT][4], isx[NT][4];
+      float zf[2][2] = {};
+      auto zero_point = [&](int m, int h, int u) {
+        const uint32_t z = lds32(sz + ROWS * 16 + (m * 16 + h * 8 + g) * 16 + sub[u]);
+        return FINE ? prepare_zero<BITS, XT>(z) : z;
+      };
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool first = FINE || u == 0;   // a sum starts with this unit
+        if constexpr (!F::INT8) {
+          if (F::EXACT && first) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) zf[m][h] = __uint_as_float(zero_point(m, h, u));
+          }
+          // which pairs share a product: one choice for the codes and the ones, or x
+          // would be copied into other register pairs
+          constexpr int B1 = F::TWO || F::BASES ? 2 : 1, B2 = F::TWO || F::BASES ? 1 : 2;
+          uint32_t xb[NT][4];
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            if constexpr (F::TWO) {
-              if (first) {
-                mma16<XT, true>(part[m][j], pl[0], ph[0], pl[2], ph[2], xb[j][0], xb[j][2]);
-                mma16<XT, true>(odd[m][j], pl[1], ph[1], pl[3], ph[3], xb[j][1], xb[j][3]);
-              } else {
-                mma16<XT, false>(part[m][j], pl[0], ph[0], pl[2], ph[2], xb[j][0], xb[j][2]);
-                mma16<XT, false>(odd[m][j], pl[1], ph[1], pl[3], ph[3], xb[j][1], xb[j][3]);
-              }
+            // (a coarse stage: piece t of unit u; FINE: piece t of chunk u -- the same place)
+            const uint4 v = lds128(xbase + xrow[j] + u * 64 + t * 16);
+            if constexpr (BITS == 8) {
+              xb[j][0] = v.x, xb[j][1] = v.y, xb[j][2] = v.z, xb[j][3] = v.w;
             } else {
-              if (first)
-                mma16<XT, true>(part[m][j], pl[0], ph[0], pl[B1], ph[B1], xb[j][0], xb[j][B1]);
-              else
-                mma16<XT, false>(part[m][j], pl[0], ph[0], pl[B1], ph[B1], xb[j][0], xb[j][B1]);
-              mma16<XT, false>(part[m][j], pl[B2], ph[B2], pl[3], ph[3], xb[j][B2], xb[j][3]);
+              xb[j][0] = __byte_perm(v.x, v.z, 0x5410), xb[j][1] = __byte_perm(v.x, v.z, 0x7632);
+              xb[j][2] = __byte_perm(v.y, v.w, 0x5410), xb[j][3] = __byte_perm(v.y, v.w, 0x7632);
+            }
+            if constexpr (!F::EXACT) {
+              if constexpr (F::BASES) {
+                if (first) {
+                  mma16<XT, true>(sx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][2]);
+                  mma16<XT, true>(sx2[j], ones[0], ones[1], ones[2], ones[3], xb[j][1], xb[j][3]);
+                } else {
+                  mma16<XT, false>(sx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][2]);
+                  mma16<XT, false>(sx2[j], ones[0], ones[1], ones[2], ones[3], xb[j][1], xb[j][3]);
+                }
+              } else {
+                if (first)
+                  mma16<XT, true>(sx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][B1]);
+                else
+                  mma16<XT, false>(sx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][B1]);
+                mma16<XT, false>(sx[j], ones[0], ones[1], ones[2], ones[3], xb[j][B2], xb[j][3]);
+              }
             }
           }
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            uint32_t pl[4], ph[4];
+            code_pairs<BITS, XT>(lo[m][u], zf[m][0], bases, pl);
+            code_pairs<BITS, XT>(hi[m][u], zf[m][1], bases, ph);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              if constexpr (F::TWO) {
+                if (first) {
+                  mma16<XT, true>(part[m][j], pl[0], ph[0], pl[2], ph[2], xb[j][0], xb[j][2]);
+                  mma16<XT, true>(odd[m][j], pl[1], ph[1], pl[3], ph[3], xb[j][1], xb[j][3]);
+                } else {
+                  mma16<XT, false>(part[m][j], pl[0], ph[0], pl[2], ph[2], xb[j][0], xb[j][2]);
+                  mma16<XT, false>(odd[m][j], pl[1], ph[1], pl[3], ph[3], xb[j][1], xb[j][3]);
+                }
+              } else {
+                if (first)
+                  mma16<XT, true>(part[m][j], pl[0], ph[0], pl[B1], ph[B1], xb[j][0], xb[j][B1]);
+                else
+                  mma16<XT, false>(part[m][j], pl[0], ph[0], pl[B1], ph[B1], xb[j][0], xb[j][B1]);
+                mma16<XT, false>(part[m][j], pl[B2], ph[B2], pl[3], ph[3], xb[j][B2], xb[j][3]);
+              }
+            }
+          }
+        } else {
+          uint32_t xb[NT][2];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const uint2 v = lds64(xbase + xrow[j] + (FINE ? u * 32 + t * 8 : t * 32 + u * 8));
+            if constexpr (BITS == 4) {
+              xb[j][0] = __byte_perm(v.x, v.y, 0x6420), xb[j][1] = __byte_perm(v.x, v.y, 0x7531);
+            } else {
+              xb[j][0] = v.x, xb[j][1] = v.y;
+            }
+            if (first)
+              mma8<true>(isx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][1]);
+            else
+              mma8<false>(isx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][1]);
+          }
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint2 bl = code_bytes<BITS>(lo[m][u]), bh = code_bytes<BITS>(hi[m][u]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              if (first)
+                mma8<true>(ipart[m][j], bl.x, bh.x, bl.y, bh.y, xb[j][0], xb[j][1]);
+              else
+                mma8<false>(ipart[m][j], bl.x, bh.x, bl.y, bh.y, xb[j][0], xb[j][1]);
+            }
+          }
+        }
+        if (FINE || u == 3) {   // the group's (or stage's) sums, scaled
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float f = __uint_as_float(lds32(sz + (m * 16 + h * 8 + g) * 16 + sub[u]));
+              if constexpr (F::INT8) {
+                const int z = (int)zero_point(m, h, u);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                  for (int i = 0; i < 2; ++i)
+                    acc[m][j][2 * h + i] =
+                        fmaf(f, (float)(ipart[m][j][2 * h + i] - z * isx[j][i]), acc[m][j][2 * h + i]);
+              } else if constexpr (F::EXACT) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                  for (int i = 0; i < 2; ++i)
+                    acc[m][j][2 * h + i] = fmaf(f, part[m][j][2 * h + i], acc[m][j][2 * h + i]);
+              } else {
+                const float z = __uint_as_float(zero_point(m, h, u));   // -(B + z)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    float v = part[m][j][2 * h + i];
+                    if constexpr (F::TWO) v = fmaf(1.f / (1 << BITS), odd[m][j][2 * h + i], v);
+                    if constexpr (F::BASES) v = fmaf(z + 56.f, sx2[j][i], v);   // -(8 + z)
+                    acc[m][j][2 * h + i] = fmaf(f, fmaf(z, sx[j][i], v), acc[m][j][2 * h + i]);
+                  }
+              }
+            }
+          }
+        }
+      }
+      if (++slot == F::STAGES) slot = 0;
+    }
+
+    // ---- the warps' sums, then the cluster's, each in a fixed order
+    constexpr int COLS = 8 * NT, CELLS = ROWS * COLS;
+    const int64_t row0 = (int64_t)tile * ROWS;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          red[warp * CELLS + (j * 8 + t * 2 + (i & 1)) * ROWS + m * 16 + (i >> 1) * 8 + g] = acc[m][j][i];
+    __syncthreads();
+    const int per = CELLS / a.ctas_k;                 // cells this CTA finishes
+    const int first = crank * per;
+    if (a.ctas_k > 1) {
+      for (int i = threadIdx.x; i < CELLS; i += blockDim.x) {
+        float v = red[i];
+#pragma unroll 8
+        for (int w = 1; w < warps; ++w) v += red[w * CELLS + i];
+        red[i] = v;                                   // cell i is this thread's alone
+      }
+      __syncwarp();
+      cluster_sync();
+    }
+    for (int i = first + threadIdx.x; i < first + per; i += blockDim.x) {
+      const int col = i / ROWS;
+      const int64_t row = row0 + i % ROWS;
+      if (col >= ntok || row >= a.p.r) continue;
+      float v = 0.f;
+      if (a.ctas_k > 1) {
+        for (int k = 0; k < a.ctas_k; ++k) {
+          float o;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(cluster_addr(red + i, k)));
+          v += o;
         }
       } else {
-        uint32_t xb[NT][2];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const uint2 v = lds64(xbase + xrow[j] + (FINE ? u * 32 + t * 8 : t * 32 + u * 8));
-          if constexpr (BITS == 4) {
-            xb[j][0] = __byte_perm(v.x, v.y, 0x6420), xb[j][1] = __byte_perm(v.x, v.y, 0x7531);
-          } else {
-            xb[j][0] = v.x, xb[j][1] = v.y;
-          }
-          if (first)
-            mma8<true>(isx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][1]);
-          else
-            mma8<false>(isx[j], ones[0], ones[1], ones[2], ones[3], xb[j][0], xb[j][1]);
-        }
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const uint2 bl = code_bytes<BITS>(lo[m][u]), bh = code_bytes<BITS>(hi[m][u]);
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            if (first)
-              mma8<true>(ipart[m][j], bl.x, bh.x, bl.y, bh.y, xb[j][0], xb[j][1]);
-            else
-              mma8<false>(ipart[m][j], bl.x, bh.x, bl.y, bh.y, xb[j][0], xb[j][1]);
-          }
-        }
-      }
-      if (FINE || u == 3) {   // the group's (or stage's) sums, scaled
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float f = __uint_as_float(lds32(sz + (m * 16 + h * 8 + g) * 16 + sub[u]));
-            if constexpr (F::INT8) {
-              const int z = (int)zero_point(m, h, u);
-#pragma unroll
-              for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  acc[m][j][2 * h + i] =
-                      fmaf(f, (float)(ipart[m][j][2 * h + i] - z * isx[j][i]), acc[m][j][2 * h + i]);
-            } else if constexpr (F::EXACT) {
-#pragma unroll
-              for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  acc[m][j][2 * h + i] = fmaf(f, part[m][j][2 * h + i], acc[m][j][2 * h + i]);
-            } else {
-              const float z = __uint_as_float(zero_point(m, h, u));   // -(B + z)
-#pragma unroll
-              for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  float v = part[m][j][2 * h + i];
-                  if constexpr (F::TWO) v = fmaf(1.f / (1 << BITS), odd[m][j][2 * h + i], v);
-                  if constexpr (F::BASES) v = fmaf(z + 56.f, sx2[j][i], v);   // -(8 + z)
-                  acc[m][j][2 * h + i] = fmaf(f, fmaf(z, sx[j][i], v), acc[m][j][2 * h + i]);
-                }
-            }
-          }
-        }
-      }
-    }
-    if (++slot == F::STAGES) slot = 0;
-  }
-
-  // ---- the warps' sums, then the cluster's, each in a fixed order
-  constexpr int COLS = 8 * NT, CELLS = ROWS * COLS;
-  const int64_t row0 = (int64_t)tile * ROWS;
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        red[warp * CELLS + (j * 8 + t * 2 + (i & 1)) * ROWS + m * 16 + (i >> 1) * 8 + g] = acc[m][j][i];
-  __syncthreads();
-  const int per = CELLS / a.ctas_k;                 // cells this CTA finishes
-  const int first = crank * per;
-  if (a.ctas_k > 1) {
-    for (int i = threadIdx.x; i < CELLS; i += blockDim.x) {
-      float v = red[i];
+        v = red[i];
 #pragma unroll 8
-      for (int w = 1; w < warps; ++w) v += red[w * CELLS + i];
-      red[i] = v;                                   // cell i is this thread's alone
-    }
-    __syncwarp();
-    cluster_sync();
-  }
-  for (int i = first + threadIdx.x; i < first + per; i += blockDim.x) {
-    const int col = i / ROWS;
-    const int64_t row = row0 + i % ROWS;
-    if (col >= ntok || row >= a.p.r) continue;
-    float v = 0.f;
-    if (a.ctas_k > 1) {
-      for (int k = 0; k < a.ctas_k; ++k) {
-        float o;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(cluster_addr(red + i, k)));
-        v += o;
+        for (int w = 1; w < warps; ++w) v += red[w * CELLS + i];
       }
-    } else {
-      v = red[i];
-#pragma unroll 8
-      for (int w = 1; w < warps; ++w) v += red[w * CELLS + i];
+      if constexpr (F::INT8) v *= a.p.x_scales[tok0 + col];
+      if constexpr (XT == GPTQ_F16) v *= 16777216.f;   // the codes were q 2^-24
+      if (a.p.bias) v += load_as_float(a.p.bias, a.p.ytype, row);
+      store_float(a.p.y, a.p.ytype, (tok0 + col) * a.p.r + row, v);
     }
-    if constexpr (F::INT8) v *= a.p.x_scales[tok0 + col];
-    if constexpr (XT == GPTQ_F16) v *= 16777216.f;   // the codes were q 2^-24
-    if (a.p.bias) v += load_as_float(a.p.bias, a.p.ytype, row);
-    store_float(a.p.y, a.p.ytype, (tok0 + col) * a.p.r + row, v);
-  }
-  if (a.ctas_k > 1) {                               // the sums stay until all have read them
-    __syncwarp();
-    cluster_sync();
-  } else if (tile + ctas < tiles) {
-    __syncthreads();                                // nor may the next tile's sums come early
-  }
+    if (a.ctas_k > 1) {                               // the sums stay until all have read them
+      __syncwarp();
+      cluster_sync();
+    } else if (tile + ctas < tiles) {
+      __syncthreads();                                // nor may the next tile's sums come early
+    }
   }
   cp_wait<0>();
 }
@@ -727,7 +737,8 @@ int launch_few(const PackedArgs &p, cudaStream_t st) {
       const int64_t rounds = (ctas + (int64_t)sms * res - 1) / ((int64_t)sms * res);
       const int64_t busy = ctas >= (int64_t)sms * res ? res : (ctas + sms - 1) / sms;
       const int64_t stage = 110 * w * busy + 480;
-      const int64_t cost = rounds * ((stages + w * c - 1) / (w * c) * stage + 170 * w + (c > 1 ? 1500 : 0)) + 3000;
+      const int64_t join = 170 * w + (c > 1 ? 1500 : 0);
+      const int64_t cost = rounds * ((stages + w * c - 1) / (w * c) * stage + join) + 3000;
       if (cost <= best) best = cost, warps = w, ck = c, fit = res, smem = need;
     }
   }
