@@ -430,6 +430,7 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
     }
   };
 
+  if (a.p.follows) asm volatile("griddepcontrol.wait;" ::: "memory");   // x
 #pragma unroll
   for (int i = 0; i < F::STAGES - 1; ++i) {
     issue(i);
@@ -749,17 +750,19 @@ int launch_few(const PackedArgs &p, cudaStream_t st) {
   int64_t clusters = (int64_t)sms * fit / (blocks * ck);
   if (clusters < 1) clusters = 1;
   if (clusters > tiles) clusters = tiles;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ck;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = ck;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * ck), (unsigned)blocks);
   cfg.blockDim = dim3(32 * warps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = ck > 1 ? 1 : 0;
+  cfg.attrs = p.follows ? at : at + 1;
+  cfg.numAttrs = (p.follows ? 1 : 0) + (ck > 1 ? 1 : 0);
   count_launch();
   const cudaError_t e = cudaLaunchKernelEx(&cfg, packed_few_kernel<BITS, XT, NT, FINE>, a);
   if (e != cudaSuccess) {

@@ -42,6 +42,8 @@ template <typename T, bool WIDEN>
 __global__ void __launch_bounds__(GATHER_THREADS)
     gather_columns_kernel(const T *__restrict__ x, const int32_t *__restrict__ perm, int d,
                           void *__restrict__ out) {
+  // (the product starts beside this kernel and waits for it before it reads x)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   using O = typename std::conditional<WIDEN, uint16_t, T>::type;
   const int j0 = (blockIdx.y * GATHER_THREADS + threadIdx.x) * 8;
   if (j0 >= d) return;   // d % 8 == 0
@@ -130,7 +132,8 @@ extern "C" int gptq_packed_linear(const void *x, int xtype, const float *x_scale
     if (widen) xtype = GPTQ_F16;
   }
   const PackedArgs a{x, x_scales, reinterpret_cast<const uint32_t *>(qweight), scales, zeros,
-                     bias, y, n, r, (int)d, bits, group, group < 0 ? 1 : (int)(d / group), xtype, ytype};
+                     bias, y, n, r, (int)d, bits, group, group < 0 ? 1 : (int)(d / group), xtype, ytype,
+                     widen || perm ? 1 : 0};
   if (!few) return launch_packed_many(a, st);
   return xtype == GPTQ_F16    ? launch_packed_few_f16(a, st)
          : xtype == GPTQ_BF16 ? launch_packed_few_bf16(a, st)

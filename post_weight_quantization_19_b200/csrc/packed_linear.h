@@ -18,6 +18,7 @@ struct PackedArgs {
   void *y;                    // [n x r] of ytype
   int64_t n, r;
   int d, bits, group, G, xtype, ytype;
+  int follows;         // x is written by a kernel just launched on the stream (griddepcontrol)
 };
 
 // Few tokens: warp-level products on codes straight from the packed rows.

@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
   if (warp == 0) {
     // ---------------------------------------------------------------- x by TMA
     if (lane == 0) {
+      if (a.p.follows) asm volatile("griddepcontrol.wait;" ::: "memory");   // x; the codes are there
       int stage = 0;
       uint32_t phase = 0, issued = 0, issued_par = 0;
       bool ok = true;
@@ -867,17 +868,19 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
   }
   static std::atomic<bool> attr[64] = {};
   if (const int rc = ensure_smem_attr(packed_many_kernel<BITS, T>, MANY_SMEM + 1024, attr)) return rc;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ck;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = ck;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(ck > 1 ? tiles * ck : (tiles < sms ? tiles : sms)));
   cfg.blockDim = dim3(MANY_THREADS);
   cfg.dynamicSmemBytes = bytes + 1024;
   cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = ck > 1 ? 1 : 0;
+  cfg.attrs = p.follows ? at : at + 1;
+  cfg.numAttrs = (p.follows ? 1 : 0) + (ck > 1 ? 1 : 0);
   count_launch();
   const cudaError_t e = cudaLaunchKernelEx(&cfg, packed_many_kernel<BITS, T>, tx, tw, a);
   if (e != cudaSuccess) {
