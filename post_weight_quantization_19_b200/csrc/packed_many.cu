@@ -1,7 +1,9 @@
 // gptq_packed_linear for many tokens: y = x W^^T + bias on the 5th-generation
 // tensor cores, the weights dequantised on their way into tensor memory.
 //
-// One CTA per tile of 128 rows of W and N <= 192 tokens, or twice N <= 160.  The
+// Up to 192 tokens: one CTA per tile of 128 rows of W and all tokens.  More: a
+// pair of CTAs per tile of 256 rows and N <= 192 tokens, or twice as many in two
+// accumulators that share the weights' conversion.  The
 // weights are the MMA's A operand, in tensor memory: TMA brings blocks of 128
 // rows x 256 columns of codes to shared memory (rows that are not multiples of
 // 16 bytes: cp.async; threads that each copied their own row's 32 bytes ran at
@@ -9,8 +11,11 @@
 // turns 64 columns of it into 16-bit weights and writes them to its TMEM lane
 // (tcgen05.st).  x is the B operand: tiles of 64 features x N tokens that TMA
 // places in 128-byte-swizzled shared memory.  So shared memory carries x and the
-// codes, not the weights, and a code costs about 2.5 instructions once per tile;
-// for prompts two accumulators share a tile's weights.
+// codes, not the weights, and a code costs about 2.5 instructions once per tile.
+// In a pair each CTA loads half of the tokens' x and the MMAs (cta_group::2) read
+// both halves: without pairs every CTA loaded all of its x from L2, 64 KB per 1024
+// clocks of MMAs for 256 tokens, and L2's bandwidth was the bound (4096 tokens x 4096
+// x 11008: 287 us, with pairs 241; 512 tokens x 8192 x 8192: 65.5 and 57.6).
 //
 //   w = T16(s (q - z)):  q - z is exact in 16 bits (code bits in the mantissa of
 //   a power of two M, minus M + z); s is split in two 16-bit parts, so w =
@@ -27,11 +32,10 @@
 // tiles than SMs the k range is split over a cluster, whose CTAs add their sums
 // through distributed shared memory in a fixed order.
 //
-// Measured (4 bits, groups of 128): 4096 tokens x 4096 x 11008, bf16, 287 us in a
-// burst = 1287 TFLOP/s (0.77 of the measured burst rate; the rest is conversion,
-// the integer pipe's 37 %, and each tile's fill and drain); 1000 tokens of 8-bit x,
-// 11008 x 4096, 107 to 111 us; 64 tokens x 4096 x 4096, 13.3 us, bound by start,
-// fill and the cluster's sums.
+// Measured (4 bits, groups of 128): 4096 tokens x 4096 x 11008, bf16, 241 us in a
+// burst = 1532 TFLOP/s (0.92 of the measured burst rate); 1000 tokens of 8-bit x,
+// 11008 x 4096, 91 us (129 tiles over 74 pairs of SMs are two rounds); 64 tokens x 4096
+// x 4096, 13.3 us, bound by start, fill and the cluster's sums.
 #include <mutex>
 
 #include "packed_linear.h"
@@ -41,7 +45,6 @@ namespace {
 
 constexpr int PM = 128;                 // rows of W per tile (UMMA M)
 constexpr int PN = 192;                 // most tokens per tile (UMMA N)
-constexpr int PN2 = 160;                // and per accumulator where a tile has two
 constexpr int PK = 64;                  // features per box of x (one 128-byte row)
 constexpr int SK = 2 * PK;              // features per step: two boxes, eight MMAs
 constexpr int ASTAGES = 2;              // TMEM stages of A: 64 columns each
@@ -122,6 +125,18 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// The same over a pair of CTAs: each CTA's 128 rows of A and D in its own tensor
+// memory, half of B's tokens in the shared memory of each.
+__device__ __forceinline__ void umma_f16_pair_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 // True in one thread of a converged warp.
@@ -325,7 +340,7 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int byt
                : "memory");
 }
 
-template <int BITS, typename T>
+template <int BITS, typename T, bool PAIR>
 __global__ void __launch_bounds__(MANY_THREADS, 1)
     packed_many_kernel(const __grid_constant__ CUtensorMap tmX,
                        const __grid_constant__ CUtensorMap tmW, const ManyArgs a) {
@@ -336,10 +351,16 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
   uint8_t *smem =
       reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int N = a.N, box_bytes = N * PK * 2, bstage_bytes = 2 * box_bytes;
-  const int crank = blockIdx.x % a.ctas_k;
-  const int ctas = gridDim.x / a.ctas_k, cta = blockIdx.x / a.ctas_k;
-  const int tiles = a.nM * a.nN;
+  // PAIR: two CTAs, `rank` 0 (which issues the MMAs) and 1, with a row tile each
+  // and half of the tokens' x.  Otherwise ctas_k CTAs share a tile along k.
+  const int N = a.N, box_bytes = (PAIR ? N / 2 : N) * PK * 2, bstage_bytes = 2 * box_bytes;
+  const int rank = PAIR ? (int)cluster_rank() : 0, sharing = PAIR ? 2 : a.ctas_k;
+  const int crank = PAIR ? 0 : blockIdx.x % a.ctas_k;
+  const int ctas = gridDim.x / sharing, cta = blockIdx.x / sharing;
+  const int nMt = PAIR ? (a.nM + 1) / 2 : a.nM;
+  const int tiles = nMt * a.nN;
+  // first row of this CTA in tile t (past the last row for an odd pair's second CTA)
+  auto first_row = [&](int t) { return (int64_t)(PAIR ? t % nMt * 2 + rank : t % nMt) * PM; };
   const int total = (a.p.d + SK - 1) / SK, blocks = (total + BLK - 1) / BLK;
   const int kb0 = (int)((int64_t)blocks * crank / a.ctas_k);          // this CTA's blocks
   const int kb1 = (int)((int64_t)blocks * (crank + 1) / a.ctas_k);
@@ -351,7 +372,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       mbar_init(&sh.empty_b[s], 1);
     }
     for (int s = 0; s < ASTAGES; ++s) {
-      mbar_init(&sh.full_a[s], 8);
+      mbar_init(&sh.full_a[s], PAIR ? 16 : 8);
       mbar_init(&sh.empty_a[s], 1);
     }
     for (int c = 0; c < C::DEPTH; ++c) {
@@ -360,7 +381,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh.acc_full[b], 1);
-      mbar_init(&sh.acc_empty[b], 4);
+      mbar_init(&sh.acc_empty[b], PAIR ? 8 : 4);
     }
     mbar_init(&sh.drain, 1);
     sh.abort = 0;
@@ -368,12 +389,21 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     prefetch_tmap(&tmX);
     if (a.aligned) prefetch_tmap(&tmW);
   }
+  __syncwarp();
   if (warp == 1) {
-    tmem_alloc(&sh.tmem_base, 512);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(&sh.tmem_base, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&sh.tmem_base, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (PAIR)
+    cluster_sync();   // both CTAs' barriers before either signals the other
+  else
+    __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
 
@@ -385,7 +415,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       uint32_t phase = 0, issued = 0, issued_par = 0;
       bool ok = true;
       for (int t = cta; t < tiles && ok; t += ctas) {
-        const int n0 = (t / a.nM) * (N * a.halves);
+        const int n0 = (t / nMt) * (N * a.halves) + rank * (N / 2);
         for (int q = ks0 * a.halves; q < ks1 * a.halves; ++q) {
           const int ks = a.halves == 2 ? q >> 1 : q, h = a.halves == 2 ? q & 1 : 0;
           if (*(volatile int *)&sh.abort) {
@@ -397,13 +427,21 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&sh.full_b[stage], bstage_bytes);
-          issued |= 1u << stage;
-          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+          if (rank == 0) {
+            mbar_arrive_expect_tx(&sh.full_b[stage], PAIR ? 2 * bstage_bytes : bstage_bytes);
+            issued |= 1u << stage;
+            issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+          }
           // feature offsets: multiples of 64 16-bit values = 128 bytes (past d: zeros)
           uint8_t *dst = smem + (size_t)stage * bstage_bytes;
-          tma_load_2d(dst, &tmX, ks * SK, n0 + h * N, &sh.full_b[stage]);
-          tma_load_2d(dst + box_bytes, &tmX, ks * SK + PK, n0 + h * N, &sh.full_b[stage]);
+          if constexpr (PAIR) {   // counted on the issuing CTA's barrier
+            const uint32_t bar = cluster_addr(&sh.full_b[stage], 0);
+            tma_load_2d_pair(dst, &tmX, ks * SK, n0 + h * N, bar);
+            tma_load_2d_pair(dst + box_bytes, &tmX, ks * SK + PK, n0 + h * N, bar);
+          } else {
+            tma_load_2d(dst, &tmX, ks * SK, n0 + h * N, &sh.full_b[stage]);
+            tma_load_2d(dst + box_bytes, &tmX, ks * SK + PK, n0 + h * N, &sh.full_b[stage]);
+          }
           if (++stage == a.bstages) {
             stage = 0;
             phase ^= 1;
@@ -412,8 +450,12 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       }
       for (int s = 0; s < MAXB; ++s)
         if (issued & (1u << s)) (void)mbar_wait_bounded(&sh.full_b[s], (issued_par >> s) & 1u);
+      // a second CTA whose loads the other may not have waited for: time to land
+      if (PAIR && rank == 1 && !ok)
+        for (const unsigned long long t0 = global_ns(); global_ns() - t0 < 1000000;) {
+        }
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------------------- the MMAs
     // The whole warp walks the loop, so that what the MMAs take (tensor-memory
     // addresses, descriptors) stays in uniform registers, and one elected thread
@@ -421,7 +463,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     // issue, as long as 120 tokens take to multiply.  Descriptors advance by
     // constants (16-byte units); a step is eight MMAs per accumulator.
     const uint32_t fmt = HALF ? 0u : 1u;
-    const uint32_t idesc = instr_desc(fmt, fmt, 0, 0, PM, N);
+    const uint32_t idesc = instr_desc(fmt, fmt, 0, 0, PAIR ? 2 * PM : PM, N);
     const uint64_t first = smem_desc(smem_u32(smem), 16, 1024, 2);
     const uint32_t box = (uint32_t)box_bytes >> 4;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -439,15 +481,26 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       tc_fence_after();
       if (elect_one()) {
         const uint32_t dt = tm + buf * PN, ad = tm + TM_A + j * (SK / 2);
-        umma_f16_ts(dt, ad, bdesc, idesc, fresh ? 0u : 1u);
+        auto mma = [&](uint32_t at, uint64_t desc, uint32_t accumulate) {
+          if constexpr (PAIR)
+            umma_f16_pair_ts(dt, at, desc, idesc, accumulate);
+          else
+            umma_f16_ts(dt, at, desc, idesc, accumulate);
+        };
+        auto commit = [&](uint64_t *bar) {
+          if constexpr (PAIR)
+            umma_commit_both(bar);
+          else
+            umma_commit(bar);
+        };
+        mma(ad, bdesc, fresh ? 0u : 1u);
 #pragma unroll
-        for (int kk = 1; kk < 4; ++kk) umma_f16_ts(dt, ad + kk * 8, bdesc + kk * 2, idesc, 1u);
+        for (int kk = 1; kk < 4; ++kk) mma(ad + kk * 8, bdesc + kk * 2, 1u);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_f16_ts(dt, ad + 32 + kk * 8, bdesc + box + kk * 2, idesc, 1u);
-        umma_commit(&sh.empty_b[bstage]);
-        if (frees_a) umma_commit(&sh.empty_a[j]);
-        if (last) umma_commit(&sh.acc_full[buf]);
+        for (int kk = 0; kk < 4; ++kk) mma(ad + 32 + kk * 8, bdesc + box + kk * 2, 1u);
+        commit(&sh.empty_b[bstage]);
+        if (frees_a) commit(&sh.empty_a[j]);
+        if (last) commit(&sh.acc_full[buf]);
       }
       __syncwarp();
       if (last) cphase ^= 1u << buf;
@@ -473,11 +526,14 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     if (!ok && lane == 0) many_timeout(a.status, sh);
     __syncwarp();
     if (elect_one()) {
-      umma_commit(&sh.drain);
+      if constexpr (PAIR)
+        umma_commit_pair_local(&sh.drain);
+      else
+        umma_commit(&sh.drain);
       (void)mbar_wait_bounded(&sh.drain, 0);
     }
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp >= 2 && warp < 4) {
     // ---------------------------------------------------------------- codes to shared memory
     const int id = threadIdx.x - 64;
     const int64_t pitch = (int64_t)(a.p.d / 32) * BITS * 4;   // bytes per row
@@ -487,7 +543,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int t = cta; t < tiles && ok; t += ctas) {
-      const int64_t m0 = (int64_t)(t % a.nM) * PM;
+      const int64_t m0 = min(first_row(t), (int64_t)(a.nM - 1) * PM);
       const int rows = (int)min((int64_t)PM, a.p.r - m0);
       const char *q0 = reinterpret_cast<const char *>(a.p.qweight) + m0 * pitch;
       for (int kb = kb0; kb < kb1; ++kb) {
@@ -541,7 +597,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp < 4 + 4 * WGS) {
+  } else if (warp >= 4 && warp < 4 + 4 * WGS) {
     // ---------------------------------------------------------------- weights to TMEM
     const int wg = (warp - 4) >> 2, quarter = warp & 3;
     const int as = wg / 2;                   // step of the block, A stage
@@ -562,7 +618,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         // PM / (4 WGS) rows, lanes along the groups
         const int ga = group_of(a, ks0 * (SK / 32)), gb = group_of(a, min(ks1 * (SK / 32), a.p.d / 32) - 1);
         constexpr int EACH = PM / (4 * WGS);
-        const int64_t m0 = (int64_t)(t % a.nM) * PM + (warp - 4) * EACH;
+        const int64_t m0 = first_row(t) + (warp - 4) * EACH;
         uint32_t top[EACH] = {};
         for (int g = ga + lane; g <= gb; g += 32) {
 #pragma unroll
@@ -633,7 +689,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&sh.full_a[as]);
+            if constexpr (PAIR)
+              mbar_arrive_cluster(cluster_addr(&sh.full_a[as], 0));
+            else
+              mbar_arrive(&sh.full_a[as]);
             mbar_arrive(&sh.empty_c[slot]);
           }
         } else if (lane == 0) {
@@ -645,7 +704,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         }
       }
     }
-  } else {
+  } else if (warp >= 4) {
     // ---------------------------------------------------------------- results
     const int quarter = warp & 3;
     const int lrow = quarter * 32 + lane;
@@ -653,7 +712,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     float *part = reinterpret_cast<float *>(smem);   // split k: [N][PM] sums of this CTA
     bool ok = true;
     for (int t = cta; t < tiles && ok; t += ctas, abuf ^= 1) {
-      const int64_t row = (int64_t)(t % a.nM) * PM + lrow;
+      const int64_t row = first_row(t) + lrow;
       const bool live = row < a.p.r;
       float f = 1.f;
       if constexpr (HALF) {
@@ -674,10 +733,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         cphase ^= 1u << buf;
         tc_fence_after();
         const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + buf * PN;
-        const int64_t t0 = ((int64_t)(t / a.nM) * a.halves + h) * N;
+        const int64_t t0 = ((int64_t)(t / nMt) * a.halves + h) * N;
         // tokens of this accumulator that exist
         const int count = (int)(a.p.n - t0 < N ? (a.p.n - t0 > 0 ? a.p.n - t0 : 0) : N);
-        if (a.ctas_k > 1) {
+        if (!PAIR && a.ctas_k > 1) {
           for (int c0 = 0; c0 < N; c0 += 16) {
             float v[16];
             tmem_ld_32x32b_x16(base + c0, v);
@@ -695,13 +754,18 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
+        if (lane == 0) {
+          if constexpr (PAIR)
+            mbar_arrive_cluster(cluster_addr(&sh.acc_empty[buf], 0));
+          else
+            mbar_arrive(&sh.acc_empty[buf]);
+        }
       }
     }
   }
 
   __syncthreads();
-  if (a.ctas_k > 1) {
+  if (!PAIR && a.ctas_k > 1) {
     // one tile per cluster: add the CTAs' sums, each CTA its share of the tokens
     __syncwarp();
     cluster_sync();
@@ -752,11 +816,19 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     cluster_sync();
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (PAIR) {
+    __syncwarp();
+    cluster_sync();   // neither CTA's memory goes while the other may touch it
+  } else {
+    __syncthreads();
+  }
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem, 512);
+    else
+      tmem_dealloc(tmem, 512);
   }
 }
 
@@ -779,6 +851,34 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+template <int BITS, typename T, bool PAIR>
+int launch_kernel(const ManyArgs &a, const CUtensorMap &tx, const CUtensorMap &tw, int64_t ctas, int cluster,
+                  size_t bytes, cudaStream_t st) {
+  static std::atomic<bool> attr[64] = {};
+  if (const int rc = ensure_smem_attr(packed_many_kernel<BITS, T, PAIR>, MANY_SMEM + 1024, attr)) return rc;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(MANY_THREADS);
+  cfg.dynamicSmemBytes = bytes + 1024;
+  cfg.stream = st;
+  cfg.attrs = a.p.follows ? at : at + 1;
+  cfg.numAttrs = (a.p.follows ? 1 : 0) + (cluster > 1 ? 1 : 0);
+  count_launch();
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, packed_many_kernel<BITS, T, PAIR>, tx, tw, a);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    set_last_error(__FILE__, __LINE__, "kernel launch", e);
+    return GPTQ_ERR_CUDA;
+  }
+  return GPTQ_OK;
+}
+
 template <int BITS, typename T>
 int launch_many(const PackedArgs &p, cudaStream_t st) {
   ManyArgs a{};
@@ -786,16 +886,18 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
   const int sms = num_sms();
   const int64_t nM = (p.r + PM - 1) / PM;
   const int steps = (p.d + SK - 1) / SK;
-  // Tokens per tile: all of them when they fit one accumulator; else the width
-  // that wastes least.  A step of a tile takes its MMAs, about 4.7 clocks per
-  // token, or the conversion of its weights, about 1000 (both measured), whichever
-  // is longer; two accumulators halve the conversions.
+  // Tokens per tile: all of them when they fit one accumulator; else pairs of CTAs,
+  // and the width that wastes least.  A step of a tile takes its MMAs, about 4.7
+  // clocks per token, or the conversion of its weights, about 1000 (both measured),
+  // whichever is longer; two accumulators halve the conversions.
+  const bool pair = p.n > PN;
+  const int64_t nMt = pair ? (nM + 1) / 2 : nM;
   int N = (int)((p.n + 15) / 16 * 16), halves = 1;
-  if (p.n > PN) {
+  if (pair) {
     int64_t best = INT64_MAX;
     for (int h = 1; h <= 2; ++h)
-      for (int c = h == 1 ? PN : PN2; c >= 80; c -= 16) {
-        const int64_t rounds = (nM * ((p.n + c * h - 1) / (c * h)) + sms - 1) / sms;
+      for (int c = PN; c >= 96; c -= 32) {
+        const int64_t rounds = (nMt * ((p.n + c * h - 1) / (c * h)) + sms / 2 - 1) / (sms / 2);
         const int64_t mma = c * h * 47 / 10, cost = rounds * (mma > 1000 ? mma : 1000);
         if (cost < best) best = cost, N = c, halves = h;
       }
@@ -806,12 +908,12 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
   a.halves = halves;
   a.nM = (int)nM;
   a.nN = (int)nN;
-  const int64_t tiles = nM * nN;
+  const int64_t tiles = nMt * nN;
   // k split over a cluster: the number of CTAs along it whose rounds over the SMs
   // take least, a CTA costing its steps and about ten more to start, fill and
   // add up (at least two blocks of codes each)
   int ck = 1;
-  if (halves == 1) {
+  if (!pair) {
     int64_t best = INT64_MAX;
     for (int c = 1; c <= 8 && (c == 1 || steps >= 2 * BLK * c); ++c) {
       // (one CTA walks several tiles without starting again; a split one does not)
@@ -821,7 +923,7 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
     }
   }
   a.ctas_k = ck;
-  const int stage = N * SK * 2;
+  const int stage = (pair ? N / 2 : N) * SK * 2;
   using C = CodeBlock<BITS>;
   a.subs = p.group < 0 || p.group % 256 == 0 ? 1 : p.group % 128 == 0 ? 2 : p.group % 64 == 0 ? 4 : 8;
   const size_t codes = (size_t)C::DEPTH * C::bytes(a.subs);
@@ -840,7 +942,7 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
   CUtensorMap tx;
   const cuuint64_t gdim[2] = {(cuuint64_t)p.d, (cuuint64_t)p.n};
   const cuuint64_t gstride[1] = {(cuuint64_t)p.d * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)PK, (cuuint32_t)N};
+  const cuuint32_t box[2] = {(cuuint32_t)PK, (cuuint32_t)(pair ? N / 2 : N)};
   const cuuint32_t es[2] = {1, 1};
   if (!enc || enc(&tx, Pair<T>::M == 0x64006400u ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -866,29 +968,10 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
       return GPTQ_ERR_CUDA;
     }
   }
-  static std::atomic<bool> attr[64] = {};
-  if (const int rc = ensure_smem_attr(packed_many_kernel<BITS, T>, MANY_SMEM + 1024, attr)) return rc;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = ck;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(ck > 1 ? tiles * ck : (tiles < sms ? tiles : sms)));
-  cfg.blockDim = dim3(MANY_THREADS);
-  cfg.dynamicSmemBytes = bytes + 1024;
-  cfg.stream = st;
-  cfg.attrs = p.follows ? at : at + 1;
-  cfg.numAttrs = (p.follows ? 1 : 0) + (ck > 1 ? 1 : 0);
-  count_launch();
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, packed_many_kernel<BITS, T>, tx, tw, a);
-  if (e != cudaSuccess) {
-    (void)cudaGetLastError();
-    set_last_error(__FILE__, __LINE__, "kernel launch", e);
-    return GPTQ_ERR_CUDA;
-  }
-  return GPTQ_OK;
+  if (pair)
+    return launch_kernel<BITS, T, true>(a, tx, tw, 2 * (tiles < sms / 2 ? tiles : sms / 2), 2, bytes, st);
+  return launch_kernel<BITS, T, false>(a, tx, tw, ck > 1 ? tiles * ck : (tiles < sms ? tiles : sms), ck, bytes,
+                                       st);
 }
 
 template <typename T>
