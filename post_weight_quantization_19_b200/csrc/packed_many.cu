@@ -3,9 +3,8 @@
 //
 // Up to 192 tokens: one CTA per tile of 128 rows of W and all tokens.  More: a
 // pair of CTAs per tile of 256 rows and N <= 192 tokens, or twice as many in two
-// accumulators that share the weights' conversion.  The
-// weights are the MMA's A operand, in tensor memory: TMA brings blocks of 128
-// rows x 256 columns of codes to shared memory (rows that are not multiples of
+// accumulators that share the weights' conversion.  The weights are the MMA's A
+// operand, in tensor memory: TMA brings blocks of 128 rows x 256 columns of codes to shared memory (rows that are not multiples of
 // 16 bytes: cp.async; threads that each copied their own row's 32 bytes ran at
 // half the speed), and thread i of a converter warpgroup, which owns row i,
 // turns 64 columns of it into 16-bit weights and writes them to its TMEM lane
@@ -28,13 +27,15 @@
 //
 // Warp 0 loads x, warp 1 issues the MMAs, warps 2-3 load codes, scales and zeros;
 // warps 4-19 are four converter warpgroups, one for each 64 columns of a block;
-// warps 20-23 drain the accumulators, one while the other fills.  With fewer
-// tiles than SMs the k range is split over a cluster, whose CTAs add their sums
-// through distributed shared memory in a fixed order.
+// warps 20-23 drain the accumulators, one while the other fills (23 ns a token; with
+// two accumulators that share weights nothing fills meanwhile.  The converter warps'
+// help there cost their own loop registers, and more time than it saved).  Up to 192
+// tokens and with fewer tiles than SMs the k range is split over a cluster, whose
+// CTAs add their sums through distributed shared memory in a fixed order.
 //
 // Measured (4 bits, groups of 128): 4096 tokens x 4096 x 11008, bf16, 241 us in a
 // burst = 1532 TFLOP/s (0.92 of the measured burst rate); 1000 tokens of 8-bit x,
-// 11008 x 4096, 91 us (129 tiles over 74 pairs of SMs are two rounds); 64 tokens x 4096
+// 11008 x 4096, 88 us (129 tiles over 74 pairs of SMs are two rounds); 64 tokens x 4096
 // x 4096, 13.3 us, bound by start, fill and the cluster's sums.
 #include <mutex>
 
@@ -52,7 +53,7 @@ constexpr int MAXB = 6;                 // shared-memory stages of x at most
 constexpr uint32_t TM_A = 2 * PN;       // TMEM column of the first A stage
 constexpr int WGS = 4;                  // converter warpgroups
 constexpr int MANY_THREADS = 32 * (4 + 4 * WGS + 4);
-constexpr size_t MANY_SMEM = 222 * 1024;   // x and codes, after alignment
+constexpr size_t MANY_SMEM = 219 * 1024;   // x and codes, after alignment
 
 constexpr int BLK = 2;                  // steps per block of codes; a warpgroup takes half a step
 constexpr int BCOLS = BLK * SK;         // its columns
@@ -102,6 +103,7 @@ struct ManyShared {
   int abort;
   uint32_t exponent[2][PM];   // fp16: row_exponent of a tile's rows
   alignas(16) uint4 stage[4][32];   // results on their way out, per warp
+  alignas(16) float scale[4][PN];   // and the scales of x's tokens
 };
 
 // D[tmem] (+)= A[tmem] * B[smem], 16-bit operands, fp32 accumulate.
@@ -301,7 +303,7 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bf
 // storing them as they lie cost 100 clocks a token.
 template <typename Y>
 __device__ __forceinline__ void write_tile(uint32_t base, int count, float f, float bias,
-                                           const float *x_scales, int64_t t0, int64_t row,
+                                           const float *scale, int64_t t0, int64_t row,
                                            const PackedArgs &p, uint4 *stage, int lane) {
   Y *y = static_cast<Y *>(p.y) + t0 * p.r + row;
   const bool live = row < p.r;
@@ -312,11 +314,9 @@ __device__ __forceinline__ void write_tile(uint32_t base, int count, float f, fl
   for (int c0 = 0; c0 < count; c0 += 16) {
     float v[16];
     tmem_ld_32x32b_x16(base + c0, v);
-    const float mine = x_scales && c0 + lane < count ? __ldg(x_scales + t0 + c0 + (lane & 15)) : 1.f;
     tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      v[i] = fmaf(v[i], f * (x_scales ? __shfl_sync(0xffffffffu, mine, i) : 1.f), bias);
+    for (int i = 0; i < 16; ++i) v[i] = fmaf(v[i], f * scale[c0 + i], bias);
     if (wide) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -726,6 +726,15 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       const float bias = a.p.bias && live ? load_as_float(a.p.bias, a.p.ytype, row) : 0.f;
       for (int h = 0; h < a.halves; ++h) {
         const uint32_t buf = a.halves == 2 ? h : abuf;
+        // the tokens' scales, while the accumulator fills (a load per 16 tokens as they
+        // were written took 5 us for 384 tokens)
+        const int64_t t0 = ((int64_t)(t / nMt) * a.halves + h) * N;
+        if (PAIR || a.ctas_k == 1) {
+          __syncwarp();
+          for (int c = lane; c < N; c += 32)
+            sh.scale[quarter][c] = a.p.x_scales && t0 + c < a.p.n ? __ldg(a.p.x_scales + t0 + c) : 1.f;
+          __syncwarp();
+        }
         ok = mbar_wait_bounded(&sh.acc_full[buf], (cphase >> buf) & 1u);
         if (!ok && lane == 0) many_timeout(a.status, sh);
         ok = __all_sync(0xffffffffu, ok);
@@ -733,7 +742,6 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         cphase ^= 1u << buf;
         tc_fence_after();
         const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + buf * PN;
-        const int64_t t0 = ((int64_t)(t / nMt) * a.halves + h) * N;
         // tokens of this accumulator that exist
         const int count = (int)(a.p.n - t0 < N ? (a.p.n - t0 > 0 ? a.p.n - t0 : 0) : N);
         if (!PAIR && a.ctas_k > 1) {
@@ -745,11 +753,11 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
             for (int i = 0; i < 16; ++i) part[(c0 + i) * PM + lrow] = v[i] * f;
           }
         } else if (a.p.ytype == GPTQ_F32) {
-          write_tile<float>(base, count, f, bias, a.p.x_scales, t0, row, a.p, sh.stage[quarter], lane);
+          write_tile<float>(base, count, f, bias, sh.scale[quarter], t0, row, a.p, sh.stage[quarter], lane);
         } else if (a.p.ytype == GPTQ_F16) {
-          write_tile<__half>(base, count, f, bias, a.p.x_scales, t0, row, a.p, sh.stage[quarter], lane);
+          write_tile<__half>(base, count, f, bias, sh.scale[quarter], t0, row, a.p, sh.stage[quarter], lane);
         } else {
-          write_tile<__nv_bfloat16>(base, count, f, bias, a.p.x_scales, t0, row, a.p, sh.stage[quarter],
+          write_tile<__nv_bfloat16>(base, count, f, bias, sh.scale[quarter], t0, row, a.p, sh.stage[quarter],
                                     lane);
         }
         tc_fence_before();
