@@ -4,11 +4,11 @@
 // Up to 192 tokens: one CTA per tile of 128 rows of W and all tokens.  More: a
 // pair of CTAs per tile of 256 rows and N <= 192 tokens, or twice as many in two
 // accumulators that share the weights' conversion.  The weights are the MMA's A
-// operand, in tensor memory: TMA brings blocks of 128 rows x 256 columns of codes to shared memory (rows that are not multiples of
-// 16 bytes: cp.async; threads that each copied their own row's 32 bytes ran at
-// half the speed), and thread i of a converter warpgroup, which owns row i,
-// turns 64 columns of it into 16-bit weights and writes them to its TMEM lane
-// (tcgen05.st).  x is the B operand: tiles of 64 features x N tokens that TMA
+// operand, in tensor memory: TMA brings blocks of 128 rows x 256 columns of codes to
+// shared memory (rows that are not multiples of 16 bytes: cp.async; threads that each
+// copied their own row's 32 bytes ran at half the speed), and thread i of a converter
+// warpgroup, which owns row i, turns 64 columns of it into 16-bit weights and writes
+// them to its TMEM lane (tcgen05.st).  x is the B operand: tiles of 64 features x N tokens that TMA
 // places in 128-byte-swizzled shared memory.  So shared memory carries x and the
 // codes, not the weights, and a code costs about 2.5 instructions once per tile.
 // In a pair each CTA loads half of the tokens' x and the MMAs (cta_group::2) read
