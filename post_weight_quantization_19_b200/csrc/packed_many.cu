@@ -53,7 +53,7 @@ constexpr int MAXB = 6;                 // shared-memory stages of x at most
 constexpr uint32_t TM_A = 2 * PN;       // TMEM column of the first A stage
 constexpr int WGS = 4;                  // converter warpgroups
 constexpr int MANY_THREADS = 32 * (4 + 4 * WGS + 4);
-constexpr size_t MANY_SMEM = 219 * 1024;   // x and codes, after alignment
+constexpr size_t MANY_SMEM = 217 * 1024;   // x and codes, after alignment
 
 constexpr int BLK = 2;                  // steps per block of codes; a warpgroup takes half a step
 constexpr int BCOLS = BLK * SK;         // its columns
@@ -102,7 +102,7 @@ struct ManyShared {
   uint32_t tmem_base;
   int abort;
   uint32_t exponent[2][PM];   // fp16: row_exponent of a tile's rows
-  alignas(16) uint4 stage[4][32];   // results on their way out, per warp
+  alignas(16) uint4 stage[4][64];   // results on their way out, per warp
   alignas(16) float scale[4][PN];   // and the scales of x's tokens
 };
 
@@ -296,11 +296,19 @@ __device__ __forceinline__ uint32_t safe_exponent(uint32_t top) {
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__half *p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ uint32_t pair_of(const __half *, float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t pair_of(const __nv_bfloat16 *, float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
 
-// One accumulator of a warp's 32 rows, `count` tokens from t0, to y.  A lane is a
-// row; 16-bit results go through 512 bytes of shared memory, eight tokens of 32
-// rows at a time, and out 16 bytes per lane (where y's rows allow it), for
-// storing them as they lie cost 100 clocks a token.
+// One accumulator of a warp's 32 rows, `count` tokens from t0 with scales `scale`, to
+// y.  A lane is a row; 16-bit results go as pairs of tokens through 1 KB of shared
+// memory, 16 tokens of 32 rows at a time, and out 16 bytes (8 rows of a token) per
+// lane, where y's rows allow it: storing them as they lie cost 100 clocks a token.
 template <typename Y>
 __device__ __forceinline__ void write_tile(uint32_t base, int count, float f, float bias,
                                            const float *scale, int64_t t0, int64_t row,
@@ -310,7 +318,7 @@ __device__ __forceinline__ void write_tile(uint32_t base, int count, float f, fl
   bool wide = false;
   if constexpr (sizeof(Y) == 2)
     wide = p.r % 8 == 0 && row - lane + 32 <= p.r && reinterpret_cast<uintptr_t>(p.y) % 16 == 0;
-  Y *yw = y - lane + (lane & 3) * 8 + (int64_t)(lane >> 2) * p.r;   // this lane's 8 rows of token lane / 4
+  Y *yw = y - lane + (lane & 3) * 8 + (int64_t)(lane >> 2) * 2 * p.r;   // this lane's 8 rows of two tokens
   for (int c0 = 0; c0 < count; c0 += 16) {
     float v[16];
     tmem_ld_32x32b_x16(base + c0, v);
@@ -318,14 +326,23 @@ __device__ __forceinline__ void write_tile(uint32_t base, int count, float f, fl
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = fmaf(v[i], f * scale[c0 + i], bias);
     if (wide) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      if constexpr (sizeof(Y) == 2) {
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) put(reinterpret_cast<Y *>(stage) + i * 32 + lane, v[h * 8 + i]);
+        for (int i = 0; i < 8; ++i)
+          reinterpret_cast<uint32_t *>(stage)[i * 32 + lane] = pair_of(y, v[2 * i], v[2 * i + 1]);
         __syncwarp();
-        if (c0 + h * 8 + (lane >> 2) < count)
-          *reinterpret_cast<uint4 *>(yw + (int64_t)(c0 + h * 8) * p.r) = stage[lane];
+        const uint4 a = stage[2 * lane], b = stage[2 * lane + 1];
+        Y *at = yw + (int64_t)c0 * p.r;
+        const int tok = c0 + (lane >> 2) * 2;
+        if (tok < count)
+          *reinterpret_cast<uint4 *>(at) =
+              make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                         __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410));
+        if (tok + 1 < count)
+          *reinterpret_cast<uint4 *>(at + p.r) =
+              make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                         __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632));
       }
     } else {
 #pragma unroll

@@ -139,6 +139,25 @@ def test_packed_linear_matches_oracle(shape, T):
     assert g.gptq_check_device_status() == 0
 
 
+@pytest.mark.parametrize("T", [F16, BF16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("n,r,d,bits,group", [
+    (193, 1, 32, 4, 32), (193, 40, 4096, 3, -1), (200, 129, 96, 8, 96), (256, 257, 1056, 2, 32),
+    (385, 128, 2080, 4, 416), (577, 384, 160, 3, 160), (1537, 136, 64, 4, 64)])
+def test_packed_linear_beyond_one_accumulator(n, r, d, bits, group, T):
+    # two row tiles at a time: one alone, an odd number of them, tokens that fill a
+    # tile exactly or by one; nothing behind y is written
+    import post_weight_quantization_19_b200 as g
+    q, s, z = layer(r, d, bits, group, seed=n + d)
+    x = activations(n, d, n + r, T)
+    room = torch.full((n * r + 128,), 7.0, dtype=T, device="cuda")
+    y = room[64:64 + n * r].view(n, r)
+    g.gptq_packed_linear(x, *dev(q, s, z), bits, group, y=y)
+    ref, absum = reference(x, q, s, z, bits, group)
+    assert_product(y, ref, absum, d, wtype=T)
+    assert bool((room[:64] == 7).all()) and bool((room[-64:] == 7).all())
+    assert g.gptq_check_device_status() == 0
+
+
 @pytest.mark.parametrize("T", [F16, BF16, F32], ids=["fp16", "bf16", "fp32"])
 @pytest.mark.parametrize("shape", SHAPES, ids=IDS)
 def test_packed_linear_int8_matches_oracle(shape, T):
