@@ -1,9 +1,9 @@
 // gptq_packed_linear for many tokens: y = x W^^T + bias on the 5th-generation
 // tensor cores, the weights dequantised on their way into tensor memory.
 //
-// Up to 192 tokens: one CTA per tile of 128 rows of W and all tokens.  More: a
-// pair of CTAs per tile of 256 rows and N <= 192 tokens, or twice as many in two
-// accumulators that share the weights' conversion.  The weights are the MMA's A
+// Up to 192 tokens, and a few hundred of small layers: one CTA per tile of 128 rows
+// of W and N <= 192 tokens.  More: a pair of CTAs per tile of 256 rows and N <= 192
+// tokens, or twice as many in two accumulators that share the weights' conversion.  The weights are the MMA's A
 // operand, in tensor memory: TMA brings blocks of 128 rows x 256 columns of codes to
 // shared memory (rows that are not multiples of 16 bytes: cp.async; threads that each
 // copied their own row's 32 bytes ran at half the speed), and thread i of a converter
@@ -29,13 +29,13 @@
 // warps 4-19 are four converter warpgroups, one for each 64 columns of a block;
 // warps 20-23 drain the accumulators, one while the other fills (23 ns a token; with
 // two accumulators that share weights nothing fills meanwhile.  The converter warps'
-// help there cost their own loop registers, and more time than it saved).  Up to 192
-// tokens and with fewer tiles than SMs the k range is split over a cluster, whose
-// CTAs add their sums through distributed shared memory in a fixed order.
+// help there cost their own loop registers, and more time than it saved).  Single CTAs
+// with fewer tiles than SMs split the k range over a cluster, whose CTAs add their
+// sums through distributed shared memory in a fixed order.
 //
 // Measured (4 bits, groups of 128): 4096 tokens x 4096 x 11008, bf16, 241 us in a
 // burst = 1532 TFLOP/s (0.92 of the measured burst rate); 1000 tokens of 8-bit x,
-// 11008 x 4096, 88 us (129 tiles over 74 pairs of SMs are two rounds); 64 tokens x 4096
+// 11008 x 4096, 84 to 88 us (129 tiles over 74 pairs of SMs are two rounds); 64 tokens x 4096
 // x 4096, 13.3 us, bound by start, fill and the cluster's sums.
 #include <mutex>
 
@@ -914,19 +914,37 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
   // Tokens per tile: all of them when they fit one accumulator; else pairs of CTAs,
   // and the width that wastes least.  A step of a tile takes its MMAs, about 4.7
   // clocks per token, or the conversion of its weights, about 1000 (both measured),
-  // whichever is longer; two accumulators halve the conversions.
-  const bool pair = p.n > PN;
-  const int64_t nMt = pair ? (nM + 1) / 2 : nM;
-  int N = (int)((p.n + 15) / 16 * 16), halves = 1;
+  // whichever is longer; two accumulators halve the conversions.  Where that leaves
+  // most SMs idle, single CTAs that split k are faster: a step takes them about 1.2
+  // times as long, and 14 steps go to start, fill and add up (pairs take ten).
+  // Measured (pairs, single; us): 256 tokens, 4096 x 4096 26.1, 20.2; 4096 x 11008
+  // 58.9, 37.3; 8192 x 8192 46.9, 51.8; 512 tokens, 4096 x 4096 27.1, 30.0.
+  bool pair = p.n > PN;
+  int N = (int)((p.n + 15) / 16 * 16), halves = 1, ck = 1;
   if (pair) {
     int64_t best = INT64_MAX;
     for (int h = 1; h <= 2; ++h)
       for (int c = PN; c >= 96; c -= 32) {
-        const int64_t rounds = (nMt * ((p.n + c * h - 1) / (c * h)) + sms / 2 - 1) / (sms / 2);
-        const int64_t mma = c * h * 47 / 10, cost = rounds * (mma > 1000 ? mma : 1000);
+        const int64_t pairs = (nM + 1) / 2 * ((p.n + c * h - 1) / (c * h));
+        const int64_t rounds = (pairs + sms / 2 - 1) / (sms / 2), mma = c * h * 47 / 10;
+        // (a round fills its pipeline again: 1000 tokens x 11008 x 4096, two rounds of 384
+        // 86 us, three of 256 95)
+        const int64_t cost = rounds * (steps * (mma > 1000 ? mma : 1000) + 3000) + 10000;
         if (cost < best) best = cost, N = c, halves = h;
       }
+    // (7/8 of the SMs and clusters of four at most: larger ones do not all find room
+    // at once; 256 tokens x 1024 x 4096 in 16 clusters of eight 24.6, of four 14.8)
+    const int64_t parts = (p.n + PN - 1) / PN;
+    for (int k = 2; k <= 4 && steps >= 2 * BLK * k && nM * parts * k <= sms * 7 / 8; ++k)
+      if (((steps + k - 1) / k + 14) * 1200 < best) {
+        best = ((steps + k - 1) / k + 14) * 1200;
+        pair = false;
+        N = (int)((p.n + parts * 16 - 1) / (parts * 16) * 16);
+        halves = 1;
+        ck = k;
+      }
   }
+  const int64_t nMt = pair ? (nM + 1) / 2 : nM;
   const int64_t nN = (p.n + N * halves - 1) / (N * halves);
   if (nM * nN > INT32_MAX / 8) return GPTQ_ERR_INVALID_ARG;
   a.N = N;
@@ -934,16 +952,18 @@ int launch_many(const PackedArgs &p, cudaStream_t st) {
   a.nM = (int)nM;
   a.nN = (int)nN;
   const int64_t tiles = nMt * nN;
-  // k split over a cluster: the number of CTAs along it whose rounds over the SMs
-  // take least, a CTA costing its steps and about ten more to start, fill and
-  // add up (at least two blocks of codes each)
-  int ck = 1;
-  if (!pair) {
+  // k split over a cluster: the number of CTAs along it that takes least, a CTA
+  // costing its steps and about ten more to start, fill and add up (at least two
+  // blocks of codes each), of those whose clusters all find room at once: pairs on
+  // every SM, up to four on 7/8 of them, eight on half (64 tokens x 2048 x 4096 as 16
+  // clusters of eight 20.9 us, of four 13.1)
+  if (p.n <= PN) {
     int64_t best = INT64_MAX;
     for (int c = 1; c <= 8 && (c == 1 || steps >= 2 * BLK * c); ++c) {
+      if (c > 1 && tiles * c > (c == 2 ? sms : c <= 4 ? sms * 7 / 8 : sms / 2)) break;
       // (one CTA walks several tiles without starting again; a split one does not)
-      const int64_t rounds = (tiles * c + sms - 1) / sms, each = (steps + c - 1) / c;
-      const int64_t cost = c == 1 ? rounds * each + 10 : rounds * (each + 12);
+      const int64_t rounds = (tiles + sms - 1) / sms, each = (steps + c - 1) / c;
+      const int64_t cost = c == 1 ? rounds * each + 10 : each + 12;
       if (cost < best) best = cost, ck = c;
     }
   }
