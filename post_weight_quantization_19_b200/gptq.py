@@ -413,7 +413,8 @@ def gptq_regroup(qweight: torch.Tensor, g_idx: torch.Tensor, bits: int, group: i
                  out: torch.Tensor | None = None, perm: torch.Tensor | None = None,
                  stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """The columns of a packed act-order layer sorted by group, and their order:
-    column j of the first result is column perm[j] of ``qweight``."""
+    column j of the first result is column perm[j] of ``qweight``.  Waits until the
+    order has been checked; the columns follow on the stream."""
     lib = _abi.load()
     if not g_idx.is_cuda or g_idx.dim() != 1:
         raise ValueError("g_idx must be a CUDA tensor [d]")
