@@ -347,7 +347,9 @@ int gptq_rmsnorm_int8(const void *x, const void *residual, const void *gamma, in
  *   columns), one rounding to `ytype`.  For few tokens (up to 8 at least) the
  *   codes and zero points enter exactly; for many, weights s (q - z) are
  *   rounded once to the 16-bit type of the tensor-core product, as
- *   gptq_dequant_fp16 does.  Results do not change from call to call.
+ *   gptq_dequant_fp16 does.  Results do not change from call to call.  Infinities
+ *   and NaN in x give what the formula gives (0 times an infinity: NaN), in their
+ *   own token.
  *   n == 0 or r == 0: nothing to do.  Asynchronous; a bounded in-kernel wait
  *   that runs out is reported by gptq_check_device_status.
  *

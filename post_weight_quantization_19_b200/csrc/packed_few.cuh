@@ -28,7 +28,8 @@
 // group adds
 //   s (sum (B + q) x - (B + z) sum x).
 // The terms that cancel are at most (B + q + z) / |q - z| times what q - z itself
-// would sum, held in fp32.  8-bit x: q and x as integers, sums exact.
+// would sum, held in fp32; results that are no numbers for it (infinities in x) are
+// formed again from q - z (settle_lost).  8-bit x: q and x as integers, sums exact.
 //
 // Each warp runs its own ring of cp.async stages of 128 columns (weights, x,
 // scales, zeros) and meets the others only at the end: the k range is split
@@ -306,6 +307,27 @@ struct FewArgs {
   uint32_t gdiv;     // ceil(2^31 / (group / 32)), 0 for one group
 };
 
+// A thread's results that are no numbers again, from their definition, after its last
+// tile.  A function of its own, with its arguments by value: as part of the kernel, in
+// or behind the loop over the tiles, it cost every call 4 to 14 % (12288 x 49152, 3 bits,
+// one token: 128 us, 134 to 146).  A thread takes a result, so a token with an infinity
+// costs milliseconds on the largest layers.
+template <int BITS, int NT>
+__device__ __noinline__ void settle_lost(const FewArgs a, int crank, int cta, int ctas) {
+  constexpr int CELLS = ROWS * 8 * NT;
+  const int per = CELLS / a.ctas_k, first = crank * per;
+  const int64_t tok0 = (int64_t)blockIdx.y * (8 * NT);
+  for (int64_t row0 = (int64_t)cta * ROWS; row0 < a.p.r; row0 += (int64_t)ctas * ROWS)
+    for (int i = first + threadIdx.x; i < first + per; i += blockDim.x) {
+      const int64_t tok = tok0 + i / ROWS, row = row0 + i % ROWS;
+      if (tok >= a.p.n || row >= a.p.r) continue;
+      if (fabsf(load_as_float(a.p.y, a.p.ytype, tok * a.p.r + row)) <= 3.402823466e38f) continue;
+      float v = sum_in_64_bits<BITS>(a.p, tok, row);
+      if (a.p.bias) v += load_as_float(a.p.bias, a.p.ytype, row);
+      store_float(a.p.y, a.p.ytype, tok * a.p.r + row, v);
+    }
+}
+
 template <int BITS, int XT, int NT, bool FINE>
 __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
     packed_few_kernel(const FewArgs a) {
@@ -457,6 +479,7 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
   int slot = 0, cslot = 0;
   // [warps][COLS][ROWS]
   float *red = reinterpret_cast<float *>(smem + warps * (F::STAGES * a.stage_bytes + F::SZWARP));
+  bool lost = false;   // a result of this thread's is not a number's
   for (int tile = cta; tile < tiles; tile += ctas) {
     float acc[2][NT][4];
 #pragma unroll
@@ -686,6 +709,8 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
       }
       if constexpr (F::INT8) v *= a.p.x_scales[tok0 + col];
       if constexpr (XT == GPTQ_F16) v *= 16777216.f;   // the codes were q 2^-24
+      if constexpr (!F::INT8)
+        lost |= !(fabsf(v) <= 3.402823466e38f);
       if (a.p.bias) v += load_as_float(a.p.bias, a.p.ytype, row);
       store_float(a.p.y, a.p.ytype, (tok0 + col) * a.p.r + row, v);
     }
@@ -697,6 +722,8 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
     }
   }
   cp_wait<0>();
+  if constexpr (!F::INT8)
+    if (lost) settle_lost<BITS, NT>(a, crank, cta, ctas);
 }
 
 template <int BITS, int XT, int NT, bool FINE>

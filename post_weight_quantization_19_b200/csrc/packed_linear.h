@@ -44,4 +44,25 @@ __device__ __forceinline__ void store_float(void *p, int type, int64_t i, float 
     reinterpret_cast<float *>(p)[i] = v;
 }
 
+// sum_j s (q - z) x of one row and token in 64 bits, x in 16 bits: what a result
+// is where the few-token kernel's sums left the numbers -- an infinity or a NaN in x
+// (it forms sum (B + q) x - (B + z) sum x, and infinities of both signs), or values
+// whose multiples leave fp32 though the result does not.
+template <int BITS>
+__device__ __forceinline__ float sum_in_64_bits(const PackedArgs &p, int64_t tok, int64_t row) {
+  const uint32_t *w = p.qweight + row * (p.d / 32) * BITS;
+  double sum = 0.0;
+#pragma unroll 1
+  for (int j = 0; j < p.d && sum == sum; ++j) {
+    const int at = j * BITS, off = at & 31;
+    uint32_t q = w[at >> 5] >> off;
+    if (off + BITS > 32) q |= w[(at >> 5) + 1] << (32 - off);
+    const int64_t g = row * p.G + (p.group < 0 ? 0 : j / p.group);
+    const int z = min(max(p.zeros[g], 0), (1 << BITS) - 1);
+    sum += (double)p.scales[g] * ((int)(q & ((1u << BITS) - 1u)) - z) *
+           load_as_float(p.x, p.xtype, tok * p.d + j);
+  }
+  return (float)sum;
+}
+
 }  // namespace gptq

@@ -1,0 +1,90 @@
+"""The packed layer's operators on the GPU at values, lengths and orders where they
+can go wrong, against the float64 oracle.  Half a step of a type, relative to the
+value, is u: fp16 2^-11, bf16 2^-8, fp32 2^-24.
+"""
+
+import numpy as np
+import pytest
+
+import oracle
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32, I8 = torch.float16, torch.bfloat16, torch.float32, torch.int8
+HALF = {F16: 2.0 ** -11, BF16: 2.0 ** -8, F32: 2.0 ** -24}
+
+
+def words(r, d, bits, seed):
+    rng = np.random.default_rng(seed)
+    return rng.integers(-2 ** 31, 2 ** 31, size=(r, d * bits // 32), dtype=np.int64).astype(np.int32)
+
+
+def dev(*arrays):
+    return tuple(torch.from_numpy(a).cuda() for a in arrays)
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+# ------------------------------------------------------------------ infinities and huge values
+
+@pytest.mark.parametrize("T", [F16, BF16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("dtype", [None, F32], ids=["same", "fp32"])
+@pytest.mark.parametrize("n,bits,group", [(1, 4, 32), (1, 3, 128), (4, 2, -1), (6, 8, 64), (12, 4, 128),
+                                          (16, 8, -1), (40, 4, 32), (40, 8, 128), (220, 3, -1)])
+def test_packed_linear_infinite_and_huge_x(n, bits, group, T, dtype):
+    # An infinity gives +-inf as the code lies above or below the zero point and
+    # NaN where it is the zero point (0 inf) or where both signs meet; a finite
+    # value whose products are representable gives them.  Every token of the
+    # batch holds one such value in turn, so each place of a tile meets each kind.
+    # Weights are exact in 16 bits (scales are powers of two), so what is left is y's own
+    # rounding, 4 (d / 32 + 128) additions of at most a half step each over sum |w x|,
+    # and with few tokens and bf16 the terms that cancel, s (2 B + q + z) |x| with B <= 64,
+    # over a group's 24 additions.
+    import post_weight_quantization_19_b200 as g
+    r, d = 67, 512
+    q = words(r, d, bits, n + bits)
+    G = 1 if group == -1 else d // group
+    s = np.full((r, G), 2.0 ** -3, dtype=np.float32)
+    z = np.random.default_rng(n).integers(0, 1 << bits, size=(r, G)).astype(np.int32)
+    rng = np.random.default_rng(5)
+    X = np.float32(rng.standard_normal((n, d)))
+    huge = np.float32(2.0 ** 14 if T == F16 else 2.0 ** (125 - bits))
+    kinds = ("inf", "-inf", "both", "huge", "nan", "plain") if n > 1 else ("inf",)
+    kind = [kinds[t % len(kinds)] for t in range(n)]
+    for t, k in enumerate(kind):
+        c = (37 * t + 5) % d
+        if k == "inf":
+            X[t, c] = np.inf
+        elif k == "-inf":
+            X[t, c] = -np.inf
+        elif k == "both":
+            X[t, c], X[t, (c + 200) % d] = np.inf, -np.inf
+        elif k == "nan":
+            X[t, c] = np.nan
+        elif k == "huge" and T == BF16:
+            X[t, c] = -huge
+    x = torch.from_numpy(X).to(T).cuda()
+    y = g.gptq_packed_linear(x, *dev(q, s, z), bits, group, dtype=dtype)
+    got = f64(y)
+    codes = oracle.unpack_rows(q, bits, d)
+    gi = np.zeros(d, dtype=np.int64) if group == -1 else np.arange(d) // group
+    W = s.astype(np.float64)[:, gi] * (codes - z[:, gi])
+    xd = f64(x)
+    seen = set()
+    for t, k in enumerate(kind):
+        with np.errstate(invalid="ignore"):
+            ref = (W * xd[t]).sum(1)
+        if k in ("huge", "plain"):
+            assert np.all(np.isfinite(got[t]))
+            absum = np.abs(W) @ np.abs(xd[t])
+            parts = (s.astype(np.float64)[:, gi] * (128 + codes + z[:, gi])) @ np.abs(xd[t])
+            tol = HALF[y.dtype] * np.abs(ref) + 4 * 2.0 ** -24 * ((d / 32 + 128) * absum + 24 * parts)
+            assert np.all(np.abs(got[t] - ref) <= tol), (t, k)
+        else:
+            np.testing.assert_array_equal(got[t], ref, err_msg=f"token {t}: {k}")
+            seen.update("nan" if v != v else str(v) for v in ref)
+    assert "inf" in seen and "-inf" in seen
+    assert g.gptq_check_device_status() == 0
