@@ -88,3 +88,31 @@ def test_packed_linear_infinite_and_huge_x(n, bits, group, T, dtype):
             seen.update("nan" if v != v else str(v) for v in ref)
     assert "inf" in seen and "-inf" in seen
     assert g.gptq_check_device_status() == 0
+
+
+# ------------------------------------------------------------------ streams
+
+@pytest.mark.parametrize("normed", [False, True])
+def test_chain_on_a_stream_beside_a_busy_one(normed):
+    # the same bits as on the current stream, while that one is kept busy
+    import post_weight_quantization_19_b200 as g
+    from synth import make_activations, make_weights
+    shapes = [(384, 256), (128, 384)]
+    Ws = [torch.from_numpy(np.ascontiguousarray(make_weights(r, d, seed=51 + i), dtype=np.float32)).cuda()
+          for i, (r, d) in enumerate(shapes)]
+    norms = [torch.ones(d, dtype=F16, device="cuda") for _, d in shapes] if normed else None
+    X0 = torch.from_numpy(make_activations(2000, 256, seed=50)).cuda()
+    kw = dict(bits=4, group=64, act_order=True, keep_inputs=True, norms=norms)
+    want = g.quantize_chain(X0, Ws, **kw)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    busy = torch.zeros(1 << 26, device="cuda")
+    for _ in range(200):
+        busy += 1
+    got = g.quantize_chain(X0, Ws, stream=side, **kw)
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert a.keys() == b.keys()
+        for k in a:
+            assert torch.equal(a[k], b[k]) if torch.is_tensor(a[k]) else a[k] == b[k], k
+    torch.cuda.synchronize()

@@ -1,0 +1,77 @@
+"""Where the packed layer's operators and the chain take and touch memory, without a
+GPU: streams of a call's own tensors, memory that two arguments share, loads of what
+another kernel is still writing.
+"""
+
+import contextlib
+import os
+import re
+
+import pytest
+
+
+torch = pytest.importorskip("torch")
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "post_weight_quantization_19_b200", "csrc")
+
+
+def code_of(name):
+    """A source file without its comments."""
+    with open(os.path.join(CSRC, name), encoding="utf-8") as f:
+        return re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+
+
+@pytest.mark.parametrize("normed", [False, True])
+def test_chain_makes_its_tensors_on_its_stream(monkeypatch, normed):
+    # Everything that a chain on a given stream allocates, fills and launches is under
+    # that stream: a fill on the current one may come before or after its use.
+    from post_weight_quantization_19_b200 import chain
+    given, current, outside = object(), [None], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        current.append(stream)
+        yield
+        current.pop()
+
+    def watch(name, result):
+        def call(*args, stream=None, **kw):
+            if current[-1] is not given or stream is not given:
+                outside.append(name)
+            return result(*args, **kw)
+        return call
+
+    def made(name, make):
+        def call(*args, **kw):
+            if current[-1] is not given:
+                outside.append(name)
+            return make(*args, **kw)
+        return call
+
+    def solve(W, H, *, bits, group, g_idx, **kw):
+        r, d = W.shape
+        g_idx.copy_(torch.arange(d) // group)
+        return {"qweight": torch.zeros((r, d * bits // 32), dtype=torch.int32), "g_idx": g_idx,
+                "scales": torch.ones((r, d // group)), "zeros": torch.zeros((r, d // group)).int()}
+
+    fakes = {"gptq_hessian_accumulate": lambda X, H: None, "gptq_quantize_layer": solve,
+             "gptq_dequant_fp16": lambda q, s, z, d, *a, **kw: torch.zeros((q.shape[0], d)).half(),
+             "gptq_linear_fp16": lambda X, W: torch.zeros((X.shape[0], W.shape[0])).half(),
+             "gptq_rmsnorm_int8": lambda X, gamma, **kw: {"codes": X.char(), "xhat": X,
+                                                          "scales": torch.ones(X.shape[0])},
+             "gptq_regroup": lambda q, g_idx, *a: (q, g_idx),
+             "gptq_packed_linear": lambda x, q, *a, **kw: torch.zeros((x.shape[0], q.shape[0])).half()}
+    for name, f in fakes.items():
+        monkeypatch.setattr(chain, name, watch(name, f))
+    monkeypatch.setattr(chain, "_on", on, raising=False)
+
+    class Torch:
+        def __getattr__(self, name):
+            return made(name, getattr(torch, name)) if name in ("zeros", "empty") else getattr(torch, name)
+
+    monkeypatch.setattr(chain, "torch", Torch())
+    X, Ws = torch.zeros((8, 64)).half(), [torch.zeros((96, 64)), torch.zeros((32, 96))]
+    norms = [torch.ones(64).half(), torch.ones(96).half()] if normed else None
+    chain.quantize_chain(X, Ws, bits=4, group=32, act_order=True, norms=norms, stream=given)
+    assert not outside, outside
