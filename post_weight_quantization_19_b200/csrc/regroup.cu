@@ -175,11 +175,11 @@ __device__ __forceinline__ void transpose(uint32_t (&a)[R]) {
 __device__ __forceinline__ int place(int c) { return c ^ ((c >> 5 & 7) << 2); }
 
 // STAGED: the order in shared memory too (2 bytes per column, as places), read
-// from global memory once in whole lines.
+// from global memory once in whole lines.  perm is still being written when this
+// kernel starts: it is read with ordinary loads, behind the wait.
 template <int BITS, bool STAGED>
 __global__ void __launch_bounds__(ROW_THREADS)
-    regroup_rows_kernel(const uint32_t *__restrict__ qweight, const int32_t *__restrict__ perm,
-                        int64_t r, int d,
+    regroup_rows_kernel(const uint32_t *__restrict__ qweight, const int32_t *perm, int64_t r, int d,
                         uint32_t *__restrict__ out) {
   using U = Unit<BITS>;
   extern __shared__ __align__(16) uint32_t columns[];   // [d]: a column's codes of the CTA's rows
@@ -217,9 +217,15 @@ __global__ void __launch_bounds__(ROW_THREADS)
       // launched beside the order's kernel: nothing was written, nothing of it read
       asm volatile("griddepcontrol.wait;" ::: "memory");
       if constexpr (STAGED) {
-#pragma unroll 16
-        for (int j = threadIdx.x; j < d; j += ROW_THREADS)
-          order[j] = (uint16_t)place(__ldg(perm + j));
+        constexpr int EACH = 16;   // loads in flight
+        for (int j0 = threadIdx.x; j0 < d; j0 += EACH * ROW_THREADS) {
+          int from[EACH];
+#pragma unroll
+          for (int i = 0; i < EACH; ++i) from[i] = j0 + i * ROW_THREADS < d ? perm[j0 + i * ROW_THREADS] : 0;
+#pragma unroll
+          for (int i = 0; i < EACH; ++i)
+            if (j0 + i * ROW_THREADS < d) order[j0 + i * ROW_THREADS] = (uint16_t)place(from[i]);
+        }
       }
     }
     __syncthreads();
@@ -240,7 +246,7 @@ __global__ void __launch_bounds__(ROW_THREADS)
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < U::ROWS; ++i) a[i] = columns[place(__ldg(perm + j + i))];
+          for (int i = 0; i < U::ROWS; ++i) a[i] = columns[place(perm[j + i])];
         }
         transpose<U::ROWS>(a);
 #pragma unroll
@@ -261,8 +267,7 @@ __global__ void __launch_bounds__(ROW_THREADS)
 
 template <int BITS>
 __global__ void __launch_bounds__(ROW_THREADS)
-    regroup_kernel(const uint32_t *__restrict__ qweight, const int32_t *__restrict__ perm,
-                   int64_t r, int d,
+    regroup_kernel(const uint32_t *__restrict__ qweight, const int32_t *perm, int64_t r, int d,
                    uint32_t *__restrict__ out) {
   extern __shared__ __align__(16) uint8_t row_codes[];   // [d]
   asm volatile("griddepcontrol.wait;" ::: "memory");     // perm
@@ -289,7 +294,7 @@ __global__ void __launch_bounds__(ROW_THREADS)
       uint32_t c[32], w[BITS];
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
-        c[j] = row_codes[__ldg(perm + k * 32 + j)];
+        c[j] = row_codes[perm[k * 32 + j]];
       }
       pack32<BITS>(c, w);
 #pragma unroll

@@ -75,3 +75,18 @@ def test_chain_makes_its_tensors_on_its_stream(monkeypatch, normed):
     norms = [torch.ones(64).half(), torch.ones(96).half()] if normed else None
     chain.quantize_chain(X, Ws, bits=4, group=32, act_order=True, norms=norms, stream=given)
     assert not outside, outside
+
+
+def test_regroup_reads_the_order_with_ordinary_loads():
+    # The rows' kernels start while the order's kernel writes perm.  A load that asks
+    # for data that nothing writes while the kernel lives (__ldg, or a const
+    # __restrict__ pointer) may be taken from a stale line or moved before the wait.
+    src = code_of("regroup.cu")
+    kernels = re.findall(r"__global__.*?\n}\n", src, flags=re.S)
+    readers = [k for k in kernels if "griddepcontrol.wait" in k]
+    assert len(readers) == 2
+    for k in readers:
+        assert "const int32_t *perm" in k
+        assert not re.search(r"__restrict__\s*perm\b", k)
+        assert not re.search(r"__ld\w+\(\s*perm", k)
+        assert not re.search(r"\bperm\b", k.split("{", 1)[1].split("griddepcontrol.wait")[0])
