@@ -304,9 +304,9 @@ int gptq_linear_fp16(const void *X, int64_t n, int64_t d, const void *W16, int64
  *            outside [0, d) are clamped to it).  h keeps the order of x.
  *   codes    device int8 [n x d], 16-byte aligned, written.
  *   scales   device fp32 [n], written.
- *   xhat     device [n x d] of `dtype`, 16-byte aligned, or NULL.  It may be
- *            h, x or residual only when it is NULL; the outputs must not
- *            overlap each other.
+ *   xhat     device [n x d] of `dtype`, 16-byte aligned, or NULL.
+ *   The outputs share no memory with each other or with an input, but for h
+ *   as said: GPTQ_ERR_INVALID_ARG.
  *   A row with a NaN or an infinity has scale NaN, codes 0 and xhat NaN; other
  *   rows are not touched by it.  The codes are those of the formula in 64 bits
  *   (where u / scale is a tie but for their rounding: one of its neighbours); the
@@ -343,6 +343,8 @@ int gptq_rmsnorm_int8(const void *x, const void *residual, const void *gamma, in
  *   workspace  device scratch of gptq_packed_linear_workspace_bytes(...) bytes,
  *            256-byte aligned (NULL when the query returns 0); contents on
  *            entry are ignored.  Calls whose work may overlap need one each.
+ *   y and the workspace share no memory with each other or with an input:
+ *   GPTQ_ERR_INVALID_ARG.
  *   Sums in fp32 (for few tokens of GPTQ_I8 exact integers over up to 128
  *   columns), one rounding to `ytype`.  For few tokens (up to 8 at least) the
  *   codes and zero points enter exactly; for many, weights s (q - z) are
@@ -374,8 +376,10 @@ int gptq_packed_linear(const void *x, int xtype, const float *x_scales, int64_t 
  *   qweight  device int32 [r x d*bits/32];  g_idx device int32 [d], each of the
  *            d / group groups given to exactly `group` columns (as
  *            gptq_quantize_layer writes it).
- *   out      device int32 [r x d*bits/32], written; must not overlap qweight.
+ *   out      device int32 [r x d*bits/32], written.
  *   perm     device int32 [d], written.
+ *   out and perm share no memory with each other or with an input:
+ *   GPTQ_ERR_INVALID_ARG.
  *   r >= 0; d, bits as gptq_dequant_gemv; group a multiple of 32 that divides d.
  *   Waits until the order is known to be good -- for the work before it on
  *   `stream`, then for the first part of its own; the rest follows on the

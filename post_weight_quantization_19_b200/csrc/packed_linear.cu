@@ -114,6 +114,14 @@ extern "C" int gptq_packed_linear(const void *x, int xtype, const float *x_scale
     return GPTQ_ERR_INVALID_ARG;
   const size_t need = gptq_packed_linear_workspace_bytes(n, r, d, bits, group, xtype, perm != nullptr);
   if (need > 0 && (!workspace || workspace_bytes < need)) return GPTQ_ERR_NO_MEMORY;
+  const int64_t G = group < 0 ? 1 : d / group;
+  const size_t params = (size_t)r * G * 4;
+  const Span out = {y, (size_t)n * r * ysize}, scratch = {workspace, need};
+  if (overlap(out, scratch)) return GPTQ_ERR_INVALID_ARG;
+  for (const Span &s : {Span{x, (size_t)n * d * (xtype == GPTQ_I8 ? 1 : 2)}, Span{x_scales, (size_t)n * 4},
+                        Span{qweight, (size_t)r * (d / 32) * bits * 4}, Span{scales, params},
+                        Span{zeros, params}, Span{perm, (size_t)d * 4}, Span{bias, (size_t)r * ysize}})
+    if (overlap(out, s) || overlap(scratch, s)) return GPTQ_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   const bool few = few_tokens(n, r, d, xtype), widen = xtype == GPTQ_I8 && !few;
   if (widen || perm) {
@@ -132,7 +140,7 @@ extern "C" int gptq_packed_linear(const void *x, int xtype, const float *x_scale
     if (widen) xtype = GPTQ_F16;
   }
   const PackedArgs a{x, x_scales, reinterpret_cast<const uint32_t *>(qweight), scales, zeros,
-                     bias, y, n, r, (int)d, bits, group, group < 0 ? 1 : (int)(d / group), xtype, ytype,
+                     bias, y, n, r, (int)d, bits, group, (int)G, xtype, ytype,
                      widen || perm ? 1 : 0};
   if (!few) return launch_packed_many(a, st);
   return xtype == GPTQ_F16    ? launch_packed_few_f16(a, st)

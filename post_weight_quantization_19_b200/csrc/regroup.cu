@@ -394,6 +394,12 @@ extern "C" int gptq_regroup(const int32_t *qweight, const int32_t *g_idx, int64_
   if (reinterpret_cast<uintptr_t>(qweight) % 4 || reinterpret_cast<uintptr_t>(g_idx) % 4 ||
       reinterpret_cast<uintptr_t>(out) % 4 || reinterpret_cast<uintptr_t>(perm) % 4)
     return GPTQ_ERR_INVALID_ARG;
+  // (the order is written while g_idx is still read)
+  const Span in[] = {{qweight, (size_t)r * (d / 32) * bits * 4}, {g_idx, (size_t)d * 4}};
+  const Span out_codes = {out, in[0].bytes}, out_perm = {perm, (size_t)d * 4};
+  if (overlap(out_codes, out_perm)) return GPTQ_ERR_INVALID_ARG;
+  for (const Span &s : in)
+    if (overlap(out_codes, s) || overlap(out_perm, s)) return GPTQ_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
   GPTQ_CUDA_TRY(cudaStreamIsCapturing(st, &capture));

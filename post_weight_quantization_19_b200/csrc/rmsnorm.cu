@@ -416,7 +416,16 @@ extern "C" int gptq_rmsnorm_int8(const void *x, const void *residual, const void
     if (reinterpret_cast<uintptr_t>(p) % 16) return GPTQ_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(scales) % 4 || reinterpret_cast<uintptr_t>(perm) % 4)
     return GPTQ_ERR_INVALID_ARG;
-  if (xhat && (xhat == h || xhat == x || xhat == residual)) return GPTQ_ERR_INVALID_ARG;
+  // a row's outputs may not be another row's inputs, nor each other
+  const size_t row16 = (size_t)n * d * 2;
+  const Span in[] = {{x, row16}, {residual, row16}, {gamma, (size_t)d * 2}, {perm, (size_t)d * 4}};
+  const Span out[] = {{h, row16}, {codes, (size_t)n * d}, {scales, (size_t)n * 4}, {xhat, row16}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = i + 1; j < 4; ++j)
+      if (overlap(out[i], out[j])) return GPTQ_ERR_INVALID_ARG;
+    for (int j = 0; j < 4; ++j)
+      if (overlap(out[i], in[j]) && !(i == 0 && j < 2 && h == in[j].p)) return GPTQ_ERR_INVALID_ARG;
+  }
   const NormArgs a{x, residual, gamma, perm, h, codes, scales, xhat, n, (int)d, eps};
   cudaStream_t st = (cudaStream_t)stream;
   return dtype == GPTQ_F16 ? launch_norm_t<__half>(a, st) : launch_norm_t<__nv_bfloat16>(a, st);

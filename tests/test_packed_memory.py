@@ -4,6 +4,7 @@ another kernel is still writing.
 """
 
 import contextlib
+import ctypes
 import os
 import re
 
@@ -90,3 +91,66 @@ def test_regroup_reads_the_order_with_ordinary_loads():
         assert not re.search(r"__restrict__\s*perm\b", k)
         assert not re.search(r"__ld\w+\(\s*perm", k)
         assert not re.search(r"\bperm\b", k.split("{", 1)[1].split("griddepcontrol.wait")[0])
+
+
+# ------------------------------------------------------------------ arguments that share memory
+# Addresses far apart that are never dereferenced: each call below is refused before any
+# CUDA call.
+
+def apart(k, offset=0):
+    return ctypes.c_void_p((1 << 40) * (k + 1) + offset)
+
+
+def test_rmsnorm_refuses_shared_memory(lib):
+    n, d = 4, 64
+    names = ("x", "residual", "gamma", "perm", "h", "codes", "scales", "xhat")
+    size = {"x": n * d * 2, "residual": n * d * 2, "gamma": d * 2, "perm": d * 4, "h": n * d * 2,
+            "codes": n * d, "scales": n * 4, "xhat": n * d * 2}
+
+    def call(**kw):
+        a = {k: kw.get(k, apart(i)) for i, k in enumerate(names)}
+        return lib.gptq_rmsnorm_int8(a["x"], a["residual"], a["gamma"], 0, n, d, 1e-5, a["perm"], a["h"],
+                                     a["codes"], a["scales"], a["xhat"], None)
+    for out in ("h", "codes", "scales", "xhat"):
+        for other in names:
+            if other == out:
+                continue
+            last = (size[other] - 1) // 16 * 16           # shares the other's last bytes
+            offsets = {0, last} if out != "h" or other not in ("x", "residual") else {16, last}
+            for offset in offsets:
+                assert call(**{out: apart(names.index(other), offset)}) == 1, (out, other, offset)
+
+
+def test_packed_linear_refuses_shared_memory(lib):
+    n, r, d, bits, group = 20, 8, 128, 4, 64
+    names = ("x", "xs", "q", "s", "z", "perm", "bias", "y", "ws")
+    need = lib.gptq_packed_linear_workspace_bytes(n, r, d, bits, group, 3, 1)
+    size = {"x": n * d, "xs": n * 4, "q": r * d * bits // 8, "s": r * 2 * 4, "z": r * 2 * 4, "perm": d * 4,
+            "bias": r * 2, "y": n * r * 2, "ws": need}
+    assert need >= n * d * 2
+
+    def call(**kw):
+        a = {k: kw.get(k, apart(i)) for i, k in enumerate(names)}
+        return lib.gptq_packed_linear(a["x"], 3, a["xs"], n, a["q"], a["s"], a["z"], a["perm"], r, d, bits,
+                                      group, a["bias"], a["y"], 0, a["ws"], need, None)
+    for other in names:
+        if other != "y":
+            for offset in {0, (size[other] - 1) // 16 * 16}:
+                assert call(y=apart(names.index(other), offset)) == 1, ("y", other, offset)
+        if other != "ws":
+            assert call(ws=apart(names.index(other))) == 1, ("ws", other)
+
+
+def test_regroup_refuses_shared_memory(lib):
+    r, d, bits, group = 4, 128, 4, 64
+    names = ("q", "g_idx", "out", "perm")
+    size = {"q": r * d * bits // 8, "g_idx": d * 4, "out": r * d * bits // 8, "perm": d * 4}
+
+    def call(**kw):
+        a = {k: kw.get(k, apart(i)) for i, k in enumerate(names)}
+        return lib.gptq_regroup(a["q"], a["g_idx"], r, d, bits, group, a["out"], a["perm"], None)
+    for mine in ("out", "perm"):
+        for other in names:
+            if other != mine:
+                for offset in (0, size[other] - 4):
+                    assert call(**{mine: apart(names.index(other), offset)}) == 1, (mine, other, offset)
