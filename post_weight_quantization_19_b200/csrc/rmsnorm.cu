@@ -12,8 +12,8 @@
 // the writing of the codes, so every input is read once and every output
 // written once: n d (2 [+ 2 residual] + 1 [+ 2 h] [+ 2 xhat]) bytes.  One CTA
 // per row, one barrier for both sums (rows of up to 2048: one warp per row).
-// Measured: 4096 x 4096 bf16 with residual and xhat 33 us = 4.5 TB/s (0.70 of the
-// copy rate); one row of 4096 2.9 us, launch and two latencies.
+// Measured: 4096 x 4096 bf16 with residual and xhat 32 us = 4.7 TB/s (0.73 of the
+// copy rate); one row of 4096 2.8 us, launch and two latencies.
 // Codes are those of the formula in 64 bits: gamma h is exact in fp32 (a product of
 // two 16-bit numbers), so 127 gamma h / max|gamma h| in fp32 decides every code
 // that is not within 2e-5 of a border k + 1/2, and there the sign of 127 gamma h -
@@ -21,11 +21,12 @@
 // (fma).  Exact ties are real (half of the row's maximum lies at 63.5) and go to
 // the even code.  At 0.5, 1.5 and 2.5, where a step is most of the value, a tie
 // follows u / scale as it comes out in 64 bits instead, with scale = max|u| (1 /
-// 127), so that the result does not depend on who computes it: about one row in
-// 300 of 4096 columns.  That part comes last, when the row's registers are free.
+// 127), as torch evaluates it on a GPU (a division by 127 or another order of the
+// products may end on the other side): about one row in 300 of 4096 columns.
+// That part comes last, when the row's registers are free.
 // Sums and scales in fp32; a row whose squares or products leave the safe fp32
-// range (bf16 values above 1e19) is gathered again from the registers with
-// values scaled by a power of two.
+// range (bf16 values above 1e18 or products below 1e-30, infinities, NaN) is done
+// again in 64 bits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -192,6 +193,69 @@ __device__ __forceinline__ void settle_ties(const NormArgs &a, int64_t row, int 
   }
 }
 
+// A whole row in 64 bits, scale, codes and xhat; returns the scale (NaN for a row with
+// a NaN or an infinity).  The row's threads have stored h.  A function of its own, with
+// its arguments by value, so that the other rows' code keeps its registers.
+template <typename T, bool WARP_ROW>
+__device__ __noinline__ float row_in_64_bits(const NormArgs a, int64_t row, int tid, int nt, int8_t *crow,
+                                             T *xh, double *part) {
+  const int words = a.d / 2;
+  const uint32_t *hsrc = reinterpret_cast<const uint32_t *>(a.h ? a.h : a.x) + row * words;
+  const uint32_t *res =
+      a.h || !a.residual ? nullptr : reinterpret_cast<const uint32_t *>(a.residual) + row * words;
+  const uint32_t *gam = reinterpret_cast<const uint32_t *>(a.gamma);
+  double h[2], g[2];
+  auto load = [&](int k) {
+    uint32_t v = hsrc[k];
+    if (res) {
+      const float2 f = Cvt<T>::up(v), e = Cvt<T>::up(res[k]);
+      v = Cvt<T>::down(f.x + e.x, f.y + e.y);
+    }
+    const float2 f = Cvt<T>::up(v), e = Cvt<T>::up(gam[k]);
+    h[0] = f.x, h[1] = f.y, g[0] = e.x, g[1] = e.y;
+  };
+  double sum = 0.0, top = 0.0;
+#pragma unroll 1
+  for (int k = tid; k < words; k += nt) {
+    load(k);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const double p = fabs(h[i] * g[i]);     // exact
+      sum += h[i] * h[i] + (p < 1e300 ? 0.0 : p);   // an infinity or a NaN in gamma: in the sum too
+      top = fmax(top, p);
+    }
+  }
+  sum = row_reduce64<WARP_ROW>(sum, false, part);
+  top = row_reduce64<WARP_ROW>(top, true, part);
+  const bool lost = !(sum < 1e300);
+  const double root = sqrt(sum / a.d + a.eps);
+  // max|u| as u is formed below: rounding keeps the order, so it is the largest product's
+  double most = 0.0;
+  if (!lost && top > 0.0) {
+#pragma unroll 1
+    for (int k = tid; k < words; k += nt) {
+      load(k);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (fabs(h[i] * g[i]) == top) most = fmax(most, fabs(h[i] / root * g[i]));
+    }
+  }
+  const double step = row_reduce64<WARP_ROW>(most, true, part) * (1.0 / 127.0);
+  const float scale = lost ? __uint_as_float(0x7FC00000u) : top > 0.0 ? (float)step : 1.f;
+  const bool live = !lost && step > 0.0;
+#pragma unroll 1
+  for (int k = tid; k < words; k += nt) {
+    load(k);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float code = live ? (float)fmin(fmax(rint(h[i] / root * g[i] / step), -128.0), 127.0) : 0.f;
+      crow[2 * k + i] = (int8_t)code;
+      if (xh) xh[2 * k + i] = Cvt<T>::one(scale * code);
+    }
+  }
+  return scale;
+}
+
 template <typename T, int V, bool WARP_ROW>
 // (40 registers let 1536 threads share an SM; the ties' part spills, not the rest)
 __global__ void __maxnreg__(WARP_ROW ? 128 : V <= 2 ? 40 : 64) rmsnorm_int8_kernel(const NormArgs a) {
@@ -239,11 +303,8 @@ __global__ void __maxnreg__(WARP_ROW ? 128 : V <= 2 ? 40 : 64) rmsnorm_int8_kern
       if (k < nvec) h[k] = hv[v];
     }
   }
-  // the powers of two that h is scaled by in the sum and in the maximum (1
-  // except where the first pass left the safe range)
-  float ps = 1.f, pt = 1.f, ss, top;
-  for (int pass = 0;; ++pass) {
-    ss = 0.f;
+  float ss = 0.f, top;
+  {
     uint32_t mb = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -254,95 +315,91 @@ __global__ void __maxnreg__(WARP_ROW ? 128 : V <= 2 ? 40 : 64) rmsnorm_int8_kern
         const uint32_t q[4] = {gv.x, gv.y, gv.z, gv.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float2 f = Cvt<T>::up(p[i]);
+          const float2 f = Cvt<T>::up(p[i]);
           const float2 g = Cvt<T>::up(q[i]);
-          mb = max(mb, max(__float_as_uint(f.x * pt * g.x) & 0x7FFFFFFFu,
-                           __float_as_uint(f.y * pt * g.y) & 0x7FFFFFFFu));
-          f.x *= ps;
-          f.y *= ps;
+          mb = max(mb, max(__float_as_uint(f.x * g.x) & 0x7FFFFFFFu, __float_as_uint(f.y * g.y) & 0x7FFFFFFFu));
           ss = fmaf(f.x, f.x, fmaf(f.y, f.y, ss));
         }
       }
     }
     top = __uint_as_float(mb);
-    row_reduce<WARP_ROW>(ss, top, part);
-    if (pass == 1 || (ss < 1e37f && top < 1e37f && (top > 1e-30f || top == 0.f))) break;
-    ps = ss < 1e37f ? 1.f : 0x1p-96f;
-    pt = top < 1e37f ? (top > 1e-30f ? 1.f : 0x1p96f) : 0x1p-96f;
   }
-  float scale, inv;
-  if (!(ss < 3.4e38f) || !(top < 3.4e38f)) {   // NaN or infinity in the row
-    scale = __uint_as_float(0x7FC00000u);
-    inv = 0.f;
-  } else if (top == 0.f) {
-    scale = 1.f;
-    inv = 0.f;
-  } else if (ps == 1.f && pt == 1.f) {
-    scale = top / (127.f * sqrtf(ss / (float)a.d + (float)a.eps));
-    inv = 127.f / top;
-  } else {
-    const double mean = (double)ss / a.d / ps / ps;
-    scale = (float)((double)top / pt / (127.0 * sqrt(mean + a.eps)));
-    inv = 127.f / top;
-  }
-  const bool lost = scale != scale;
-  const bool plain = !lost && ps == 1.f && pt == 1.f && inv > 0.f;
-  if (tid == 0) a.scales[row] = scale;
-  // ---- the codes, eight of a vector in two words
-  uint2 c[V];
-  bool tie = false;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int k = tid + v * nt;
-    c[v] = make_uint2(0, 0);
-    if (k < nvec) {
-      const uint4 gv = __ldg(gam + k);
-      const uint32_t p[4] = {hv[v].x, hv[v].y, hv[v].z, hv[v].w};
-      const uint32_t q[4] = {gv.x, gv.y, gv.z, gv.w};
-      float u[8], far = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = Cvt<T>::up(p[i]), g = Cvt<T>::up(q[i]);
-        u[2 * i] = lost ? 0.f : f.x * pt * g.x * inv;
-        u[2 * i + 1] = lost ? 0.f : f.y * pt * g.y * inv;
-        far = fmaxf(far, fmaxf(fabsf(u[2 * i] - rintf(u[2 * i])), fabsf(u[2 * i + 1] - rintf(u[2 * i + 1]))));
-      }
-      if (plain && far > 0.49998f) {   // a border is near
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 f = Cvt<T>::up(p[i / 2]), g = Cvt<T>::up(q[i / 2]);
-          if (fabsf(u[i] - rintf(u[i])) > 0.49998f)
-            u[i] = near_code((i & 1) ? f.y * g.y : f.x * g.x, top, u[i], tie);
-        }
-      }
-      c[v].x = pack4(u[0], u[1], u[2], u[3]);
-      c[v].y = pack4(u[4], u[5], u[6], u[7]);
-    }
-  }
+  row_reduce<WARP_ROW>(ss, top, part);
   int8_t *crow = a.perm ? row_codes + (WARP_ROW ? (size_t)warp * a.d : 0) : a.codes + row * a.d;
   uint4 *xh = a.perm ? nullptr : reinterpret_cast<uint4 *>(a.xhat);
+  T *xhrow = xh ? reinterpret_cast<T *>(xh + row * nvec) : nullptr;
+  bool zeros = false;   // a row of zeros (and not of products too small for fp32)
+  if (top == 0.f) {
+    uint32_t bits = 0;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int k = tid + v * nt;
-    if (k < nvec) {
-      *reinterpret_cast<uint2 *>(crow + (size_t)k * 8) = c[v];
-      if (xh) {
-        uint32_t o[4];
+    for (int v = 0; v < V; ++v) bits |= hv[v].x | hv[v].y | hv[v].z | hv[v].w;
+    bits &= 0x7FFF7FFFu;
+    zeros = WARP_ROW ? !__any_sync(0xffffffffu, bits) : !__syncthreads_or(bits);
+  }
+  float scale;
+  if (zeros || (ss < 1e37f && top < 1e37f && top > 1e-30f)) {
+    scale = zeros ? 1.f : top / (127.f * sqrtf(ss / (float)a.d + (float)a.eps));
+    const float inv = zeros ? 0.f : 127.f / top;
+    // ---- the codes, eight of a vector in two words
+    uint2 c[V];
+    bool tie = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int k = tid + v * nt;
+      c[v] = make_uint2(0, 0);
+      if (k < nvec) {
+        const uint4 gv = __ldg(gam + k);
+        const uint32_t p[4] = {hv[v].x, hv[v].y, hv[v].z, hv[v].w};
+        const uint32_t q[4] = {gv.x, gv.y, gv.z, gv.w};
+        float u[8], far = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t w = i < 2 ? c[v].x : c[v].y;
-          const int s0 = (i & 1) * 16;
-          o[i] = Cvt<T>::down(scale * (float)(int8_t)(w >> s0), scale * (float)(int8_t)(w >> (s0 + 8)));
+          const float2 f = Cvt<T>::up(p[i]), g = Cvt<T>::up(q[i]);
+          u[2 * i] = f.x * g.x * inv;
+          u[2 * i + 1] = f.y * g.y * inv;
+          far = fmaxf(far, fmaxf(fabsf(u[2 * i] - rintf(u[2 * i])), fabsf(u[2 * i + 1] - rintf(u[2 * i + 1]))));
         }
-        xh[row * nvec + k] = make_uint4(o[0], o[1], o[2], o[3]);
+        if (far > 0.49998f) {   // a border is near
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 f = Cvt<T>::up(p[i / 2]), g = Cvt<T>::up(q[i / 2]);
+            if (fabsf(u[i] - rintf(u[i])) > 0.49998f)
+              u[i] = near_code((i & 1) ? f.y * g.y : f.x * g.x, top, u[i], tie);
+          }
+        }
+        c[v].x = pack4(u[0], u[1], u[2], u[3]);
+        c[v].y = pack4(u[4], u[5], u[6], u[7]);
       }
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int k = tid + v * nt;
+      if (k < nvec) {
+        *reinterpret_cast<uint2 *>(crow + (size_t)k * 8) = c[v];
+        if (xh) {
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w = i < 2 ? c[v].x : c[v].y;
+            const int s0 = (i & 1) * 16;
+            o[i] = Cvt<T>::down(scale * (float)(int8_t)(w >> s0), scale * (float)(int8_t)(w >> (s0 + 8)));
+          }
+          xh[row * nvec + k] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+    }
+    if (WARP_ROW ? __any_sync(0xffffffffu, tie) : __syncthreads_or(tie)) {   // the codes are stored
+      if constexpr (WARP_ROW) __syncwarp();
+      settle_ties<T, WARP_ROW>(a, row, tid, nt, top, inv, scale, crow, xhrow, part64);
+    }
+  } else {
+    if constexpr (WARP_ROW)
+      __syncwarp();
+    else
+      __syncthreads();   // h is stored
+    scale = row_in_64_bits<T, WARP_ROW>(a, row, tid, nt, crow, xhrow, part64);
   }
-  if (WARP_ROW ? __any_sync(0xffffffffu, tie) : __syncthreads_or(tie)) {   // the codes are stored
-    if constexpr (WARP_ROW) __syncwarp();
-    settle_ties<T, WARP_ROW>(a, row, tid, nt, top, inv, scale, crow,
-                             xh ? reinterpret_cast<T *>(xh + row * nvec) : nullptr, part64);
-  }
+  if (tid == 0) a.scales[row] = scale;
   if (a.perm) {
     if constexpr (WARP_ROW)
       __syncwarp();

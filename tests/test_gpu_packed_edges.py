@@ -116,3 +116,76 @@ def test_chain_on_a_stream_beside_a_busy_one(normed):
         for k in a:
             assert torch.equal(a[k], b[k]) if torch.is_tensor(a[k]) else a[k] == b[k], k
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ the norm's rows outside fp32
+
+@pytest.mark.parametrize("d", [96, 2048, 4096, 8192, 16384, 65536])
+def test_rmsnorm_int8_rows_whose_products_leave_fp32(d):
+    # Large values that gamma takes out (0 times them), squares beyond fp32, products
+    # far below it, zero rows: scale and codes are the oracle's.  A code may differ
+    # by one only where u / scale is within 1e-12 of a half (its value in 64 bits).
+    # The scale is one rounding to fp32 (of a number that may be subnormal) away from
+    # the value in 64 bits where the row left fp32, else 140 half steps (a sum of
+    # squares through at most 128 additions and five more operations).
+    import post_weight_quantization_19_b200 as g
+    rng = np.random.default_rng(d)
+    gamma = rng.standard_normal(d).astype(np.float32)
+    gamma[0], gamma[1], gamma[2] = 0.0, 2.0 ** -130, 2.0 ** 60
+    gamma = torch.from_numpy(gamma).to(BF16).cuda()
+    X = rng.standard_normal((11, d)).astype(np.float32)
+    X[:, 2] = 0
+    X[0] *= 2.0 ** -103
+    X[0, 0] = 2.0 ** 34                       # times 2^96 an infinity, and gamma is 0
+    X[1] *= 2.0 ** -103
+    X[1, 0] = -2.0 ** 120
+    X[2], X[2, 1] = 0, 2.0 ** -120            # one product, 2^-250
+    X[3] *= 2.0 ** 90                         # squares beyond fp32
+    X[4, 2] = 2.0 ** 100                      # a product beyond it
+    X[5] *= 2.0 ** -120
+    X[6] = 0
+    X[7], X[7, 0] = 0, 5.0                    # u = 0 all along
+    X[8, 5] = np.inf
+    X[9, 0] = np.nan                          # where gamma is 0
+    x = torch.from_numpy(X).to(BF16).cuda()
+    lost, outside = [8, 9], [0, 1, 2, 3, 4, 5, 6, 7]
+    good = [i for i in range(11) if i not in lost]
+    h, gm = f64(x), f64(gamma)
+    codes, scales = oracle.rmsnorm_int8(h[good], gm, 1e-5)
+    perm = np.random.default_rng(3).permutation(d).astype(np.int32)
+    zero = torch.zeros_like(x)
+    for kw in (dict(), dict(residual=zero), dict(residual=zero.clone(), outputs="residual"),
+               dict(perm=dev(perm)[0])):
+        x2 = x.clone()
+        if kw.get("outputs"):
+            kw["outputs"] = {"h": kw["residual"]}
+        out = g.gptq_rmsnorm_int8(x2, gamma, eps=1e-5, xhat=True, **kw)
+        got = out["codes"].cpu().numpy().astype(np.int64)
+        if "perm" in kw:
+            back = np.empty(d, dtype=np.int64)
+            back[perm] = np.arange(d)
+            got = got[:, back]
+        s = f64(out["scales"])
+        assert np.isnan(s[lost]).all() and not got[lost].any()
+        assert bool(torch.isnan(out["xhat"][lost]).all())
+        for k, i in enumerate(good):
+            half = 2.0 ** -24 * scales[k] + 2.0 ** -150
+            assert abs(s[i] - scales[k]) <= (1.0001 if i in outside else 140) * half, (i, s[i], scales[k])
+            diff = got[i] != codes[k]
+            if diff.any():
+                u = gm * h[i] / np.sqrt((h[i] ** 2).mean() + 1e-5)
+                off = np.abs(np.abs(u[diff] / scales[k]) % 1 - 0.5)
+                assert np.abs(got[i] - codes[k]).max() <= 1 and off.max() <= 1e-12, i
+        want = (out["codes"].float() * out["scales"][:, None]).to(BF16)
+        assert torch.equal(out["xhat"].nan_to_num(7.0), want.nan_to_num(7.0))
+
+
+def test_rmsnorm_int8_gamma_without_a_number():
+    # a NaN or an infinity in gamma spoils every row that it meets
+    import post_weight_quantization_19_b200 as g
+    x = torch.ones((3, 4096), dtype=F16, device="cuda")
+    for bad in (float("nan"), float("inf")):
+        gamma = torch.ones(4096, dtype=F16, device="cuda")
+        gamma[77] = bad
+        out = g.gptq_rmsnorm_int8(x, gamma, eps=1e-5)
+        assert bool(torch.isnan(out["scales"]).all()) and not bool(out["codes"].any())
