@@ -17,9 +17,13 @@
 // unit t of every chunk (FINE).
 //
 // 16-bit x: the operand is B + q, whose bits are the code's bits and a constant:
-//   fp16: B = 0, the code as a subnormal number, q 2^-24 (exact, and so are its
-//         products in fp32); every second code stays one place higher, q 2^(bits -
-//         24), and is summed apart, which saves a shift;
+//   fp16: B = 0, the code as a subnormal number in its upper bits, q 2^(2 bits - 34)
+//         (8-bit codes q 2^-24; exact, and so are its products in fp32); every second
+//         code stays one place higher, 2^bits times that, and is summed apart, which
+//         saves a shift.  (The tensor core aligns products by their exponents, a
+//         subnormal number's as if it were 2^-14, and drops what lies 25 bits
+//         below: codes in the lowest bits, and sum x from ones of 2^-24, left sums good
+//         to 2^-17.  12288 x 49152, one token: 90.3 us so, 93.5 with codes in the upper bits);
 //   bf16: B = 16 or 4 for 4- or 2-bit codes, the code in the upper mantissa
 //         bits; 3-bit codes B = 64 and 8 in turn, at two places of the mantissa,
 //         which saves two shifts of four.  (8-bit codes do not fit: q - z
@@ -37,7 +41,7 @@
 // through distributed shared memory in a fixed order.
 //
 // Measured, one token: 12288 x 49152, 3 bits, bf16 126 us (2.1 TB/s; the integer pipe
-// is busy 64 % of the time, 2.3 instructions per clock); 4 bits, fp16 91 us (3.7
+// is busy 64 % of the time, 2.3 instructions per clock); 4 bits, fp16 93 us (3.6
 // TB/s); 4096 x 4096, 4 bits 5.9 us, most of it launch, fill and the last sums;
 // 11008 x 4096 with 8-bit x 9.6 us.
 #pragma once
@@ -209,15 +213,21 @@ constexpr float operand_base() {
   return XT == GPTQ_BF16 && BITS != 8 ? (BITS == 4 ? 16.f : BITS == 3 ? 64.f : 4.f) : 0.f;
 }
 
+// fp16: what a code of 1 stands for (the first of each two, code_pairs).
+template <int BITS>
+constexpr float CODE_UNIT = BITS == 8 ? 0x1p-24f : BITS == 4 ? 0x1p-22f : BITS == 3 ? 0x1p-20f : 0x1p-18f;
+
 // A zero point, clamped to the codes, as its group uses it: itself for 8-bit x, 2^23
-// + z for 8-bit codes with bf16, else -(B + z) (as float bits).
+// + z for 8-bit codes with bf16, else -(B + z) in units of the operands' codes (as
+// float bits).
 template <int BITS, int XT>
 __device__ __forceinline__ uint32_t prepare_zero(uint32_t raw) {
   const uint32_t z = (uint32_t)min(max((int)raw, 0), (1 << BITS) - 1);
   if constexpr (XT == GPTQ_I8) return z;
   const float f = __uint_as_float(0x4B000000u | z);   // 2^23 + z
   if constexpr (BITS == 8 && XT == GPTQ_BF16) return __float_as_uint(f);
-  return __float_as_uint((8388608.f - operand_base<BITS, XT>()) - f);
+  const float v = (8388608.f - operand_base<BITS, XT>()) - f;
+  return __float_as_uint(XT == GPTQ_F16 ? v * CODE_UNIT<BITS> : v);
 }
 
 // The eight codes of a unit as four pairs of operands: (0,4), (1,5), (2,6),
@@ -251,9 +261,10 @@ __device__ __forceinline__ void code_pairs(uint2 w, float zf, const uint32_t (&b
     if constexpr (BITS == 2) v = __byte_perm(v, 0, 0x4140);
     constexpr uint32_t mask = ((1u << BITS) - 1u) * 0x00010001u;
     if constexpr (XT == GPTQ_F16) {
-      const uint32_t h = v >> (2 * BITS);
-      o[0] = v & mask, o[1] = v & (mask << BITS);
-      o[2] = h & mask, o[3] = h & (mask << BITS);
+      constexpr int P = 10 - 2 * BITS, R = 2 * BITS - P;
+      const uint32_t u = v << P, h = R > 0 ? v >> (R > 0 ? R : 0) : v << (R < 0 ? -R : 0);
+      o[0] = u & (mask << P), o[1] = u & (mask << (P + BITS));
+      o[2] = h & (mask << P), o[3] = h & (mask << (P + BITS));
     } else if constexpr (BITS == 3) {
       // codes 0 and 2 at bit 1 (64 + q), 1 and 3 at bit 4 (8 + q)
       const uint32_t u = v << 1, h = v >> 5;
@@ -458,14 +469,14 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
     issue(i);
     cp_commit();
   }
-  // The matrix of ones (fp16: 2^-24, the unit of its codes), as values the compiler
-  // does not see through: it would set four registers anew for every product.
+  // The matrix of ones, as values the compiler does not see through: it would set four
+  // registers anew for every product.
   uint32_t ones[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     asm volatile("mov.b32 %0, %1;"
                  : "=r"(ones[i])
-                 : "n"(XT == GPTQ_F16 ? 0x00010001 : XT == GPTQ_BF16 ? 0x3F803F80 : 0x01010101));
+                 : "n"(XT == GPTQ_F16 ? 0x3C003C00 : XT == GPTQ_BF16 ? 0x3F803F80 : 0x01010101));
   // bf16: 2^BITS at the top of the mantissa; 3-bit codes 64 and 8 (code_pairs)
   uint32_t bases[2];
   asm volatile("mov.b32 %0, %1;"
@@ -708,7 +719,7 @@ __global__ void __launch_bounds__(32 * Few<BITS, XT, NT, FINE>::MAX_WARPS)
         for (int w = 1; w < warps; ++w) v += red[w * CELLS + i];
       }
       if constexpr (F::INT8) v *= a.p.x_scales[tok0 + col];
-      if constexpr (XT == GPTQ_F16) v *= 16777216.f;   // the codes were q 2^-24
+      if constexpr (XT == GPTQ_F16) v *= 1.f / CODE_UNIT<BITS>;   // the codes were q times that
       if constexpr (!F::INT8)
         lost |= !(fabsf(v) <= 3.402823466e38f);
       if (a.p.bias) v += load_as_float(a.p.bias, a.p.ytype, row);

@@ -189,3 +189,31 @@ def test_rmsnorm_int8_gamma_without_a_number():
         gamma[77] = bad
         out = g.gptq_rmsnorm_int8(x, gamma, eps=1e-5)
         assert bool(torch.isnan(out["scales"]).all()) and not bool(out["codes"].any())
+
+
+# ------------------------------------------------------------------ sums of few tokens
+
+@pytest.mark.parametrize("T", [F16, BF16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("bits", [2, 3, 4, 8])
+@pytest.mark.parametrize("n,group", [(1, 128), (4, 32), (8, 64), (9, 128), (16, 32), (16, -1)])
+def test_packed_linear_few_tokens_sums_are_fp32(n, group, bits, T):
+    # Whole numbers of a unit whose partial sums all stay below 2^24 units in magnitude:
+    # fp32 sums are exact in any order, with (B + q) x and (B + z) x summed apart too
+    # (B <= 64), so the result is.  One value of a token is large, the others are small
+    # beside it.
+    import post_weight_quantization_19_b200 as g
+    r, d = 70, 512
+    rng = np.random.default_rng(n + bits)
+    q = words(r, d, bits, bits)
+    G = 1 if group == -1 else d // group
+    z = rng.integers(0, 1 << bits, size=(r, G)).astype(np.int32)
+    unit = 0.25 if T == F16 and bits < 8 else 1.0
+    X = rng.integers(-8, 9, size=(n, d)) * unit
+    X[np.arange(n), rng.integers(d, size=n)] = 32768 * rng.choice([-1, 1], size=n)
+    size = d if group == -1 else group
+    codes = oracle.unpack_rows(q, bits, d)
+    gi = np.arange(d) // size
+    assert np.abs(X).sum(1).max() * ((1 << bits) + (64 if T == BF16 else 0)) / unit < 2 ** 24
+    y = g.gptq_packed_linear(torch.from_numpy(X.astype(np.float32)).to(T).cuda(),
+                             *dev(q, np.ones((r, G), dtype=np.float32), z), bits, group, dtype=F32)
+    np.testing.assert_array_equal(f64(y), X @ (codes - z[:, gi]).T)
