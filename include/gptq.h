@@ -348,12 +348,16 @@ int gptq_rmsnorm_int8(const void *x, const void *residual, const void *gamma, in
  *   y and the workspace share no memory with each other or with an input:
  *   GPTQ_ERR_INVALID_ARG.
  *   Sums in fp32 (for few tokens of GPTQ_I8 exact integers over up to 128
- *   columns), one rounding to `ytype`.  For few tokens (up to 8 at least) the
- *   codes and zero points enter exactly; for many, weights s (q - z) are
- *   rounded once to the 16-bit type of the tensor-core product, as
- *   gptq_dequant_fp16 does.  Results do not change from call to call.  Infinities
- *   and NaN in x give what the formula gives (0 times an infinity: NaN), in their
- *   own token.
+ *   columns), one rounding to `ytype`.  With GPTQ_F32 results the weights
+ *   s (q - z) enter to fp32 accuracy for any number of tokens, and at most 256
+ *   columns are summed in the tensor core at a time.  With 16-bit results and few
+ *   tokens (up to 8 at least) the codes and zero points enter exactly; for many,
+ *   the weights are rounded once to the 16-bit type of the tensor-core product, as
+ *   gptq_dequant_fp16 does, and that product's sums over a row lose up to 2^-24 of
+ *   sum |w x| per 16 columns, always in magnitude, where all products have one
+ *   sign (measured: half of that, 1e-4 for 65536 columns).
+ *   Results do not change from call to call.  Infinities and NaN in x give what
+ *   the formula gives (0 times an infinity: NaN), in their own token.
  *   n == 0 or r == 0: nothing to do.  Asynchronous; a bounded in-kernel wait
  *   that runs out is reported by gptq_check_device_status.
  *

@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgptq_b200.so")
 SOURCES = ["hessian_tc.cu", "gemm_tc.cu", "factor.cu", "leaf.cu", "sweep.cu", "pack.cu", "api.cu",
            "noalloc.cu", "gemv.cu", "linear_tc.cu", "rmsnorm.cu", "regroup.cu",
-           "packed_linear.cu", "packed_few_f16.cu", "packed_few_bf16.cu", "packed_few_i8.cu", "packed_many.cu"]
+           "packed_linear.cu", "packed_few_f16.cu", "packed_few_bf16.cu", "packed_few_i8.cu", "packed_many.cu",
+           "packed_many_f32.cu"]
 
 
 def nvcc() -> str:

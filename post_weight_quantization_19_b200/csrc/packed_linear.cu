@@ -19,16 +19,19 @@
 namespace gptq {
 namespace {
 
-constexpr int FEW_TOKENS = 16;   // the most that the warp-level products take
-
 // Which product: few tokens at once are bound by the weights' bytes and codes, and
 // warp-level products, which need no start-up, are faster: always up to 8
 // tokens, with 8-bit x up to 16, and with 16-bit x for layers of up to 2^25 codes.
 // Measured (warp-level, tcgen05; us): 16 tokens, 4 bits, fp16, 4096 x 4096 12.8,
 // 12.6; 9 tokens 8.9, 12.2; 8192 x 8192, 8 tokens 25.7, 25.1, 16 tokens 35.8,
 // 25.1; 16 tokens of 8-bit x, 11008 x 4096 16.2, 25.2.
-bool few_tokens(int64_t n, int64_t r, int64_t d, int xtype) {
-  return n <= 8 || (n <= FEW_TOKENS && (xtype == GPTQ_I8 || r * d <= (1 << 25)));
+// fp32 results take the tensor core two or three parts of every weight: the warp-level
+// products, 16 tokens at a time, up to 32 tokens, of 8-bit x up to 64.  Measured: 4096 x
+// 11008, 32 tokens fp16 44.0, 41.4, bf16 45.2, 62.7, 64 tokens 79.4, 43.1 and 80.6, 65.3;
+// 11008 x 4096, 64 tokens of 8-bit x 45.6, 59.3, 128 tokens 88.4, 63.6.
+bool few_tokens(int64_t n, int64_t r, int64_t d, int xtype, int ytype) {
+  if (ytype == GPTQ_F32) return n <= (xtype == GPTQ_I8 ? 64 : 32);
+  return n <= 8 || (n <= 16 && (xtype == GPTQ_I8 || r * d <= (1 << 25)));
 }
 
 // x in the layer's column order: out[t, j] = x[t, perm[j]], entries outside
@@ -91,7 +94,8 @@ using namespace gptq;
 extern "C" size_t gptq_packed_linear_workspace_bytes(int64_t n, int64_t r, int64_t d, int bits,
                                                      int group, int xtype, int permuted) {
   if (!valid_packed(n, r, d, bits, group, xtype) || n == 0 || r == 0) return 0;
-  const bool widen = xtype == GPTQ_I8 && !few_tokens(n, r, d, xtype);
+  // (fp32 results may do with less)
+  const bool widen = xtype == GPTQ_I8 && !few_tokens(n, r, d, xtype, GPTQ_F16);
   if (!permuted && !widen) return 0;
   return align_up((size_t)n * d * (xtype == GPTQ_I8 && !widen ? 1 : 2), 256);
 }
@@ -123,7 +127,7 @@ extern "C" int gptq_packed_linear(const void *x, int xtype, const float *x_scale
                         Span{zeros, params}, Span{perm, (size_t)d * 4}, Span{bias, (size_t)r * ysize}})
     if (overlap(out, s) || overlap(scratch, s)) return GPTQ_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
-  const bool few = few_tokens(n, r, d, xtype), widen = xtype == GPTQ_I8 && !few;
+  const bool few = few_tokens(n, r, d, xtype, ytype), widen = xtype == GPTQ_I8 && !few;
   if (widen || perm) {
     const dim3 grid((unsigned)n, (unsigned)((d / 8 + GATHER_THREADS - 1) / GATHER_THREADS));
     if (widen)
@@ -142,7 +146,7 @@ extern "C" int gptq_packed_linear(const void *x, int xtype, const float *x_scale
   const PackedArgs a{x, x_scales, reinterpret_cast<const uint32_t *>(qweight), scales, zeros,
                      bias, y, n, r, (int)d, bits, group, (int)G, xtype, ytype,
                      widen || perm ? 1 : 0};
-  if (!few) return launch_packed_many(a, st);
+  if (!few) return ytype == GPTQ_F32 ? launch_packed_many_f32(a, st) : launch_packed_many(a, st);
   return xtype == GPTQ_F16    ? launch_packed_few_f16(a, st)
          : xtype == GPTQ_BF16 ? launch_packed_few_bf16(a, st)
                               : launch_packed_few_i8(a, st);

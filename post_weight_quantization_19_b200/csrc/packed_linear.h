@@ -27,7 +27,8 @@ int launch_packed_few_bf16(const PackedArgs &a, cudaStream_t st);
 int launch_packed_few_i8(const PackedArgs &a, cudaStream_t st);
 // Many tokens: weights dequantised into tensor memory, tcgen05 products.  x in
 // 16 bits (xtype GPTQ_F16 or GPTQ_BF16; x_scales may still be given).
-int launch_packed_many(const PackedArgs &a, cudaStream_t st);
+int launch_packed_many(const PackedArgs &a, cudaStream_t st);       // y in 16 bits
+int launch_packed_many_f32(const PackedArgs &a, cudaStream_t st);   // y in fp32
 
 __device__ __forceinline__ float load_as_float(const void *p, int type, int64_t i) {
   if (type == GPTQ_F16) return __half2float(reinterpret_cast<const __half *>(p)[i]);
