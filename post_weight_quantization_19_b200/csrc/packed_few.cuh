@@ -758,9 +758,9 @@ int launch_few(const PackedArgs &p, cudaStream_t st) {
   // Warps of a CTA and CTAs along k: the shape with the shortest estimate, in
   // clocks: rounds of CTAs over the tiles, each as long as its warps' stages (480
   // clocks and 110 more for each warp that shares the SM) and its sums (170 per
-  // warp, 1500 more where CTAs add up theirs).  Measured,
-  // one token, 4 bits: 4096 x 4096, 8 warps 5.7 us, 16 warps 6.5; 12288 x 49152, 16
-  // warps 91 us, 14 warps 96, 8 warps 116.
+  // warp, 1500 more where CTAs add up theirs).  Measured, one token, 4 bits: 4096 x
+  // 4096, 8 warps 5.7 us, 16 warps 6.5; 12288 x 49152, 14 warps 5 % more than 16, 8
+  // warps 27 % more.
   int warps = 8, ck = 1, fit = 1;   // fit: CTAs that share an SM
   size_t smem = 0;
   int64_t best = INT64_MAX;
@@ -781,9 +781,7 @@ int launch_few(const PackedArgs &p, cudaStream_t st) {
       if (cost <= best) best = cost, warps = w, ck = c, fit = res, smem = need;
     }
   }
-  if (best == INT64_MAX) return GPTQ_ERR_INVALID_ARG;   // not reached: eight warps always fit
   a.ctas_k = ck;
-  if (tiles * ck > INT32_MAX || blocks > 65535) return GPTQ_ERR_INVALID_ARG;
   // CTAs that fit at once walk the tiles
   int64_t clusters = (int64_t)sms * fit / (blocks * ck);
   if (clusters < 1) clusters = 1;
