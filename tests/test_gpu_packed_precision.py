@@ -189,3 +189,52 @@ def test_16_bit_results_of_long_rows_of_one_sign(n, d, bits, group):
     assert bool(torch.isfinite(y).all())
     mean = float(((y.double() - ref) / ref).mean())
     assert abs(mean) <= 2.0 ** -24 * d / 16 + 5 * 2.0 ** -11 / (n * r) ** 0.5, mean
+
+
+# ------------------------------------------------------------------ which kernel takes 9 to 16 tokens
+
+@pytest.mark.parametrize("T", [F16, BF16, I8], ids=["fp16", "bf16", "int8"])
+@pytest.mark.parametrize("n,r,d,bits,group", [(9, 64, 160, 3, 160), (13, 16, 4096, 4, 64), (16, 1000, 640, 3, 32),
+                                              (16, 48, 2048, 8, -1), (11, 300, 1056, 2, 96),
+                                              (15, 129, 4096, 4, 128), (16, 255, 288, 8, 32)])
+def test_up_to_16_tokens_codes_enter_exactly(n, r, d, bits, group, T):
+    # 16-bit results of 9 to 16 tokens (8-bit x, or layers of up to 2^25 codes): no weight is
+    # rounded, so besides y's own rounding only the sums' is left.  The bound on those
+    # is as for fp32 results of few tokens; a weight rounded to 16 bits would add up to
+    # 2^-11 (bf16 2^-8) of sum |w x|.
+    import post_weight_quantization_19_b200 as g
+    q, s, z = layer(r, d, bits, group, n + r)
+    x, xs = activations(n, d, n + d, T)
+    for dtype in ((F16, BF16) if T is I8 else (T,)):
+        bias = torch.linspace(-1, 1, r, device="cuda").to(dtype) if r % 2 else None
+        y = g.gptq_packed_linear(x, q, s, z, bits, group, x_scales=xs, bias=bias, dtype=dtype)
+        ref, a, parts = reference(x, q, s, z, bits, group, xs, bias)
+        u = 2.0 ** -11 if dtype is F16 else 2.0 ** -8
+        tol = u * ref.abs() * (1 + 2.0 ** -6) + tolerance(T, d, ref, a, parts, True)
+        if dtype is F16:
+            tol = tol + 2.0 ** -25                      # subnormal results
+        assert bool(((y.double() - ref).abs() <= tol).all())
+        # y's rounding alone: at most u of the 2-norm, and u / sqrt(3) where it is even over
+        # a step; a weight's rounding of the same size, independent, would make it sqrt(2) of that
+        if n * r >= 4000:
+            rel = float((y.double() - ref).norm() / ref.norm())
+            assert rel <= u / 3 ** 0.5, rel
+
+
+@pytest.mark.parametrize("T", [F16, BF16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("n", [9, 16])
+def test_layers_of_up_to_2_25_codes_take_the_exact_kernel(n, T):
+    # On the border the tokens' results are those of the exact codes; one row tile past it,
+    # those of the tensor-core product, whatever the number of tokens up to 192.
+    import post_weight_quantization_19_b200 as g
+    d, bits, group = 4096, 4, 128
+    x, _ = activations(17, d, n, T)
+    for r, exact in ((8192, True), (8224, False)):
+        q, s, z = layer(r, d, bits, group, r)
+        few = g.gptq_packed_linear(x[:n].contiguous(), q, s, z, bits, group)
+        many = g.gptq_packed_linear(x, q, s, z, bits, group)[:n]
+        assert torch.equal(few, many) != exact
+        ref = reference(x[:n], q, s, z, bits, group)[0]
+        rel = [float((y.double() - ref).norm() / ref.norm()) for y in (few, many)]
+        u = 2.0 ** -11 if T is F16 else 2.0 ** -8
+        assert rel[0] <= (u / 3 ** 0.5 if exact else u) and rel[1] <= u
