@@ -426,6 +426,7 @@ template <int BITS>
 __device__ __noinline__ void settle_result(const PackedArgs p, int64_t tok, int64_t row) {
   float *y = static_cast<float *>(p.y) + tok * p.r + row;
   if (fabsf(*y) <= 3.402823466e38f) return;
+  if (p.x_scales && !(fabsf(p.x_scales[tok]) <= 3.402823466e38f)) return;   // the token's scale is none
   float v = sum_in_64_bits<BITS>(p, tok, row);
   if (p.x_scales) v *= p.x_scales[tok];
   *y = p.bias ? v + static_cast<const float *>(p.bias)[row] : v;
