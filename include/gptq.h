@@ -311,9 +311,8 @@ int gptq_linear_fp16(const void *X, int64_t n, int64_t d, const void *W16, int64
  *   rows are not touched by it.  The codes are those of the formula in 64 bits.
  *   Where u / scale is a tie but for its rounding there, either neighbour would do;
  *   this call gives the even one, and at 0.5, 1.5 and 2.5 the one that u / scale
- *   with scale = max|u| (1 / 127) rounds to in 64 bits.  The scale's sum of squares
- *   is in fp32, in 64 bits for a row that leaves its range (squares that sum to
- *   1e37, max|gamma h| above 1e37 or below 1e-30).
+ *   with scale = max|u| (1 / 127) rounds to in 64 bits.  The scale is the formula's in
+ *   64 bits, rounded once.
  *   n == 0: nothing to do.  Asynchronous: one kernel.
  */
 int gptq_rmsnorm_int8(const void *x, const void *residual, const void *gamma, int dtype,

@@ -12,8 +12,8 @@
 // the writing of the codes, so every input is read once and every output
 // written once: n d (2 [+ 2 residual] + 1 [+ 2 h] [+ 2 xhat]) bytes.  One CTA
 // per row, one barrier for both sums (rows of up to 2048: one warp per row).
-// Measured: 4096 x 4096 bf16 with residual and xhat 32 us = 4.7 TB/s (0.73 of the
-// copy rate); one row of 4096 2.8 us, launch and two latencies.
+// Measured: 4096 x 4096 bf16 with residual and xhat 33 us = 4.6 TB/s (0.71 of the
+// copy rate); one row of 4096 3.0 us, launch and two latencies.
 // Codes are those of the formula in 64 bits: gamma h is exact in fp32 (a product of
 // two 16-bit numbers), so 127 gamma h / max|gamma h| in fp32 decides every code
 // that is not within 2e-5 of a border k + 1/2, and there the sign of 127 gamma h -
@@ -24,9 +24,11 @@
 // 127), as torch evaluates it on a GPU (a division by 127 or another order of the
 // products may end on the other side): about one row in 300 of 4096 columns.
 // That part comes last, when the row's registers are free.
-// Sums and scales in fp32; a row whose squares or products leave the safe fp32
-// range (bf16 values above 1e18 or products below 1e-30, infinities, NaN) is done
-// again in 64 bits.
+// The sum of squares is in 64 bits (a square is exact in fp32) and the scale rounded once:
+// with the sum in fp32, 35 % of the scales, and the xhat near a rounding border with
+// them, had another last bit (4096 x 4096 31.9 us so, 33.0 in 64 bits).  A row whose
+// squares or products leave the safe fp32 range (bf16 values above 1e18 or products
+// below 1e-30, infinities, NaN) is done again in 64 bits altogether.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -69,29 +71,43 @@ struct NormArgs {
   void *xhat;
   int64_t n;
   int d;
-  double eps;
+  double eps, inv_d;
 };
 
-// sum of v and maximum of the non-negative m over the row's threads, in every
+// sum of v in 64 bits and maximum of the non-negative m over the row's threads, in every
 // thread; a NaN in m survives (its bits compare above every number's).
+struct Part {
+  double v;
+  uint32_t mb;
+};
 template <bool WARP_ROW>
-__device__ __forceinline__ void row_reduce(float &v, float &m, float2 *part) {
+__device__ __forceinline__ void row_reduce(double &v, float &m, Part *part) {
   uint32_t mb = __float_as_uint(m);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   mb = __reduce_max_sync(0xffffffffu, mb);
   if constexpr (!WARP_ROW) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    __syncthreads();   // part may hold the previous reduction's values
-    if (lane == 0) part[warp] = make_float2(v, __uint_as_float(mb));
+    if (lane == 0) part[warp] = Part{v, mb};
     __syncthreads();
-    const float2 p = lane < nw ? part[lane] : make_float2(0.f, 0.f);
-    v = p.x;
+    const Part p = lane < nw ? part[lane] : Part{0.0, 0u};
+    v = p.v;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    mb = __reduce_max_sync(0xffffffffu, __float_as_uint(p.y));
+    mb = __reduce_max_sync(0xffffffffu, p.mb);
   }
   m = __uint_as_float(mb);
+}
+
+// top / (127 sqrt(mean)), rounded once: in fp32, and then what that is off by, from
+// top^2 - (127 scale)^2 mean in 64 bits.
+__device__ __forceinline__ float scale_of(float top, double mean) {
+  const float s = top / (127.f * sqrtf((float)mean));
+  if (!(s < 3e38f)) return s;
+  const float p2 = __uint_as_float(254u * 0x800000u - (__float_as_uint(top) & 0x7F800000u));   // top p2 in [1, 2)
+  const double t = (double)(top * p2), u = (double)s * (127.0 * p2);
+  const float off = (float)(t * t - u * u * mean) / (2.f * (top * p2) * (top * p2));
+  return (float)(s + (double)(s * off));
 }
 
 // sum, or maximum of non-negative values, over the row's threads in 64 bits
@@ -260,7 +276,7 @@ template <typename T, int V, bool WARP_ROW>
 // (40 registers let 1536 threads share an SM; the ties' part spills, not the rest)
 __global__ void __maxnreg__(WARP_ROW ? 128 : V <= 2 ? 40 : 64) rmsnorm_int8_kernel(const NormArgs a) {
   extern __shared__ __align__(16) int8_t row_codes[];   // perm: [rows of the CTA][d]
-  __shared__ float2 part[32];
+  __shared__ Part part[32];
   __shared__ double part64[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tid = WARP_ROW ? lane : (int)threadIdx.x;
@@ -303,7 +319,8 @@ __global__ void __maxnreg__(WARP_ROW ? 128 : V <= 2 ? 40 : 64) rmsnorm_int8_kern
       if (k < nvec) h[k] = hv[v];
     }
   }
-  float ss = 0.f, top;
+  double ss = 0.0;
+  float top;
   {
     uint32_t mb = 0;
 #pragma unroll
@@ -318,7 +335,8 @@ __global__ void __maxnreg__(WARP_ROW ? 128 : V <= 2 ? 40 : 64) rmsnorm_int8_kern
           const float2 f = Cvt<T>::up(p[i]);
           const float2 g = Cvt<T>::up(q[i]);
           mb = max(mb, max(__float_as_uint(f.x * g.x) & 0x7FFFFFFFu, __float_as_uint(f.y * g.y) & 0x7FFFFFFFu));
-          ss = fmaf(f.x, f.x, fmaf(f.y, f.y, ss));
+          ss += (double)(f.x * f.x);
+          ss += (double)(f.y * f.y);
         }
       }
     }
@@ -337,8 +355,8 @@ __global__ void __maxnreg__(WARP_ROW ? 128 : V <= 2 ? 40 : 64) rmsnorm_int8_kern
     zeros = WARP_ROW ? !__any_sync(0xffffffffu, bits) : !__syncthreads_or(bits);
   }
   float scale;
-  if (zeros || (ss < 1e37f && top < 1e37f && top > 1e-30f)) {
-    scale = zeros ? 1.f : top / (127.f * sqrtf(ss / (float)a.d + (float)a.eps));
+  if (zeros || (ss < 1e37 && top < 1e37f && top > 1e-30f)) {
+    scale = zeros ? 1.f : scale_of(top, ss * a.inv_d + a.eps);
     const float inv = zeros ? 0.f : 127.f / top;
     // ---- the codes, eight of a vector in two words
     uint2 c[V];
@@ -444,9 +462,10 @@ int launch_norm_t(const NormArgs &a, cudaStream_t st) {
   }
   // Vectors per thread: few where the rows are few and a row's latency counts, two
   // (the CTAs of an SM then wait at their barriers at different times) where they
-  // are many.  4096 rows of 4096: 36.9 us with one, 33.3 with two; 2048 of 8192: 50.9
-  // and 34.9; one row of 8192: 3.5 and 4.2.  1024 rows of 16384: 44.6 us with two
-  // (1024 threads), 39.0 with four; of 12288: 29.2 with two (768), 34.9 with four.
+  // are many.  bf16 with residual and xhat, us: 4096 rows of 4096 35.1 with one, 31.8 with
+  // two, 34.4 with four; 2048 of 8192: 50.1, 34.2, 37.3; one row of 4096: 2.8, 3.6, 4.8;
+  // 1024 rows of 16384: 43.8 with two (1024 threads), 38.6 with four.  (Before the sums
+  // were in 64 bits, which cost all of them 3 %.)
   const bool many = a.n > 2 * (int64_t)num_sms();
   auto threads = [&](int v) { return ((nvec + v - 1) / v + 31) / 32 * 32; };
   if (!many && threads(1) <= 1024) return launch_norm<T, 1>(a, false, threads(1), st);
@@ -483,7 +502,7 @@ extern "C" int gptq_rmsnorm_int8(const void *x, const void *residual, const void
     for (int j = 0; j < 4; ++j)
       if (overlap(out[i], in[j]) && !(i == 0 && j < 2 && h == in[j].p)) return GPTQ_ERR_INVALID_ARG;
   }
-  const NormArgs a{x, residual, gamma, perm, h, codes, scales, xhat, n, (int)d, eps};
+  const NormArgs a{x, residual, gamma, perm, h, codes, scales, xhat, n, (int)d, eps, 1.0 / (double)d};
   cudaStream_t st = (cudaStream_t)stream;
   return dtype == GPTQ_F16 ? launch_norm_t<__half>(a, st) : launch_norm_t<__nv_bfloat16>(a, st);
 }

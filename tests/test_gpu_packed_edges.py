@@ -217,3 +217,23 @@ def test_packed_linear_few_tokens_sums_are_fp32(n, group, bits, T):
     y = g.gptq_packed_linear(torch.from_numpy(X.astype(np.float32)).to(T).cuda(),
                              *dev(q, np.ones((r, G), dtype=np.float32), z), bits, group, dtype=F32)
     np.testing.assert_array_equal(f64(y), X @ (codes - z[:, gi]).T)
+
+
+@pytest.mark.parametrize("T", [F16, BF16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("n,d,eps", [(64, 32, 1e-5), (200, 1024, 1e-5), (300, 2080, 1e-6), (500, 4096, 1e-5),
+                                     (40, 11008, 1e-5), (7, 65536, 1e-5), (64, 512, 1e20), (64, 512, 1e-30)])
+def test_rmsnorm_int8_scales_are_rounded_once(n, d, eps, T):
+    # The scale is the formula's value in 64 bits rounded to fp32: at most half a step
+    # from it, and 2^-20 of a step for the operations in 64 bits and the correction of
+    # the fp32 quotient (2^-24 of what it is off by, which is at most a few steps).
+    import post_weight_quantization_19_b200 as g
+    rng = np.random.default_rng(d)
+    x = rng.standard_normal((n, d)) * np.exp(rng.standard_normal(d)) * 10.0 ** rng.uniform(-3, 2, size=(n, 1))
+    x = torch.from_numpy(x.astype(np.float32)).to(T).cuda()
+    gamma = torch.from_numpy((1 + 0.3 * rng.standard_normal(d)).astype(np.float32)).to(T).cuda()
+    out = g.gptq_rmsnorm_int8(x, gamma, eps=eps, xhat=True)
+    scales = oracle.rmsnorm_int8(f64(x), f64(gamma), eps)[1]
+    step = np.spacing(scales.astype(np.float32)).astype(np.float64)
+    assert np.all(np.abs(f64(out["scales"]) - scales) <= step * (0.5 + 2.0 ** -20))
+    want = (out["codes"].float() * out["scales"][:, None]).to(T)
+    assert torch.equal(out["xhat"], want)
