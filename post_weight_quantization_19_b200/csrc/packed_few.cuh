@@ -40,10 +40,10 @@
 // over the CTA's warps and over a cluster of CTAs, whose partial sums are added
 // through distributed shared memory in a fixed order.
 //
-// Measured, one token: 12288 x 49152, 3 bits, bf16 126 us (2.1 TB/s; the integer pipe
-// is busy 64 % of the time, 2.3 instructions per clock); 4 bits, fp16 93 us (3.6
-// TB/s); 4096 x 4096, 4 bits 5.9 us, most of it launch, fill and the last sums;
-// 11008 x 4096 with 8-bit x 9.6 us.
+// Measured, one token, inputs from HBM: 12288 x 49152, 3 bits, bf16 129 us (2.1 TB/s; the
+// integer pipe is busy 65 % of the time, 2.3 instructions per clock); 4 bits, fp16 94 us
+// (3.6 TB/s); 4096 x 4096, 4 bits 5.9 us, most of it launch, fill and the last sums; 11008
+// x 4096 with 8-bit x 10.5 us.
 #pragma once
 
 #include "packed_linear.h"

@@ -14,7 +14,7 @@
 // In a pair each CTA loads half of the tokens' x and the MMAs (cta_group::2) read
 // both halves: without pairs every CTA loaded all of its x from L2, 64 KB per 1024
 // clocks of MMAs for 256 tokens, and L2's bandwidth was the bound (4096 tokens x 4096
-// x 11008: 287 us, with pairs 241; 512 tokens x 8192 x 8192: 65.5 and 57.6).
+// x 11008: 287 us when pairs made it 241; 512 tokens x 8192 x 8192: 65.5 and 57.6).
 //
 //   w = T16(s (q - z)):  q - z is exact in 16 bits (code bits in the mantissa of
 //   a power of two M, minus M + z); s is split in two 16-bit parts, so w =
@@ -33,10 +33,10 @@
 // with fewer tiles than SMs split the k range over a cluster, whose CTAs add their
 // sums through distributed shared memory in a fixed order.
 //
-// Measured (4 bits, groups of 128): 4096 tokens x 4096 x 11008, bf16, 241 us in a
-// burst = 1532 TFLOP/s (0.92 of the measured burst rate); 1000 tokens of 8-bit x,
-// 11008 x 4096, 84 to 88 us (129 tiles over 74 pairs of SMs are two rounds); 64 tokens x 4096
-// x 4096, 13.3 us, bound by start, fill and the cluster's sums.
+// Measured (4 bits, groups of 128): 4096 tokens x 4096 x 11008, bf16, 247 to 252 us in a
+// burst = 1480 TFLOP/s (0.89 of the measured burst rate), 292 us under the power cap;
+// 1000 tokens of 8-bit x, 11008 x 4096, 82 us (129 tiles over 74 pairs of SMs are two
+// rounds); 64 tokens x 4096 x 4096, 13.3 us, bound by start, fill and the cluster's sums.
 //
 // fp32 results (FP32): a weight s (q - z) enters as an fp32 number, the sum of two fp16 or
 // three bf16 parts that the MMAs take one after the other with the same x, and a sum
