@@ -22,7 +22,6 @@
 // Codes of 2 and 3 bits travel as nibbles.  Rows too long for that (d > 49152)
 // go through bytes in shared memory, one row at a time.
 #include <mutex>
-#include <vector>
 
 #include "gptq_internal.h"
 #include "pack_bits.cuh"
@@ -336,30 +335,40 @@ int launch_regroup(const uint32_t *q, int32_t *perm, int64_t r, int d, uint32_t 
                              : launch_rows<BITS, false>(q, perm, r, d, out, st);
 }
 
-// Words of mapped host memory that calls report in: one per call in flight,
-// kept for later calls.  (A copy of one word to the host's stack cost more than
-// the kernels.)
+// Words of mapped host memory that calls report in: one per call in flight, kept for
+// later calls in a list through the words themselves.  (A copy of one word to the
+// host's stack cost more than the kernels.)
+struct Word {
+  int value;
+  Word *next;
+};
 std::mutex g_words_mutex;
-std::vector<int *> g_words;
+Word *g_words = nullptr;
 
-int take_word(int **word) {
+int take_word(Word **word) {
   {
     std::lock_guard<std::mutex> lock(g_words_mutex);
-    if (!g_words.empty()) {
-      *word = g_words.back();
-      g_words.pop_back();
+    if (g_words) {
+      *word = g_words;
+      g_words = g_words->next;
       return GPTQ_OK;
     }
   }
+  // (allowed while another stream is being captured, whose capture it would end otherwise)
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  GPTQ_CUDA_TRY(cudaThreadExchangeStreamCaptureMode(&mode));
   void *p = nullptr;
-  GPTQ_CUDA_TRY(cudaHostAlloc(&p, 64, cudaHostAllocMapped | cudaHostAllocPortable));
-  *word = static_cast<int *>(p);
+  const cudaError_t e = cudaHostAlloc(&p, 64, cudaHostAllocMapped | cudaHostAllocPortable);
+  (void)cudaThreadExchangeStreamCaptureMode(&mode);
+  GPTQ_CUDA_TRY(e);
+  *word = static_cast<Word *>(p);
   return GPTQ_OK;
 }
 
-void give_word(int *word) {
+void give_word(Word *word) {
   std::lock_guard<std::mutex> lock(g_words_mutex);
-  g_words.push_back(word);
+  word->next = g_words;
+  g_words = word;
 }
 
 int enqueue_regroup(const uint32_t *q, const int32_t *g_idx, int64_t r, int d, int bits, int group,
@@ -404,12 +413,12 @@ extern "C" int gptq_regroup(const int32_t *qweight, const int32_t *g_idx, int64_
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
   GPTQ_CUDA_TRY(cudaStreamIsCapturing(st, &capture));
   if (capture != cudaStreamCaptureStatusNone) return GPTQ_ERR_INVALID_ARG;   // it waits for its result
-  int *word = nullptr;
+  Word *word = nullptr;
   if (const int rc = take_word(&word)) return rc;
-  volatile int *seen = word;
+  volatile int *seen = &word->value;
   *seen = PENDING;
   int rc = enqueue_regroup(reinterpret_cast<const uint32_t *>(qweight), g_idx, r, (int)d, bits, group,
-                           reinterpret_cast<uint32_t *>(out), perm, word, st);
+                           reinterpret_cast<uint32_t *>(out), perm, &word->value, st);
   // (before the order's kernel has run the word is pending; a launch that failed
   // or a fault on the device ends the wait through the stream's state)
   for (unsigned spins = 1; *seen == PENDING; ++spins) {

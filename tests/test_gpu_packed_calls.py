@@ -2,6 +2,9 @@
 at odd places, no tokens or rows, calls from several threads, offsets past 32 bits.
 """
 
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -183,3 +186,74 @@ def test_rmsnorm_and_regroup_past_32_bits():
     tail = q[-3:].contiguous()
     want, order = g.gptq_regroup(tail, g_idx, bits, group)
     assert torch.equal(perm, order) and torch.equal(got[-3:], want)
+
+
+# ------------------------------------------------------------------ captures in a new process
+
+FIRST_CALLS = """
+import threading, torch, post_weight_quantization_19_b200 as g
+d, bits, group = 512, 4, 64
+def layer(r):
+    q = torch.randint(-2**31, 2**31, (r, d * bits // 32), device="cuda", dtype=torch.int64).to(torch.int32)
+    return q, torch.rand(r, d // group, device="cuda"), torch.full((r, d // group), 7, device="cuda", dtype=torch.int32)
+q, s, z = layer(200)
+"""
+
+REGROUP_BESIDE_A_CAPTURE = FIRST_CALLS + """
+g_idx = (torch.arange(d, device="cuda") // group).to(torch.int32)[torch.randperm(d, device="cuda")]
+out, perm = torch.empty_like(q), torch.empty_like(g_idx)
+side, x, said = torch.cuda.Stream(), torch.zeros(8, device="cuda"), []
+torch.cuda.synchronize()
+def regroup():
+    try:
+        g.gptq_regroup(q, g_idx, bits, group, out=out, perm=perm, stream=side)
+        said.append(None)
+    except BaseException as e:
+        said.append(repr(e))
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    x += 1
+    t = threading.Thread(target=regroup)
+    t.start()
+    t.join()
+    regroup()
+    x += 1
+assert said == [None, None], said
+graph.replay()
+torch.cuda.synchronize()
+assert x[0] == 2 and torch.equal(perm.long(), torch.sort(g_idx, stable=True)[1])
+print("done")
+"""
+
+FIRST_CALL_IS_CAPTURED = FIRST_CALLS + """
+gamma = torch.ones(d, dtype=torch.float16, device="cuda")
+perm = torch.randperm(d, device="cuda").to(torch.int32)
+xs = [torch.randn(n, d, device="cuda").half() for n in (3, 40, 400)]
+torch.cuda.synchronize()
+def calls():
+    ys = []
+    for x in xs:
+        n = g.gptq_rmsnorm_int8(x, gamma, eps=1e-5, xhat=True)
+        ys += [n["codes"], n["scales"], n["xhat"]]
+        for dtype in (torch.float16, torch.float32):
+            ys.append(g.gptq_packed_linear(x, q, s, z, bits, group, perm=perm, dtype=dtype))
+            ys.append(g.gptq_packed_linear(n["codes"], q, s, z, bits, group, x_scales=n["scales"], dtype=dtype))
+    return ys
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = calls()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, calls()))
+print("done")
+"""
+
+
+@pytest.mark.parametrize("program", [REGROUP_BESIDE_A_CAPTURE, FIRST_CALL_IS_CAPTURED],
+                         ids=["regroup_beside_a_capture", "first_call_is_captured"])
+def test_first_calls_of_a_process_and_captures(program):
+    # what a call sets up once per process neither ends a capture (of its own stream or
+    # of another one) nor is refused by it
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", program], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and run.stdout.strip() == "done", run.stderr[-2000:]
