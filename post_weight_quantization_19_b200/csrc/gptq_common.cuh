@@ -45,16 +45,6 @@ void set_last_error_msg(const char *file, int line, const char *msg);
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// Memory that a call reads or writes, and whether two such share a byte.
-struct Span {
-  const void *p;
-  size_t bytes;
-};
-inline bool overlap(const Span &a, const Span &b) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
-}
-
 // Device status word of this library (timeouts of asynchronous kernels).
 int *device_status_word();
 

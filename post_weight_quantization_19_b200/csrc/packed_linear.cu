@@ -14,6 +14,7 @@
 // layer's column order and, for many tokens, 8-bit codes into fp16.
 #include <type_traits>
 
+#include "overlap.h"
 #include "packed_linear.h"
 
 namespace gptq {

@@ -24,6 +24,7 @@
 #include <mutex>
 
 #include "gptq_internal.h"
+#include "overlap.h"
 #include "pack_bits.cuh"
 #include "unpack_bits.cuh"
 

@@ -33,6 +33,7 @@
 #include <cuda_fp16.h>
 
 #include "gptq_internal.h"
+#include "overlap.h"
 
 namespace gptq {
 namespace {
