@@ -2,7 +2,8 @@
 
 With fp32 results a weight enters to fp32 accuracy for any number of tokens: exactly
 (few tokens), or as s (q - z) rounded to fp32 once (2^-24) and split into parts of 16
-bits (fp16: two, the second rounded, another 2^-24 at most; bf16: three, exactly).
+bits (bf16: three, exactly; fp16: two, of which the second is at most half a step of the
+first, 2^-11 of w, and is rounded to 11 bits itself: 2^-23 of w).
 
 Sums: the tensor core adds at most 256 features of one result before they are added
 in fp32, in at most PARTS * 16 instructions of 16 products each.  It truncates: what an
@@ -11,7 +12,7 @@ so far, and 16 steps more for what the products lose among themselves.  The d / 
 which grow evenly (so half of them counts), and up to 24 more additions (warps, CTAs,
 bias, the scale of the token) are rounded, 2^-24 each.  So, with a = sum |w x|,
 
-    |y - ref| <= 2^-24 |ref| + (2 * 2^-24 + (PARTS * 32 + 16) 2^-23 + (d / 512 + 24) 2^-24) a
+    |y - ref| <= 2^-24 |ref| + (3 * 2^-24 + (PARTS * 32 + 16) 2^-23 + (d / 512 + 24) 2^-24) a
 
 and with few tokens the terms that cancel in s (sum (B + q) x - (B + z) sum x) add 24
 additions of a group over sum s (2 B + q + z) |x|, B <= 64, at four half steps.
@@ -76,7 +77,7 @@ def few_tokens(n, T):
 
 
 def tolerance(T, d, ref, a, parts, few):
-    tol = 2.0 ** -24 * ref.abs() + (2 * 2.0 ** -24 + (PARTS[T] * 32 + 16) * 2.0 ** -23
+    tol = 2.0 ** -24 * ref.abs() + (3 * 2.0 ** -24 + (PARTS[T] * 32 + 16) * 2.0 ** -23
                                     + (d / 512 + 24) * 2.0 ** -24) * a
     return tol + (4 * 24 * 2.0 ** -24 * parts if few and T is not I8 else 0)
 
