@@ -21,9 +21,9 @@
 //   fma(q - z, s_hi, (q - z) s_lo) is s (q - z) rounded once (up to the second
 //   part's own rounding, 2^-10 of half a step).  This rounding is
 //   gptq_dequant_fp16's; fp32 weights would need three times the tensor work.
-//   With fp16, s is divided by a power of two per row (the largest scale's) and
-//   the row's sums multiplied by it again, so scales outside fp16's range lose
-//   nothing.
+//   With fp16, s is multiplied by a power of two per row (that brings the largest weight
+//   to fp16's upper range) and the row's sums divided by it again, so scales outside
+//   fp16's range lose nothing, nor those far below the row's largest.
 //
 // Warp 0 loads x, warp 1 issues the MMAs, warps 2-3 load codes, scales and zeros;
 // warps 4-19 are four converter warpgroups, one for each 64 columns of a block;
@@ -119,7 +119,7 @@ struct ManyShared {
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
-  uint32_t exponent[2][PM];   // fp16: row_exponent of a tile's rows
+  uint32_t exponent[2][PM];   // fp16: safe_exponent of a tile's rows
   alignas(16) uint4 stage[4][64];   // results on their way out, per warp
   alignas(16) float scale[4][PN];   // and the scales of x's tokens
 };
@@ -333,11 +333,15 @@ __device__ __forceinline__ int group_of(const ManyArgs &a, int c) {
   return (int)(((uint64_t)(uint32_t)c * a.gdiv) >> 31);
 }
 
-// Exponent bits of the power of two that a row's scales are divided by for
-// fp16: the largest one's, from the bits of its magnitude; 2^(254 - e) is its
-// reciprocal.
+// fp16: a row's scales are multiplied by 2^(LIFT + 127 - e), with e the exponent bits of
+// the largest one (from the bits of its magnitude), and its sums by the reciprocal:
+// the largest weights, below 2^(LIFT + 1 + BITS) = 2^15, fill fp16's range, so that groups
+// with scales of up to 2^(LIFT + 14) less than the row's largest are still normal numbers.
+template <int BITS>
+constexpr uint32_t LIFT = 14 - BITS;
+template <int BITS>
 __device__ __forceinline__ uint32_t safe_exponent(uint32_t top) {
-  return min(max(top >> 23, 1u), 253u);
+  return min(max(top >> 23, LIFT<BITS> + 1u), 253u);
 }
 
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
@@ -773,12 +777,12 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         }
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
-          const uint32_t e = safe_exponent(__reduce_max_sync(0xffffffffu, top[i]));
+          const uint32_t e = safe_exponent<BITS>(__reduce_max_sync(0xffffffffu, top[i]));
           if (lane == 0) sh.exponent[parity][(warp - 4) * EACH + i] = e;
         }
         // (the other parity's values were read before this barrier)
         asm volatile("bar.sync 1, %0;" ::"n"(128 * WGS) : "memory");
-        inv = __uint_as_float((254u - sh.exponent[parity][lrow]) << 23);
+        inv = __uint_as_float((254u + LIFT<BITS> - sh.exponent[parity][lrow]) << 23);
       }
       for (int kb = kb0; kb < kb1 && ok; ++kb) {
         if (!mbar_wait_bounded(&sh.full_c[slot], phase)) {
@@ -902,7 +906,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         uint32_t top = 0;
 #pragma unroll 4
         for (int g = ga; g <= gb; ++g) top = max(top, __float_as_uint(__ldg(srow + g)) & 0x7FFFFFFFu);
-        f = __uint_as_float(safe_exponent(top) << 23);
+        f = __uint_as_float((safe_exponent<BITS>(top) - LIFT<BITS>) << 23);
       }
       const float bias = a.p.bias && live ? load_as_float(a.p.bias, a.p.ytype, row) : 0.f;
       for (int h = 0; h < a.halves; ++h) {

@@ -239,3 +239,42 @@ def test_layers_of_up_to_2_25_codes_take_the_exact_kernel(n, T):
         rel = [float((y.double() - ref).norm() / ref.norm()) for y in (few, many)]
         u = 2.0 ** -11 if T is F16 else 2.0 ** -8
         assert rel[0] <= (u / 3 ** 0.5 if exact else u) and rel[1] <= u
+
+
+# ------------------------------------------------------------------ scales of one row far apart
+
+@pytest.mark.parametrize("T", [F16, BF16, I8], ids=["fp16", "bf16", "int8"])
+@pytest.mark.parametrize("n,bits", [(4, 4), (40, 2), (40, 8), (150, 3), (300, 4), (300, 8)])
+def test_groups_with_small_scales_keep_their_accuracy(n, bits, T):
+    # Groups whose scale is 2^-k of the row's largest one, met by x alone (x is 0 elsewhere): their
+    # weights are as good as any.  fp32 results for k = 8; 16-bit results for k = 18 with
+    # 2 to 4 bits (fp16 products hold codes down to 2^(bits - 24) of the row's largest
+    # scale at full precision) and k = 12 with 8.
+    import post_weight_quantization_19_b200 as g
+    r, d, group = 130, 512, 128
+    q, s, z = layer(r, d, bits, group, n + bits)
+    z = torch.full_like(z, (1 << bits) // 2)
+    x, xs = activations(n, d, n, T)
+    x[:, :128] = 0
+    x[:, 256:384] = 0
+    for dtype, k in ((F32, 8), (F16 if T is I8 else T, 12 if bits == 8 else 18)):
+        scales = s.clone()
+        scales[:, 1] *= 2.0 ** -k
+        scales[:, 3] *= 2.0 ** -k
+        scales[:, 0] = s.max()
+        ref, a, parts = reference(x, q, scales, z, bits, group, xs)
+        lift = 2.0 ** k if dtype is F16 else 1.0     # fp16 results in its normal range
+        if dtype is F16:
+            if xs is None:
+                scales, ref, a, parts = scales * lift, ref * lift, a * lift, parts * lift
+            else:
+                xs, ref, a, parts = xs * lift, ref * lift, a * lift, parts * lift
+        y = g.gptq_packed_linear(x, q, scales, z, bits, group, x_scales=xs, dtype=dtype)
+        err = (y.double() - ref).abs()
+        tol = tolerance(T, d, ref, a, parts, n <= 8 or (dtype is F32 and few_tokens(n, T)))
+        if dtype is not F32:
+            u = 2.0 ** -8 if dtype is BF16 else 2.0 ** -11
+            tol = tol + u * ref.abs() * (1 + 2.0 ** -6) + (0 if n <= 8 else u * a)
+            if dtype is F16:
+                tol = tol + 2.0 ** -25
+        assert bool((err <= tol).all()), float((err / tol).max())
