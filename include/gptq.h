@@ -396,6 +396,101 @@ int gptq_regroup(const int32_t *qweight, const int32_t *g_idx, int64_t r, int64_
                  int group, int32_t *out, int32_t *perm, gptq_stream_t stream);
 
 /*
+ * The 8-bit feed-forward block: layers with one scale per row as 8-bit integers,
+ * their product with 8-bit activations, the gated projections in one kernel, and the
+ * activation in 8 bits for the layer that follows.  Integers, scales and the symmetric
+ * quantiser as above ("LLM 量化技术" §1.2: a value is s q, so a product of two
+ * quantised vectors is the integers' product times both scales).
+ *
+ * Activation functions, of v:
+ *   GPTQ_ACT_NONE v;  GPTQ_ACT_RELU max(v, 0);  GPTQ_ACT_SILU v / (1 + exp(-v));
+ *   GPTQ_ACT_GELU v (1 + erf(v / sqrt 2)) / 2.
+ */
+#define GPTQ_ACT_NONE 0
+#define GPTQ_ACT_RELU 1
+#define GPTQ_ACT_SILU 2
+#define GPTQ_ACT_GELU 3
+
+/*
+ * gptq_int8_weights -- a packed layer with one scale per row (group = -1) as 8-bit
+ * integers: w[i, j] = q[i, j] - zeros[i].  Done once per layer.
+ *
+ *   qweight  device int32 [r x d*bits/32];  scales device fp32 [r];  zeros device
+ *            int32 [r], as gptq_quantize_layer writes them with group = -1.  Zero
+ *            points outside [0, 2^bits - 1] are clamped to it.
+ *   w        device int8 [r x d], 16-byte aligned, written.
+ *   w_scales device fp32 [r], written: scales, but NaN for a row in which some
+ *            q - zero is outside [-128, 127] (its w hold the nearest integers).  That can
+ *            be with 8 bits only; layers of the symmetric quantiser (GPTQ_SYMMETRIC)
+ *            always fit.
+ *   w and w_scales share no memory with each other or with an input:
+ *   GPTQ_ERR_INVALID_ARG.
+ *   r >= 0, d > 0, d % 32 == 0, d <= 65536;  bits 2, 3, 4 or 8.  Asynchronous.
+ */
+int gptq_int8_weights(const int32_t *qweight, const float *scales, const int32_t *zeros, int64_t r,
+                      int64_t d, int bits, int8_t *w, float *w_scales, gptq_stream_t stream);
+
+/*
+ * gptq_int8_linear -- y[t, i] = x_scales[t] w_scales[i] sum_j x[t, j] w[i, j] + bias[i],
+ * for any number of tokens.
+ *
+ *   x        device int8 [n x d], 16-byte aligned;  x_scales device fp32 [n] (as
+ *            gptq_rmsnorm_int8 and gptq_activation_int8 write them).
+ *   w        device int8 [r x d], 16-byte aligned;  w_scales device fp32 [r].
+ *   bias     device [r] of `ytype`, or NULL.
+ *   y        device [n x r] of `ytype` (GPTQ_F16, GPTQ_BF16 or GPTQ_F32), element
+ *            aligned, written.  Shares no memory with an input: GPTQ_ERR_INVALID_ARG.
+ *   n, r >= 0, d > 0, d % 32 == 0, d <= 65536.
+ *   Sums are exact integers; then ((float)sum x_scales) w_scales + bias in fp32, and one
+ *   rounding to `ytype`.  A scale that is NaN or infinite gives what that formula
+ *   gives, in its own token or row.
+ *   n == 0 or r == 0: nothing to do.  Asynchronous; a bounded in-kernel wait that runs
+ *   out is reported by gptq_check_device_status.
+ */
+int gptq_int8_linear(const int8_t *x, const float *x_scales, int64_t n, const int8_t *w,
+                     const float *w_scales, int64_t r, int64_t d, const void *bias, void *y,
+                     int ytype, gptq_stream_t stream);
+
+/*
+ * gptq_int8_gated -- the gated half of a feed-forward block in one kernel:
+ *   y[t, i] = act(g[t, i]) u[t, i], g and u the products of x with `gate` and `up` as
+ * gptq_int8_linear forms them, in fp32 up to the one rounding to `ytype`.
+ *
+ *   gate, up  device int8 [r x d], 16-byte aligned (they may be the same), with
+ *             gate_scales and up_scales device fp32 [r].
+ *   gate_bias, up_bias  device [r] of `ytype`, or NULL, each by itself.
+ *   activation  GPTQ_ACT_*.
+ *   Other arguments and conditions as gptq_int8_linear.
+ */
+int gptq_int8_gated(const int8_t *x, const float *x_scales, int64_t n, const int8_t *gate,
+                    const float *gate_scales, const int8_t *up, const float *up_scales, int64_t r,
+                    int64_t d, const void *gate_bias, const void *up_bias, int activation, void *y,
+                    int ytype, gptq_stream_t stream);
+
+/*
+ * gptq_activation_int8 -- u = act(x) or, with `up`, act(x) up, in symmetric 8-bit codes
+ * with one scale per token:
+ *   scale = max|u| / 127 (1 for a row of zeros)
+ *   code = rint(127 u / max|u|), rint to nearest, ties to even
+ *   xhat = scale * code, rounded to the type
+ *
+ *   x, up    device [n x d] of `dtype` (GPTQ_F16 or GPTQ_BF16), row-major, 16-byte
+ *            aligned.  up may be NULL.
+ *   activation  GPTQ_ACT_*.
+ *   n, d     n >= 0, d > 0, d % 32 == 0, d <= 65536.
+ *   perm, codes, scales, xhat   as gptq_rmsnorm_int8.
+ *   The outputs share no memory with each other or with an input:
+ *   GPTQ_ERR_INVALID_ARG.
+ *   u is not rounded: codes and scale are those of the formula in 64 bits, the scale
+ *   rounded once.  A row with a u that is NaN or infinite has scale NaN, codes 0 and xhat
+ *   NaN; other rows are not touched by it.
+ *   n == 0: nothing to do.  Asynchronous: one kernel.
+ */
+int gptq_activation_int8(const void *x, const void *up, int dtype, int64_t n, int64_t d,
+                         int activation, const int32_t *perm, int8_t *codes, float *scales,
+                         void *xhat, gptq_stream_t stream);
+
+/*
  * gptq_quantize_layer_noalloc -- gptq_quantize_layer for callers that cannot
  * allocate device memory.  (The GPTQ pages have no counterpart: this is a
  * deployment convenience of this library, not a step of the method.)

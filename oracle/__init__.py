@@ -7,6 +7,8 @@ baseline leg import this package.  The library under
 
 from .gptq_ref import (  # noqa: F401
     act_order_perm,
+    activation,
+    activation_int8,
     brute_force_min_loss,
     dampen,
     dequant_gemv,
@@ -16,6 +18,7 @@ from .gptq_ref import (  # noqa: F401
     gptq_sweep,
     hessian,
     hessian_rows,
+    int8_product,
     inverse_upper_cholesky,
     inverse_upper_cholesky_lowmem,
     layer_loss,

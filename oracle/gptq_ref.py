@@ -58,6 +58,7 @@ Parity status: every function here is pinned by tests under ``tests/``
 from __future__ import annotations
 
 import itertools
+import math
 
 import numpy as np
 
@@ -660,3 +661,37 @@ def regroup(codes: np.ndarray, g_idx: np.ndarray) -> tuple[np.ndarray, np.ndarra
     """(codes with the columns in the stable order of g_idx, that order)."""
     perm = np.argsort(np.asarray(g_idx), kind="stable")
     return np.asarray(codes)[:, perm], perm
+
+
+def activation(v: np.ndarray, name: str) -> np.ndarray:
+    """none, relu, silu = v / (1 + exp(-v)), gelu = v (1 + erf(v / sqrt 2)) / 2, elementwise."""
+    v = np.asarray(v, dtype=F64)
+    if name == "none":
+        return v
+    if name == "relu":
+        return np.where(v < 0, 0.0, v)
+    with np.errstate(over="ignore", invalid="ignore"):
+        if name == "silu":
+            return v / (1.0 + np.exp(-v))
+        if name == "gelu":   # 1 + erf(z) = erfc(-z), which does not cancel for negative v
+            return 0.5 * v * np.vectorize(math.erfc, otypes=[F64])(-v / math.sqrt(2.0))
+    raise ValueError(name)
+
+
+def activation_int8(x: np.ndarray, up: np.ndarray | None, name: str) -> tuple[np.ndarray, np.ndarray]:
+    """(codes int64 [n x d], scales [n]) of u = act(x) (* up) per row: scale = max|u| / 127
+    (1 for a zero row), code = rint(127 u / max|u|)."""
+    u = activation(x, name)
+    if up is not None:
+        u = u * np.asarray(up, dtype=F64)
+    top = np.abs(u).max(axis=1, keepdims=True)
+    codes = np.round(np.where(top > 0, 127.0 * u / np.where(top > 0, top, 1.0), 0.0)).astype(np.int64)
+    return codes, np.where(top > 0, top / 127.0, 1.0)[:, 0]
+
+
+def int8_product(x: np.ndarray, xs: np.ndarray, w: np.ndarray, ws: np.ndarray,
+                 bias: np.ndarray | None = None) -> np.ndarray:
+    """xs[t] ws[i] sum_j x[t, j] w[i, j] + bias[i]; the sum of integers is exact."""
+    y = (np.asarray(x, dtype=F64) @ np.asarray(w, dtype=F64).T) * np.asarray(xs, dtype=F64)[:, None]
+    y = y * np.asarray(ws, dtype=F64)
+    return y if bias is None else y + np.asarray(bias, dtype=F64)

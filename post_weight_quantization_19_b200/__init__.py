@@ -13,8 +13,12 @@ same entry-point names.
 
 from .gptq import (  # noqa: F401
     GPTQError,
+    gptq_activation_int8,
     gptq_check_device_status,
     gptq_hessian_accumulate,
+    gptq_int8_gated,
+    gptq_int8_linear,
+    gptq_int8_weights,
     gptq_last_phase_ms,
     gptq_launch_count,
     gptq_layer_host_workspace_bytes,

@@ -53,6 +53,14 @@ SIGNATURES = {
                                    c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
     "gptq_regroup": (c_int, [c_void_p, c_void_p, c_int64, c_int64, c_int, c_int, c_void_p,
                              c_void_p, c_void_p]),
+    "gptq_int8_weights": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int, c_void_p,
+                                  c_void_p, c_void_p]),
+    "gptq_int8_linear": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_int64,
+                                 c_void_p, c_void_p, c_int, c_void_p]),
+    "gptq_int8_gated": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p,
+                                c_int64, c_int64, c_void_p, c_void_p, c_int, c_void_p, c_int, c_void_p]),
+    "gptq_activation_int8": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int64, c_int, c_void_p,
+                                     c_void_p, c_void_p, c_void_p, c_void_p]),
     "gptq_quantize_layer_noalloc": (c_int, [c_void_p, c_int64, c_int64, c_void_p, c_int, c_int,
                                             c_int, c_float, c_int, c_void_p, c_void_p, c_void_p,
                                             c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),

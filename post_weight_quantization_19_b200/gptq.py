@@ -433,6 +433,137 @@ def gptq_regroup(qweight: torch.Tensor, g_idx: torch.Tensor, bits: int, group: i
     return out, perm
 
 
+_ACTIVATION = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+
+
+def _activation(name: str) -> int:
+    if name not in _ACTIVATION:
+        raise ValueError(f"activation must be one of {', '.join(_ACTIVATION)}, got {name!r}")
+    return _ACTIVATION[name]
+
+
+def gptq_int8_weights(qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, d: int, bits: int, *,
+                      w: torch.Tensor | None = None, w_scales: torch.Tensor | None = None,
+                      stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """A packed layer with one scale per row (group -1) as 8-bit integers: w int8
+    [r, d] = q - zeros, and w_scales fp32 [r], for ``gptq_int8_linear`` and
+    ``gptq_int8_gated``.
+
+    Layers of 2, 3 and 4 bits, and 8-bit ones of the symmetric quantiser (``sym=True``); a
+    row whose q - zero leaves int8 has scale NaN.
+    """
+    lib = _abi.load()
+    if not qweight.is_cuda or qweight.dim() != 2:
+        raise ValueError("qweight must be a CUDA tensor [rows, words]")
+    if bits not in (2, 3, 4, 8):
+        raise GPTQError(1, "gptq_int8_weights")
+    r, dev = qweight.shape[0], qweight.device
+    with _on(stream):
+        if w is None:
+            w = torch.empty((r, d), dtype=torch.int8, device=dev)
+        if w_scales is None:
+            w_scales = torch.empty(r, dtype=torch.float32, device=dev)
+    _check(_launch(
+        dev, stream, lib.gptq_int8_weights, _shaped(qweight, torch.int32, (r, d * bits // 32), dev, "qweight"),
+        _shaped(scales, torch.float32, (r, 1), dev, "scales"), _shaped(zeros, torch.int32, (r, 1), dev, "zeros"),
+        r, d, bits, _shaped(w, torch.int8, (r, d), dev, "w"),
+        _shaped(w_scales, torch.float32, (r,), dev, "w_scales")), "gptq_int8_weights")
+    return w, w_scales
+
+
+def _result(y: torch.Tensor | None, dtype: torch.dtype | None, shape: tuple, device: torch.device,
+            stream) -> torch.Tensor:
+    """The given y, or a new one (fp16 by default)."""
+    if y is None:
+        with _on(stream):
+            y = torch.empty(shape, dtype=torch.float16 if dtype is None else dtype, device=device)
+    elif dtype is not None and y.dtype != dtype:
+        raise ValueError(f"y must be {dtype}, got {y.dtype}")
+    if y.dtype not in (torch.float16, torch.bfloat16, torch.float32):
+        raise ValueError(f"y must be float16, bfloat16 or float32, got {y.dtype}")
+    return y
+
+
+def gptq_int8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, *,
+                     bias: torch.Tensor | None = None, dtype: torch.dtype | None = None,
+                     y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y [n, r] = x_scales w_scales (x w^T) + bias in 8-bit integers, for any number of tokens.
+
+    x int8 [n, d] with x_scales fp32 [n] (from ``gptq_rmsnorm_int8`` or
+    ``gptq_activation_int8``), w int8 [r, d] with w_scales fp32 [r] (from
+    ``gptq_int8_weights``).  y has ``dtype`` (or the given y's type): fp16 by default,
+    bf16 or fp32; a bias has it too.  Sums are exact.
+    """
+    lib = _abi.load()
+    _activations(x, (torch.int8,))
+    n, d = x.shape
+    r, dev = w.shape[0], x.device
+    y = _result(y, dtype, (n, r), dev, stream)
+    _check(_launch(
+        dev, stream, lib.gptq_int8_linear, _shaped(x, torch.int8, (n, d), dev, "x"),
+        _shaped(x_scales, torch.float32, (n,), dev, "x_scales"), n, _shaped(w, torch.int8, (r, d), dev, "w"),
+        _shaped(w_scales, torch.float32, (r,), dev, "w_scales"), r, d, _shaped(bias, y.dtype, (r,), dev, "bias"),
+        _shaped(y, y.dtype, (n, r), dev, "y"), _DTYPE[y.dtype]), "gptq_int8_linear")
+    return y
+
+
+def gptq_int8_gated(x: torch.Tensor, x_scales: torch.Tensor, gate: torch.Tensor, gate_scales: torch.Tensor,
+                    up: torch.Tensor, up_scales: torch.Tensor, *, activation: str = "silu",
+                    gate_bias: torch.Tensor | None = None, up_bias: torch.Tensor | None = None,
+                    dtype: torch.dtype | None = None, y: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """y [n, r] = act(gate product) * (up product), both as ``gptq_int8_linear``, in one
+    kernel.  ``activation``: "none", "relu", "silu" or "gelu" (with erf)."""
+    lib = _abi.load()
+    _activations(x, (torch.int8,))
+    act = _activation(activation)
+    n, d = x.shape
+    r, dev = gate.shape[0], x.device
+    y = _result(y, dtype, (n, r), dev, stream)
+    _check(_launch(
+        dev, stream, lib.gptq_int8_gated, _shaped(x, torch.int8, (n, d), dev, "x"),
+        _shaped(x_scales, torch.float32, (n,), dev, "x_scales"), n,
+        _shaped(gate, torch.int8, (r, d), dev, "gate"), _shaped(gate_scales, torch.float32, (r,), dev, "gate_scales"),
+        _shaped(up, torch.int8, (r, d), dev, "up"), _shaped(up_scales, torch.float32, (r,), dev, "up_scales"), r, d,
+        _shaped(gate_bias, y.dtype, (r,), dev, "gate_bias"), _shaped(up_bias, y.dtype, (r,), dev, "up_bias"), act,
+        _shaped(y, y.dtype, (n, r), dev, "y"), _DTYPE[y.dtype]), "gptq_int8_gated")
+    return y
+
+
+def gptq_activation_int8(x: torch.Tensor, up: torch.Tensor | None = None, *, activation: str = "silu",
+                         perm: torch.Tensor | None = None, xhat: bool = False, outputs: dict | None = None,
+                         stream=None) -> dict:
+    """u = act(x), times ``up`` when given, in symmetric 8-bit codes with one scale per token.
+
+    x and up [n, d] fp16 or bf16; ``activation`` as ``gptq_int8_gated``.  Returns ``codes``
+    int8 [n, d], ``scales`` fp32 [n], and ``xhat`` = scales * codes in x's type when asked
+    for; ``perm`` and ``outputs`` as ``gptq_rmsnorm_int8``.
+    """
+    lib = _abi.load()
+    _activations(x, (torch.float16, torch.bfloat16))
+    act = _activation(activation)
+    n, d = x.shape
+    dev, T = x.device, x.dtype
+    out = dict(outputs or {})
+    codes, scales, xh = (out.get(k) for k in ("codes", "scales", "xhat"))
+    with _on(stream):
+        if codes is None:
+            codes = torch.empty((n, d), dtype=torch.int8, device=dev)
+        if scales is None:
+            scales = torch.empty(n, dtype=torch.float32, device=dev)
+        if xh is None and xhat:
+            xh = torch.empty((n, d), dtype=T, device=dev)
+    _check(_launch(
+        dev, stream, lib.gptq_activation_int8, _shaped(x, T, (n, d), dev, "x"), _shaped(up, T, (n, d), dev, "up"),
+        _DTYPE[T], n, d, act, _shaped(perm, torch.int32, (d,), dev, "perm"),
+        _shaped(codes, torch.int8, (n, d), dev, "codes"), _shaped(scales, torch.float32, (n,), dev, "scales"),
+        _shaped(xh, T, (n, d), dev, "xhat")), "gptq_activation_int8")
+    res = {"codes": codes, "scales": scales}
+    if xh is not None:
+        res["xhat"] = xh
+    return res
+
+
 def gptq_pack(codes: torch.Tensor, bits: int, qweight: torch.Tensor | None = None,
               stream=None) -> torch.Tensor:
     lib = _abi.load()
