@@ -55,6 +55,7 @@ int int8_product(const Int8Args &a, int layers, int64_t d, cudaStream_t st) {
                           Span{a.bias[k], (size_t)a.r * ysize}})
       if (overlap(out, s)) return GPTQ_ERR_INVALID_ARG;
   }
+  if (a.n > 256) return launch_int8_pair(a, st);
   return launch_int8_single(a, st);
 }
 

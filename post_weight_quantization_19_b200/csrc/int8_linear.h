@@ -24,6 +24,8 @@ struct Int8Args {
 
 // Weights as the MMA's rows: any number of tokens, k split over clusters when tiles are few.
 int launch_int8_single(const Int8Args &a, cudaStream_t st);
+// Many tokens: pairs of CTAs, tokens as the MMA's rows.
+int launch_int8_pair(const Int8Args &a, cudaStream_t st);
 
 // A sum with its token's and row's scales, and the bias.
 __device__ __forceinline__ float scaled_sum(int sum, float xs, float ws, float bias) {

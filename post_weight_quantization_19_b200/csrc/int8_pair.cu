@@ -1,0 +1,337 @@
+// gptq_int8_linear and gptq_int8_gated for many tokens: pairs of CTAs, tokens as the rows
+// of the tensor-core product.
+//
+// A pair takes a tile of 256 tokens and N <= 256 rows of W with one MMA of both tensor
+// cores (cta_group::2, M = 256): each CTA loads its own 128 tokens of x and half of W's
+// rows, so a 128-column slab of a 256 x 256 tile costs each CTA 32 KB in the 512 clocks
+// that its MMAs take, where a single CTA's tile of 128 x 256 loads 48 KB.  In a gated
+// block one CTA loads N / 2 rows of the gate and the other the same rows of the up
+// projection: the sums of both lie in the two halves of a token's columns of tensor
+// memory, and the thread that owns the token writes their product alone.
+// Two accumulators of 256 columns: eight warps of each CTA write one out, a thread a
+// token, while the other fills.
+#include "int8_linear.h"
+
+namespace gptq {
+namespace {
+
+constexpr int TOKENS = 128;               // per CTA of a pair
+constexpr int SLAB = 128;                 // columns per stage
+constexpr int ROWS = 256;                 // most rows of W per tile (UMMA N)
+constexpr int STAGES = 6;
+constexpr int X_BYTES = TOKENS * SLAB;
+constexpr int OUT_WARPS = 8;
+constexpr int PAIR_THREADS = 32 * (2 + OUT_WARPS);
+constexpr size_t PAIR_SMEM = (size_t)STAGES * (X_BYTES + ROWS / 2 * SLAB);
+
+struct PairArgs {
+  Int8Args p;
+  int N;              // rows of W per tile, of both layers together; a multiple of 32
+  int nT, nR;         // tiles along the tokens and along the rows
+  int *status;
+};
+
+struct PairShared {
+  uint64_t full[STAGES], empty[STAGES];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  alignas(16) float scale[2][ROWS], bias[2][ROWS];   // of a tile's columns, by accumulator
+};
+
+__device__ __forceinline__ void pair_timeout(int *status, PairShared &sh) {
+  atomicCAS(status, 0, (int)GPTQ_ERR_TIMEOUT);
+  *(volatile int *)&sh.abort = 1;
+}
+
+__device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// 16 results of one token to its row of y, `left` of them in y.
+template <typename Y>
+__device__ __forceinline__ void write16(Y *y, const float (&v)[16], int64_t left, int align) {
+  if (left >= 16 && align >= 16) {
+    constexpr int WORDS = 16 * sizeof(Y) / 4;
+    uint32_t o[WORDS];
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      if constexpr (sizeof(Y) == 2)
+        o[i] = to_pair<Y>(v[2 * i], v[2 * i + 1]);
+      else
+        o[i] = __float_as_uint(v[i]);
+    }
+    if (align >= 32) {
+#pragma unroll
+      for (int i = 0; i < WORDS; i += 8) {
+        const uint32_t w[8] = {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6], o[i + 7]};
+        store32(reinterpret_cast<uint32_t *>(y) + i, w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < WORDS; i += 4)
+        reinterpret_cast<uint4 *>(y)[i / 4] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < left) y[i] = to_result<Y>(v[i]);
+  }
+}
+
+template <bool GATED, int ACT, typename Y>
+__global__ void __launch_bounds__(PAIR_THREADS, 1)
+    int8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                     const __grid_constant__ CUtensorMap tmU, const PairArgs a) {
+  extern __shared__ uint8_t dyn_smem[];
+  __shared__ PairShared sh;
+  uint8_t *smem =
+      reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int half = a.N / 2, stage_bytes = X_BYTES + half * SLAB;
+  const int per_tile = GATED ? half : a.N;          // rows of y's columns per tile
+  const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+  const int tiles = a.nT * a.nR;
+  const int slabs = (a.p.d + SLAB - 1) / SLAB;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh.acc_full[b], 1);
+      mbar_init(&sh.acc_empty[b], 2 * OUT_WARPS);
+    }
+    mbar_init(&sh.drain, 1);
+    sh.abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmX);
+    prefetch_tmap(&tmW);
+    if constexpr (GATED) prefetch_tmap(&tmU);
+  }
+  __syncwarp();
+  if (warp == 1) {
+    tmem_alloc_pair(&sh.tmem_base, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();   // both CTAs' barriers before either signals the other
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- x and W by TMA
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, issued_par = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        const int t0 = t % a.nT * (2 * TOKENS) + rank * TOKENS, r0 = t / a.nT * per_tile;
+        const CUtensorMap *tm = GATED && rank ? &tmU : &tmW;
+        const int row = GATED ? r0 : r0 + rank * half;
+        for (int k = 0; k < slabs; ++k) {
+          ok = !*(volatile int *)&sh.abort && mbar_wait_bounded(&sh.empty[stage], phase ^ 1);
+          if (!ok) {
+            pair_timeout(a.status, sh);
+            break;
+          }
+          if (rank == 0) {
+            mbar_arrive_expect_tx(&sh.full[stage], 2 * stage_bytes);
+            issued |= 1u << stage;
+            issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+          }
+          uint8_t *dst = smem + (size_t)stage * stage_bytes;
+          const uint32_t bar = cluster_addr(&sh.full[stage], 0);   // the issuing CTA's
+          // columns from multiples of 128 bytes (past d, r and n: zeros)
+          tma_load_2d_pair(dst, &tmX, k * SLAB, t0, bar);
+          tma_load_2d_pair(dst + X_BYTES, tm, k * SLAB, row, bar);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      for (int s = 0; s < STAGES; ++s)
+        if (issued & (1u << s)) (void)mbar_wait_bounded(&sh.full[s], (issued_par >> s) & 1u);
+      // a second CTA whose loads the other may not have waited for: time to land
+      if (rank == 1 && !ok)
+        for (const unsigned long long t0 = global_ns(); global_ns() - t0 < 1000000;) {
+        }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---------------------------------------------------------------- the MMAs
+    const uint32_t idesc = instr_desc_i8(2 * TOKENS, a.N);
+    const uint64_t first = smem_desc(smem_u32(smem), 16, 1024, 2);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    int stage = 0;
+    uint32_t phase = 0, buf = 0, cphase = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      ok = mbar_wait_bounded(&sh.acc_empty[buf], ((cphase >> buf) & 1u) ^ 1u);
+      for (int k = 0; k < slabs; ++k) {
+        ok = ok && mbar_wait_bounded(&sh.full[stage], phase);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_lane()) {
+          const uint64_t x = first + (uint64_t)(stage * stage_bytes >> 4), w = x + (X_BYTES >> 4);
+#pragma unroll
+          for (int q = 0; q < SLAB / 32; ++q)
+            umma_i8_pair(tm + buf * ROWS, x + q * 2, w + q * 2, idesc, k > 0 || q > 0);
+          umma_commit_both(&sh.empty[stage]);
+          if (k == slabs - 1) umma_commit_both(&sh.acc_full[buf]);
+        }
+        __syncwarp();
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      cphase ^= 1u << buf;
+      buf ^= 1;
+    }
+    if (!ok && lane == 0) pair_timeout(a.status, sh);
+    __syncwarp();
+    if (elect_lane()) {
+      umma_commit_pair_local(&sh.drain);
+      (void)mbar_wait_bounded(&sh.drain, 0);
+    }
+    __syncwarp();
+  } else if (warp >= 2) {
+    // ---------------------------------------------------------------- results
+    const int quarter = warp & 3, side = (warp - 2) >> 2;
+    const int c_begin = side * (per_tile / 2 / 16 * 16), c_end = side ? per_tile : per_tile / 2 / 16 * 16;
+    const int64_t pitch = a.p.r * (int64_t)sizeof(Y);
+    // the largest power of two, up to 32, that all rows of y and 16 columns are multiples of
+    const uintptr_t base = reinterpret_cast<uintptr_t>(a.p.y) | (uintptr_t)pitch;
+    const int align = base % 32 == 0 ? 32 : base % 16 == 0 ? 16 : 1;
+    uint32_t buf = 0, cphase = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      const int64_t tok = (int64_t)(t % a.nT) * (2 * TOKENS) + rank * TOKENS + quarter * 32 + lane;
+      const int64_t r0 = (int64_t)(t / a.nT) * per_tile;
+      // the columns' scales and biases, while the accumulator fills
+      for (int c = (warp - 2) * 32 + lane; c < a.N; c += 32 * OUT_WARPS) {
+        const int l = GATED ? c / half : 0;
+        const int64_t row = r0 + (GATED ? c % half : c);
+        const bool live = row < a.p.r;
+        sh.scale[buf][c] = live ? __ldg(a.p.w_scales[l] + row) : 0.f;
+        sh.bias[buf][c] = live && a.p.bias[l] ? load_typed(a.p.bias[l], a.p.ytype, row) : 0.f;
+      }
+      const float xs = tok < a.p.n ? __ldg(a.p.x_scales + tok) : 0.f;
+      // (the other accumulator's parameters are still being read by slower warps, this one's
+      // were read before the barrier of the tile between)
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * OUT_WARPS) : "memory");
+      ok = mbar_wait_bounded(&sh.acc_full[buf], (cphase >> buf) & 1u);
+      if (!ok && lane == 0) pair_timeout(a.status, sh);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        tc_fence_after();
+        const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * ROWS;
+        Y *y = static_cast<Y *>(a.p.y) + tok * a.p.r + r0;
+        for (int c = c_begin; c < c_end; c += 16) {
+          float s0[16], s1[16], v[16];   // sums' bits
+          tmem_ld_32x32b_x16(acc + c, s0);
+          if constexpr (GATED) tmem_ld_32x32b_x16(acc + half + c, s1);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            v[i] = scaled_sum(__float_as_int(s0[i]), xs, sh.scale[buf][c + i], sh.bias[buf][c + i]);
+            if constexpr (GATED)
+              v[i] = activate<ACT>(v[i]) *
+                     scaled_sum(__float_as_int(s1[i]), xs, sh.scale[buf][half + c + i], sh.bias[buf][half + c + i]);
+          }
+          if (tok < a.p.n) write16<Y>(y + c, v, a.p.r - r0 - c, align);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(&sh.acc_empty[buf], 0));
+      }
+      cphase ^= 1u << buf;
+      buf ^= 1;
+    }
+  }
+
+  __syncthreads();
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();   // neither CTA's memory goes while the other may touch it
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <bool GATED, int ACT, typename Y>
+int launch_typed(const PairArgs &a, const CUtensorMap &tx, const CUtensorMap &tw, const CUtensorMap &tu,
+                 unsigned ctas, cudaStream_t st) {
+  static std::atomic<bool> attr[64] = {};
+  if (const int rc = ensure_smem_attr(int8_pair_kernel<GATED, ACT, Y>, PAIR_SMEM + 1024, attr)) return rc;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 2;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(PAIR_THREADS);
+  cfg.dynamicSmemBytes = PAIR_SMEM + 1024;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  count_launch();
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, int8_pair_kernel<GATED, ACT, Y>, tx, tw, tu, a);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    set_last_error(__FILE__, __LINE__, "kernel launch", e);
+    return GPTQ_ERR_CUDA;
+  }
+  return GPTQ_OK;
+}
+
+template <bool GATED, int ACT, typename... A>
+int launch_act(const PairArgs &a, A &&...rest) {
+  switch (a.p.ytype) {
+    case GPTQ_F16: return launch_typed<GATED, ACT, __half>(a, rest...);
+    case GPTQ_BF16: return launch_typed<GATED, ACT, __nv_bfloat16>(a, rest...);
+    default: return launch_typed<GATED, ACT, float>(a, rest...);
+  }
+}
+
+}  // namespace
+
+int launch_int8_pair(const Int8Args &p, cudaStream_t st) {
+  PairArgs a{};
+  a.p = p;
+  const int pairs = num_sms() / 2;
+  a.N = ROWS;
+  const int per_tile = p.gated ? a.N / 2 : a.N;
+  const int64_t nT = (p.n + 2 * TOKENS - 1) / (2 * TOKENS), nR = (p.r + per_tile - 1) / per_tile;
+  if (nT * nR > INT32_MAX / 8) return GPTQ_ERR_INVALID_ARG;
+  a.nT = (int)nT;
+  a.nR = (int)nR;
+  a.status = device_status_word();
+  if (!a.status) return GPTQ_ERR_CUDA;
+  CUtensorMap tx, tw, tu;
+  if (const int rc = int8_map(&tx, p.x, p.n, p.d, TOKENS)) return rc;
+  if (const int rc = int8_map(&tw, p.w[0], p.r, p.d, a.N / 2)) return rc;
+  tu = tw;
+  if (p.gated)
+    if (const int rc = int8_map(&tu, p.w[1], p.r, p.d, a.N / 2)) return rc;
+  const unsigned ctas = 2 * (unsigned)(nT * nR < pairs ? nT * nR : pairs);
+  if (!p.gated) return launch_act<false, GPTQ_ACT_NONE>(a, tx, tw, tu, ctas, st);
+  switch (p.activation) {
+    case GPTQ_ACT_NONE: return launch_act<true, GPTQ_ACT_NONE>(a, tx, tw, tu, ctas, st);
+    case GPTQ_ACT_RELU: return launch_act<true, GPTQ_ACT_RELU>(a, tx, tw, tu, ctas, st);
+    case GPTQ_ACT_SILU: return launch_act<true, GPTQ_ACT_SILU>(a, tx, tw, tu, ctas, st);
+    default: return launch_act<true, GPTQ_ACT_GELU>(a, tx, tw, tu, ctas, st);
+  }
+}
+
+}  // namespace gptq
