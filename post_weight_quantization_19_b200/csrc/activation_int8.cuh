@@ -13,9 +13,8 @@
 // with relu (a product of two 16-bit numbers); then what decides a code near a border k +
 // 1/2 is the sign of 127 u - (k + 1/2) max|u|, each product taken with its exact
 // rounding error (fma), and exact ties go to the even code.  With silu and gelu, u in fp32 is
-// off by up to 6e-7 (gelu: 2e-5, at arguments around -13) of its value: values that
-// near a border are formed again in 64 bits, and so is the row's maximum, from the
-// values within that of the largest.  A row that leaves the safe range of fp32, with an
+// off by up to 8e-7 of its value: values that near a border are formed again in 64 bits,
+// and so is the row's maximum, from the values within that of the largest.  A row that leaves the safe range of fp32, with an
 // infinity or a NaN among them, is done in 64 bits altogether.
 #pragma once
 
@@ -38,6 +37,7 @@ struct Half16<__half> {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
   }
+  static constexpr bool WIDE = false;
   static __device__ __forceinline__ float one(__half v) { return __half2float(v); }
   static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
 };
@@ -50,54 +50,73 @@ struct Half16<__nv_bfloat16> {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
   }
+  static constexpr bool WIDE = true;   // fp32's range
   static __device__ __forceinline__ float one(__nv_bfloat16 v) { return __bfloat162float(v); }
   static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
 };
 
 template <int ACT>
 constexpr bool EXACT = ACT == GPTQ_ACT_NONE || ACT == GPTQ_ACT_RELU;
-// How far a value in fp32 may be off, and twice that of 127 u / max|u|.
+// How far a value in fp32 may be off (of it), and 127 u / max|u| with its own roundings.
 template <int ACT>
-constexpr float VALUE_OFF = ACT == GPTQ_ACT_GELU ? 2e-5f : 6e-7f;
+constexpr float VALUE_OFF = 1e-6f;
 template <int ACT>
-constexpr float QUOTIENT_OFF = 2.f * VALUE_OFF<ACT> + 3e-7f;
+constexpr float QUOTIENT_OFF = EXACT<ACT> ? 4e-7f : 2.f * VALUE_OFF<ACT> + 4e-7f;
 // A row is safe with its maximum between these and every |up| at most UP_MOST: values that
-// fp32 loses (act below 3e-37, products below 1e-38) then have code 0.
-constexpr float LEAST_TOP = 1e-24f, MOST_TOP = 1e36f, UP_MOST = 1e6f;
+// fp32 loses (act below 1e-35, products below 1e-38) then have code 0.
+constexpr int STREAM_THREADS = 768;
+constexpr size_t STREAM_SMEM = 224 * 1024;
+constexpr float LEAST_TOP = 1e-22f, MOST_TOP = 1e36f, UP_MOST = 1e6f;
 
-// Value i of a row in 64 bits.
+// The value at an index in 64 bits.
 template <typename T, int ACT>
-__device__ __forceinline__ double value64(const ActivationArgs &a, int64_t at) {
-  const double v = activate64<ACT>((double)Half16<T>::one(static_cast<const T *>(a.x)[at]));
-  return a.up ? v * (double)Half16<T>::one(static_cast<const T *>(a.up)[at]) : v;
+__device__ __forceinline__ double value64(const void *x, const void *up, int64_t at) {
+  const double v = activate64<ACT>((double)Half16<T>::one(static_cast<const T *>(x)[at]));
+  return up ? v * (double)Half16<T>::one(static_cast<const T *>(up)[at]) : v;
 }
 
-// Eight values of a row in fp32 from their vectors; the largest magnitude's bits are returned,
-// an infinity's where the row is not safe.
+// `bytes` (a multiple of 16) from 16-byte aligned memory to shared memory.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Eight values of a row in fp32 from their vectors, and `top` raised to their largest
+// magnitude, to infinity where the row is not safe (NaN: some value is).
 template <typename T, int ACT>
-__device__ __forceinline__ uint32_t eight_values(const uint4 &x, const uint4 &up, bool gated, float (&u)[8]) {
+__device__ __forceinline__ void eight_values(const uint4 &x, const uint4 &up, bool gated, float (&u)[8],
+                                             float &top) {
   const uint32_t p[4] = {x.x, x.y, x.z, x.w}, q[4] = {up.x, up.y, up.z, up.w};
-  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = Half16<T>::up(p[i]);
-    u[2 * i] = activate<ACT>(f.x);
-    u[2 * i + 1] = activate<ACT>(f.y);
+    u[2 * i] = activate_fast<ACT>(f.x);
+    u[2 * i + 1] = activate_fast<ACT>(f.y);
   }
   if (gated) {
-    float most = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = Half16<T>::up(q[i]);
       u[2 * i] *= f.x;
       u[2 * i + 1] *= f.y;
-      most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
     }
-    if (!EXACT<ACT> && !(most <= UP_MOST)) top = 0x7F800000u;
+    if constexpr (!EXACT<ACT> && Half16<T>::WIDE) {   // (fp16 does not reach UP_MOST)
+      __nv_bfloat162 most = __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&q[0]));
+#pragma unroll
+      for (int i = 1; i < 4; ++i) most = __hmax2(most, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&q[i])));
+      if (!(fmaxf(__low2float(most), __high2float(most)) <= UP_MOST)) top = max_or_nan(top, __uint_as_float(0x7F800000u));
+    }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(u[i]) & 0x7FFFFFFFu);
-  return top;
+  for (int i = 0; i < 8; ++i) top = max_or_nan(top, fabsf(u[i]));
 }
 
 // The code of u near a border, as a float.
@@ -111,43 +130,51 @@ __device__ __forceinline__ float near_code(const ActivationArgs &a, int64_t at, 
     const float over = (m - b) + (em - eb);                     // m and b are close: m - b is exact
     return over == 0.f ? rintf(border) : over > 0.f ? border + 0.5f : border - 0.5f;
   } else {
-    return (float)rint(127.0 * value64<T, ACT>(a, at) / top64);
+    return (float)rint(127.0 * value64<T, ACT>(a.x, a.up, at) / top64);
   }
 }
 
-// The eight codes of a vector, as floats.
+// 1.5 2^23: a sum with it leaves the number rounded to an integer, to even on ties, in the
+// low bits.
+constexpr float MAGIC = 12582912.f;
+
+// The eight codes of a vector, as MAGIC + code.
 template <typename T, int ACT>
 __device__ __forceinline__ void eight_codes(const ActivationArgs &a, int64_t at, const float (&u)[8], float top,
-                                            double top64, float inv, float (&c)[8]) {
+                                            double top64, float inv, float (&m)[8]) {
   float far = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float q = u[i] * inv;
-    c[i] = rintf(q);
-    // (over 1/2 - the quotient's error: a border is near)
-    far = fmaxf(far, fmaf(fabsf(q), EXACT<ACT> ? 4e-7f : QUOTIENT_OFF<ACT>, fabsf(q - c[i])));
+    m[i] = fmaf(u[i], inv, MAGIC);
+    const float c = m[i] - MAGIC;
+    // (over 1/2 less the quotient's error: a border is near)
+    far = fmaxf(far, fmaf(fabsf(c), QUOTIENT_OFF<ACT>, fabsf(fmaf(u[i], inv, -c))));
   }
-  if (far >= 0.5f) {
-#pragma unroll 1
+  if (far >= 0.49999f - QUOTIENT_OFF<ACT>) {
+    uint32_t near = 0;
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
+      const float c = m[i] - MAGIC;
+      if (fmaf(fabsf(c), QUOTIENT_OFF<ACT>, fabsf(fmaf(u[i], inv, -c))) >= 0.49999f - QUOTIENT_OFF<ACT>) near |= 1u << i;
+    }
+#pragma unroll 1
+    for (; near; near &= near - 1) {
+      const int i = __ffs(near) - 1;
       float ui = u[0];
 #pragma unroll
       for (int k = 1; k < 8; ++k) ui = i == k ? u[k] : ui;
-      const float q = ui * inv, n = rintf(q);
-      if (fmaf(fabsf(q), EXACT<ACT> ? 4e-7f : QUOTIENT_OFF<ACT>, fabsf(q - n)) < 0.5f) continue;
-      const float code = near_code<T, ACT>(a, at + i, ui, top, top64, q);
+      const float code = MAGIC + near_code<T, ACT>(a, at + i, ui, top, top64, ui * inv);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) c[k] = i == k ? code : c[k];
+      for (int k = 0; k < 8; ++k) m[k] = i == k ? code : m[k];
     }
   }
 }
 
+// The low bytes of four MAGIC + code.
 __device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float d) {
-  uint32_t r;
-  const int ia = __float2int_rn(a), ib = __float2int_rn(b), ic = __float2int_rn(c), id = __float2int_rn(d);
-  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, 0;" : "=r"(r) : "r"(id), "r"(ic));
-  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %0;" : "+r"(r) : "r"(ib), "r"(ia));
-  return r;
+  const uint32_t lo = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
 }
 
 // Largest of a value's bits over the row's threads, in every thread.  `slot`: one word
@@ -203,7 +230,7 @@ __device__ __noinline__ float row_in_64_bits(const ActivationArgs a, int64_t row
   }
 #pragma unroll 1
   for (int k = tid; k < a.d; k += nt) {
-    const double u = fabs(value64<T, ACT>(a, row * a.d + k));
+    const double u = fabs(value64<T, ACT>(a.x, a.up, row * a.d + k));
     if (u <= 1.7e308)
       top = fmax(top, u);
     else
@@ -215,105 +242,220 @@ __device__ __noinline__ float row_in_64_bits(const ActivationArgs a, int64_t row
 #pragma unroll 1
   for (int k = tid; k < a.d; k += nt) {
     float code = 0.f;
-    if (!lost && top > 0.0) code = (float)rint(127.0 * value64<T, ACT>(a, row * a.d + k) / top);
+    if (!lost && top > 0.0) code = (float)rint(127.0 * value64<T, ACT>(a.x, a.up, row * a.d + k) / top);
     crow[k] = (int8_t)code;   // |code| <= 127
     if (xh) xh[k] = Half16<T>::put(scale * code);
   }
   return scale;
 }
 
-// V vectors of eight values per thread in registers.  LONG: the row's other vectors are
-// formed twice.
-template <typename T, int ACT, int V, bool WARP_ROW, bool LONG>
-__global__ void __launch_bounds__(WARP_ROW ? 256 : 1024) activation_int8_kernel(const ActivationArgs a) {
-  extern __shared__ __align__(16) int8_t row_codes[];   // perm: [rows of the CTA][d]
-  __shared__ uint32_t words[3][32];
-  __shared__ double slot[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tid = WARP_ROW ? lane : (int)threadIdx.x, nt = WARP_ROW ? 32 : (int)blockDim.x;
-  const int64_t row = WARP_ROW ? (int64_t)blockIdx.x * (blockDim.x >> 5) + warp : (int64_t)blockIdx.x;
-  if (row >= a.n) return;   // whole warps (WARP_ROW) or whole CTAs
+// Where a row's vectors are, and its shared words.
+struct RowIn {
+  const uint4 *x, *up;
+  bool gated;
+  uint32_t *words;   // [32]
+  double *slot;      // zero
+};
+
+// One row: V vectors of eight values per thread in registers, of longer rows (LONG) the
+// others formed twice.  `read` is called when no thread reads the row's vectors any more (by
+// way of RowIn; values in 64 bits are read from memory).  Returns the scale.
+template <typename T, int ACT, int V, bool WARP_ROW, bool LONG, typename Read>
+__device__ __forceinline__ float one_row(const ActivationArgs &a, const RowIn &in, int64_t row, int tid, int nt,
+                                         int8_t *crow, T *xhrow, double *slots, uint32_t *words, Read read) {
   const int nvec = a.d / 8;
-  const bool gated = a.up != nullptr;
-  const uint4 *x = reinterpret_cast<const uint4 *>(a.x) + row * nvec;
-  const uint4 *up = reinterpret_cast<const uint4 *>(a.up) + row * nvec;
   const uint4 none = make_uint4(0, 0, 0, 0);
-  float u[V][8];
-  uint32_t mb = 0;
+  auto values = [&](int k, float (&u)[8], float &top) {
+    eight_values<T, ACT>(in.x[k], in.gated ? in.up[k] : none, in.gated, u, top);
+  };
+  float u[V][8], mine = 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int k = tid + v * nt;
-    const uint4 xv = k < nvec ? __ldg(x + k) : none, uv = gated && k < nvec ? __ldg(up + k) : none;
-    mb = max(mb, eight_values<T, ACT>(xv, uv, gated, u[v]));
+    const bool live = k < nvec;
+    eight_values<T, ACT>(live ? in.x[k] : none, live && in.gated ? in.up[k] : none, in.gated, u[v], mine);
   }
   if constexpr (LONG)
     for (int k = tid + V * nt; k < nvec; k += nt) {
       float w[8];
-      mb = max(mb, eight_values<T, ACT>(__ldg(x + k), gated ? __ldg(up + k) : none, gated, w));
+      values(k, w, mine);
     }
-  const float top = __uint_as_float(row_max<WARP_ROW>(mb, words[0]));
-  int8_t *crow = a.perm ? row_codes + (WARP_ROW ? (size_t)warp * a.d : 0) : a.codes + row * a.d;
-  T *xhrow = a.xhat && !a.perm ? static_cast<T *>(a.xhat) + row * a.d : nullptr;
-  float scale;
-  if (top > LEAST_TOP && top < MOST_TOP) {
-    double top64 = top;
-    if constexpr (!EXACT<ACT>) {
-      // the largest value in 64 bits: of those that may be it
-      const float least = top * (1.f - 3.f * VALUE_OFF<ACT>);
-      double m = 0.0;
-      if (__uint_as_float(mb) >= least) {
-#pragma unroll 1
-        for (int k = tid; k < nvec; k += nt) {
-          float w[8];
-          (void)eight_values<T, ACT>(__ldg(x + k), gated ? __ldg(up + k) : none, gated, w);
-#pragma unroll 1
-          for (int i = 0; i < 8; ++i) {
-            float wi = w[0];
+  const float top = __uint_as_float(row_max<WARP_ROW>(__float_as_uint(mine) & 0x7FFFFFFFu, in.words));
+  if (!(top > LEAST_TOP && top < MOST_TOP)) {
+    read();
+    return row_in_64_bits<T, ACT, WARP_ROW>(a, row, tid, nt, crow, xhrow, slots, words);
+  }
+  double top64 = top;
+  if constexpr (!EXACT<ACT>) {
+    // the largest value in 64 bits: of those that may be it
+    const float least = top * (1.f - 3.f * VALUE_OFF<ACT>);
+    double m = 0.0;
+    if (mine >= least) {
+      // (four vectors at a time, a bit for each value that may be it)
 #pragma unroll
-            for (int j = 1; j < 8; ++j) wi = i == j ? w[j] : wi;
-            if (fabsf(wi) >= least) m = fmax(m, fabs(value64<T, ACT>(a, row * a.d + k * 8 + i)));
-          }
+      for (int v0 = 0; v0 < V; v0 += 4) {
+        uint32_t some = 0;
+#pragma unroll
+        for (int v = v0; v < V && v < v0 + 4; ++v)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (fabsf(u[v][i]) >= least) some |= 1u << ((v - v0) * 8 + i);
+#pragma unroll 1
+        for (; some; some &= some - 1) {
+          const int b = __ffs(some) - 1;
+          m = fmax(m, fabs(value64<T, ACT>(in.x, in.gated ? in.up : nullptr, (tid + (v0 + b / 8) * nt) * 8 + b % 8)));
         }
       }
-      top64 = row_max64<WARP_ROW>(m, slot);
-    }
-    scale = (float)(top64 / 127.0);
-    const float inv = 127.f / top;
-    auto finish = [&](int k, const float (&w)[8]) {
-      float c[8];
-      eight_codes<T, ACT>(a, row * a.d + k * 8, w, top, top64, inv, c);
-      *reinterpret_cast<uint2 *>(crow + (size_t)k * 8) =
-          make_uint2(pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7]));
-      if (xhrow)
-        reinterpret_cast<uint4 *>(xhrow)[k] =
-            make_uint4(Half16<T>::down(scale * c[0], scale * c[1]), Half16<T>::down(scale * c[2], scale * c[3]),
-                       Half16<T>::down(scale * c[4], scale * c[5]), Half16<T>::down(scale * c[6], scale * c[7]));
-    };
+      if constexpr (LONG) {
+#pragma unroll 1
+        for (int k = tid + V * nt; k < nvec; k += nt) {
+          float w[8], wtop = 0.f;
+          values(k, w, wtop);
+          if (wtop < least) continue;
+          uint32_t some = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (tid + v * nt < nvec) finish(tid + v * nt, u[v]);
-    if constexpr (LONG)
-      for (int k = tid + V * nt; k < nvec; k += nt) {
-        float w[8];
-        (void)eight_values<T, ACT>(__ldg(x + k), gated ? __ldg(up + k) : none, gated, w);
-        finish(k, w);
+          for (int i = 0; i < 8; ++i)
+            if (fabsf(w[i]) >= least) some |= 1u << i;
+#pragma unroll 1
+          for (; some; some &= some - 1)
+            m = fmax(m, fabs(value64<T, ACT>(in.x, in.gated ? in.up : nullptr, k * 8 + __ffs(some) - 1)));
+        }
       }
-  } else {
-    scale = row_in_64_bits<T, ACT, WARP_ROW>(a, row, tid, nt, crow, xhrow, slot, words[1]);
-  }
-  if (tid == 0) a.scales[row] = scale;
-  if (a.perm) {
-    if constexpr (WARP_ROW)
-      __syncwarp();
-    else
+    }
+    if constexpr (WARP_ROW) {
+      top64 = row_max64<true>(m, nullptr);
+    } else {   // few threads have one; non-negative numbers are ordered as their bits
+      if (m > 0.0)
+        atomicMax(reinterpret_cast<unsigned long long *>(in.slot), (unsigned long long)__double_as_longlong(m));
       __syncthreads();
-    T *xhp = static_cast<T *>(a.xhat);
-    for (int j = tid; j < a.d; j += nt) {
-      const int8_t c = crow[min(max(__ldg(a.perm + j), 0), a.d - 1)];
-      a.codes[row * a.d + j] = c;
-      if (xhp) xhp[row * a.d + j] = Half16<T>::put(scale * (float)c);
+      top64 = *in.slot;
     }
   }
+  if constexpr (!LONG) read();
+  const float scale = (float)(top64 * (1.0 / 127.0));   // (good to 2^-52 before it is rounded)
+  const float inv = 127.f / top;
+  auto finish = [&](int k, const float (&w)[8]) {
+    float m[8];
+    eight_codes<T, ACT>(a, row * a.d + k * 8, w, top, top64, inv, m);
+    *reinterpret_cast<uint2 *>(crow + (size_t)k * 8) =
+        make_uint2(pack_codes(m[0], m[1], m[2], m[3]), pack_codes(m[4], m[5], m[6], m[7]));
+    if (xhrow) {
+      float c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = scale * (m[i] - MAGIC);
+      reinterpret_cast<uint4 *>(xhrow)[k] =
+          make_uint4(Half16<T>::down(c[0], c[1]), Half16<T>::down(c[2], c[3]), Half16<T>::down(c[4], c[5]),
+                     Half16<T>::down(c[6], c[7]));
+    }
+  };
+  if constexpr (LONG) {
+    for (int k = tid + V * nt; k < nvec; k += nt) {
+      float w[8], unused = 0.f;
+      values(k, w, unused);
+      finish(k, w);
+    }
+    __syncthreads();
+    read();
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (tid + v * nt < nvec) finish(tid + v * nt, u[v]);
+  return scale;
+}
+
+// The scale, and with perm the codes (from shared memory) and xhat in its order.
+template <typename T, bool WARP_ROW>
+__device__ __forceinline__ void finish_row(const ActivationArgs &a, int64_t row, int tid, int nt, float scale,
+                                           const int8_t *crow) {
+  if (tid == 0) a.scales[row] = scale;
+  if (!a.perm) return;
+  if constexpr (WARP_ROW)
+    __syncwarp();
+  else
+    __syncthreads();
+  T *xh = static_cast<T *>(a.xhat);
+  for (int j = tid; j < a.d; j += nt) {
+    const int8_t c = crow[min(max(__ldg(a.perm + j), 0), a.d - 1)];
+    a.codes[row * a.d + j] = c;
+    if (xh) xh[row * a.d + j] = Half16<T>::put(scale * (float)c);
+  }
+}
+
+// A row per CTA or per warp, straight from memory.
+template <typename T, int ACT, int V, bool WARP_ROW, bool LONG>
+__global__ void __launch_bounds__(WARP_ROW ? 256 : 1024) activation_rows_kernel(const ActivationArgs a) {
+  extern __shared__ __align__(16) int8_t row_codes[];   // perm: [rows of the CTA][d]
+  __shared__ uint32_t words[3][32];
+  __shared__ double slots[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = WARP_ROW ? lane : (int)threadIdx.x, nt = WARP_ROW ? 32 : (int)blockDim.x;
+  const int64_t row = WARP_ROW ? (int64_t)blockIdx.x * (blockDim.x >> 5) + warp : (int64_t)blockIdx.x;
+  if (row >= a.n) return;   // whole warps (WARP_ROW) or whole CTAs
+  if (!WARP_ROW && tid == 0) slots[0] = 0.0;
+  const int nvec = a.d / 8;
+  const RowIn in{reinterpret_cast<const uint4 *>(a.x) + row * nvec, reinterpret_cast<const uint4 *>(a.up) + row * nvec,
+                 a.up != nullptr, words[0], slots};
+  int8_t *crow = a.perm ? row_codes + (WARP_ROW ? (size_t)warp * a.d : 0) : a.codes + row * a.d;
+  T *xhrow = a.xhat && !a.perm ? static_cast<T *>(a.xhat) + row * a.d : nullptr;
+  const float scale =
+      one_row<T, ACT, V, WARP_ROW, LONG>(a, in, row, tid, nt, crow, xhrow, slots, words[1], [] {});
+  finish_row<T, WARP_ROW>(a, row, tid, nt, scale, crow);
+}
+
+// Many rows: a CTA walks its share of them, and the copy engine brings the next rows to
+// shared memory (two at a time) while it works on one.  With loads by the threads
+// themselves a CTA alternated between waiting for memory and for its barriers.
+template <typename T, int ACT, int V, bool LONG>
+__global__ void __launch_bounds__(STREAM_THREADS) activation_stream_kernel(const ActivationArgs a, int *status) {
+  extern __shared__ __align__(16) uint8_t stream_smem[];   // two rows of x and up, then perm's codes
+  __shared__ uint64_t full[2];
+  __shared__ uint32_t words[2][32], words64[2][32];
+  __shared__ double slot[2], slots64[32];
+  __shared__ int abort;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const bool gated = a.up != nullptr;
+  const uint32_t half = (uint32_t)a.d * 2, stage = gated ? 2 * half : half;
+  auto load = [&](int64_t row, int s) {   // thread 0
+    mbar_arrive_expect_tx(&full[s], stage);
+    bulk_load(stream_smem + (size_t)s * stage, static_cast<const uint8_t *>(a.x) + row * half, half, &full[s]);
+    if (gated)
+      bulk_load(stream_smem + (size_t)s * stage + half, static_cast<const uint8_t *>(a.up) + row * half, half,
+                &full[s]);
+  };
+  if (tid == 0) {
+    mbar_init(&full[0], 1);
+    mbar_init(&full[1], 1);
+    abort = 0;
+    fence_mbar_init();
+    for (int s = 0; s < 2; ++s)
+      if (blockIdx.x + (int64_t)s * gridDim.x < a.n) load(blockIdx.x + (int64_t)s * gridDim.x, s);
+  }
+  __syncthreads();
+  int i = 0;
+  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x, ++i) {
+    const int s = i & 1;
+    // (words and slots of both parities: a slower thread may still read the last row's)
+    if (tid == 0) slot[s] = 0.0;
+    if (!*(volatile int *)&abort && !mbar_wait_bounded(&full[s], (uint32_t)(i >> 1) & 1u)) {
+      atomicCAS(status, 0, (int)GPTQ_ERR_TIMEOUT);
+      *(volatile int *)&abort = 1;   // the rows' results are lost, the barriers are still met
+    }
+    const uint8_t *src = stream_smem + (size_t)s * stage;
+    const RowIn in{reinterpret_cast<const uint4 *>(src), reinterpret_cast<const uint4 *>(src + half), gated, words[s],
+                   &slot[s]};
+    int8_t *crow = a.perm ? reinterpret_cast<int8_t *>(stream_smem) + 2 * (size_t)stage : a.codes + row * a.d;
+    T *xhrow = a.xhat && !a.perm ? static_cast<T *>(a.xhat) + row * a.d : nullptr;
+    const int64_t next = row + 2 * (int64_t)gridDim.x;
+    const float scale = one_row<T, ACT, V, false, LONG>(a, in, row, tid, nt, crow, xhrow, slots64, words64[0], [&] {
+      if (tid == 0 && next < a.n && !*(volatile int *)&abort) load(next, s);
+    });
+    finish_row<T, false>(a, row, tid, nt, scale, crow);
+    // (perm's codes are read by all before the next row's are written: a barrier lies between)
+  }
+  // copies that nobody waited for: time to land
+  if (tid == 0 && *(volatile int *)&abort)
+    for (const unsigned long long t0 = global_ns(); global_ns() - t0 < 1000000;) {
+    }
 }
 
 template <typename T, int ACT, int V, bool WARP_ROW, bool LONG>
@@ -322,10 +464,23 @@ int launch_rows(const ActivationArgs &a, int threads, cudaStream_t st) {
   if constexpr (!WARP_ROW) {
     static std::atomic<bool> attr[64] = {};
     if (a.perm)
-      if (const int rc = ensure_smem_attr(activation_int8_kernel<T, ACT, V, WARP_ROW, LONG>, 65536, attr)) return rc;
+      if (const int rc = ensure_smem_attr(activation_rows_kernel<T, ACT, V, WARP_ROW, LONG>, 65536, attr)) return rc;
   }
   const unsigned ctas = (unsigned)(WARP_ROW ? (a.n + 7) / 8 : a.n);
-  activation_int8_kernel<T, ACT, V, WARP_ROW, LONG><<<ctas, WARP_ROW ? 256 : threads, smem, st>>>(a);
+  activation_rows_kernel<T, ACT, V, WARP_ROW, LONG><<<ctas, WARP_ROW ? 256 : threads, smem, st>>>(a);
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
+}
+
+template <typename T, int ACT, bool LONG>
+int launch_stream(const ActivationArgs &a, int threads, size_t smem, int per_sm, cudaStream_t st) {
+  constexpr auto kernel = activation_stream_kernel<T, ACT, 4, LONG>;
+  static std::atomic<bool> attr[64] = {};
+  if (const int rc = ensure_smem_attr(kernel, STREAM_SMEM, attr)) return rc;
+  int *status = device_status_word();
+  if (!status) return GPTQ_ERR_CUDA;
+  const int64_t fit = (int64_t)num_sms() * per_sm;
+  kernel<<<(unsigned)(a.n < fit ? a.n : fit), threads, smem, st>>>(a, status);
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
@@ -338,6 +493,16 @@ int launch_act(const ActivationArgs &a, cudaStream_t st) {
     return launch_rows<T, ACT, 8, true, false>(a, 0, st);
   }
   auto threads = [&](int v) { return ((nvec + v - 1) / v + 31) / 32 * 32; };
+  // many rows: two of them in shared memory per CTA, as many CTAs as fit
+  const size_t smem = (size_t)a.d * ((a.up ? 8 : 4) + (a.perm ? 1 : 0));
+  if (a.n > num_sms() && smem <= STREAM_SMEM) {
+    const int t = threads(4) < STREAM_THREADS ? threads(4) : STREAM_THREADS;
+    int per_sm = (int)((224u << 10) / (smem + 2048));
+    const int most = 768 / t < 1 ? 1 : 768 / t;
+    per_sm = per_sm < 1 ? 1 : per_sm > most ? most : per_sm;
+    if (threads(4) <= STREAM_THREADS) return launch_stream<T, ACT, false>(a, t, smem, per_sm, st);
+    return launch_stream<T, ACT, true>(a, t, smem, per_sm, st);
+  }
   if (threads(2) <= 1024) return launch_rows<T, ACT, 2, false, false>(a, threads(2), st);
   return launch_rows<T, ACT, 2, false, true>(a, 1024, st);
 }
