@@ -28,38 +28,75 @@ __device__ __forceinline__ float reciprocal_approx(float v) {   // within 2^-23;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-// exp(v) within 4e-7 of it, v <= 88: 2^t with t = v log2 e rounded, and what t is off by, a few
-// 1e-6 at most, to first order (ln 2 in two parts).
-__device__ __forceinline__ float exp_fast(float v) {
-  const float t = v * 1.44269504088896341f;
-  const float rest = fmaf(t, -1.42860677e-6f, fmaf(t, -0.693145751953125f, v));
-  const float e = exp2_approx(t);
-  return fmaf(e, rest, e);
+// Two fp32 numbers that one instruction works on.
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ uint64_t bits(const F2 &a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ F2 numbers(uint64_t v) {
+  F2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 both(float v) { return F2{v, v}; }
+__device__ __forceinline__ F2 fma2(const F2 &a, const F2 &b, const F2 &c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return numbers(r);
+}
+__device__ __forceinline__ F2 mul2(const F2 &a, const F2 &b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return numbers(r);
+}
+__device__ __forceinline__ F2 add2(const F2 &a, const F2 &b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return numbers(r);
 }
 
-// The same functions of a number of 16 bits (its square is exact) in fewer instructions, within
-// 8e-7 of the value, values below 1e-35 lost.  gelu: erfc(z) = t exp(-z^2 + P(t)), t = 1 /
-// (1 + z / 2), the Chebyshev fit of Numerical Recipes (Press et al., "Error
-// function"), good to 1.2e-7 of the value for every z >= 0.
+// exp(v) within 4e-7 of it, |v| <= 88: 2^t with t = v log2 e rounded, and what t is off by, a
+// few 1e-6 at most, to first order (ln 2 in two parts).
+__device__ __forceinline__ F2 exp_fast(const F2 &v) {
+  const F2 t = mul2(v, both(1.44269504088896341f));
+  const F2 rest = fma2(t, both(-1.42860677e-6f), fma2(t, both(-0.693145751953125f), v));
+  const F2 e{exp2_approx(t.x), exp2_approx(t.y)};
+  return fma2(e, rest, e);
+}
+
+// The same functions of two numbers of 16 bits (whose squares are exact) in fewer
+// instructions, within 8e-7 of the value, values below 1e-35 lost.  gelu: erfc(z) = t
+// exp(-z^2 + P(t)), t = 1 / (1 + z / 2), the Chebyshev fit of Numerical Recipes (Press et
+// al., "Error function"), good to 1.2e-7 of the value for every z >= 0.
 template <int ACT>
-__device__ __forceinline__ float activate_fast(float v) {
-  if constexpr (ACT == GPTQ_ACT_SILU) return v * reciprocal_approx(1.f + exp_fast(fminf(-v, 88.f)));
-  if constexpr (ACT == GPTQ_ACT_GELU) {
-    const float t = reciprocal_approx(fmaf(fabsf(v), 0.353553390593273762f, 1.f));
-    float p = fmaf(t, 0.17087277f, -0.82215223f);
-    p = fmaf(t, p, 1.48851587f);
-    p = fmaf(t, p, -1.13520398f);
-    p = fmaf(t, p, 0.27886807f);
-    p = fmaf(t, p, -0.18628806f);
-    p = fmaf(t, p, 0.09678418f);
-    p = fmaf(t, p, 0.37409196f);
-    p = fmaf(t, p, 1.00002368f);
-    p = fmaf(t, p, -1.26551223f);
-    // (beyond 13.2 the half tail is below 1e-38)
-    const float tail = 0.5f * t * exp_fast(p) * exp_fast(fmaxf(v * v * -0.5f, -88.f));
-    return v * (v > 0.f ? 1.f - tail : tail);
+__device__ __forceinline__ F2 activate_fast(const F2 &v) {
+  if constexpr (ACT == GPTQ_ACT_SILU) {
+    const F2 e = add2(exp_fast(F2{fminf(-v.x, 88.f), fminf(-v.y, 88.f)}), both(1.f));
+    return mul2(v, F2{reciprocal_approx(e.x), reciprocal_approx(e.y)});
   }
-  return activate<ACT>(v);
+  if constexpr (ACT == GPTQ_ACT_GELU) {
+    const F2 z = fma2(F2{fabsf(v.x), fabsf(v.y)}, both(0.353553390593273762f), both(1.f));
+    const F2 t{reciprocal_approx(z.x), reciprocal_approx(z.y)};
+    F2 p = fma2(t, both(0.17087277f), both(-0.82215223f));
+    p = fma2(t, p, both(1.48851587f));
+    p = fma2(t, p, both(-1.13520398f));
+    p = fma2(t, p, both(0.27886807f));
+    p = fma2(t, p, both(-0.18628806f));
+    p = fma2(t, p, both(0.09678418f));
+    p = fma2(t, p, both(0.37409196f));
+    p = fma2(t, p, both(1.00002368f));
+    p = fma2(t, p, both(-1.26551223f));
+    // (beyond 13.2 the half tail is below 1e-38)
+    const F2 s = mul2(mul2(v, v), both(-0.5f));
+    const F2 tail = mul2(mul2(mul2(t, both(0.5f)), exp_fast(p)), exp_fast(F2{fmaxf(s.x, -88.f), fmaxf(s.y, -88.f)}));
+    const F2 rest = fma2(tail, both(-1.f), both(1.f));
+    return mul2(v, F2{v.x > 0.f ? rest.x : tail.x, v.y > 0.f ? rest.y : tail.y});
+  }
+  return F2{activate<ACT>(v.x), activate<ACT>(v.y)};
 }
 
 template <int ACT>

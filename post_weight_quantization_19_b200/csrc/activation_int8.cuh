@@ -61,7 +61,7 @@ constexpr bool EXACT = ACT == GPTQ_ACT_NONE || ACT == GPTQ_ACT_RELU;
 template <int ACT>
 constexpr float VALUE_OFF = 1e-6f;
 template <int ACT>
-constexpr float QUOTIENT_OFF = EXACT<ACT> ? 4e-7f : 2.f * VALUE_OFF<ACT> + 4e-7f;
+constexpr float QUOTIENT_OFF = EXACT<ACT> ? 5e-7f : 2.f * VALUE_OFF<ACT> + 5e-7f;
 // A row is safe with its maximum between these and every |up| at most UP_MOST: values that
 // fp32 loses (act below 1e-35, products below 1e-38) then have code 0.
 constexpr int STREAM_THREADS = 768;
@@ -98,15 +98,17 @@ __device__ __forceinline__ void eight_values(const uint4 &x, const uint4 &up, bo
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = Half16<T>::up(p[i]);
-    u[2 * i] = activate_fast<ACT>(f.x);
-    u[2 * i + 1] = activate_fast<ACT>(f.y);
+    const F2 r = activate_fast<ACT>(F2{f.x, f.y});
+    u[2 * i] = r.x;
+    u[2 * i + 1] = r.y;
   }
   if (gated) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = Half16<T>::up(q[i]);
-      u[2 * i] *= f.x;
-      u[2 * i + 1] *= f.y;
+      const F2 r = mul2(F2{u[2 * i], u[2 * i + 1]}, F2{f.x, f.y});
+      u[2 * i] = r.x;
+      u[2 * i + 1] = r.y;
     }
     if constexpr (!EXACT<ACT> && Half16<T>::WIDE) {   // (fp16 does not reach UP_MOST)
       __nv_bfloat162 most = __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&q[0]));
@@ -138,19 +140,22 @@ __device__ __forceinline__ float near_code(const ActivationArgs &a, int64_t at, 
 // low bits.
 constexpr float MAGIC = 12582912.f;
 
-// The eight codes of a vector, as MAGIC + code.
+// The eight codes of a vector, as MAGIC + code.  `away`: how far from an integer 127 u / max|u|
+// may be before a border is near, for every value of this thread.
 template <typename T, int ACT>
 __device__ __forceinline__ void eight_codes(const ActivationArgs &a, int64_t at, const float (&u)[8], float top,
-                                            double top64, float inv, float (&m)[8]) {
+                                            double top64, float inv, float away, float (&m)[8]) {
   float far = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    m[i] = fmaf(u[i], inv, MAGIC);
-    const float c = m[i] - MAGIC;
-    // (over 1/2 less the quotient's error: a border is near)
-    far = fmaxf(far, fmaf(fabsf(c), QUOTIENT_OFF<ACT>, fabsf(fmaf(u[i], inv, -c))));
+  for (int i = 0; i < 8; i += 2) {
+    const F2 v{u[i], u[i + 1]}, sum = fma2(v, both(inv), both(MAGIC));
+    const F2 c = add2(sum, both(-MAGIC));
+    const F2 off = fma2(v, both(-inv), c);
+    m[i] = sum.x;
+    m[i + 1] = sum.y;
+    far = fmaxf(far, fmaxf(fabsf(off.x), fabsf(off.y)));
   }
-  if (far >= 0.49999f - QUOTIENT_OFF<ACT>) {
+  if (far >= away) {
     uint32_t near = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -271,9 +276,8 @@ __device__ __forceinline__ float one_row(const ActivationArgs &a, const RowIn &i
   float u[V][8], mine = 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int k = tid + v * nt;
-    const bool live = k < nvec;
-    eight_values<T, ACT>(live ? in.x[k] : none, live && in.gated ? in.up[k] : none, in.gated, u[v], mine);
+    const int k = min(tid + v * nt, nvec - 1);   // (the last one again: the maximum is the same)
+    eight_values<T, ACT>(in.x[k], in.gated ? in.up[k] : none, in.gated, u[v], mine);
   }
   if constexpr (LONG)
     for (int k = tid + V * nt; k < nvec; k += nt) {
@@ -303,7 +307,7 @@ __device__ __forceinline__ float one_row(const ActivationArgs &a, const RowIn &i
 #pragma unroll 1
         for (; some; some &= some - 1) {
           const int b = __ffs(some) - 1;
-          m = fmax(m, fabs(value64<T, ACT>(in.x, in.gated ? in.up : nullptr, (tid + (v0 + b / 8) * nt) * 8 + b % 8)));
+          m = fmax(m, fabs(value64<T, ACT>(in.x, in.gated ? in.up : nullptr, min(tid + (v0 + b / 8) * nt, nvec - 1) * 8 + b % 8)));
         }
       }
       if constexpr (LONG) {
@@ -333,10 +337,10 @@ __device__ __forceinline__ float one_row(const ActivationArgs &a, const RowIn &i
   }
   if constexpr (!LONG) read();
   const float scale = (float)(top64 * (1.0 / 127.0));   // (good to 2^-52 before it is rounded)
-  const float inv = 127.f / top;
+  const float inv = __fdividef(127.f, top), away = 0.49999f - QUOTIENT_OFF<ACT> * fmaf(mine, inv, 1.f);
   auto finish = [&](int k, const float (&w)[8]) {
     float m[8];
-    eight_codes<T, ACT>(a, row * a.d + k * 8, w, top, top64, inv, m);
+    eight_codes<T, ACT>(a, row * a.d + k * 8, w, top, top64, inv, away, m);
     *reinterpret_cast<uint2 *>(crow + (size_t)k * 8) =
         make_uint2(pack_codes(m[0], m[1], m[2], m[3]), pack_codes(m[4], m[5], m[6], m[7]));
     if (xhrow) {
