@@ -6,7 +6,7 @@
 // ("LLM 量化技术" §1.2, the symmetric quantiser with 8 bits over a token.)  A row's u stay in
 // registers in fp32 between the maximum and the codes, so every input is read once and
 // every output written once: n d (2 [+ 2 up] + 1 [+ 2 xhat]) bytes.  One CTA per row (rows
-// of up to 2048: one warp per row); of rows longer than a CTA's registers hold, the
+// of up to 1024: one warp per row); of rows longer than a CTA's registers hold, the
 // rest is read a second time.
 //
 // Codes are those of the formula in 64 bits.  u is exact in fp32 without an activation and
@@ -22,6 +22,7 @@
 #include <cuda_fp16.h>
 
 #include "activation_int8.h"
+#include "launch_after.h"
 
 namespace gptq {
 namespace {
@@ -379,7 +380,7 @@ __device__ __forceinline__ void finish_row(const ActivationArgs &a, int64_t row,
     __syncthreads();
   T *xh = static_cast<T *>(a.xhat);
   for (int j = tid; j < a.d; j += nt) {
-    const int8_t c = crow[min(max(__ldg(a.perm + j), 0), a.d - 1)];
+    const int8_t c = crow[min(max(__ldcg(a.perm + j), 0), a.d - 1)];
     a.codes[row * a.d + j] = c;
     if (xh) xh[row * a.d + j] = Half16<T>::put(scale * (float)c);
   }
@@ -394,6 +395,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : 1024) activation_rows_kernel(
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tid = WARP_ROW ? lane : (int)threadIdx.x, nt = WARP_ROW ? 32 : (int)blockDim.x;
   const int64_t row = WARP_ROW ? (int64_t)blockIdx.x * (blockDim.x >> 5) + warp : (int64_t)blockIdx.x;
+  pdl_wait_then_release();
   if (row >= a.n) return;   // whole warps (WARP_ROW) or whole CTAs
   if (!WARP_ROW && tid == 0) slots[0] = 0.0;
   const int nvec = a.d / 8;
@@ -426,6 +428,7 @@ __global__ void __launch_bounds__(STREAM_THREADS) activation_stream_kernel(const
       bulk_load(stream_smem + (size_t)s * stage + half, static_cast<const uint8_t *>(a.up) + row * half, half,
                 &full[s]);
   };
+  pdl_wait_then_release();
   if (tid == 0) {
     mbar_init(&full[0], 1);
     mbar_init(&full[1], 1);
@@ -464,16 +467,14 @@ __global__ void __launch_bounds__(STREAM_THREADS) activation_stream_kernel(const
 
 template <typename T, int ACT, int V, bool WARP_ROW, bool LONG>
 int launch_rows(const ActivationArgs &a, int threads, cudaStream_t st) {
-  const size_t smem = a.perm ? (size_t)(WARP_ROW ? 8 : 1) * a.d : 0;   // WARP_ROW: d <= 2048
+  const size_t smem = a.perm ? (size_t)(WARP_ROW ? 8 : 1) * a.d : 0;   // WARP_ROW: d <= 1024
   if constexpr (!WARP_ROW) {
     static std::atomic<bool> attr[64] = {};
     if (a.perm)
       if (const int rc = ensure_smem_attr(activation_rows_kernel<T, ACT, V, WARP_ROW, LONG>, 65536, attr)) return rc;
   }
   const unsigned ctas = (unsigned)(WARP_ROW ? (a.n + 7) / 8 : a.n);
-  activation_rows_kernel<T, ACT, V, WARP_ROW, LONG><<<ctas, WARP_ROW ? 256 : threads, smem, st>>>(a);
-  GPTQ_LAUNCH_CHECK();
-  return GPTQ_OK;
+  return launch_after(activation_rows_kernel<T, ACT, V, WARP_ROW, LONG>, ctas, WARP_ROW ? 256 : threads, smem, 1, st, a);
 }
 
 template <typename T, int ACT, bool LONG>
@@ -484,22 +485,25 @@ int launch_stream(const ActivationArgs &a, int threads, size_t smem, int per_sm,
   int *status = device_status_word();
   if (!status) return GPTQ_ERR_CUDA;
   const int64_t fit = (int64_t)num_sms() * per_sm;
-  kernel<<<(unsigned)(a.n < fit ? a.n : fit), threads, smem, st>>>(a, status);
-  GPTQ_LAUNCH_CHECK();
-  return GPTQ_OK;
+  return launch_after(kernel, (unsigned)(a.n < fit ? a.n : fit), threads, smem, 1, st, a, status);
 }
 
 template <typename T, int ACT>
 int launch_act(const ActivationArgs &a, cudaStream_t st) {
   const int nvec = a.d / 8;
-  if (a.d <= 2048) {
+  // Many rows: the copy engine.  For wide rows it pays from one row per SM on, where the
+  // others run one or two CTAs to an SM (us, this kernel and the other): 300 x 11008 gated
+  // 10.4, 11.1, 1000 x 11008 20.4, 25.8; for narrow ones when its start is spread over
+  // many: 2000 x 4096 15.2, 14.2, 4096 x 4096 24.5, 25.3, 1000 x 2048 7.0, 5.5, 10000 x 1024 19.3, 22.3.
+  const bool many = a.n > (int64_t)num_sms() * (a.d > 6144 ? 1 : 18);
+  if (a.d <= 512 || (a.d <= 1024 && !many)) {
     if (nvec <= 64) return launch_rows<T, ACT, 2, true, false>(a, 0, st);
-    return launch_rows<T, ACT, 8, true, false>(a, 0, st);
+    return launch_rows<T, ACT, 4, true, false>(a, 0, st);
   }
   auto threads = [&](int v) { return ((nvec + v - 1) / v + 31) / 32 * 32; };
-  // many rows: two of them in shared memory per CTA, as many CTAs as fit
+  // two rows in shared memory per CTA, as many CTAs as fit
   const size_t smem = (size_t)a.d * ((a.up ? 8 : 4) + (a.perm ? 1 : 0));
-  if (a.n > num_sms() && smem <= STREAM_SMEM) {
+  if (many && smem <= STREAM_SMEM) {
     const int t = threads(4) < STREAM_THREADS ? threads(4) : STREAM_THREADS;
     int per_sm = (int)((224u << 10) / (smem + 2048));
     const int most = 768 / t < 1 ? 1 : 768 / t;

@@ -81,6 +81,14 @@ __device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 
+// A box of a map into L2.
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap *tmap, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
 // Instruction descriptor for kind::i8: 32-bit integer sums, both operands signed and K-major.
 __host__ __device__ constexpr uint32_t instr_desc_i8(uint32_t M, uint32_t N) {
   return (2u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);

@@ -11,6 +11,7 @@
 // Two accumulators of 256 columns: eight warps of each CTA write one out, a thread a
 // token, while the other fills.
 #include "int8_linear.h"
+#include "launch_after.h"
 
 namespace gptq {
 namespace {
@@ -124,6 +125,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
   cluster_sync();   // both CTAs' barriers before either signals the other
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
+  pdl_wait_then_release();
 
   if (warp == 0) {
     // ---------------------------------------------------------------- x and W by TMA
@@ -221,10 +223,10 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         const int l = GATED ? c / half : 0;
         const int64_t row = r0 + (GATED ? c % half : c);
         const bool live = row < a.p.r;
-        sh.scale[buf][c] = live ? __ldg(a.p.w_scales[l] + row) : 0.f;
+        sh.scale[buf][c] = live ? __ldcg(a.p.w_scales[l] + row) : 0.f;
         sh.bias[buf][c] = live && a.p.bias[l] ? load_typed(a.p.bias[l], a.p.ytype, row) : 0.f;
       }
-      const float xs = tok < a.p.n ? __ldg(a.p.x_scales + tok) : 0.f;
+      const float xs = tok < a.p.n ? __ldcg(a.p.x_scales + tok) : 0.f;
       // (the other accumulator's parameters are still being read by slower warps, this one's
       // were read before the barrier of the tile between)
       asm volatile("bar.sync 1, %0;" ::"n"(32 * OUT_WARPS) : "memory");
@@ -274,25 +276,7 @@ int launch_typed(const PairArgs &a, const CUtensorMap &tx, const CUtensorMap &tw
                  unsigned ctas, cudaStream_t st) {
   static std::atomic<bool> attr[64] = {};
   if (const int rc = ensure_smem_attr(int8_pair_kernel<GATED, ACT, Y>, PAIR_SMEM + 1024, attr)) return rc;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = 2;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(PAIR_THREADS);
-  cfg.dynamicSmemBytes = PAIR_SMEM + 1024;
-  cfg.stream = st;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  count_launch();
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, int8_pair_kernel<GATED, ACT, Y>, tx, tw, tu, a);
-  if (e != cudaSuccess) {
-    (void)cudaGetLastError();
-    set_last_error(__FILE__, __LINE__, "kernel launch", e);
-    return GPTQ_ERR_CUDA;
-  }
-  return GPTQ_OK;
+  return launch_after(int8_pair_kernel<GATED, ACT, Y>, ctas, PAIR_THREADS, PAIR_SMEM + 1024, 2, st, tx, tw, tu, a);
 }
 
 template <bool GATED, int ACT, typename... A>

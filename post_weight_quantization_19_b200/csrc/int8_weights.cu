@@ -9,7 +9,7 @@
 //
 // r d (bits/8 + 1) bytes, read and written once.  A thread turns 32 codes (BITS words)
 // into 32 bytes; the threads of a row stand side by side, several rows to a CTA.
-#include "gptq_internal.h"
+#include "launch_after.h"
 #include "overlap.h"
 #include "unpack_bits.cuh"
 
@@ -32,16 +32,16 @@ __device__ __forceinline__ uint32_t four_codes(const uint32_t (&w)[BITS], int k)
 
 template <int BITS>
 __global__ void __launch_bounds__(THREADS)
-    int8_weights_kernel(const uint32_t *__restrict__ qweight, const float *__restrict__ scales,
-                        const int32_t *__restrict__ zeros, int64_t r, int chunks, int per_row,
-                        int8_t *__restrict__ w, float *__restrict__ w_scales) {
+    int8_weights_kernel(const uint32_t *qweight, const float *scales, const int32_t *zeros, int64_t r, int chunks,
+                        int per_row, int8_t *w, float *w_scales) {
   __shared__ int outside[THREADS / 32];   // per row of the CTA
   const int rows = THREADS / per_row, mine = threadIdx.x / per_row, at = threadIdx.x % per_row;
   const int64_t row = (int64_t)blockIdx.x * rows + mine;
   if (at == 0) outside[mine] = 0;
+  pdl_wait_then_release();
   __syncthreads();
   if (row < r) {
-    const int z = min(max(__ldg(zeros + row), 0), (1 << BITS) - 1);
+    const int z = min(max(__ldcg(zeros + row), 0), (1 << BITS) - 1);
     const uint32_t zzzz = (uint32_t)z * 0x01010101u;
     bool lost = false;
 #pragma unroll 4
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(THREADS)
       const uint32_t *src = qweight + (row * chunks + c) * BITS;
       uint32_t q[BITS], o[8];
 #pragma unroll
-      for (int i = 0; i < BITS; ++i) q[i] = __ldg(src + i);
+      for (int i = 0; i < BITS; ++i) q[i] = __ldcg(src + i);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const uint32_t v = four_codes<BITS>(q, k);
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(THREADS)
     if (lost) outside[mine] = 1;
   }
   __syncthreads();
-  if (row < r && at == 0) w_scales[row] = outside[mine] ? __uint_as_float(0x7FC00000u) : __ldg(scales + row);
+  if (row < r && at == 0) w_scales[row] = outside[mine] ? __uint_as_float(0x7FC00000u) : __ldcg(scales + row);
 }
 
 template <int BITS>
@@ -84,9 +84,8 @@ int launch_weights(const uint32_t *q, const float *s, const int32_t *z, int64_t 
   int per_row = 32;
   while (per_row < THREADS && per_row * 4 < chunks) per_row *= 2;
   const int rows = THREADS / per_row;
-  int8_weights_kernel<BITS><<<(unsigned)((r + rows - 1) / rows), THREADS, 0, st>>>(q, s, z, r, chunks, per_row, w, ws);
-  GPTQ_LAUNCH_CHECK();
-  return GPTQ_OK;
+  return launch_after(int8_weights_kernel<BITS>, (unsigned)((r + rows - 1) / rows), THREADS, 0, 1, st, q, s, z, r,
+                      chunks, per_row, w, ws);
 }
 
 }  // namespace
