@@ -55,7 +55,8 @@ int int8_product(const Int8Args &a, int layers, int64_t d, cudaStream_t st) {
                           Span{a.bias[k], (size_t)a.r * ysize}})
       if (overlap(out, s)) return GPTQ_ERR_INVALID_ARG;
   }
-  if (a.n > 256) return launch_int8_pair(a, st);
+  // up to 64 tokens W's bytes are the bound; more, its products or x's bytes
+  if (a.n > FEW_TOKENS && int8_pairs_faster(a, num_sms())) return launch_int8_pair(a, st);
   return launch_int8_single(a, st);
 }
 

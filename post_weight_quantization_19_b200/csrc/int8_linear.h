@@ -22,10 +22,14 @@ struct Int8Args {
   bool gated;
 };
 
+constexpr int FEW_TOKENS = 64;
 // Weights as the MMA's rows: any number of tokens, k split over clusters when tiles are few.
 int launch_int8_single(const Int8Args &a, cudaStream_t st);
+// For more than FEW_TOKENS: the CTAs that it would split k over.
+int int8_split(const Int8Args &a, int sms);
 // Many tokens: pairs of CTAs, tokens as the MMA's rows.
 int launch_int8_pair(const Int8Args &a, cudaStream_t st);
+bool int8_pairs_faster(const Int8Args &a, int sms);
 
 // A sum with its token's and row's scales, and the bias.
 __device__ __forceinline__ float scaled_sum(int sum, float xs, float ws, float bias) {
@@ -81,6 +85,22 @@ __device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 
+// Boxes of a map to shared memory, by addresses: tma_load_2d, tma_load_2d_pair.
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap *tmap, int x, int y, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap *tmap, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
 // A box of a map into L2.
 __device__ __forceinline__ void prefetch_2d(const CUtensorMap *tmap, int x, int y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
@@ -99,6 +119,17 @@ __device__ __forceinline__ bool elect_lane() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
+}
+
+// Wait for a phase, giving up where the CTA has; false then, or when the wait ran out.
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, const int *abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  while (true) {
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*(const volatile int *)abort || global_ns() - t0 > kWaitLimitNs) return false;
+  }
 }
 
 // A map of a matrix [rows x d] of 8-bit integers, loaded in boxes of box_rows rows x 128

@@ -19,16 +19,17 @@ namespace {
 constexpr int TOKENS = 128;               // per CTA of a pair
 constexpr int SLAB = 128;                 // columns per stage
 constexpr int ROWS = 256;                 // most rows of W per tile (UMMA N)
-constexpr int STAGES = 6;
+constexpr int STAGES = 10;                // at most
 constexpr int X_BYTES = TOKENS * SLAB;
 constexpr int OUT_WARPS = 8;
 constexpr int PAIR_THREADS = 32 * (2 + OUT_WARPS);
-constexpr size_t PAIR_SMEM = (size_t)STAGES * (X_BYTES + ROWS / 2 * SLAB);
+constexpr size_t PAIR_SMEM = (size_t)6 * (X_BYTES + ROWS / 2 * SLAB);
 
 struct PairArgs {
   Int8Args p;
   int N;              // rows of W per tile, of both layers together; a multiple of 32
   int nT, nR;         // tiles along the tokens and along the rows
+  int stages;
   int *status;
 };
 
@@ -131,36 +132,36 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     // ---------------------------------------------------------------- x and W by TMA
     if (lane == 0) {
       int stage = 0;
-      uint32_t phase = 0, issued = 0, issued_par = 0;
-      bool ok = true;
+      uint32_t phase = 0;
+      bool ok = true, full = false;   // full: every stage has been asked for
+      const CUtensorMap *tm = GATED && rank ? &tmU : &tmW;
+      const uint32_t ring = smem_u32(smem), bars = cluster_addr(&sh.full[0], 0);   // the issuing CTA's
       for (int t = pair; t < tiles && ok; t += pairs) {
         const int t0 = t % a.nT * (2 * TOKENS) + rank * TOKENS, r0 = t / a.nT * per_tile;
-        const CUtensorMap *tm = GATED && rank ? &tmU : &tmW;
         const int row = GATED ? r0 : r0 + rank * half;
         for (int k = 0; k < slabs; ++k) {
-          ok = !*(volatile int *)&sh.abort && mbar_wait_bounded(&sh.empty[stage], phase ^ 1);
+          ok = wait_or_abort(&sh.empty[stage], phase ^ 1, &sh.abort);
           if (!ok) {
             pair_timeout(a.status, sh);
             break;
           }
-          if (rank == 0) {
-            mbar_arrive_expect_tx(&sh.full[stage], 2 * stage_bytes);
-            issued |= 1u << stage;
-            issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-          }
-          uint8_t *dst = smem + (size_t)stage * stage_bytes;
-          const uint32_t bar = cluster_addr(&sh.full[stage], 0);   // the issuing CTA's
+          if (rank == 0) mbar_arrive_expect_tx(&sh.full[stage], 2 * stage_bytes);
+          const uint32_t dst = ring + stage * stage_bytes, bar = bars + stage * 8;
           // columns from multiples of 128 bytes (past d, r and n: zeros)
-          tma_load_2d_pair(dst, &tmX, k * SLAB, t0, bar);
-          tma_load_2d_pair(dst + X_BYTES, tm, k * SLAB, row, bar);
-          if (++stage == STAGES) {
+          load_2d_pair(dst, &tmX, k * SLAB, t0, bar);
+          load_2d_pair(dst + X_BYTES, tm, k * SLAB, row, bar);
+          if (++stage == a.stages) {
             stage = 0;
             phase ^= 1;
+            full = true;
           }
         }
       }
-      for (int s = 0; s < STAGES; ++s)
-        if (issued & (1u << s)) (void)mbar_wait_bounded(&sh.full[s], (issued_par >> s) & 1u);
+      // the last load of every stage has landed (counted on the first CTA's barriers): stages
+      // before `stage` in this phase, the others in the one before
+      if (rank == 0)
+        for (int s = 0; s < a.stages; ++s)
+          if (full || s < stage) (void)mbar_wait_bounded(&sh.full[s], s < stage ? phase : phase ^ 1);
       // a second CTA whose loads the other may not have waited for: time to land
       if (rank == 1 && !ok)
         for (const unsigned long long t0 = global_ns(); global_ns() - t0 < 1000000;) {
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
           if (k == slabs - 1) umma_commit_both(&sh.acc_full[buf]);
         }
         __syncwarp();
-        if (++stage == STAGES) {
+        if (++stage == a.stages) {
           stage = 0;
           phase ^= 1;
         }
@@ -290,12 +291,42 @@ int launch_act(const PairArgs &a, A &&...rest) {
 
 }  // namespace
 
+// Rows of W per tile, and what it takes (us).  A slab of a tile takes its MMAs, 0.32 us for
+// 256 rows, but below 100 rows the copy of x bounds it.  Measured (us, N = 64, 128, 160, 256):
+// 128 tokens, 4096 x 4096 10.2, 10.3, 10.9, 14.1; 64 tokens, 11008 x 4096 22.5, 16.9, 12.0,
+// 14.6; 1000 tokens, 11008 x 4096 69, 39, 35.1, 34.3; 4096 tokens, 4096 x 11008 244, 135, 125,
+// 115; gated, 333 tokens, 11008 x 4096 68, 39, 35.2, 34.7 (224: 33.9).
+static double pair_rows(const Int8Args &p, int pairs, int *rows) {
+  const int64_t nT = (p.n + 2 * TOKENS - 1) / (2 * TOKENS), slabs = (p.d + SLAB - 1) / SLAB;
+  double best = 1e30;
+  for (int N = ROWS; N >= 64; N -= 32) {
+    const int64_t per_tile = p.gated ? N / 2 : N, tiles = nT * ((p.r + per_tile - 1) / per_tile);
+    const double slab = 0.115 + 0.0008 * N;
+    const double us = (double)((tiles + pairs - 1) / pairs * slabs) * (slab < 0.195 ? 0.195 : slab) + 4.2 + 0.004 * N;
+    if (us < best) best = us, *rows = N;
+  }
+  return best;
+}
+
+bool int8_pairs_faster(const Int8Args &p, int sms) {
+  const int split = int8_split(p, sms);
+  if (split == 1) return true;
+  // single CTAs that split k: 100 GB/s a CTA, and their sums' way (128 tokens, 4096 x 11008
+  // 16.4 us, pairs 20.4; 256 tokens 21.5, 21.0; 128 tokens, 4096 x 4096 11.5, 10.2)
+  const int64_t slabs = (p.d + SLAB - 1) / SLAB, layers = p.gated ? 2 : 1;
+  const double bytes = (double)((slabs + split - 1) / split) * (double)((layers * 128 + p.n) * SLAB);
+  int rows;
+  return pair_rows(p, sms / 2, &rows) <= 7.0 + 0.0156 * layers * p.n + bytes * 1e-5;
+}
+
 int launch_int8_pair(const Int8Args &p, cudaStream_t st) {
   PairArgs a{};
   a.p = p;
   const int pairs = num_sms() / 2;
-  a.N = ROWS;
+  (void)pair_rows(p, pairs, &a.N);
   const int per_tile = p.gated ? a.N / 2 : a.N;
+  a.stages = (int)(PAIR_SMEM / (X_BYTES + a.N / 2 * SLAB));
+  if (a.stages > STAGES) a.stages = STAGES;
   const int64_t nT = (p.n + 2 * TOKENS - 1) / (2 * TOKENS), nR = (p.r + per_tile - 1) / per_tile;
   if (nT * nR > INT32_MAX / 8) return GPTQ_ERR_INVALID_ARG;
   a.nT = (int)nT;

@@ -26,14 +26,16 @@ namespace {
 constexpr int ROWS = 128;                 // rows of W per tile (UMMA M)
 constexpr int SLAB = 128;                 // columns per stage
 constexpr int TOKENS = 256;               // most tokens per tile (UMMA N)
-constexpr int STAGES = 8;                 // at most
+constexpr int STAGES = 12;                // at most
 constexpr int SINGLE_THREADS = 32 * 6;
 constexpr size_t SINGLE_SMEM = 208 * 1024;
-constexpr size_t SHARED_SM = 108 * 1024;  // where two CTAs share an SM
+constexpr size_t SHARED_SM = 102 * 1024;  // where two CTAs share an SM
 
 struct SingleArgs {
   Int8Args p;
   int N;              // tokens per tile, a multiple of 16
+  int rows;           // of W per tile, a multiple of 8
+  int deep;           // slabs per stage
   int nM, nN;         // tiles
   int ctas_k;         // CTAs of a cluster, along k
   int stages;
@@ -50,6 +52,7 @@ struct SingleShared {
   uint32_t tmem_base;
   int abort;
   alignas(16) uint16_t stage[4][16 * 32];   // results on their way out, per warp: [token][row]
+  alignas(16) float xs[4][TOKENS];          // scales of a tile's tokens, per warp
 };
 
 __device__ __forceinline__ void single_timeout(int *status, SingleShared &sh) {
@@ -87,16 +90,15 @@ __device__ __forceinline__ float result(int s0, int s1, float xs, const Row &r) 
   return activate<ACT>(v) * scaled_sum(s1, xs, r.scale[1], r.bias[1]);
 }
 
-// 16 tokens of an accumulator's 32 rows to y; a lane is a row.  16-bit results go
-// through shared memory and out 16 bytes, eight rows of a token, per lane, where y's
-// rows allow it.
+// 16 tokens of an accumulator's 32 rows to y, `live` of the rows in the tile; a lane is a
+// row.  16-bit results go through shared memory and out 16 bytes, eight rows of a token,
+// per lane, where y's rows allow it.
 template <typename Y>
-__device__ __forceinline__ void write_tokens(const float (&v)[16], int count, int64_t t0, int64_t row,
+__device__ __forceinline__ void write_tokens(const float (&v)[16], int count, int64_t t0, int64_t row0, int live,
                                              const Int8Args &p, uint16_t *stage, int lane) {
   Y *y = static_cast<Y *>(p.y);
   bool wide = false;
-  if constexpr (sizeof(Y) == 2)
-    wide = p.r % 8 == 0 && row - lane + 32 <= p.r && reinterpret_cast<uintptr_t>(p.y) % 16 == 0;
+  if constexpr (sizeof(Y) == 2) wide = p.r % 8 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0;
   if (wide) {
     if constexpr (sizeof(Y) == 2) {
       __syncwarp();
@@ -107,14 +109,14 @@ __device__ __forceinline__ void write_tokens(const float (&v)[16], int count, in
       for (int h = 0; h < 2; ++h) {
         const int tok = h * 8 + (lane >> 2);
         const uint4 o = reinterpret_cast<const uint4 *>(stage)[h * 32 + lane];
-        if (tok < count)
-          *reinterpret_cast<uint4 *>(y + (t0 + tok) * p.r + (row - lane) + (lane & 3) * 8) = o;
+        if (tok < count && (lane & 3) * 8 < live)   // live: a multiple of 8
+          *reinterpret_cast<uint4 *>(y + (t0 + tok) * p.r + row0 + (lane & 3) * 8) = o;
       }
     }
-  } else if (row < p.r) {
+  } else if (lane < live) {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (i < count) y[(t0 + i) * p.r + row] = to_result<Y>(v[i]);
+      if (i < count) y[(t0 + i) * p.r + row0 + lane] = to_result<Y>(v[i]);
   }
 }
 
@@ -127,27 +129,37 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
   uint8_t *smem =
       reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
   constexpr int LAYERS = GATED ? 2 : 1;
-  constexpr int W_BYTES = LAYERS * ROWS * SLAB;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int N = a.N, stage_bytes = W_BYTES + N * SLAB;
+  const int N = a.N, w_bytes = a.rows * SLAB, x_at = a.deep * LAYERS * w_bytes;
+  const int stage_bytes = x_at + a.deep * N * SLAB;
   const int crank = blockIdx.x % a.ctas_k, ctas = gridDim.x / a.ctas_k, cta = blockIdx.x / a.ctas_k;
   const int tiles = a.nM * a.nN;
-  const int slabs = (a.p.d + SLAB - 1) / SLAB;
-  const int k0 = (int)((int64_t)slabs * crank / a.ctas_k);
-  const int k1 = (int)((int64_t)slabs * (crank + 1) / a.ctas_k);
+  const int steps = (a.p.d + SLAB * a.deep - 1) / (SLAB * a.deep);
+  const int k0 = (int)((int64_t)steps * crank / a.ctas_k);
+  const int k1 = (int)((int64_t)steps * (crank + 1) / a.ctas_k);
   const uint32_t acc_columns = LAYERS * N;
 
   // the tokens of a split tile that exist, in fours
   const int fours = a.ctas_k > 1 ? (int)((min((int64_t)N, a.p.n - (int64_t)(cta / a.nM) * N) + 3) / 4) : 0;
-  const int owned = ROWS / a.ctas_k;   // rows
-  auto load = [&](int t, int k, int stage) {
-    mbar_arrive_expect_tx(&sh.full[stage], stage_bytes);
-    uint8_t *dst = smem + (size_t)stage * stage_bytes;
+  const int owned = a.rows / a.ctas_k;   // rows
+  // (what a load takes is kept ready: one thread issues them all, and divisions in its loop
+  // cost 800 clocks a step, more than the step's data)
+  auto load = [&](int m0, int n0, int k, uint32_t dst, uint64_t *bar) {
+    mbar_arrive_expect_tx(bar, stage_bytes);
     // columns from multiples of 128 bytes (past d, r and n: zeros)
-    tma_load_2d(dst, &tmW, k * SLAB, t % a.nM * ROWS, &sh.full[stage]);
-    if constexpr (GATED) tma_load_2d(dst + ROWS * SLAB, &tmU, k * SLAB, t % a.nM * ROWS, &sh.full[stage]);
-    tma_load_2d(dst + W_BYTES, &tmX, k * SLAB, t / a.nM * N, &sh.full[stage]);
+    int col = k * (a.deep * SLAB);
+    uint32_t x = dst + x_at;
+    for (int j = 0; j < a.deep; ++j, col += SLAB, x += N * SLAB) {
+      load_2d(dst, &tmW, col, m0, bar);
+      dst += w_bytes;
+      if constexpr (GATED) {
+        load_2d(dst, &tmU, col, m0, bar);
+        dst += w_bytes;
+      }
+      load_2d(x, &tmX, col, n0, bar);
+    }
   };
+  const uint32_t ring = smem_u32(smem);
   int ahead = 0;   // thread 0: slabs of the first tile asked for at the start
 
   if (threadIdx.x == 0) {
@@ -164,12 +176,15 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
     sh.abort = 0;
     fence_mbar_init();
     if (a.ctas_k > 1) mbar_arrive_expect_tx(&sh.sums, (a.ctas_k - 1) * LAYERS * fours * owned * 16);
-    for (int k = k0; k < k1 && k < k0 + a.stages; ++k) {   // (into L2, whoever wrote them)
-      prefetch_2d(&tmW, k * SLAB, cta % a.nM * ROWS);
-      if constexpr (GATED) prefetch_2d(&tmU, k * SLAB, cta % a.nM * ROWS);
-    }
+    for (int k = k0; k < k1 && k < k0 + a.stages; ++k)   // (into L2, whoever wrote them)
+      for (int j = 0; j < a.deep; ++j) {
+        prefetch_2d(&tmW, (k * a.deep + j) * SLAB, cta % a.nM * a.rows);
+        if constexpr (GATED) prefetch_2d(&tmU, (k * a.deep + j) * SLAB, cta % a.nM * a.rows);
+      }
     pdl_wait_then_release();
-    for (; ahead < a.stages && k0 + ahead < k1; ++ahead) load(cta, k0 + ahead, ahead);
+    const int m0 = cta % a.nM * a.rows, n0 = cta / a.nM * N;
+    for (; ahead < a.stages && k0 + ahead < k1; ++ahead)
+      load(m0, n0, k0 + ahead, ring + ahead * stage_bytes, &sh.full[ahead]);
   } else {
     if (warp == 1) {
       tmem_alloc(&sh.tmem_base, a.columns);
@@ -188,26 +203,28 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
     // ---------------------------------------------------------------- W and x by TMA
     if (lane == 0) {
       int stage = ahead == a.stages ? 0 : ahead;
-      uint32_t phase = ahead == a.stages ? 1 : 0, issued = (1u << ahead) - 1u, issued_par = 0;
-      bool ok = true;
+      uint32_t phase = ahead == a.stages ? 1 : 0;
+      bool ok = true, full = phase != 0;   // full: every stage has been asked for
       for (int t = cta; t < tiles && ok; t += ctas) {
+        const int m0 = t % a.nM * a.rows, n0 = t / a.nM * N;
         for (int k = t == cta ? k0 + ahead : k0; k < k1; ++k) {
-          ok = !*(volatile int *)&sh.abort && mbar_wait_bounded(&sh.empty[stage], phase ^ 1);
+          ok = wait_or_abort(&sh.empty[stage], phase ^ 1, &sh.abort);
           if (!ok) {
             single_timeout(a.status, sh);
             break;
           }
-          issued |= 1u << stage;
-          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-          load(t, k, stage);
+          load(m0, n0, k, ring + stage * stage_bytes, &sh.full[stage]);
           if (++stage == a.stages) {
             stage = 0;
             phase ^= 1;
+            full = true;
           }
         }
       }
-      for (int s = 0; s < STAGES; ++s)
-        if (issued & (1u << s)) (void)mbar_wait_bounded(&sh.full[s], (issued_par >> s) & 1u);
+      // the last load of every stage has landed: stages before `stage` in this phase, the
+      // others in the one before
+      for (int s = 0; s < a.stages; ++s)
+        if (full || s < stage) (void)mbar_wait_bounded(&sh.full[s], s < stage ? phase : phase ^ 1);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- the MMAs
@@ -225,14 +242,17 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         if (elect_lane()) {
-          const uint64_t w = first + (uint64_t)(stage * stage_bytes >> 4), x = w + (W_BYTES >> 4);
+          // (a tile of fewer rows multiplies what lies behind them too, for results that
+          // nobody reads)
           const uint32_t d0 = tm + buf * acc_columns;
+          uint64_t w = first + (uint64_t)(stage * stage_bytes >> 4), x = w + (x_at >> 4);
+          for (int j = 0; j < a.deep; ++j, w += LAYERS * w_bytes >> 4, x += N * SLAB >> 4)
 #pragma unroll
-          for (int q = 0; q < SLAB / 32; ++q) {
-            umma_i8_ss(d0, w + q * 2, x + q * 2, idesc, k > k0 || q > 0);
-            if constexpr (GATED)
-              umma_i8_ss(d0 + N, w + (ROWS * SLAB >> 4) + q * 2, x + q * 2, idesc, k > k0 || q > 0);
-          }
+            for (int q = 0; q < SLAB / 32; ++q) {
+              umma_i8_ss(d0, w + q * 2, x + q * 2, idesc, k > k0 || j > 0 || q > 0);
+              if constexpr (GATED)
+                umma_i8_ss(d0 + N, w + (w_bytes >> 4) + q * 2, x + q * 2, idesc, k > k0 || j > 0 || q > 0);
+            }
           umma_commit(&sh.empty[stage]);
           if (k == k1 - 1) umma_commit(&sh.acc_full[buf]);
         }
@@ -254,31 +274,34 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
     __syncwarp();
   } else if (a.ctas_k == 1) {
     // ---------------------------------------------------------------- results
-    const int quarter = warp & 3, lrow = quarter * 32 + lane;
+    const int quarter = warp & 3;
     uint32_t buf = 0, cphase = 0;
     bool ok = true;
     for (int t = cta; t < tiles && ok; t += ctas) {
-      const int64_t row = (int64_t)(t % a.nM) * ROWS + lrow, t0 = (int64_t)(t / a.nM) * N;
+      const int64_t row0 = (int64_t)(t % a.nM) * a.rows + quarter * 32, t0 = (int64_t)(t / a.nM) * N;
+      const int64_t left = min((int64_t)a.rows - quarter * 32, a.p.r - row0);
+      const int live = left < 0 ? 0 : left < 32 ? (int)left : 32;
       const int count = (int)(a.p.n - t0 < N ? a.p.n - t0 : N);
-      const Row par = row_of<GATED>(a.p, row);
+      const Row par = row_of<GATED>(a.p, row0 + lane);
+      __syncwarp();
+      for (int c = lane; c < N; c += 32) sh.xs[quarter][c] = c < count ? __ldcg(a.p.x_scales + t0 + c) : 0.f;
+      __syncwarp();
       ok = mbar_wait_bounded(&sh.acc_full[buf], (cphase >> buf) & 1u);
       if (!ok && lane == 0) single_timeout(a.status, sh);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + buf * acc_columns;
-      for (int c0 = 0; c0 < count; c0 += 16) {
+      for (int c0 = 0; c0 < count && live > 0; c0 += 16) {
         float s0[16], s1[16];   // sums' bits
         tmem_ld_32x32b_x16(base + c0, s0);
         if constexpr (GATED) tmem_ld_32x32b_x16(base + N + c0, s1);
         tmem_wait_ld();
         float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float xs = c0 + i < count ? __ldcg(a.p.x_scales + t0 + c0 + i) : 0.f;
-          v[i] = result<GATED, ACT>(__float_as_int(s0[i]), GATED ? __float_as_int(s1[i]) : 0, xs, par);
-        }
-        write_tokens<Y>(v, count - c0, t0 + c0, row, a.p, sh.stage[quarter], lane);
+        for (int i = 0; i < 16; ++i)
+          v[i] = result<GATED, ACT>(__float_as_int(s0[i]), GATED ? __float_as_int(s1[i]) : 0, sh.xs[quarter][c0 + i], par);
+        write_tokens<Y>(v, count - c0, t0 + c0, row0, live, a.p, sh.stage[quarter], lane);
       }
       tc_fence_before();
       __syncwarp();
@@ -326,16 +349,21 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
         }
       }
     }
+    // what the results need, while the sums arrive: a thread keeps to one row
+    const int64_t m0 = (int64_t)(cta % a.nM) * a.rows + crank * owned, t0 = (int64_t)(cta / a.nM) * N;
+    const int64_t row = m0 + threadIdx.x % owned;   // SINGLE_THREADS % owned == 0
+    const Row par = row_of<GATED>(a.p, row);
+    float *xs = sh.xs[0];
+    for (int c = threadIdx.x; c < fours * 4; c += SINGLE_THREADS)
+      xs[c] = t0 + c < a.p.n ? __ldcg(a.p.x_scales + t0 + c) : 0.f;
     // (a CTA that gave up pushed its sums all the same, whatever they are)
     if (!mbar_wait_bounded(&sh.sums, 0)) single_timeout(a.status, sh);
     __syncthreads();
     if (!*(volatile int *)&sh.abort) {
-      const int64_t m0 = (int64_t)(cta % a.nM) * ROWS + crank * owned, t0 = (int64_t)(cta / a.nM) * N;
-      Y *y = static_cast<Y *>(a.p.y);
-      for (int i = threadIdx.x; i < fours * owned; i += SINGLE_THREADS) {
-        const int64_t row = m0 + i % owned, tok = t0 + i / owned * 4;
-        if (row >= a.p.r) continue;
-        const Row par = row_of<GATED>(a.p, row);
+      Y *y = static_cast<Y *>(a.p.y) + row;
+      for (int i = threadIdx.x; i < fours * owned && row < a.p.r; i += SINGLE_THREADS) {
+        const int64_t tok = t0 + i / owned * 4;
+        const float4 scale = *reinterpret_cast<const float4 *>(xs + i / owned * 4);
         int4 s[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -347,11 +375,10 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
           }
         }
         const int s0[4] = {s[0].x, s[0].y, s[0].z, s[0].w}, s1[4] = {s[1].x, s[1].y, s[1].z, s[1].w};
+        const float f[4] = {scale.x, scale.y, scale.z, scale.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (tok + q < a.p.n)
-            y[(tok + q) * a.p.r + row] =
-                to_result<Y>(result<GATED, ACT>(s0[q], s1[q], __ldcg(a.p.x_scales + tok + q), par));
+          if (tok + q < a.p.n) y[(tok + q) * a.p.r] = to_result<Y>(result<GATED, ACT>(s0[q], s1[q], f[q], par));
       }
     }
   }
@@ -383,46 +410,98 @@ int launch_act(const SingleArgs &a, A &&...rest) {
 
 }  // namespace
 
+namespace {
+
+// Rows of W per tile, CTAs along k, and whether two CTAs share an SM, for up to 64 tokens,
+// which are bound by the copies of W: all SMs copying, with as few steps as it takes to
+// meet.  Measured (us; tiles of 128 rows split over 2, 4, 8 CTAs, and unsplit tiles that make
+// 148 or 296):
+//   1 token, 4096 x 4096     8.7, 7.7, 7.2   7.9, 10.4   (32 tiles)
+//   24 tokens, 4096 x 11008  15.9, 12.5, 11.6   15.8, 21.5
+//   16 tokens, 8192 x 8192   15.1, 14.4, 17.6   16.6, 15.9   (64 tiles)
+//   1 token, 11008 x 4096    14.1, 17.5, 20.1   11.7, 10.9   (86 tiles)
+//   1 token, 12288 x 49152   97.7, 102.8, 99.3   100.1, 91.9
+//   64 tokens, 11008 x 4096  24.0, 26.4, 26.0   12.4, 14.1
+//   gated, 24 tokens, 4096 x 4096  13.1, 10.4, 12.2
+//   gated, 16 tokens, 5120 x 5120  15.4, 15.5, 19.5   15.4, 19.7   (40 tiles)
+//   gated, 1 token, 11008 x 4096   22.9, 25.9, 28.5   16.6, 16.8
+//   16 tokens, 512 x 512     4.0, 3.9, 3.9   3.3, 3.3
+// Gated tiles have twice the bytes, so that one CTA fills an SM's share.
+struct Shape {
+  int rows, ctas_k;
+  bool shared;
+};
+Shape shape_for(int64_t r, int slabs, int N, bool gated, int sms) {
+  const int64_t tiles = (r + ROWS - 1) / ROWS, fit = gated ? sms : 2 * sms;
+  if (slabs >= 8)
+    for (int c = 8; c >= 2; c /= 2)
+      if (slabs >= 2 * c && tiles * c <= fit && (gated || c > 2)) return Shape{ROWS, c, tiles * c > sms};
+  const int64_t parts = gated || N > 48 ? sms : 2 * sms;
+  const int64_t rows = (r + 8 * parts - 1) / (8 * parts) * 8;
+  const bool shared = !gated && N <= 48 && (r + rows - 1) / rows > sms;
+  return Shape{rows < ROWS ? (int)rows : ROWS, 1, shared};
+}
+
+}  // namespace
+
+int int8_split(const Int8Args &p, int sms) {   // the widest split that finds room, or 1
+  const int64_t tiles = (p.r + ROWS - 1) / ROWS;
+  const int slabs = (p.d + SLAB - 1) / SLAB, layers = p.gated ? 2 : 1;
+  for (int c = 4; c >= 2; c /= 2)
+    if (tiles * c <= sms && slabs >= 2 * c && p.n <= TOKENS / layers) return c;
+  return 1;
+}
+
 int launch_int8_single(const Int8Args &p, cudaStream_t st) {
   SingleArgs a{};
   a.p = p;
   const int sms = num_sms(), layers = p.gated ? 2 : 1;
   const int slabs = (p.d + SLAB - 1) / SLAB;
-  const int64_t nM = (p.r + ROWS - 1) / ROWS;
   // tokens in equal parts
   const int64_t parts = (p.n + TOKENS - 1) / TOKENS;
   a.N = (int)((p.n + parts * 16 - 1) / (parts * 16) * 16);
   const int64_t nN = (p.n + a.N - 1) / a.N;
+  const Shape shape = p.n <= FEW_TOKENS ? shape_for(p.r, slabs, a.N, p.gated, sms) : Shape{ROWS, int8_split(p, sms), false};
+  a.rows = shape.rows;
+  a.ctas_k = shape.ctas_k;
+  const int64_t nM = (p.r + a.rows - 1) / a.rows;
   if (nM * nN > INT32_MAX / 8) return GPTQ_ERR_INVALID_ARG;
   a.nM = (int)nM;
   a.nN = (int)nN;
   const int64_t tiles = nM * nN;
-  const bool shared = a.N <= 64;
-  a.ctas_k = 1;
-  for (int c = 2; c <= 8; c *= 2)
-    if (tiles * c <= sms && slabs >= 2 * c) a.ctas_k = c;
-  const size_t stage = (size_t)(layers * ROWS + a.N) * SLAB;
-  const size_t meet = (size_t)layers * a.N * ROWS * 4;   // split k: the sums of the rows that a CTA owns
-  if (meet > SINGLE_SMEM / stage * stage) a.ctas_k = 1;
-  const size_t apart = a.ctas_k > 1 && a.N <= 32 ? meet : 0;
-  const size_t fit = ((shared ? SHARED_SM : SINGLE_SMEM) - apart) / stage;
+  // stages of 16 KB of W, at least four of them
+  const size_t room = shape.shared ? SHARED_SM : SINGLE_SMEM, slab = (size_t)(layers * a.rows + a.N) * SLAB;
+  a.deep = ROWS / a.rows;
+  while (a.deep > 1 && a.deep * slab * 4 > room) --a.deep;
+  const int steps = (slabs + a.deep - 1) / a.deep;
+  const size_t stage = slab * a.deep;
+  // a tile of fewer rows reads up to 128 rows of the last stage
+  const size_t pad = (size_t)(ROWS - a.rows) * SLAB;
+  // split k: the sums of the rows that a CTA owns meet beside the ring, or in it
+  const size_t meet = a.ctas_k > 1 ? (size_t)layers * a.N * a.rows * 4 : 0;
+  const size_t apart = a.N * layers <= 32 ? meet : 0;
+  const size_t fit = (room - apart - pad) / stage;
+  if (fit < 2 || meet > SINGLE_SMEM) return GPTQ_ERR_INVALID_ARG;   // (never: 64 KB a stage at most)
   a.stages = fit > STAGES ? STAGES : (int)fit;
+  const int64_t work = a.ctas_k > 1 ? (steps + a.ctas_k - 1) / a.ctas_k : (tiles + sms - 1) / sms * steps;
+  if (a.stages > work) a.stages = (int)work;   // no more than there are steps
   size_t bytes = a.stages * stage;
   a.slots = apart ? (int)bytes : 0;
   bytes += apart;
-  if (a.ctas_k > 1 && bytes < meet) bytes = meet;
-  a.buffers = a.ctas_k == 1 && 2 * layers * a.N <= (shared ? 256 : 512) ? 2 : 1;
+  if (bytes < meet) bytes = meet;
+  bytes += pad;
+  a.buffers = a.ctas_k == 1 && 2 * layers * a.N <= (shape.shared ? 256 : 512) ? 2 : 1;
   a.columns = 32;
   while (a.columns < (uint32_t)(a.buffers * layers * a.N)) a.columns *= 2;
   a.status = device_status_word();
   if (!a.status) return GPTQ_ERR_CUDA;
   CUtensorMap tx, tw, tu;
   if (const int rc = int8_map(&tx, p.x, p.n, p.d, a.N)) return rc;
-  if (const int rc = int8_map(&tw, p.w[0], p.r, p.d, ROWS)) return rc;
+  if (const int rc = int8_map(&tw, p.w[0], p.r, p.d, a.rows)) return rc;
   tu = tw;
   if (p.gated)
-    if (const int rc = int8_map(&tu, p.w[1], p.r, p.d, ROWS)) return rc;
-  const int64_t most = shared ? 2 * sms : sms;
+    if (const int rc = int8_map(&tu, p.w[1], p.r, p.d, a.rows)) return rc;
+  const int64_t most = shape.shared ? 2 * sms : sms;
   const unsigned ctas = (unsigned)(a.ctas_k > 1 ? tiles * a.ctas_k : (tiles < most ? tiles : most));
   if (!p.gated) return launch_act<false, GPTQ_ACT_NONE>(a, tx, tw, tu, ctas, bytes, st);
   switch (p.activation) {

@@ -33,7 +33,7 @@ __device__ __forceinline__ uint32_t four_codes(const uint32_t (&w)[BITS], int k)
 template <int BITS>
 __global__ void __launch_bounds__(THREADS)
     int8_weights_kernel(const uint32_t *qweight, const float *scales, const int32_t *zeros, int64_t r, int chunks,
-                        int per_row, int8_t *w, float *w_scales) {
+                        int per_row, bool wide, int8_t *w, float *w_scales) {
   __shared__ int outside[THREADS / 32];   // per row of the CTA
   const int rows = THREADS / per_row, mine = threadIdx.x / per_row, at = threadIdx.x % per_row;
   const int64_t row = (int64_t)blockIdx.x * rows + mine;
@@ -48,8 +48,16 @@ __global__ void __launch_bounds__(THREADS)
     for (int c = at; c < chunks; c += per_row) {
       const uint32_t *src = qweight + (row * chunks + c) * BITS;
       uint32_t q[BITS], o[8];
+      if (BITS >= 4 && wide) {   // four words at a time
 #pragma unroll
-      for (int i = 0; i < BITS; ++i) q[i] = __ldcg(src + i);
+        for (int i = 0; i + 4 <= BITS; i += 4) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(src + i);
+          q[i] = v.x, q[i + 1] = v.y, q[i + 2] = v.z, q[i + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < BITS; ++i) q[i] = src[i];
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const uint32_t v = four_codes<BITS>(q, k);
@@ -85,7 +93,7 @@ int launch_weights(const uint32_t *q, const float *s, const int32_t *z, int64_t 
   while (per_row < THREADS && per_row * 4 < chunks) per_row *= 2;
   const int rows = THREADS / per_row;
   return launch_after(int8_weights_kernel<BITS>, (unsigned)((r + rows - 1) / rows), THREADS, 0, 1, st, q, s, z, r,
-                      chunks, per_row, w, ws);
+                      chunks, per_row, reinterpret_cast<uintptr_t>(q) % 16 == 0, w, ws);
 }
 
 }  // namespace
