@@ -244,11 +244,19 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
           if constexpr (GATED) tmem_ld_32x32b_x16(acc + half + c, s1);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 16; ++i)
             v[i] = scaled_sum(__float_as_int(s0[i]), xs, sh.scale[buf][c + i], sh.bias[buf][c + i]);
-            if constexpr (GATED)
-              v[i] = activate<ACT>(v[i]) *
-                     scaled_sum(__float_as_int(s1[i]), xs, sh.scale[buf][half + c + i], sh.bias[buf][half + c + i]);
+          if constexpr (GATED) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const int at = half + c + i;
+              const F2 r = gated_pair<ACT, Y>(
+                  F2{v[i], v[i + 1]},
+                  F2{scaled_sum(__float_as_int(s1[i]), xs, sh.scale[buf][at], sh.bias[buf][at]),
+                     scaled_sum(__float_as_int(s1[i + 1]), xs, sh.scale[buf][at + 1], sh.bias[buf][at + 1])});
+              v[i] = r.x;
+              v[i + 1] = r.y;
+            }
           }
           if (tok < a.p.n) write16<Y>(y + c, v, a.p.r - r0 - c, align);
         }

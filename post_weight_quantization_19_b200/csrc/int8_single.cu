@@ -83,11 +83,13 @@ __device__ __forceinline__ Row row_of(const Int8Args &p, int64_t row) {
   return r;
 }
 
-template <bool GATED, int ACT>
-__device__ __forceinline__ float result(int s0, int s1, float xs, const Row &r) {
-  const float v = scaled_sum(s0, xs, r.scale[0], r.bias[0]);
+// Results of one row and two tokens from their sums.
+template <bool GATED, int ACT, typename Y>
+__device__ __forceinline__ F2 results(int a0, int a1, int b0, int b1, float x0, float x1, const Row &r) {
+  const F2 v{scaled_sum(a0, x0, r.scale[0], r.bias[0]), scaled_sum(a1, x1, r.scale[0], r.bias[0])};
   if constexpr (!GATED) return v;
-  return activate<ACT>(v) * scaled_sum(s1, xs, r.scale[1], r.bias[1]);
+  return gated_pair<ACT, Y>(
+      v, F2{scaled_sum(b0, x0, r.scale[1], r.bias[1]), scaled_sum(b1, x1, r.scale[1], r.bias[1])});
 }
 
 // 16 tokens of an accumulator's 32 rows to y, `live` of the rows in the tile; a lane is a
@@ -299,8 +301,13 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
         tmem_wait_ld();
         float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          v[i] = result<GATED, ACT>(__float_as_int(s0[i]), GATED ? __float_as_int(s1[i]) : 0, sh.xs[quarter][c0 + i], par);
+        for (int i = 0; i < 16; i += 2) {
+          const F2 f = results<GATED, ACT, Y>(
+              __float_as_int(s0[i]), __float_as_int(s0[i + 1]), GATED ? __float_as_int(s1[i]) : 0,
+              GATED ? __float_as_int(s1[i + 1]) : 0, sh.xs[quarter][c0 + i], sh.xs[quarter][c0 + i + 1], par);
+          v[i] = f.x;
+          v[i + 1] = f.y;
+        }
         write_tokens<Y>(v, count - c0, t0 + c0, row0, live, a.p, sh.stage[quarter], lane);
       }
       tc_fence_before();
@@ -374,11 +381,12 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
             s[l].x += v.x, s[l].y += v.y, s[l].z += v.z, s[l].w += v.w;
           }
         }
-        const int s0[4] = {s[0].x, s[0].y, s[0].z, s[0].w}, s1[4] = {s[1].x, s[1].y, s[1].z, s[1].w};
-        const float f[4] = {scale.x, scale.y, scale.z, scale.w};
+        const F2 lo = results<GATED, ACT, Y>(s[0].x, s[0].y, s[1].x, s[1].y, scale.x, scale.y, par);
+        const F2 hi = results<GATED, ACT, Y>(s[0].z, s[0].w, s[1].z, s[1].w, scale.z, scale.w, par);
+        const float f[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (tok + q < a.p.n) y[(tok + q) * a.p.r] = to_result<Y>(result<GATED, ACT>(s0[q], s1[q], f[q], par));
+          if (tok + q < a.p.n) y[(tok + q) * a.p.r] = to_result<Y>(f[q]);
       }
     }
   }

@@ -30,10 +30,25 @@ __device__ __forceinline__ uint32_t four_codes(const uint32_t (&w)[BITS], int k)
          code_at<BITS>(w, 4 * k + 3) << 24;
 }
 
+// A chunk's words, four at a time where they are aligned (wide).
+template <int BITS>
+__device__ __forceinline__ void read_chunk(const uint32_t *src, bool wide, uint32_t (&q)[BITS]) {
+  if (BITS >= 4 && wide) {
+#pragma unroll
+    for (int i = 0; i + 4 <= BITS; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(src + i);
+      q[i] = v.x, q[i + 1] = v.y, q[i + 2] = v.z, q[i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < BITS; ++i) q[i] = src[i];
+  }
+}
+
 template <int BITS>
 __global__ void __launch_bounds__(THREADS)
     int8_weights_kernel(const uint32_t *qweight, const float *scales, const int32_t *zeros, int64_t r, int chunks,
-                        int per_row, bool wide, int8_t *w, float *w_scales) {
+                        int per_row, bool wide, bool whole, int8_t *w, float *w_scales) {
   __shared__ int outside[THREADS / 32];   // per row of the CTA
   const int rows = THREADS / per_row, mine = threadIdx.x / per_row, at = threadIdx.x % per_row;
   const int64_t row = (int64_t)blockIdx.x * rows + mine;
@@ -44,40 +59,45 @@ __global__ void __launch_bounds__(THREADS)
     const int z = min(max(__ldcg(zeros + row), 0), (1 << BITS) - 1);
     const uint32_t zzzz = (uint32_t)z * 0x01010101u;
     bool lost = false;
-#pragma unroll 4
-    for (int c = at; c < chunks; c += per_row) {
-      const uint32_t *src = qweight + (row * chunks + c) * BITS;
-      uint32_t q[BITS], o[8];
-      if (BITS >= 4 && wide) {   // four words at a time
+    // (several chunks are read before any is written: the compiler may not move reads over writes)
+    constexpr int AT_ONCE = BITS == 8 ? 2 : 4;
+    for (int c0 = at; c0 < chunks; c0 += AT_ONCE * per_row) {
+      uint32_t q[AT_ONCE][BITS];
 #pragma unroll
-        for (int i = 0; i + 4 <= BITS; i += 4) {
-          const uint4 v = *reinterpret_cast<const uint4 *>(src + i);
-          q[i] = v.x, q[i + 1] = v.y, q[i + 2] = v.z, q[i + 3] = v.w;
-        }
-      } else {
+      for (int j = 0; j < AT_ONCE; ++j)
+        if (c0 + j * per_row < chunks) read_chunk<BITS>(qweight + (row * chunks + c0 + j * per_row) * BITS, wide, q[j]);
 #pragma unroll
-        for (int i = 0; i < BITS; ++i) q[i] = src[i];
-      }
+      for (int j = 0; j < AT_ONCE; ++j) {
+        const int c = c0 + j * per_row;
+        if (c >= chunks) break;
+        uint32_t o[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t v = four_codes<BITS>(q, k);
-        if constexpr (BITS < 8) {
-          o[k] = ((v | 0x80808080u) - zzzz) ^ 0x80808080u;   // per byte: no borrow leaves it
-        } else if (z == 128) {
-          o[k] = v ^ 0x80808080u;
-        } else {
-          o[k] = 0;
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t v = four_codes<BITS>(q[j], k);
+          if constexpr (BITS < 8) {
+            o[k] = ((v | 0x80808080u) - zzzz) ^ 0x80808080u;   // per byte: no borrow leaves it
+          } else if (z == 128) {
+            o[k] = v ^ 0x80808080u;
+          } else {
+            o[k] = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int e = (int)((v >> (8 * i)) & 0xFFu) - z;
-            lost |= e < -128 || e > 127;
-            o[k] |= ((uint32_t)min(max(e, -128), 127) & 0xFFu) << (8 * i);
+            for (int i = 0; i < 4; ++i) {
+              const int e = (int)((v >> (8 * i)) & 0xFFu) - z;
+              lost |= e < -128 || e > 127;
+              o[k] |= ((uint32_t)min(max(e, -128), 127) & 0xFFu) << (8 * i);
+            }
           }
         }
+        int8_t *dst = w + (row * chunks + c) * 32;
+        if (whole) {   // a sector in one store
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(o[0]), "r"(o[1]),
+                       "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                       : "memory");
+        } else {
+          reinterpret_cast<uint4 *>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+          reinterpret_cast<uint4 *>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
       }
-      uint4 *dst = reinterpret_cast<uint4 *>(w + (row * chunks + c) * 32);
-      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
     if (lost) outside[mine] = 1;
   }
@@ -93,7 +113,8 @@ int launch_weights(const uint32_t *q, const float *s, const int32_t *z, int64_t 
   while (per_row < THREADS && per_row * 4 < chunks) per_row *= 2;
   const int rows = THREADS / per_row;
   return launch_after(int8_weights_kernel<BITS>, (unsigned)((r + rows - 1) / rows), THREADS, 0, 1, st, q, s, z, r,
-                      chunks, per_row, reinterpret_cast<uintptr_t>(q) % 16 == 0, w, ws);
+                      chunks, per_row, reinterpret_cast<uintptr_t>(q) % 16 == 0, reinterpret_cast<uintptr_t>(w) % 32 == 0,
+                      w, ws);
 }
 
 }  // namespace
