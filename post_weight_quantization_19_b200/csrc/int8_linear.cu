@@ -37,7 +37,9 @@ bool misaligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p)
 
 // Checks and launches; layers: 1, or 2 of a gated block.
 int int8_product(const Int8Args &a, int layers, int64_t d, cudaStream_t st) {
-  if (a.n < 0 || a.n > (int64_t)INT32_MAX || a.r < 0 || a.r > (int64_t)INT32_MAX) return GPTQ_ERR_INVALID_ARG;
+  // (the last tile's coordinates, too, are 32-bit)
+  constexpr int64_t MOST = (int64_t)INT32_MAX - 512;
+  if (a.n < 0 || a.n > MOST || a.r < 0 || a.r > MOST) return GPTQ_ERR_INVALID_ARG;
   if (d <= 0 || d % 32 != 0 || d > 65536) return GPTQ_ERR_INVALID_ARG;
   if (a.ytype != GPTQ_F16 && a.ytype != GPTQ_BF16 && a.ytype != GPTQ_F32) return GPTQ_ERR_INVALID_ARG;
   if (a.n == 0 || a.r == 0) return GPTQ_OK;

@@ -544,15 +544,17 @@ def gptq_activation_int8(x: torch.Tensor, up: torch.Tensor | None = None, *, act
     act = _activation(activation)
     n, d = x.shape
     dev, T = x.device, x.dtype
-    out = dict(outputs or {})
-    codes, scales, xh = (out.get(k) for k in ("codes", "scales", "xhat"))
-    with _on(stream):
-        if codes is None:
-            codes = torch.empty((n, d), dtype=torch.int8, device=dev)
-        if scales is None:
-            scales = torch.empty(n, dtype=torch.float32, device=dev)
-        if xh is None and xhat:
-            xh = torch.empty((n, d), dtype=T, device=dev)
+    codes = scales = xh = None
+    if outputs:
+        codes, scales, xh = outputs.get("codes"), outputs.get("scales"), outputs.get("xhat")
+    if codes is None or scales is None or (xhat and xh is None):
+        with _on(stream):
+            if codes is None:
+                codes = torch.empty((n, d), dtype=torch.int8, device=dev)
+            if scales is None:
+                scales = torch.empty(n, dtype=torch.float32, device=dev)
+            if xh is None and xhat:
+                xh = torch.empty((n, d), dtype=T, device=dev)
     _check(_launch(
         dev, stream, lib.gptq_activation_int8, _shaped(x, T, (n, d), dev, "x"), _shaped(up, T, (n, d), dev, "up"),
         _DTYPE[T], n, d, act, _shaped(perm, torch.int32, (d,), dev, "perm"),

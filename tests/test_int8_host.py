@@ -143,3 +143,19 @@ def test_oracle_int8_product_pins():
     z = np.full((5, 1), 128)
     np.testing.assert_allclose(oracle.int8_product(x, xs, w, ws),
                                oracle.dequant_gemv(packed, ws[:, None], z, 8, -1, x * xs[:, None]), rtol=1e-12)
+
+
+@pytest.mark.parametrize("name", ["int8_single.cu", "int8_pair.cu", "int8_linear.h", "int8_weights.cu",
+                                  "activation_int8.cuh"])
+def test_kernels_read_behind_the_wait_with_ordinary_loads(name):
+    # These kernels start while the one before them on the stream still runs, so what they
+    # read may be written while they live: no loads that take it for constant.
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                        "post_weight_quantization_19_b200", "csrc")
+    with open(os.path.join(csrc, name), encoding="utf-8") as f:
+        src = re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+    assert "__ldg" not in src and "__restrict__" not in src and "ld.global.nc" not in src
+    for kernel in re.findall(r"__global__.*?\n}\n", src, flags=re.S):
+        assert "pdl_wait_then_release()" in kernel
