@@ -16,8 +16,9 @@ namespace gptq {
 // successor launch.  So when a kernel starts, every grid before its
 // predecessor has completed, and at most two grids of the sequence are in
 // flight.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait_then_release() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_wait();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 

@@ -183,16 +183,14 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
         prefetch_2d(&tmW, (k * a.deep + j) * SLAB, cta % a.nM * a.rows);
         if constexpr (GATED) prefetch_2d(&tmU, (k * a.deep + j) * SLAB, cta % a.nM * a.rows);
       }
-    pdl_wait_then_release();
+    pdl_wait();
     const int m0 = cta % a.nM * a.rows, n0 = cta / a.nM * N;
     for (; ahead < a.stages && k0 + ahead < k1; ++ahead)
       load(m0, n0, k0 + ahead, ring + ahead * stage_bytes, &sh.full[ahead]);
-  } else {
-    if (warp == 1) {
-      tmem_alloc(&sh.tmem_base, a.columns);
-      tmem_relinquish();
-    }
-    pdl_wait_then_release();
+  } else if (warp == 1) {
+    pdl_wait();
+    tmem_alloc(&sh.tmem_base, a.columns);
+    tmem_relinquish();
   }
   __syncwarp();
   if (a.ctas_k > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // barriers are there
@@ -200,6 +198,9 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
+  // (tensor memory is taken when the kernel before is done with it and before the next one
+  // may start: CTAs that wait for it then wait for kernels that do not wait for them)
+  pdl_wait_then_release();
 
   if (warp == 0) {
     // ---------------------------------------------------------------- W and x by TMA
