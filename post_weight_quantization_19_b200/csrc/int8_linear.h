@@ -40,7 +40,7 @@ __device__ __forceinline__ float scaled_sum(int sum, float xs, float ws, float b
 // instructions (within 6e-6 of the value for gelu, whose arguments are rounded here).
 template <int ACT, typename Y>
 __device__ __forceinline__ F2 gated_pair(const F2 &g, const F2 &u) {
-  if constexpr (sizeof(Y) == 2) return mul2(activate_fast<ACT>(g), u);
+  if constexpr (sizeof(Y) == 2) return mul2(activate_fast<ACT, true>(g), u);
   return F2{activate<ACT>(g.x) * u.x, activate<ACT>(g.y) * u.y};
 }
 

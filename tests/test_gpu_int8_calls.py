@@ -11,7 +11,7 @@ import threading
 import numpy as np
 import pytest
 
-from test_gpu_int8 import (ACTS, BF16, F16, F32, I8, TYPES, act_inputs, assert_close, assert_codes, codes8, f64,
+from test_gpu_int8 import (ACTS, BF16, F16, F32, HALF, I8, TYPES, act_inputs, assert_close, assert_codes, codes8, f64,
                            gated_reference, layer8, product)
 
 torch = pytest.importorskip("torch")
@@ -55,6 +55,38 @@ def test_a_token_does_not_depend_on_the_others(n):
         whole = g.gptq_int8_gated(x, xs, w, ws, u, us, dtype=T)
         part = g.gptq_int8_gated(x[:n].contiguous(), xs[:n].contiguous(), w, ws, u, us, dtype=T)
         assert torch.equal(part, whole[:n])
+
+
+@pytest.mark.parametrize("T", TYPES, ids=str)
+@pytest.mark.parametrize("n", [1, 70, 300])
+@pytest.mark.parametrize("act", ACTS)
+def test_gate_values_at_the_ends_of_the_range(act, n, T):
+    # infinite, NaN and huge gates of both signs, times ups of 0, -2 and infinity: as the formula
+    import oracle
+    import post_weight_quantization_19_b200 as g
+    d, inf = 64, float("inf")
+    x = torch.zeros((n, d), dtype=I8, device="cuda")
+    x[:, 0] = 1
+    xs = torch.ones(n, device="cuda")
+    gates = [inf, -inf, float("nan"), 3.4e38, -3.4e38, 2.4e38, 1e38, -1e38, 100.0, -50.0, 0.0, 1.0]
+    ups = [1.0, 0.0, -2.0, inf]
+    r = len(gates) * len(ups)
+    w = torch.zeros((r, d), dtype=I8, device="cuda")
+    w[:, 0] = 1
+    gs = torch.tensor(gates, device="cuda").repeat_interleave(len(ups))
+    us = torch.tensor(ups, device="cuda").repeat(len(gates))
+    y = f64(g.gptq_int8_gated(x, xs, w, gs, w, us, activation=act, dtype=T))
+    with np.errstate(all="ignore"):
+        want = oracle.activation(f64(gs), act) * f64(us)
+        want = np.where(np.abs(want) > float(torch.finfo(T).max), np.sign(want) * np.inf, want)
+    want = np.broadcast_to(want, y.shape)
+    finite = np.isfinite(want)
+    np.testing.assert_array_equal(y[~finite], want[~finite])
+    # act to 1e-6, one product and one rounding; fp16's subnormal numbers are 2^-24 apart, so
+    # the rounding of a value below 2^-14 is off by up to 2^-25 whatever its size
+    tiny = 2.0 ** -25 if T == F16 else 1e-36
+    assert np.all(np.abs(y[finite] - want[finite]) <= (HALF[T] + 1.2e-6) * np.abs(want[finite]) + tiny)
+    assert g.gptq_check_device_status() == 0
 
 
 def moved(t, by):
