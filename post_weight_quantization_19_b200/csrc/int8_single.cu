@@ -30,6 +30,7 @@ constexpr int STAGES = 12;                // at most
 constexpr int SINGLE_THREADS = 32 * 6;
 constexpr size_t SINGLE_SMEM = 208 * 1024;
 constexpr size_t SHARED_SM = 102 * 1024;  // where two CTAs share an SM
+constexpr size_t LEAST_SMEM = 48 * 1024;  // the solve's products hold 185 KB or more
 
 struct SingleArgs {
   Int8Args p;
@@ -188,7 +189,6 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
     for (; ahead < a.stages && k0 + ahead < k1; ++ahead)
       load(m0, n0, k0 + ahead, ring + ahead * stage_bytes, &sh.full[ahead]);
   } else if (warp == 1) {
-    pdl_wait();
     tmem_alloc(&sh.tmem_base, a.columns);
     tmem_relinquish();
   }
@@ -198,8 +198,10 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
-  // (tensor memory is taken when the kernel before is done with it and before the next one
-  // may start: CTAs that wait for it then wait for kernels that do not wait for them)
+  // Tensor memory is there before the next kernel may start, so that its CTAs cannot take it
+  // from one that they wait for.  (Products of the solve, which take it later, leave no CTA
+  // of this kernel room beside them: LEAST_SMEM.  Taken behind the wait: one token x
+  // 4096 x 4096 8.0 us, not 7.3.)
   pdl_wait_then_release();
 
   if (warp == 0) {
@@ -499,6 +501,7 @@ int launch_int8_single(const Int8Args &p, cudaStream_t st) {
   bytes += apart;
   if (bytes < meet) bytes = meet;
   bytes += pad;
+  if (bytes < LEAST_SMEM) bytes = LEAST_SMEM;
   a.buffers = a.ctas_k == 1 && 2 * layers * a.N <= (shape.shared ? 256 : 512) ? 2 : 1;
   a.columns = 32;
   while (a.columns < (uint32_t)(a.buffers * layers * a.N)) a.columns *= 2;

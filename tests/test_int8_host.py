@@ -159,3 +159,20 @@ def test_kernels_read_behind_the_wait_with_ordinary_loads(name):
     assert "__ldg" not in src and "__restrict__" not in src and "ld.global.nc" not in src
     for kernel in re.findall(r"__global__.*?\n}\n", src, flags=re.S):
         assert "pdl_wait_then_release()" in kernel
+
+
+@pytest.mark.parametrize("name", ["int8_single.cu", "int8_pair.cu"])
+def test_products_take_tensor_memory_before_the_next_kernel_may_start(name):
+    # else the next kernel's CTAs could take it first, and wait for this one without end
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                        "post_weight_quantization_19_b200", "csrc")
+    with open(os.path.join(csrc, name), encoding="utf-8") as f:
+        src = re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+    (kernel,) = re.findall(r"__global__.*?\n}\n", src, flags=re.S)
+    release = kernel.index("pdl_wait_then_release()")
+    assert kernel.count("pdl_wait_then_release()") == 1
+    taken = kernel.index("tmem_alloc")
+    met = kernel.index("__syncthreads()" if name == "int8_single.cu" else "cluster_sync()", taken)
+    assert taken < met < release
