@@ -69,10 +69,12 @@ constexpr int STREAM_THREADS = 768;
 constexpr size_t STREAM_SMEM = 224 * 1024;
 constexpr float LEAST_TOP = 1e-22f, MOST_TOP = 1e36f, UP_MOST = 1e6f;
 
-// The value at an index in 64 bits.
-template <typename T, int ACT>
+// The value at an index in 64 bits.  SINGLE: of a row that is safe, and not far below its
+// largest.
+template <typename T, int ACT, bool SINGLE = true>
 __device__ __forceinline__ double value64(const void *x, const void *up, int64_t at) {
-  const double v = activate64<ACT>((double)Half16<T>::one(static_cast<const T *>(x)[at]));
+  const double f = (double)Half16<T>::one(static_cast<const T *>(x)[at]);
+  const double v = SINGLE ? activate64_single<ACT>(f) : activate64<ACT>(f);
   return up ? v * (double)Half16<T>::one(static_cast<const T *>(up)[at]) : v;
 }
 
@@ -236,7 +238,7 @@ __device__ __noinline__ float row_in_64_bits(const ActivationArgs a, int64_t row
   }
 #pragma unroll 1
   for (int k = tid; k < a.d; k += nt) {
-    const double u = fabs(value64<T, ACT>(a.x, a.up, row * a.d + k));
+    const double u = fabs(value64<T, ACT, false>(a.x, a.up, row * a.d + k));
     if (u <= 1.7e308)
       top = fmax(top, u);
     else
@@ -248,7 +250,7 @@ __device__ __noinline__ float row_in_64_bits(const ActivationArgs a, int64_t row
 #pragma unroll 1
   for (int k = tid; k < a.d; k += nt) {
     float code = 0.f;
-    if (!lost && top > 0.0) code = (float)rint(127.0 * value64<T, ACT>(a.x, a.up, row * a.d + k) / top);
+    if (!lost && top > 0.0) code = (float)rint(127.0 * value64<T, ACT, false>(a.x, a.up, row * a.d + k) / top);
     crow[k] = (int8_t)code;   // |code| <= 127
     if (xh) xh[k] = Half16<T>::put(scale * code);
   }
