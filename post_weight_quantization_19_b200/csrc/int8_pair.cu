@@ -221,11 +221,13 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       const int64_t r0 = (int64_t)(t / a.nT) * per_tile;
       // the columns' scales and biases, while the accumulator fills
       for (int c = (warp - 2) * 32 + lane; c < a.N; c += 32 * OUT_WARPS) {
-        const int l = GATED ? c / half : 0;
-        const int64_t row = r0 + (GATED ? c % half : c);
+        const bool second = GATED && c >= half;
+        const float *scales = second ? a.p.w_scales[1] : a.p.w_scales[0];
+        const void *bias = second ? a.p.bias[1] : a.p.bias[0];
+        const int64_t row = r0 + (second ? c - half : c);
         const bool live = row < a.p.r;
-        sh.scale[buf][c] = live ? __ldcg(a.p.w_scales[l] + row) : 0.f;
-        sh.bias[buf][c] = live && a.p.bias[l] ? load_typed(a.p.bias[l], a.p.ytype, row) : 0.f;
+        sh.scale[buf][c] = live ? __ldcg(scales + row) : 0.f;
+        sh.bias[buf][c] = live && bias ? load_typed(bias, a.p.ytype, row) : 0.f;
       }
       const float xs = tok < a.p.n ? __ldcg(a.p.x_scales + tok) : 0.f;
       // (the other accumulator's parameters are still being read by slower warps, this one's
