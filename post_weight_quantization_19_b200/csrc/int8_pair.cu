@@ -40,6 +40,7 @@ struct PairShared {
   uint32_t tmem_base;
   int abort;
   alignas(16) float scale[2][ROWS], bias[2][ROWS];   // of a tile's columns, by accumulator
+  uint32_t stage[OUT_WARPS][32 * 17];                // results of 32 tokens on their way out, per warp
 };
 
 __device__ __forceinline__ void pair_timeout(int *status, PairShared &sh) {
@@ -53,35 +54,50 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
                : "memory");
 }
 
-// 16 results of one token to its row of y, `left` of them in y.
+// 16 results of one token to its row of y, all of them in y, whose rows are multiples of
+// `align` bytes, 16 or 32.
 template <typename Y>
-__device__ __forceinline__ void write16(Y *y, const float (&v)[16], int64_t left, int align) {
-  if (left >= 16 && align >= 16) {
-    constexpr int WORDS = 16 * sizeof(Y) / 4;
-    uint32_t o[WORDS];
+__device__ __forceinline__ void write16(Y *y, const float (&v)[16], int align) {
+  constexpr int WORDS = 16 * sizeof(Y) / 4;
+  uint32_t o[WORDS];
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-      if constexpr (sizeof(Y) == 2)
-        o[i] = to_pair<Y>(v[2 * i], v[2 * i + 1]);
-      else
-        o[i] = __float_as_uint(v[i]);
-    }
-    if (align >= 32) {
+  for (int i = 0; i < WORDS; ++i) {
+    if constexpr (sizeof(Y) == 2)
+      o[i] = to_pair<Y>(v[2 * i], v[2 * i + 1]);
+    else
+      o[i] = __float_as_uint(v[i]);
+  }
+  if (align >= 32) {
 #pragma unroll
-      for (int i = 0; i < WORDS; i += 8) {
-        const uint32_t w[8] = {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6], o[i + 7]};
-        store32(reinterpret_cast<uint32_t *>(y) + i, w);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < WORDS; i += 4)
-        reinterpret_cast<uint4 *>(y)[i / 4] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    for (int i = 0; i < WORDS; i += 8) {
+      const uint32_t w[8] = {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6], o[i + 7]};
+      store32(reinterpret_cast<uint32_t *>(y) + i, w);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < left) y[i] = to_result<Y>(v[i]);
+    for (int i = 0; i < WORDS; i += 4)
+      reinterpret_cast<uint4 *>(y)[i / 4] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
   }
+}
+
+// Results that a thread cannot write by vectors, y's rows not being multiples of 16 bytes or
+// ending: through shared memory, [token][column], so that a store writes 64 bytes of a row
+// and not a column of 32 rows.  393 tokens x 13021x736 12 us, one column at a time 67.
+template <typename Y>
+constexpr int STAGED = 64 / (int)sizeof(Y);   // columns
+template <typename Y>
+constexpr int STAGE_PITCH = STAGED<Y> + 1;
+template <typename Y>
+__device__ __forceinline__ void write_staged(Y *y, const Y *stage, int64_t r, int tokens, int columns, int lane) {
+  __syncwarp();
+  constexpr int EACH = 32 / STAGED<Y>;   // tokens per store
+  const int c = lane % STAGED<Y>, t0 = lane / STAGED<Y>;
+  const Y *src = stage + t0 * STAGE_PITCH<Y> + c;
+  Y *dst = y + t0 * r + c;
+  if (c < columns)
+#pragma unroll 8
+    for (int t = t0; t < tokens; t += EACH, src += EACH * STAGE_PITCH<Y>, dst += EACH * r) *dst = *src;
+  __syncwarp();
 }
 
 template <bool GATED, int ACT, typename Y>
@@ -240,6 +256,10 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         tc_fence_after();
         const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * ROWS;
         Y *y = static_cast<Y *>(a.p.y) + tok * a.p.r + r0;
+        // (the same for the whole warp)
+        const bool vectors = align >= 16 && r0 + per_tile <= a.p.r;
+        const int64_t tokens = a.p.n - (tok - lane);
+        Y *stage = reinterpret_cast<Y *>(sh.stage[warp - 2]);
         for (int c = c_begin; c < c_end; c += 16) {
           float s0[16], s1[16], v[16];   // sums' bits
           tmem_ld_32x32b_x16(acc + c, s0);
@@ -260,7 +280,18 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
               v[i + 1] = r.y;
             }
           }
-          if (tok < a.p.n) write16<Y>(y + c, v, a.p.r - r0 - c, align);
+          if (vectors) {
+            if (tok < a.p.n) write16<Y>(y + c, v, align);
+          } else {
+            const int at = (c - c_begin) % STAGED<Y>;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) stage[lane * STAGE_PITCH<Y> + at + i] = to_result<Y>(v[i]);
+            if (at + 16 == STAGED<Y> || c + 16 >= c_end) {
+              const int64_t left = a.p.r - r0 - (c - at);
+              write_staged<Y>(y - lane * a.p.r + c - at, stage, a.p.r, (int)(tokens < 32 ? tokens : 32),
+                              (int)(left < at + 16 ? left : at + 16), lane);
+            }
+          }
         }
         tc_fence_before();
         __syncwarp();
