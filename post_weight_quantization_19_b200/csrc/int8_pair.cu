@@ -353,7 +353,8 @@ bool int8_pairs_faster(const Int8Args &p, int sms) {
   const int split = int8_split(p, sms);
   if (split == 1) return true;
   // single CTAs that split k: 100 GB/s a CTA, and their sums' way (128 tokens, 4096 x 11008
-  // 16.4 us, pairs 20.4; 256 tokens 21.5, 21.0; 128 tokens, 4096 x 4096 11.5, 10.2)
+  // 16.4 us, pairs 20.4; 256 tokens 21.5, 21.0; 128 tokens, 4096 x 4096 11.5, 10.2; 223
+  // tokens, 645 x 27424 20.0 over 8 CTAs, 29.1 over 4)
   const int64_t slabs = (p.d + SLAB - 1) / SLAB, layers = p.gated ? 2 : 1;
   const double bytes = (double)((slabs + split - 1) / split) * (double)((layers * 128 + p.n) * SLAB);
   int rows;

@@ -438,15 +438,30 @@ namespace {
 //   gated, 1 token, 11008 x 4096   22.9, 25.9, 28.5   16.6, 16.8
 //   16 tokens, 512 x 512     4.0, 3.9, 3.9   3.3, 3.3
 // Gated tiles have twice the bytes, so that one CTA fills an SM's share.
+
+// Clusters of c CTAs that run at once, one or two CTAs to an SM: the SMs of a cluster lie in
+// one part of the chip, whose last few stay empty, so fewer than the SMs would hold; one more
+// is a second round.  Measured: 15 of 8, 33 with two to an SM, 33 of 4 (10 tokens,
+// 4224 x 8192 9.2 us as 33 x 8 CTAs, 4352 x 8192 15.1 as 34 x 8; gated, 10 tokens, 2048 x 8192
+// 17.0 as 16 x 8, 12.1 as 16 x 4).
+int clusters_at_once(int c, int per_sm, int sms) {
+  if (c == 8) return sms * (per_sm == 2 ? 33 : 15) / 148;
+  if (c == 4) return sms * 33 / 148 * per_sm;
+  return sms / 2 * per_sm;
+}
+
 struct Shape {
   int rows, ctas_k;
   bool shared;
 };
 Shape shape_for(int64_t r, int slabs, int N, bool gated, int sms) {
-  const int64_t tiles = (r + ROWS - 1) / ROWS, fit = gated ? sms : 2 * sms;
+  const int64_t tiles = (r + ROWS - 1) / ROWS;
   if (slabs >= 8)
-    for (int c = 8; c >= 2; c /= 2)
-      if (slabs >= 2 * c && tiles * c <= fit && (gated || c > 2)) return Shape{ROWS, c, tiles * c > sms};
+    for (int c = 8; c >= (gated ? 2 : 4); c /= 2) {
+      if (slabs < 2 * c) continue;
+      if (tiles <= clusters_at_once(c, 1, sms)) return Shape{ROWS, c, false};
+      if (!gated && tiles <= clusters_at_once(c, 2, sms)) return Shape{ROWS, c, true};
+    }
   const int64_t parts = gated || N > 48 ? sms : 2 * sms;
   const int64_t rows = (r + 8 * parts - 1) / (8 * parts) * 8;
   const bool shared = !gated && N <= 48 && (r + rows - 1) / rows > sms;
@@ -458,8 +473,8 @@ Shape shape_for(int64_t r, int slabs, int N, bool gated, int sms) {
 int int8_split(const Int8Args &p, int sms) {   // the widest split that finds room, or 1
   const int64_t tiles = (p.r + ROWS - 1) / ROWS;
   const int slabs = (p.d + SLAB - 1) / SLAB, layers = p.gated ? 2 : 1;
-  for (int c = 4; c >= 2; c /= 2)
-    if (tiles * c <= sms && slabs >= 2 * c && p.n <= TOKENS / layers) return c;
+  for (int c = 8; c >= 2; c /= 2)
+    if (tiles <= clusters_at_once(c, 1, sms) && slabs >= 2 * c && p.n <= TOKENS / layers) return c;
   return 1;
 }
 
