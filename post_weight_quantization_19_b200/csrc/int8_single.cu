@@ -436,7 +436,7 @@ namespace {
 //   gated, 24 tokens, 4096 x 4096  13.1, 10.4, 12.2
 //   gated, 16 tokens, 5120 x 5120  15.4, 15.5, 19.5   15.4, 19.7   (40 tiles)
 //   gated, 1 token, 11008 x 4096   22.9, 25.9, 28.5   16.6, 16.8
-//   16 tokens, 512 x 512     4.0, 3.9, 3.9   3.3, 3.3
+//   16 tokens, 512 x 512     4.0, 3.9, 3.9   3.3, 3.3   (2.7 with stages no deeper than d)
 // Gated tiles have twice the bytes, so that one CTA fills an SM's share.
 
 // Clusters of c CTAs that run at once, one or two CTAs to an SM: the SMs of a cluster lie in
@@ -500,6 +500,7 @@ int launch_int8_single(const Int8Args &p, cudaStream_t st) {
   a.deep = ROWS / a.rows;
   while (a.deep > 1 && a.deep * slab * 4 > room) --a.deep;
   const int steps = (slabs + a.deep - 1) / a.deep;
+  a.deep = (slabs + steps - 1) / steps;   // slabs past d would be loaded and multiplied as zeros
   const size_t stage = slab * a.deep;
   // a tile of fewer rows reads up to 128 rows of the last stage
   const size_t pad = (size_t)(ROWS - a.rows) * SLAB;
