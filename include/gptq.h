@@ -598,6 +598,24 @@ int gptq_last_phase_ms(float *ms, int n);
 int gptq_selftest_timeout(float *buf, gptq_stream_t stream);
 
 /*
+ * gptq_selftest_int8_timeout -- the same check of the kernels of gptq_int8_linear: the
+ * product with fp32 results in which some of the kernel's threads take one of their waits
+ * for run out, as they would where it had lasted a second.  The others go on; the
+ * kernel records GPTQ_ERR_TIMEOUT in the device status word, waits (bounded) for what it
+ * has in flight and returns.  Nothing faults and the context stays usable; y is lost, and
+ * gptq_check_device_status(stream) afterwards returns GPTQ_ERR_TIMEOUT once.
+ *
+ *   what  GPTQ_GIVE_UP_WARP: in each CTA with several tiles, one warp of those that write
+ *         results, at the last tile but one.
+ *   Other arguments and conditions as gptq_int8_linear, ytype GPTQ_F32.  A product
+ *   without such a wait (one tile to a CTA, say) is computed and reports nothing.
+ */
+#define GPTQ_GIVE_UP_WARP 1
+int gptq_selftest_int8_timeout(const int8_t *x, const float *x_scales, int64_t n, const int8_t *w,
+                               const float *w_scales, int64_t r, int64_t d, int what, float *y,
+                               gptq_stream_t stream);
+
+/*
  * gptq_gemm_pair_form -- which launch form the library's two-CTA tensor-core
  * product (the trailing updates and the factorisation's products with two or
  * more 128-row tiles) runs in on the current device; a diagnostic with no page

@@ -20,7 +20,14 @@ struct Int8Args {
   int64_t n, r;
   int d, ytype, activation;
   bool gated;
+  int give_up = 0;            // self-test only: GPTQ_GIVE_UP_* (gptq_selftest_int8_timeout)
 };
+
+// Self-test: whether a warp that writes results takes its wait for this tile, the last but
+// one of its CTA, for run out: the first such warp of a CTA does.
+__device__ __forceinline__ bool gives_up(const Int8Args &p, int warp, int tile, int step, int tiles) {
+  return p.give_up == GPTQ_GIVE_UP_WARP && warp == 2 && tile + step < tiles && tile + 2 * step >= tiles;
+}
 
 constexpr int FEW_TOKENS = 64;
 // Weights as the MMA's rows: any number of tokens, k split over clusters when tiles are few.

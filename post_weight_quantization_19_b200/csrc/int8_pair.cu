@@ -232,7 +232,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     const int align = base % 32 == 0 ? 32 : base % 16 == 0 ? 16 : 1;
     uint32_t buf = 0, cphase = 0;
     bool ok = true;
-    for (int t = pair; t < tiles && ok; t += pairs) {
+    // (a warp that gave up still walks the tiles: the others wait for it at their barrier)
+    for (int t = pair; t < tiles; t += pairs) {
       const int64_t tok = (int64_t)(t % a.nT) * (2 * TOKENS) + rank * TOKENS + quarter * 32 + lane;
       const int64_t r0 = (int64_t)(t / a.nT) * per_tile;
       // the columns' scales and biases, while the accumulator fills
@@ -249,7 +250,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       // (the other accumulator's parameters are still being read by slower warps, this one's
       // were read before the barrier of the tile between)
       asm volatile("bar.sync 1, %0;" ::"n"(32 * OUT_WARPS) : "memory");
-      ok = mbar_wait_bounded(&sh.acc_full[buf], (cphase >> buf) & 1u);
+      if (gives_up(a.p, warp, t, pairs, tiles)) ok = false;
+      ok = ok && mbar_wait_bounded(&sh.acc_full[buf], (cphase >> buf) & 1u);
       if (!ok && lane == 0) pair_timeout(a.status, sh);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
