@@ -360,6 +360,8 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
         }
       }
     }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // this CTA's sums are on their way
     // what the results need, while the sums arrive: a thread keeps to one row
     const int64_t m0 = (int64_t)(cta % a.nM) * a.rows + crank * owned, t0 = (int64_t)(cta / a.nM) * N;
     const int64_t row = m0 + threadIdx.x % owned;   // SINGLE_THREADS % owned == 0
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
     for (int c = threadIdx.x; c < fours * 4; c += SINGLE_THREADS)
       xs[c] = t0 + c < a.p.n ? __ldcg(a.p.x_scales + t0 + c) : 0.f;
     // (a CTA that gave up pushed its sums all the same, whatever they are)
-    if (!mbar_wait_bounded(&sh.sums, 0)) single_timeout(a.status, sh);
+    if ((a.p.give_up == GPTQ_GIVE_UP_SUMS && crank == 0) || !mbar_wait_bounded(&sh.sums, 0)) single_timeout(a.status, sh);
     __syncthreads();
     if (!*(volatile int *)&sh.abort) {
       Y *y = static_cast<Y *>(a.p.y) + row;
@@ -393,6 +395,11 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
           if (tok + q < a.p.n) y[(tok + q) * a.p.r] = to_result<Y>(f[q]);
       }
     }
+    // No CTA's memory goes while sums may be on their way to it: one that gave up waits until
+    // every CTA has sent its own, and then for them to land.
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (*(volatile int *)&sh.abort) (void)mbar_wait_bounded(&sh.sums, 0);
   }
   tc_fence_before();
   __syncthreads();

@@ -14,7 +14,7 @@ from test_gpu_int8 import F32, assert_close, codes8, layer8, product
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-WARP = 1
+WARP, SUMS = 1, 2
 TIMEOUT = 5
 
 # (n, r, d), several tiles to a CTA: single CTAs, pairs, pairs with the tokens' last tile ragged
@@ -50,6 +50,20 @@ def test_a_warp_that_gives_up_leaves_no_other_waiting(lib, shape):
     assert int(written.sum()) < int((whole != 0).sum())
 
 
+# columns split over 4 and 8 CTAs, their sums beside the ring of stages (up to 32 tokens) and in it
+@pytest.mark.parametrize("shape", [(1, 300, 4096), (20, 3000, 4096), (10, 4608, 16384), (64, 300, 8192), (256, 130, 16384)],
+                         ids="n{0[0]}_r{0[1]}_d{0[2]}".format)
+def test_a_cta_that_gives_up_on_sums_stays_until_they_landed(lib, shape):
+    # (the others push their sums to its memory, which must not have gone)
+    for _ in range(5):
+        status, y, whole = give_up(lib, shape, SUMS)
+        assert status == TIMEOUT
+        written = y != 0
+        assert bool(written.any()) and torch.equal(y[written], whole[written])
+        assert int(written.sum()) < int((whole != 0).sum())
+
+
 def test_a_product_without_such_a_wait_is_computed(lib):
-    status, y, whole = give_up(lib, (3, 64, 96), WARP)
-    assert status == 0 and torch.equal(y, whole)
+    for what in (WARP, SUMS):
+        status, y, whole = give_up(lib, (3, 64, 96), what)
+        assert status == 0 and torch.equal(y, whole)
