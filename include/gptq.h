@@ -606,14 +606,15 @@ int gptq_selftest_timeout(float *buf, gptq_stream_t stream);
  * gptq_check_device_status(stream) afterwards returns GPTQ_ERR_TIMEOUT once.
  *
  *   what  GPTQ_GIVE_UP_WARP: in each CTA with several tiles, one warp of those that write
- *         results, at the last tile but one.  GPTQ_GIVE_UP_SUMS: where the columns are
- *         split over CTAs, the first of them, which then has the others' sums of its rows still
- *         coming.
+ *         results, at the last tile but one;  GPTQ_GIVE_UP_THREAD: one thread of that warp.
+ *         GPTQ_GIVE_UP_SUMS: where the columns are split over CTAs, the first of them, which
+ *         then has the others' sums of its rows still coming.
  *   Other arguments and conditions as gptq_int8_linear, ytype GPTQ_F32.  A product
  *   without such a wait (one tile to a CTA, say) is computed and reports nothing.
  */
 #define GPTQ_GIVE_UP_WARP 1
 #define GPTQ_GIVE_UP_SUMS 2
+#define GPTQ_GIVE_UP_THREAD 3
 int gptq_selftest_int8_timeout(const int8_t *x, const float *x_scales, int64_t n, const int8_t *w,
                                const float *w_scales, int64_t r, int64_t d, int what, float *y,
                                gptq_stream_t stream);

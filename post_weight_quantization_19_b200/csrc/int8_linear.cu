@@ -104,7 +104,7 @@ extern "C" int gptq_int8_gated(const int8_t *x, const float *x_scales, int64_t n
 extern "C" int gptq_selftest_int8_timeout(const int8_t *x, const float *x_scales, int64_t n, const int8_t *w,
                                           const float *w_scales, int64_t r, int64_t d, int what, float *y,
                                           gptq_stream_t stream) {
-  if (what != GPTQ_GIVE_UP_WARP && what != GPTQ_GIVE_UP_SUMS) return GPTQ_ERR_INVALID_ARG;
+  if (what < GPTQ_GIVE_UP_WARP || what > GPTQ_GIVE_UP_THREAD) return GPTQ_ERR_INVALID_ARG;
   Int8Args a{x, x_scales, {w, nullptr}, {w_scales, nullptr}, {nullptr, nullptr}, y, n, r, (int)d, GPTQ_F32,
              GPTQ_ACT_NONE, false};
   a.give_up = what;

@@ -23,10 +23,11 @@ struct Int8Args {
   int give_up = 0;            // self-test only: GPTQ_GIVE_UP_* (gptq_selftest_int8_timeout)
 };
 
-// Self-test: whether a warp that writes results takes its wait for this tile, the last but
-// one of its CTA, for run out: the first such warp of a CTA does.
-__device__ __forceinline__ bool gives_up(const Int8Args &p, int warp, int tile, int step, int tiles) {
-  return p.give_up == GPTQ_GIVE_UP_WARP && warp == 2 && tile + step < tiles && tile + 2 * step >= tiles;
+// Self-test: whether a thread that writes results takes its wait for this tile, the last but
+// one of its CTA, for run out: those of the CTA's first such warp do, or its last lane alone.
+__device__ __forceinline__ bool gives_up(const Int8Args &p, int warp, int lane, int tile, int step, int tiles) {
+  return (p.give_up == GPTQ_GIVE_UP_WARP || (p.give_up == GPTQ_GIVE_UP_THREAD && lane == 31)) && warp == 2 &&
+         tile + step < tiles && tile + 2 * step >= tiles;
 }
 
 constexpr int FEW_TOKENS = 64;

@@ -250,10 +250,10 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       // (the other accumulator's parameters are still being read by slower warps, this one's
       // were read before the barrier of the tile between)
       asm volatile("bar.sync 1, %0;" ::"n"(32 * OUT_WARPS) : "memory");
-      if (gives_up(a.p, warp, t, pairs, tiles)) ok = false;
+      if (gives_up(a.p, warp, lane, t, pairs, tiles)) ok = false;
       ok = ok && mbar_wait_bounded(&sh.acc_full[buf], (cphase >> buf) & 1u);
+      ok = __all_sync(0xffffffffu, ok);   // (one lane's wait may run out alone)
       if (!ok && lane == 0) pair_timeout(a.status, sh);
-      ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         tc_fence_after();
         const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * ROWS;

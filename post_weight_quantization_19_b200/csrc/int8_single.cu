@@ -291,10 +291,10 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
       __syncwarp();
       for (int c = lane; c < N; c += 32) sh.xs[quarter][c] = c < count ? __ldcg(a.p.x_scales + t0 + c) : 0.f;
       __syncwarp();
-      if (gives_up(a.p, warp, t, ctas, tiles)) ok = false;
+      if (gives_up(a.p, warp, lane, t, ctas, tiles)) ok = false;
       ok = ok && mbar_wait_bounded(&sh.acc_full[buf], (cphase >> buf) & 1u);
+      ok = __all_sync(0xffffffffu, ok);   // (one lane's wait may run out alone)
       if (!ok && lane == 0) single_timeout(a.status, sh);
-      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + buf * acc_columns;

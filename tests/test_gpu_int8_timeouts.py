@@ -14,7 +14,7 @@ from test_gpu_int8 import F32, assert_close, codes8, layer8, product
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-WARP, SUMS = 1, 2
+WARP, SUMS, THREAD = 1, 2, 3
 TIMEOUT = 5
 
 # (n, r, d), several tiles to a CTA: single CTAs, pairs, pairs with the tokens' last tile ragged
@@ -50,6 +50,14 @@ def test_a_warp_that_gives_up_leaves_no_other_waiting(lib, shape):
     assert int(written.sum()) < int((whole != 0).sum())
 
 
+@pytest.mark.parametrize("shape", MANY_TILES, ids=IDS)
+def test_a_thread_that_gives_up_alone_is_reported(lib, shape):
+    # its warp writes nothing then, and the caller has to hear of it
+    status, y, whole = give_up(lib, shape, THREAD)
+    assert int((y != 0).sum()) < int((whole != 0).sum())
+    assert status == TIMEOUT
+
+
 # columns split over 4 and 8 CTAs, their sums beside the ring of stages (up to 32 tokens) and in it
 @pytest.mark.parametrize("shape", [(1, 300, 4096), (20, 3000, 4096), (10, 4608, 16384), (64, 300, 8192), (256, 130, 16384)],
                          ids="n{0[0]}_r{0[1]}_d{0[2]}".format)
@@ -64,6 +72,6 @@ def test_a_cta_that_gives_up_on_sums_stays_until_they_landed(lib, shape):
 
 
 def test_a_product_without_such_a_wait_is_computed(lib):
-    for what in (WARP, SUMS):
+    for what in (WARP, SUMS, THREAD):
         status, y, whole = give_up(lib, (3, 64, 96), what)
         assert status == 0 and torch.equal(y, whole)

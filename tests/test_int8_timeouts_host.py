@@ -8,7 +8,7 @@ def give_up(lib, x=X, xs=XS, n=4, w=W, ws=WS, r=8, d=128, what=1, y=Y):
 
 
 def test_selftest_refusals(lib):
-    for bad in (dict(what=0), dict(what=-1), dict(what=3), dict(x=None), dict(xs=None), dict(w=None), dict(ws=None),
+    for bad in (dict(what=0), dict(what=-1), dict(what=4), dict(x=None), dict(xs=None), dict(w=None), dict(ws=None),
                 dict(y=None), dict(n=-1), dict(r=-1), dict(d=100), dict(d=0), dict(y=X), dict(y=WS)):
         assert give_up(lib, **bad) == 1, bad
     assert give_up(lib, n=0) == 0 and give_up(lib, r=0) == 0
