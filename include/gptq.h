@@ -620,6 +620,20 @@ int gptq_selftest_int8_timeout(const int8_t *x, const float *x_scales, int64_t n
                                gptq_stream_t stream);
 
 /*
+ * gptq_int8_plan -- a host-only diagnostic of gptq_int8_linear (gated 0) and gptq_int8_gated
+ * (else): how they would launch n x r x d on a device of `sms` SMs, without touching one.
+ *
+ *   plan  int64 [8], written: 0 for single CTAs with the weights as the tensor-core product's rows,
+ *         1 for pairs with the tokens as rows;  CTAs;  CTAs of a cluster (single CTAs: those
+ *         that the columns are split over);  tokens of a tile;  rows of a layer of a tile;
+ *         stages of shared memory;  columns of tensor memory per CTA;  bytes of shared
+ *         memory per CTA.
+ * Returns GPTQ_OK, or GPTQ_ERR_INVALID_ARG for sizes that those refuse, n, r or plan of 0, or
+ * sms < 2.
+ */
+int gptq_int8_plan(int64_t n, int64_t r, int64_t d, int gated, int sms, int64_t *plan);
+
+/*
  * gptq_gemm_pair_form -- which launch form the library's two-CTA tensor-core
  * product (the trailing updates and the factorisation's products with two or
  * more 128-row tiles) runs in on the current device; a diagnostic with no page

@@ -35,12 +35,18 @@ EncodeTiledFn encode_fn() {
 
 bool misaligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
-// Checks and launches; layers: 1, or 2 of a gated block.
-int int8_product(const Int8Args &a, int layers, int64_t d, cudaStream_t st) {
+bool valid_sizes(int64_t n, int64_t r, int64_t d) {
   // (the last tile's coordinates, too, are 32-bit)
   constexpr int64_t MOST = (int64_t)INT32_MAX - 512;
-  if (a.n < 0 || a.n > MOST || a.r < 0 || a.r > MOST) return GPTQ_ERR_INVALID_ARG;
-  if (d <= 0 || d % 32 != 0 || d > 65536) return GPTQ_ERR_INVALID_ARG;
+  return n >= 0 && n <= MOST && r >= 0 && r <= MOST && d > 0 && d % 32 == 0 && d <= 65536;
+}
+
+// up to 64 tokens W's bytes are the bound; more, its products or x's bytes
+bool by_pairs(const Int8Args &a, int sms) { return a.n > FEW_TOKENS && int8_pairs_faster(a, sms); }
+
+// Checks and launches; layers: 1, or 2 of a gated block.
+int int8_product(const Int8Args &a, int layers, int64_t d, cudaStream_t st) {
+  if (!valid_sizes(a.n, a.r, d)) return GPTQ_ERR_INVALID_ARG;
   if (a.ytype != GPTQ_F16 && a.ytype != GPTQ_BF16 && a.ytype != GPTQ_F32) return GPTQ_ERR_INVALID_ARG;
   if (a.n == 0 || a.r == 0) return GPTQ_OK;
   const size_t ysize = a.ytype == GPTQ_F32 ? 4 : 2;
@@ -57,9 +63,7 @@ int int8_product(const Int8Args &a, int layers, int64_t d, cudaStream_t st) {
                           Span{a.bias[k], (size_t)a.r * ysize}})
       if (overlap(out, s)) return GPTQ_ERR_INVALID_ARG;
   }
-  // up to 64 tokens W's bytes are the bound; more, its products or x's bytes
-  if (a.n > FEW_TOKENS && int8_pairs_faster(a, num_sms())) return launch_int8_pair(a, st);
-  return launch_int8_single(a, st);
+  return by_pairs(a, num_sms()) ? launch_int8_pair(a, st) : launch_int8_single(a, st);
 }
 
 }  // namespace
@@ -109,4 +113,18 @@ extern "C" int gptq_selftest_int8_timeout(const int8_t *x, const float *x_scales
              GPTQ_ACT_NONE, false};
   a.give_up = what;
   return int8_product(a, 1, d, (cudaStream_t)stream);
+}
+
+extern "C" int gptq_int8_plan(int64_t n, int64_t r, int64_t d, int gated, int sms, int64_t *plan) {
+  if (!valid_sizes(n, r, d) || n == 0 || r == 0 || sms < 2 || !plan) return GPTQ_ERR_INVALID_ARG;
+  Int8Args a{};
+  a.n = n;
+  a.r = r;
+  a.d = (int)d;
+  a.gated = gated != 0;
+  Int8Plan p;
+  if (const int rc = by_pairs(a, sms) ? int8_pair_plan(a, sms, p) : int8_single_plan(a, sms, p)) return rc;
+  const int64_t v[] = {p.pairs, p.ctas, p.cluster, p.tokens, p.rows, p.stages, p.columns, (int64_t)p.smem};
+  for (int i = 0; i < 8; ++i) plan[i] = v[i];
+  return GPTQ_OK;
 }

@@ -30,13 +30,25 @@ __device__ __forceinline__ bool gives_up(const Int8Args &p, int warp, int lane, 
          tile + step < tiles && tile + 2 * step >= tiles;
 }
 
+// How a product is launched.
+struct Int8Plan {
+  bool pairs;
+  int ctas, cluster;          // CTAs, and of a cluster
+  int tokens, rows, stages;   // per tile, rows of each layer; stages of shared memory
+  int columns;                // of tensor memory, per CTA
+  size_t smem;                // per CTA
+};
+
 constexpr int FEW_TOKENS = 64;
-// Weights as the MMA's rows: any number of tokens, k split over clusters when tiles are few.
+// Weights as the MMA's rows: up to FEW_TOKENS, and where int8_split is not 1; k split over
+// clusters when tiles are few.  Other products: GPTQ_ERR_INVALID_ARG.
 int launch_int8_single(const Int8Args &a, cudaStream_t st);
+int int8_single_plan(const Int8Args &a, int sms, Int8Plan &plan);
 // For more than FEW_TOKENS: the CTAs that it would split k over.
 int int8_split(const Int8Args &a, int sms);
 // Many tokens: pairs of CTAs, tokens as the MMA's rows.
 int launch_int8_pair(const Int8Args &a, cudaStream_t st);
+int int8_pair_plan(const Int8Args &a, int sms, Int8Plan &plan);
 bool int8_pairs_faster(const Int8Args &a, int sms);
 
 // A sum with its token's and row's scales, and the bias.

@@ -363,10 +363,9 @@ bool int8_pairs_faster(const Int8Args &p, int sms) {
   return pair_rows(p, sms / 2, &rows) <= 7.0 + 0.0156 * layers * p.n + bytes * 1e-5;
 }
 
-int launch_int8_pair(const Int8Args &p, cudaStream_t st) {
-  PairArgs a{};
+static int pair_plan(const Int8Args &p, int sms, PairArgs &a, unsigned &ctas) {
   a.p = p;
-  const int pairs = num_sms() / 2;
+  const int pairs = sms / 2;
   (void)pair_rows(p, pairs, &a.N);
   const int per_tile = p.gated ? a.N / 2 : a.N;
   a.stages = (int)(PAIR_SMEM / (X_BYTES + a.N / 2 * SLAB));
@@ -375,6 +374,23 @@ int launch_int8_pair(const Int8Args &p, cudaStream_t st) {
   if (nT * nR > INT32_MAX / 8) return GPTQ_ERR_INVALID_ARG;
   a.nT = (int)nT;
   a.nR = (int)nR;
+  ctas = 2 * (unsigned)(nT * nR < pairs ? nT * nR : pairs);
+  return GPTQ_OK;
+}
+
+int int8_pair_plan(const Int8Args &p, int sms, Int8Plan &plan) {
+  PairArgs a{};
+  unsigned ctas;
+  if (const int rc = pair_plan(p, sms, a, ctas)) return rc;
+  plan = Int8Plan{true, (int)ctas, 2, 2 * TOKENS, p.gated ? a.N / 2 : a.N, a.stages, 512,
+                  PAIR_SMEM + 1024 + sizeof(PairShared)};
+  return GPTQ_OK;
+}
+
+int launch_int8_pair(const Int8Args &p, cudaStream_t st) {
+  PairArgs a{};
+  unsigned ctas;
+  if (const int rc = pair_plan(p, num_sms(), a, ctas)) return rc;
   a.status = device_status_word();
   if (!a.status) return GPTQ_ERR_CUDA;
   CUtensorMap tx, tw, tu;
@@ -383,7 +399,6 @@ int launch_int8_pair(const Int8Args &p, cudaStream_t st) {
   tu = tw;
   if (p.gated)
     if (const int rc = int8_map(&tu, p.w[1], p.r, p.d, a.N / 2)) return rc;
-  const unsigned ctas = 2 * (unsigned)(nT * nR < pairs ? nT * nR : pairs);
   if (!p.gated) return launch_act<false, GPTQ_ACT_NONE>(a, tx, tw, tu, ctas, st);
   switch (p.activation) {
     case GPTQ_ACT_NONE: return launch_act<true, GPTQ_ACT_NONE>(a, tx, tw, tu, ctas, st);

@@ -1,10 +1,10 @@
-// gptq_int8_linear and gptq_int8_gated, weights as the rows of the tensor-core product:
-// any number of tokens, and the kernel for up to a few hundred of them.
+// gptq_int8_linear and gptq_int8_gated, weights as the rows of the tensor-core product: up to
+// 64 tokens, and up to 256 (gated: 128) where k is split.
 //
 //   y[t, i] = xs[t] ws[i] sum_j x[t, j] w[i, j] + bias[i]
 //   gated:  y = act(the gate's) * (the up projection's)
 //
-// One CTA per tile of 128 rows of W and N <= 256 tokens; a gated tile has the 128
+// One CTA per tile of 128 rows of W and all N <= 256 tokens; a gated tile has the 128
 // rows of both layers, each with its sums in its own columns of tensor memory, so that a
 // thread ends up with both projections of a row and writes their product alone.
 // TMA brings slabs of 128 columns of W and x to 128-byte-swizzled shared memory, one
@@ -25,7 +25,7 @@ namespace {
 
 constexpr int ROWS = 128;                 // rows of W per tile (UMMA M)
 constexpr int SLAB = 128;                 // columns per stage
-constexpr int TOKENS = 256;               // most tokens per tile (UMMA N)
+constexpr int TOKENS = 256;               // most tokens (UMMA N), of both layers' sums together
 constexpr int STAGES = 12;                // at most
 constexpr int SINGLE_THREADS = 32 * 6;
 constexpr size_t SINGLE_SMEM = 208 * 1024;
@@ -34,14 +34,13 @@ constexpr size_t LEAST_SMEM = 48 * 1024;  // the solve's products hold 185 KB or
 
 struct SingleArgs {
   Int8Args p;
-  int N;              // tokens per tile, a multiple of 16
+  int N;              // tokens, rounded up to a multiple of 16
   int rows;           // of W per tile, a multiple of 8
   int deep;           // slabs per stage
-  int nM, nN;         // tiles
+  int tiles;
   int ctas_k;         // CTAs of a cluster, along k
   int stages;
-  uint32_t columns;   // of tensor memory
-  int buffers;        // accumulators, 1 or 2
+  uint32_t columns;   // of tensor memory: two accumulators, with k split one
   int slots;          // split k: where the CTAs' sums meet, an offset in shared memory; 0: in the ring
   int *status;
 };
@@ -97,7 +96,7 @@ __device__ __forceinline__ F2 results(int a0, int a1, int b0, int b1, float x0, 
 // row.  16-bit results go through shared memory and out 16 bytes, eight rows of a token,
 // per lane, where y's rows allow it.
 template <typename Y>
-__device__ __forceinline__ void write_tokens(const float (&v)[16], int count, int64_t t0, int64_t row0, int live,
+__device__ __forceinline__ void write_tokens(const float (&v)[16], int count, int t0, int64_t row0, int live,
                                              const Int8Args &p, uint16_t *stage, int lane) {
   Y *y = static_cast<Y *>(p.y);
   bool wide = false;
@@ -113,13 +112,13 @@ __device__ __forceinline__ void write_tokens(const float (&v)[16], int count, in
         const int tok = h * 8 + (lane >> 2);
         const uint4 o = reinterpret_cast<const uint4 *>(stage)[h * 32 + lane];
         if (tok < count && (lane & 3) * 8 < live)   // live: a multiple of 8
-          *reinterpret_cast<uint4 *>(y + (t0 + tok) * p.r + row0 + (lane & 3) * 8) = o;
+          *reinterpret_cast<uint4 *>(y + (int64_t)(t0 + tok) * p.r + row0 + (lane & 3) * 8) = o;
       }
     }
   } else if (lane < live) {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (i < count) y[(t0 + i) * p.r + row0 + lane] = to_result<Y>(v[i]);
+      if (i < count) y[(int64_t)(t0 + i) * p.r + row0 + lane] = to_result<Y>(v[i]);
   }
 }
 
@@ -136,18 +135,17 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
   const int N = a.N, w_bytes = a.rows * SLAB, x_at = a.deep * LAYERS * w_bytes;
   const int stage_bytes = x_at + a.deep * N * SLAB;
   const int crank = blockIdx.x % a.ctas_k, ctas = gridDim.x / a.ctas_k, cta = blockIdx.x / a.ctas_k;
-  const int tiles = a.nM * a.nN;
+  const int tiles = a.tiles;
   const int steps = (a.p.d + SLAB * a.deep - 1) / (SLAB * a.deep);
   const int k0 = (int)((int64_t)steps * crank / a.ctas_k);
   const int k1 = (int)((int64_t)steps * (crank + 1) / a.ctas_k);
   const uint32_t acc_columns = LAYERS * N;
 
-  // the tokens of a split tile that exist, in fours
-  const int fours = a.ctas_k > 1 ? (int)((min((int64_t)N, a.p.n - (int64_t)(cta / a.nM) * N) + 3) / 4) : 0;
+  const int n = (int)a.p.n, fours = (n + 3) / 4;   // tokens, in fours
   const int owned = a.rows / a.ctas_k;   // rows
   // (what a load takes is kept ready: one thread issues them all, and divisions in its loop
   // cost 800 clocks a step, more than the step's data)
-  auto load = [&](int m0, int n0, int k, uint32_t dst, uint64_t *bar) {
+  auto load = [&](int m0, int k, uint32_t dst, uint64_t *bar) {
     mbar_arrive_expect_tx(bar, stage_bytes);
     // columns from multiples of 128 bytes (past d, r and n: zeros)
     int col = k * (a.deep * SLAB);
@@ -159,7 +157,7 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
         load_2d(dst, &tmU, col, m0, bar);
         dst += w_bytes;
       }
-      load_2d(x, &tmX, col, n0, bar);
+      load_2d(x, &tmX, col, 0, bar);
     }
   };
   const uint32_t ring = smem_u32(smem);
@@ -181,13 +179,12 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
     if (a.ctas_k > 1) mbar_arrive_expect_tx(&sh.sums, (a.ctas_k - 1) * LAYERS * fours * owned * 16);
     for (int k = k0; k < k1 && k < k0 + a.stages; ++k)   // (into L2, whoever wrote them)
       for (int j = 0; j < a.deep; ++j) {
-        prefetch_2d(&tmW, (k * a.deep + j) * SLAB, cta % a.nM * a.rows);
-        if constexpr (GATED) prefetch_2d(&tmU, (k * a.deep + j) * SLAB, cta % a.nM * a.rows);
+        prefetch_2d(&tmW, (k * a.deep + j) * SLAB, cta * a.rows);
+        if constexpr (GATED) prefetch_2d(&tmU, (k * a.deep + j) * SLAB, cta * a.rows);
       }
     pdl_wait();
-    const int m0 = cta % a.nM * a.rows, n0 = cta / a.nM * N;
     for (; ahead < a.stages && k0 + ahead < k1; ++ahead)
-      load(m0, n0, k0 + ahead, ring + ahead * stage_bytes, &sh.full[ahead]);
+      load(cta * a.rows, k0 + ahead, ring + ahead * stage_bytes, &sh.full[ahead]);
   } else if (warp == 1) {
     tmem_alloc(&sh.tmem_base, a.columns);
     tmem_relinquish();
@@ -211,14 +208,13 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
       uint32_t phase = ahead == a.stages ? 1 : 0;
       bool ok = true, full = phase != 0;   // full: every stage has been asked for
       for (int t = cta; t < tiles && ok; t += ctas) {
-        const int m0 = t % a.nM * a.rows, n0 = t / a.nM * N;
         for (int k = t == cta ? k0 + ahead : k0; k < k1; ++k) {
           ok = wait_or_abort(&sh.empty[stage], phase ^ 1, &sh.abort);
           if (!ok) {
             single_timeout(a.status, sh);
             break;
           }
-          load(m0, n0, k, ring + stage * stage_bytes, &sh.full[stage]);
+          load(t * a.rows, k, ring + stage * stage_bytes, &sh.full[stage]);
           if (++stage == a.stages) {
             stage = 0;
             phase ^= 1;
@@ -268,7 +264,7 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
         }
       }
       cphase ^= 1u << buf;
-      if (a.buffers == 2) buf ^= 1;
+      buf ^= 1;
     }
     if (!ok && lane == 0) single_timeout(a.status, sh);
     __syncwarp();
@@ -283,13 +279,12 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
     uint32_t buf = 0, cphase = 0;
     bool ok = true;
     for (int t = cta; t < tiles && ok; t += ctas) {
-      const int64_t row0 = (int64_t)(t % a.nM) * a.rows + quarter * 32, t0 = (int64_t)(t / a.nM) * N;
+      const int64_t row0 = (int64_t)t * a.rows + quarter * 32;
       const int64_t left = min((int64_t)a.rows - quarter * 32, a.p.r - row0);
       const int live = left < 0 ? 0 : left < 32 ? (int)left : 32;
-      const int count = (int)(a.p.n - t0 < N ? a.p.n - t0 : N);
       const Row par = row_of<GATED>(a.p, row0 + lane);
       __syncwarp();
-      for (int c = lane; c < N; c += 32) sh.xs[quarter][c] = c < count ? __ldcg(a.p.x_scales + t0 + c) : 0.f;
+      for (int c = lane; c < N; c += 32) sh.xs[quarter][c] = c < n ? __ldcg(a.p.x_scales + c) : 0.f;
       __syncwarp();
       if (gives_up(a.p, warp, lane, t, ctas, tiles)) ok = false;
       ok = ok && mbar_wait_bounded(&sh.acc_full[buf], (cphase >> buf) & 1u);
@@ -298,7 +293,7 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + buf * acc_columns;
-      for (int c0 = 0; c0 < count && live > 0; c0 += 16) {
+      for (int c0 = 0; c0 < n && live > 0; c0 += 16) {
         float s0[16], s1[16];   // sums' bits
         tmem_ld_32x32b_x16(base + c0, s0);
         if constexpr (GATED) tmem_ld_32x32b_x16(base + N + c0, s1);
@@ -312,13 +307,13 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
           v[i] = f.x;
           v[i + 1] = f.y;
         }
-        write_tokens<Y>(v, count - c0, t0 + c0, row0, live, a.p, sh.stage[quarter], lane);
+        write_tokens<Y>(v, n - c0, c0, row0, live, a.p, sh.stage[quarter], lane);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
       cphase ^= 1u << buf;
-      if (a.buffers == 2) buf ^= 1;
+      buf ^= 1;
     }
   }
 
@@ -363,20 +358,19 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // this CTA's sums are on their way
     // what the results need, while the sums arrive: a thread keeps to one row
-    const int64_t m0 = (int64_t)(cta % a.nM) * a.rows + crank * owned, t0 = (int64_t)(cta / a.nM) * N;
-    const int64_t row = m0 + threadIdx.x % owned;   // SINGLE_THREADS % owned == 0
+    const int64_t row = (int64_t)cta * a.rows + crank * owned + threadIdx.x % owned;   // SINGLE_THREADS % owned == 0
     const Row par = row_of<GATED>(a.p, row);
     float *xs = sh.xs[0];
     for (int c = threadIdx.x; c < fours * 4; c += SINGLE_THREADS)
-      xs[c] = t0 + c < a.p.n ? __ldcg(a.p.x_scales + t0 + c) : 0.f;
+      xs[c] = c < n ? __ldcg(a.p.x_scales + c) : 0.f;
     // (a CTA that gave up pushed its sums all the same, whatever they are)
     if ((a.p.give_up == GPTQ_GIVE_UP_SUMS && crank == 0) || !mbar_wait_bounded(&sh.sums, 0)) single_timeout(a.status, sh);
     __syncthreads();
     if (!*(volatile int *)&sh.abort) {
       Y *y = static_cast<Y *>(a.p.y) + row;
       for (int i = threadIdx.x; i < fours * owned && row < a.p.r; i += SINGLE_THREADS) {
-        const int64_t tok = t0 + i / owned * 4;
-        const float4 scale = *reinterpret_cast<const float4 *>(xs + i / owned * 4);
+        const int tok = i / owned * 4;
+        const float4 scale = *reinterpret_cast<const float4 *>(xs + tok);
         int4 s[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -392,7 +386,7 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
         const float f[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (tok + q < a.p.n) y[(tok + q) * a.p.r] = to_result<Y>(f[q]);
+          if (tok + q < n) y[(int64_t)(tok + q) * a.p.r] = to_result<Y>(f[q]);
       }
     }
     // No CTA's memory goes while sums may be on their way to it: one that gave up waits until
@@ -486,23 +480,21 @@ int int8_split(const Int8Args &p, int sms) {   // the widest split that finds ro
   return 1;
 }
 
-int launch_int8_single(const Int8Args &p, cudaStream_t st) {
-  SingleArgs a{};
+namespace {
+
+// What a launch takes but its tensor maps and the status word.
+int single_plan(const Int8Args &p, int sms, SingleArgs &a, unsigned &ctas, size_t &bytes) {
+  const int layers = p.gated ? 2 : 1, slabs = (p.d + SLAB - 1) / SLAB;
+  const int split = p.n > FEW_TOKENS ? int8_split(p, sms) : 0;
+  if (split == 1) return GPTQ_ERR_INVALID_ARG;   // (more than 64 tokens: only with k split)
   a.p = p;
-  const int sms = num_sms(), layers = p.gated ? 2 : 1;
-  const int slabs = (p.d + SLAB - 1) / SLAB;
-  // tokens in equal parts
-  const int64_t parts = (p.n + TOKENS - 1) / TOKENS;
-  a.N = (int)((p.n + parts * 16 - 1) / (parts * 16) * 16);
-  const int64_t nN = (p.n + a.N - 1) / a.N;
-  const Shape shape = p.n <= FEW_TOKENS ? shape_for(p.r, slabs, a.N, p.gated, sms) : Shape{ROWS, int8_split(p, sms), false};
+  a.N = (int)((p.n + 15) / 16 * 16);
+  const Shape shape = split ? Shape{ROWS, split, false} : shape_for(p.r, slabs, a.N, p.gated, sms);
   a.rows = shape.rows;
   a.ctas_k = shape.ctas_k;
-  const int64_t nM = (p.r + a.rows - 1) / a.rows;
-  if (nM * nN > INT32_MAX / 8) return GPTQ_ERR_INVALID_ARG;
-  a.nM = (int)nM;
-  a.nN = (int)nN;
-  const int64_t tiles = nM * nN;
+  const int64_t tiles = (p.r + a.rows - 1) / a.rows;
+  if (tiles > INT32_MAX / 8) return GPTQ_ERR_INVALID_ARG;
+  a.tiles = (int)tiles;
   // stages of 16 KB of W, at least four of them
   const size_t room = shape.shared ? SHARED_SM : SINGLE_SMEM, slab = (size_t)(layers * a.rows + a.N) * SLAB;
   a.deep = ROWS / a.rows;
@@ -520,15 +512,35 @@ int launch_int8_single(const Int8Args &p, cudaStream_t st) {
   a.stages = fit > STAGES ? STAGES : (int)fit;
   const int64_t work = a.ctas_k > 1 ? (steps + a.ctas_k - 1) / a.ctas_k : (tiles + sms - 1) / sms * steps;
   if (a.stages > work) a.stages = (int)work;   // no more than there are steps
-  size_t bytes = a.stages * stage;
+  bytes = a.stages * stage;
   a.slots = apart ? (int)bytes : 0;
   bytes += apart;
   if (bytes < meet) bytes = meet;
   bytes += pad;
   if (bytes < LEAST_SMEM) bytes = LEAST_SMEM;
-  a.buffers = a.ctas_k == 1 && 2 * layers * a.N <= (shape.shared ? 256 : 512) ? 2 : 1;
   a.columns = 32;
-  while (a.columns < (uint32_t)(a.buffers * layers * a.N)) a.columns *= 2;
+  while (a.columns < (uint32_t)((a.ctas_k > 1 ? 1 : 2) * layers * a.N)) a.columns *= 2;
+  const int64_t most = shape.shared ? 2 * sms : sms;
+  ctas = (unsigned)(a.ctas_k > 1 ? tiles * a.ctas_k : (tiles < most ? tiles : most));
+  return GPTQ_OK;
+}
+
+}  // namespace
+
+int int8_single_plan(const Int8Args &p, int sms, Int8Plan &plan) {
+  SingleArgs a{};
+  unsigned ctas;
+  size_t bytes;
+  if (const int rc = single_plan(p, sms, a, ctas, bytes)) return rc;
+  plan = Int8Plan{false, (int)ctas, a.ctas_k, a.N, a.rows, a.stages, (int)a.columns, bytes + 1024 + sizeof(SingleShared)};
+  return GPTQ_OK;
+}
+
+int launch_int8_single(const Int8Args &p, cudaStream_t st) {
+  SingleArgs a{};
+  unsigned ctas;
+  size_t bytes;
+  if (const int rc = single_plan(p, num_sms(), a, ctas, bytes)) return rc;
   a.status = device_status_word();
   if (!a.status) return GPTQ_ERR_CUDA;
   CUtensorMap tx, tw, tu;
@@ -537,8 +549,6 @@ int launch_int8_single(const Int8Args &p, cudaStream_t st) {
   tu = tw;
   if (p.gated)
     if (const int rc = int8_map(&tu, p.w[1], p.r, p.d, a.rows)) return rc;
-  const int64_t most = shape.shared ? 2 * sms : sms;
-  const unsigned ctas = (unsigned)(a.ctas_k > 1 ? tiles * a.ctas_k : (tiles < most ? tiles : most));
   if (!p.gated) return launch_act<false, GPTQ_ACT_NONE>(a, tx, tw, tu, ctas, bytes, st);
   switch (p.activation) {
     case GPTQ_ACT_NONE: return launch_act<true, GPTQ_ACT_NONE>(a, tx, tw, tu, ctas, bytes, st);
