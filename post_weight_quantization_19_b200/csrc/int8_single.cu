@@ -30,7 +30,15 @@ constexpr int STAGES = 12;                // at most
 constexpr int SINGLE_THREADS = 32 * 6;
 constexpr size_t SINGLE_SMEM = 208 * 1024;
 constexpr size_t SHARED_SM = 102 * 1024;  // where two CTAs share an SM
-constexpr size_t LEAST_SMEM = 48 * 1024;  // the solve's products hold 185 KB or more
+// Tensor memory is taken CTA by CTA, without a limit on the wait, and the CTAs of a cluster then
+// wait for each other.  So CTAs of several streams' kernels that meet on one SM must never ask
+// for more than its 512 columns together: two clusters could each hold what the other waits
+// for.  Shared memory keeps them apart, 228 KB to an SM.  At least LEAST_SMEM each, 57 KB with
+// what is static: three at most, of 128 columns or fewer.  With more, up to 256, at least
+// WIDE_SMEM: two of them leave no room for a third.  (Kernels that take all columns leave none
+// for any of these: 185 KB or more, or the packed layer's 768 threads of 72 registers or more.)
+constexpr size_t SM_SMEM = 228 * 1024, CTA_RESERVED = 1024;
+constexpr size_t LEAST_SMEM = 48 * 1024, WIDE_SMEM = 78 * 1024;
 
 struct SingleArgs {
   Int8Args p;
@@ -54,6 +62,10 @@ struct SingleShared {
   alignas(16) uint16_t stage[4][16 * 32];   // results on their way out, per warp: [token][row]
   alignas(16) float xs[4][TOKENS];          // scales of a tile's tokens, per warp
 };
+
+constexpr size_t smem_held(size_t bytes) { return bytes + 1024 + sizeof(SingleShared) + CTA_RESERVED; }
+static_assert(4 * smem_held(LEAST_SMEM) > SM_SMEM, "more CTAs to an SM than columns of tensor memory");
+static_assert(2 * smem_held(WIDE_SMEM) + smem_held(LEAST_SMEM) > SM_SMEM, "more columns asked for than there are");
 
 __device__ __forceinline__ void single_timeout(int *status, SingleShared &sh) {
   atomicCAS(status, 0, (int)GPTQ_ERR_TIMEOUT);
@@ -197,7 +209,7 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
   const uint32_t tmem = sh.tmem_base;
   // Tensor memory is there before the next kernel may start, so that its CTAs cannot take it
   // from one that they wait for.  (Products of the solve, which take it later, leave no CTA
-  // of this kernel room beside them: LEAST_SMEM.  Taken behind the wait: one token x
+  // of this kernel room beside them.  Taken behind the wait: one token x
   // 4096 x 4096 8.0 us, not 7.3.)
   pdl_wait_then_release();
 
@@ -517,9 +529,10 @@ int single_plan(const Int8Args &p, int sms, SingleArgs &a, unsigned &ctas, size_
   bytes += apart;
   if (bytes < meet) bytes = meet;
   bytes += pad;
-  if (bytes < LEAST_SMEM) bytes = LEAST_SMEM;
   a.columns = 32;
   while (a.columns < (uint32_t)((a.ctas_k > 1 ? 1 : 2) * layers * a.N)) a.columns *= 2;
+  const size_t least = a.columns > 128 ? WIDE_SMEM : LEAST_SMEM;
+  if (bytes < least) bytes = least;
   const int64_t most = shape.shared ? 2 * sms : sms;
   ctas = (unsigned)(a.ctas_k > 1 ? tiles * a.ctas_k : (tiles < most ? tiles : most));
   return GPTQ_OK;

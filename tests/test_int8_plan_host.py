@@ -5,6 +5,8 @@ import ctypes
 import random
 
 SMEM_CTA = 227 * 1024      # most shared memory of a CTA
+SMEM_SM = 228 * 1024       # of an SM, 1 KB of it reserved for each CTA
+COLUMNS_SM = 512           # of tensor memory
 
 
 def plan(lib, n, r, d, gated, sms=148):
@@ -57,3 +59,22 @@ def test_single_ctas_take_all_tokens_in_one_tile(lib):
             assert n <= 64 and p["ctas"] <= min(tiles, 2 * sms), case
     assert {(0, 8, False), (0, 4, False), (1, 8, False), (1, 4, False), (1, 2, False), (0, 1, False), (1, 1, False),
             (0, 8, True), (1, 8, True)} <= seen, sorted(seen)
+
+
+def test_ctas_that_fit_on_an_sm_together_find_their_tensor_memory(lib):
+    # Each CTA takes its columns without a limit on the wait, and CTAs of a cluster then wait for
+    # each other: if those that shared memory lets onto an SM together, of whatever streams'
+    # kernels, could ask for more columns than it has, two clusters could hold what the
+    # other waits for.
+    least = {}   # columns -> least shared memory that goes with them, and where
+    for n, r, d, gated, sms in sizes():
+        p = plan(lib, n, r, d, gated, sms)
+        held = p["smem"] + 1024
+        if held < least.get(p["columns"], (1 << 30,))[0]:
+            least[p["columns"]] = held, (n, r, d, gated, sms)
+    assert set(least) == {32, 64, 128, 256, 512}
+
+    def most(room, columns):   # columns that the CTAs in this much shared memory can ask for
+        return max([0] + [c + most(room - held, c) for c, (held, _) in least.items() if held <= room and c <= columns])
+
+    assert most(SMEM_SM, COLUMNS_SM) <= COLUMNS_SM, least
