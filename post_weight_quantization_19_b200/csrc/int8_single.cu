@@ -27,6 +27,9 @@ constexpr int ROWS = 128;                 // rows of W per tile (UMMA M)
 constexpr int SLAB = 128;                 // columns per stage
 constexpr int TOKENS = 256;               // most tokens (UMMA N), of both layers' sums together
 constexpr int STAGES = 12;                // at most
+// Waits of a CTA that may run out one behind the other before it sends its sums: the loader's for
+// a free stage and for the last load of each, the MMAs' for an accumulator, a stage and their end.
+constexpr int SETTLE = STAGES + 4;
 constexpr int SINGLE_THREADS = 32 * 6;
 constexpr size_t SINGLE_SMEM = 208 * 1024;
 constexpr size_t SHARED_SM = 102 * 1024;  // where two CTAs share an SM
@@ -367,8 +370,6 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
         }
       }
     }
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // this CTA's sums are on their way
     // what the results need, while the sums arrive: a thread keeps to one row
     const int64_t row = (int64_t)cta * a.rows + crank * owned + threadIdx.x % owned;   // SINGLE_THREADS % owned == 0
     const Row par = row_of<GATED>(a.p, row);
@@ -401,11 +402,12 @@ __global__ void __launch_bounds__(SINGLE_THREADS, 1)
           if (tok + q < n) y[(int64_t)(tok + q) * a.p.r] = to_result<Y>(f[q]);
       }
     }
-    // No CTA's memory goes while sums may be on their way to it: one that gave up waits until
-    // every CTA has sent its own, and then for them to land.
-    __syncwarp();
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (*(volatile int *)&sh.abort) (void)mbar_wait_bounded(&sh.sums, 0);
+    // No CTA's memory goes while sums may be on their way to it: one that gave up stays until
+    // they have landed.  Every CTA sends its own, after SETTLE waits that ran out at most.
+    // (A cluster barrier in every launch's way out cost 0.1 to 0.5 us.)
+    if (*(volatile int *)&sh.abort)
+      for (int i = 0; i < SETTLE && !mbar_wait_bounded(&sh.sums, 0); ++i) {
+      }
   }
   tc_fence_before();
   __syncthreads();
