@@ -460,6 +460,8 @@ int gptq_int8_linear(const int8_t *x, const float *x_scales, int64_t n, const in
  *             gate_scales and up_scales device fp32 [r].
  *   gate_bias, up_bias  device [r] of `ytype`, or NULL, each by itself.
  *   activation  GPTQ_ACT_*.
+ *   act is within 6e-7 of its value (gelu of a negative g: 1e-7 g^2 more, for the rounding
+ *   of its argument).  In results of 16 bits an act below 1e-35 may count as zero.
  *   Other arguments and conditions as gptq_int8_linear.
  */
 int gptq_int8_gated(const int8_t *x, const float *x_scales, int64_t n, const int8_t *gate,

@@ -7,17 +7,6 @@
 
 namespace gptq {
 
-// In fp32, within 6e-7 of the value (gelu of a negative v: 1e-7 v^2 more, its argument's
-// rounding).  A NaN stays one.
-template <int ACT>
-__device__ __forceinline__ float activate(float v) {
-  if constexpr (ACT == GPTQ_ACT_RELU) return v < 0.f ? 0.f : v;
-  if constexpr (ACT == GPTQ_ACT_SILU) return __fdividef(v, 1.f + expf(-v));
-  // (not 1 + erf, which cancels for negative v)
-  if constexpr (ACT == GPTQ_ACT_GELU) return 0.5f * v * erfcf(v * -0.707106781186547524f);
-  return v;
-}
-
 __device__ __forceinline__ float exp2_approx(float v) {   // within 2^-22
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -27,6 +16,22 @@ __device__ __forceinline__ float reciprocal_approx(float v) {   // within 2^-23;
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
+}
+
+// In fp32, within 6e-7 of the value (gelu of a negative v: 1e-7 v^2 more, its argument's
+// rounding) and, of values that fp32 holds with fewer digits, 3e-43.  A NaN stays one.
+template <int ACT>
+__device__ __forceinline__ float activate(float v) {
+  if constexpr (ACT == GPTQ_ACT_RELU) return v < 0.f ? 0.f : v;
+  if constexpr (ACT == GPTQ_ACT_SILU) {
+    // (of a negative v as v exp(v) / (1 + exp(v)): 1 + exp(-v) passes what has a reciprocal, 2^126,
+    // where the value is still 1e-36)
+    const float e = expf(-fabsf(v));
+    return (v < 0.f ? v * e : v) * reciprocal_approx(1.f + e);
+  }
+  // (not 1 + erf, which cancels for negative v)
+  if constexpr (ACT == GPTQ_ACT_GELU) return 0.5f * v * erfcf(v * -0.707106781186547524f);
+  return v;
 }
 // Two fp32 numbers that one instruction works on.
 struct F2 {
