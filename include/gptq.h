@@ -460,8 +460,9 @@ int gptq_int8_linear(const int8_t *x, const float *x_scales, int64_t n, const in
  *             gate_scales and up_scales device fp32 [r].
  *   gate_bias, up_bias  device [r] of `ytype`, or NULL, each by itself.
  *   activation  GPTQ_ACT_*.
- *   act is within 6e-7 of its value (gelu of a negative g: 1e-7 g^2 more, for the rounding
- *   of its argument).  In results of 16 bits an act below 1e-35 may count as zero.
+ *   act is within 6e-7 of its value, in results of 16 bits within 1e-6 (gelu of a negative g:
+ *   1e-7 g^2 more, for the rounding of its argument).  In results of 16 bits an act below 1e-35
+ *   may count as zero.
  *   Other arguments and conditions as gptq_int8_linear.
  */
 int gptq_int8_gated(const int8_t *x, const float *x_scales, int64_t n, const int8_t *gate,
@@ -484,7 +485,8 @@ int gptq_int8_gated(const int8_t *x, const float *x_scales, int64_t n, const int
  *   The outputs share no memory with each other or with an input:
  *   GPTQ_ERR_INVALID_ARG.
  *   u is not rounded: codes and scale are those of the formula in 64 bits, the scale
- *   rounded once.  A row with a u that is NaN or infinite has scale NaN, codes 0 and xhat
+ *   rounded once.  (silu and gelu are formed to 1e-13 of their value there: where
+ *   127 u / max|u| is within 3e-11 of half way between two codes, it may be either.)  A row with a u that is NaN or infinite has scale NaN, codes 0 and xhat
  *   NaN; other rows are not touched by it.
  *   n == 0: nothing to do.  Asynchronous: one kernel.
  */
@@ -620,6 +622,21 @@ int gptq_selftest_timeout(float *buf, gptq_stream_t stream);
 int gptq_selftest_int8_timeout(const int8_t *x, const float *x_scales, int64_t n, const int8_t *w,
                                const float *w_scales, int64_t r, int64_t d, int what, float *y,
                                gptq_stream_t stream);
+
+/*
+ * gptq_selftest_activation -- the activation functions by themselves, for checks of how exact
+ * they are.
+ *
+ *   v         device fp32 [n];  activation  GPTQ_ACT_*.
+ *   values    device fp32 [3 x n], written: as gptq_int8_gated forms fp32 results; as it forms
+ *             those of 16 bits; as gptq_activation_int8 forms its values, for v that are numbers
+ *             of 16 bits.
+ *   values64  device fp64 [n], written: as gptq_activation_int8 forms a value again that lies near
+ *             a border between two codes.
+ * Asynchronous.
+ */
+int gptq_selftest_activation(const float *v, int64_t n, int activation, float *values, double *values64,
+                             gptq_stream_t stream);
 
 /*
  * gptq_int8_plan -- a host-only diagnostic of gptq_int8_linear (gated 0) and gptq_int8_gated

@@ -75,6 +75,7 @@ SIGNATURES = {
     "gptq_set_phase_timing": (c_int, [c_int]),
     "gptq_last_phase_ms": (c_int, [c_void_p, c_int]),
     "gptq_factor_plan": (c_size_t, [c_int64, c_int64, c_int, c_void_p, c_size_t]),
+    "gptq_selftest_activation": (c_int, [c_void_p, c_int64, c_int, c_void_p, c_void_p, c_void_p]),
     "gptq_int8_plan": (c_int, [c_int64, c_int64, c_int64, c_int, c_int, c_void_p]),
     "gptq_selftest_timeout": (c_int, [c_void_p, c_void_p]),
     "gptq_selftest_int8_timeout": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_int64,

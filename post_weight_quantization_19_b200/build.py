@@ -20,7 +20,7 @@ SOURCES = ["hessian_tc.cu", "gemm_tc.cu", "factor.cu", "leaf.cu", "sweep.cu", "p
            "noalloc.cu", "gemv.cu", "linear_tc.cu", "rmsnorm.cu", "regroup.cu",
            "packed_linear.cu", "packed_few_f16.cu", "packed_few_bf16.cu", "packed_few_i8.cu", "packed_many.cu",
            "packed_many_f32.cu", "int8_weights.cu", "int8_linear.cu", "int8_single.cu", "int8_pair.cu",
-           "activation_f16.cu", "activation_bf16.cu"]
+           "activation_f16.cu", "activation_bf16.cu", "activation_values.cu"]
 
 
 def nvcc() -> str:

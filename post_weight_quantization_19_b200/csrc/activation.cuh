@@ -74,11 +74,12 @@ __device__ __forceinline__ F2 exp_fast(const F2 &v) {
 }
 
 // The same functions of two numbers of 16 bits (whose squares are exact) in fewer
-// instructions, within 4.3e-7 of the value (of all there are), values below 1e-35 lost.
-// WHOLE: for arguments of fp32's whole range, infinities among them; else silu of a v above
-// 2.3e38 is NaN, and gelu of one beyond 1e19.  gelu: erfc(z) exp(z^2)
-// / 2 is t = 1 / (1 + |v| / 4) times a polynomial in t, z = |v| / sqrt 2: the one of degree
-// 8 with the least relative error (5e-8) up to |v| = 13.5, by reweighted least squares.
+// instructions, within 4.3e-7 of the value (of all there are: the tests go through them), values
+// below 1e-35 lost.  WHOLE: for arguments of fp32's whole range, infinities among them, of which
+// 1e-6 (gelu: and 3.1e-8 v^2, the square's rounding); else silu of a v above 2.3e38 is NaN, and gelu
+// of one beyond 1e19.  gelu: erfc(z) exp(z^2) / 2 is t = 1 / (1 + |v| / 4) times a polynomial in
+// t, z = |v| / sqrt 2: the one of degree 8 with the least relative error up to |v| = 13.5, by
+// reweighted least squares, 7.1e-8 with its coefficients in fp32.
 template <int ACT, bool WHOLE>
 __device__ __forceinline__ F2 activate_fast(const F2 &v) {
   if constexpr (ACT == GPTQ_ACT_SILU) {
@@ -147,8 +148,11 @@ __device__ __forceinline__ double reciprocal64(double v) {
 }
 
 // activate64 for single values of rows that stay inside fp32's range, in fewer dependent
-// steps, to 1e-13 of the value, values below 1e-32 lost.  gelu: erfc as in activate_fast, by the
-// interpolation in 16 Chebyshev points for |v| up to 14 (3e-14), t = 1 / (1 + |v| / 5).
+// steps, to 1e-13 of a value of at least 1e-31 (others are not asked for: a u that is not coded as
+// 0 is 1e-22 / 254 or more, and up 1e6 at most).  gelu: erfc as in activate_fast, by the
+// interpolation in 16 Chebyshev points for |v| up to 14 (2.9e-14), t = 1 / (1 + |v| / 5); exp64
+// of a square that is off by 2^-53 of up to 98.  A code's 127 u / max|u| is good to
+// 127 (2e-13 + four roundings) < 3e-11.
 // (4096 x 11008 gated silu 60.0 us, 500 x 49152 gated gelu 70; with activate64 61.6, 76)
 template <int ACT>
 __device__ __forceinline__ double activate64_single(double v) {

@@ -57,7 +57,7 @@ __device__ __forceinline__ float scaled_sum(int sum, float xs, float ws, float b
 }
 
 // A gated result from its two sums in fp32: what a type of 16 bits takes is formed in fewer
-// instructions (within 6e-6 of the value for gelu, whose arguments are rounded here).
+// instructions (activate_fast).
 template <int ACT, typename Y>
 __device__ __forceinline__ F2 gated_pair(const F2 &g, const F2 &u) {
   if constexpr (sizeof(Y) == 2) return mul2(activate_fast<ACT, true>(g), u);
