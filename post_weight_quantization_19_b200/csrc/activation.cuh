@@ -64,11 +64,12 @@ __device__ __forceinline__ F2 add2(const F2 &a, const F2 &b) {
   return numbers(r);
 }
 
-// exp(v) within 4e-7 of it, |v| <= 88: 2^t with t = v log2 e rounded, and what t is off by, a
-// few 1e-6 at most, to first order (ln 2 in two parts).
+// exp(v) within 3e-7 of it, |v| <= 88: 2^t with t = v log2 e rounded, and what v - t ln 2 leaves, a
+// few 1e-6 at most, to first order.  (ln 2 as the nearest fp32 number and the rest of it: a fused
+// multiply-add rounds once v has cancelled the product.)
 __device__ __forceinline__ F2 exp_fast(const F2 &v) {
   const F2 t = mul2(v, both(1.44269504088896341f));
-  const F2 rest = fma2(t, both(-1.42860677e-6f), fma2(t, both(-0.693145751953125f), v));
+  const F2 rest = fma2(t, both(1.90465430e-9f), fma2(t, both(-0.693147182f), v));
   const F2 e{exp2_approx(t.x), exp2_approx(t.y)};
   return fma2(e, rest, e);
 }
