@@ -633,7 +633,7 @@ int gptq_selftest_int8_timeout(const int8_t *x, const float *x_scales, int64_t n
  *             of 16 bits.
  *   values64  device fp64 [n], written: as gptq_activation_int8 forms a value again that lies near
  *             a border between two codes.
- * Asynchronous.
+ *   The three share no memory: GPTQ_ERR_INVALID_ARG.  Asynchronous.
  */
 int gptq_selftest_activation(const float *v, int64_t n, int activation, float *values, double *values64,
                              gptq_stream_t stream);
@@ -648,7 +648,7 @@ int gptq_selftest_activation(const float *v, int64_t n, int activation, float *v
  *         stages of shared memory;  columns of tensor memory per CTA;  bytes of shared
  *         memory per CTA.
  * Returns GPTQ_OK, or GPTQ_ERR_INVALID_ARG for sizes that those refuse, n, r or plan of 0, or
- * sms < 2.
+ * sms outside [2, 4096].
  */
 int gptq_int8_plan(int64_t n, int64_t r, int64_t d, int gated, int sms, int64_t *plan);
 

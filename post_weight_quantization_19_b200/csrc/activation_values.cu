@@ -2,6 +2,7 @@
 // their values are.
 #include "activation.cuh"
 #include "launch_after.h"
+#include "overlap.h"
 
 namespace gptq {
 namespace {
@@ -33,6 +34,8 @@ extern "C" int gptq_selftest_activation(const float *v, int64_t n, int activatio
   if (!v || !values || !values64 || reinterpret_cast<uintptr_t>(v) % 4 || reinterpret_cast<uintptr_t>(values) % 4 ||
       reinterpret_cast<uintptr_t>(values64) % 8)
     return GPTQ_ERR_INVALID_ARG;
+  const Span in = {v, (size_t)n * 4}, out = {values, (size_t)n * 12}, out64 = {values64, (size_t)n * 8};
+  if (overlap(in, out) || overlap(in, out64) || overlap(out, out64)) return GPTQ_ERR_INVALID_ARG;
   const auto kernel = activation == GPTQ_ACT_NONE   ? activation_values_kernel<GPTQ_ACT_NONE>
                       : activation == GPTQ_ACT_RELU ? activation_values_kernel<GPTQ_ACT_RELU>
                       : activation == GPTQ_ACT_SILU ? activation_values_kernel<GPTQ_ACT_SILU>

@@ -116,7 +116,7 @@ extern "C" int gptq_selftest_int8_timeout(const int8_t *x, const float *x_scales
 }
 
 extern "C" int gptq_int8_plan(int64_t n, int64_t r, int64_t d, int gated, int sms, int64_t *plan) {
-  if (!valid_sizes(n, r, d) || n == 0 || r == 0 || sms < 2 || !plan) return GPTQ_ERR_INVALID_ARG;
+  if (!valid_sizes(n, r, d) || n == 0 || r == 0 || sms < 2 || sms > 4096 || !plan) return GPTQ_ERR_INVALID_ARG;
   Int8Args a{};
   a.n = n;
   a.r = r;

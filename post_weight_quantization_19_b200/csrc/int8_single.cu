@@ -442,7 +442,7 @@ namespace {
 // Rows of W per tile, CTAs along k, and whether two CTAs share an SM, for up to 64 tokens,
 // which are bound by the copies of W: all SMs copying, with as few steps as it takes to
 // meet.  Measured (us; tiles of 128 rows split over 2, 4, 8 CTAs, and unsplit tiles that make
-// 148 or 296):
+// 148 or 296; the split ones take 0.2 to 0.3 less since there is one tile of tokens alone):
 //   1 token, 4096 x 4096     8.7, 7.7, 7.2   7.9, 10.4   (32 tiles)
 //   24 tokens, 4096 x 11008  15.9, 12.5, 11.6   15.8, 21.5
 //   16 tokens, 8192 x 8192   15.1, 14.4, 17.6   16.6, 15.9   (64 tiles)

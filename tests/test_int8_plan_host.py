@@ -29,7 +29,7 @@ def sizes(count=20000):
 def test_refusals(lib):
     out = (ctypes.c_int64 * 8)()
     for bad in ((0, 8, 64, 0, 148), (8, 0, 64, 0, 148), (-1, 8, 64, 0, 148), (8, -1, 64, 0, 148), (8, 8, 40, 0, 148),
-                (8, 8, 0, 0, 148), (8, 8, 65568, 0, 148), (1 << 31, 8, 64, 0, 148), (8, 8, 64, 0, 1)):
+                (8, 8, 0, 0, 148), (8, 8, 65568, 0, 148), (1 << 31, 8, 64, 0, 148), (8, 8, 64, 0, 1), (8, 8, 64, 0, 4097)):
         assert lib.gptq_int8_plan(*bad, out) == 1, bad
     assert lib.gptq_int8_plan(8, 8, 64, 0, 148, None) == 1
 

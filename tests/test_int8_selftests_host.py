@@ -18,6 +18,7 @@ def test_selftest_of_activations_refusals(lib):
     def call(v=X, n=4, act=2, values=Y, values64=W):
         return lib.gptq_selftest_activation(v, n, act, values, values64, None)
     for bad in (dict(n=-1), dict(n=1 << 31), dict(act=-1), dict(act=4), dict(v=None), dict(values=None),
-                dict(values64=None), dict(v=at(1, 2)), dict(values=at(9, 2)), dict(values64=at(3, 4))):
+                dict(values64=None), dict(v=at(1, 2)), dict(values=at(9, 2)), dict(values64=at(3, 4)),
+                dict(values=X), dict(values64=X), dict(values64=Y), dict(values64=at(9, 40))):
         assert call(**bad) == 1, bad
     assert call(n=0, v=None) == 0
